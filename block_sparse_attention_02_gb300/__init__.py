@@ -13,13 +13,13 @@ The pipelines at the bottom (``decode_step``, ``prefill_layer`` and
 from __future__ import annotations
 
 import ctypes as C
-from typing import Dict, Optional
+from typing import Dict, NamedTuple, Optional
 
 import torch
 
 from . import _abi
-from ._abi import (MSA_DEVERR_BAD_LEN, MSA_DEVERR_BAD_PAGE, MSA_DEVERR_BAD_SEL, MSA_DEVERR_TIMEOUT,
-                   MSA_MODE_CHUNK, MSA_MODE_DECODE, MSA_MODE_PREFILL, MSAError)
+from ._abi import (MSA_DEVERR_BAD_LEN, MSA_DEVERR_BAD_PAGE, MSA_DEVERR_BAD_SEL, MSA_DEVERR_NO_PAGES,
+                   MSA_DEVERR_TIMEOUT, MSA_MODE_CHUNK, MSA_MODE_DECODE, MSA_MODE_PREFILL, MSAError)
 
 __all__ = [
     "msa_index_score", "msa_topk_blocks", "msa_build_page_table", "msa_sparse_attn_prefill",
@@ -27,9 +27,12 @@ __all__ = [
     "msa_sparse_attn_decode_workspace_size", "msa_cache_append", "decode_step", "prefill_layer", "chunk_layer",
     "msa_dense_attn_decode", "msa_dense_attn_decode_workspace_size", "dense_decode_buffers", "dense_decode_step",
     "msa_dense_attn_prefill", "dense_prefill_layer",
+    "msa_plan_step", "msa_release_pages", "plan_buffers", "msa_qk_norm_rope", "Q4Cache", "q4_cache",
+    "msa_cache_append_q4", "msa_cache_expand_q4", "msa_attn_decode_q4_workspace_size", "msa_sparse_attn_decode_q4",
+    "msa_dense_attn_decode_q4", "decode_q4_buffers", "decode_step_q4",
     "lib", "MSAError",
     "MSA_MODE_PREFILL", "MSA_MODE_DECODE", "MSA_MODE_CHUNK", "MSA_DEVERR_TIMEOUT", "MSA_DEVERR_BAD_PAGE",
-    "MSA_DEVERR_BAD_SEL", "MSA_DEVERR_BAD_LEN", "Bk", "D", "dI",
+    "MSA_DEVERR_BAD_SEL", "MSA_DEVERR_BAD_LEN", "MSA_DEVERR_NO_PAGES", "Bk", "D", "dI",
 ]
 
 Bk = 128
@@ -448,6 +451,283 @@ def msa_cache_append(K_new: torch.Tensor, V_new: torch.Tensor, kidx_new: torch.T
 
 
 # ---------------------------------------------------------------------------
+# the serving step around the cache: page tables and slots, norm with rotation,
+# and the cache held in 4 bits
+# ---------------------------------------------------------------------------
+
+def _cuda(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device, dim: int) -> int:
+    """The pointer of a tensor that has to be of this type, device and number of dimensions."""
+    if t.dtype != dtype or t.dim() != dim or t.device != device:
+        raise ValueError(f"{name}: need a {dim}-dimensional {dtype} tensor on {device}, got {t.dim()} dimensions of "
+                         f"{t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+def _dense(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device, dim: int) -> int:
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return _cuda(t, name, dtype, device, dim)
+
+
+def _err_ptr(dev_err: Optional[torch.Tensor], device: torch.device):
+    if dev_err is None:
+        return None
+    if dev_err.numel() < 1:
+        raise ValueError("dev_err: need an int32 tensor of one value")
+    return _dense(dev_err, "dev_err", torch.int32, device, dev_err.dim())
+
+
+def _on(device: torch.device, stream, name: str, *args) -> None:
+    """Calls the entry point with the tensors' device current, on ``stream`` or on that device's current stream."""
+    if device.type != "cuda":
+        raise ValueError(f"{name}: tensors must be on a CUDA device, got {device}")
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif isinstance(stream, torch.cuda.Stream) and stream.device != device:
+        raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on {device}")
+    raw = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if torch.cuda.current_device() == device.index:
+        _abi.check(getattr(lib(), name)(*args, raw), name)
+    else:
+        with torch.cuda.device(device):
+            _abi.check(getattr(lib(), name)(*args, raw), name)
+
+
+def plan_buffers(B: int, N: int, device) -> Dict[str, torch.Tensor]:
+    """Outputs of ``msa_plan_step`` for B requests and N token rows."""
+    dev = torch.device(device)
+    i32 = dict(dtype=torch.int32, device=dev)
+    return {"seq_len_out": torch.empty(B, **i32), "free_count_out": torch.empty(1, **i32),
+            "cu": torch.empty(B + 1, **i32), "tok_slot": torch.empty(N, dtype=torch.int64, device=dev),
+            "tok_pos": torch.empty(N, **i32), "tok_seq": torch.empty(N, **i32)}
+
+
+def msa_plan_step(seq_len: torch.Tensor, new_len: torch.Tensor, seq_pt: torch.Tensor, free_pages: torch.Tensor,
+                  free_count: torch.Tensor, seq_len_out: torch.Tensor, free_count_out: torch.Tensor, cu: torch.Tensor,
+                  tok_slot: torch.Tensor, tok_pos: torch.Tensor, tok_seq: Optional[torch.Tensor] = None, *,
+                  num_pages: int, dev_err: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Pages, positions and slots of the new tokens of every request (see msa.h, page tables and token slots).
+
+    seq_len, new_len [B] int32 (cached and new tokens); seq_pt [B,max_pages] int32, written where pages are given;
+    free_pages [F] int32 with free_count [1] int32 (a stack of page ids).  Outputs: seq_len_out [B] (may be seq_len),
+    free_count_out [1] (may be free_count), cu [B+1], and for N token rows tok_slot [N] int64, tok_pos and tok_seq [N]
+    int32 (-1 in rows past the last token and in those of requests that were not served).
+    """
+    d, i32 = seq_len.device, torch.int32
+    B, N = seq_len.shape[0], tok_slot.shape[0]
+    if new_len.shape[0] != B or seq_pt.shape[0] != B or seq_len_out.shape[0] != B or cu.shape[0] != B + 1:
+        raise ValueError(f"B = {B}: new_len, seq_pt and seq_len_out need B rows, cu B + 1")
+    if tok_pos.shape[0] != N or (tok_seq is not None and tok_seq.shape[0] != N):
+        raise ValueError(f"tok_slot, tok_pos and tok_seq need the same number of rows, got {N}, {tok_pos.shape[0]}")
+    if free_count.numel() != 1 or free_count_out.numel() != 1:
+        raise ValueError("free_count and free_count_out hold one value")
+    a = _abi.PlanArgs(
+        B, Bk, N, _dense(seq_len, "seq_len", i32, d, 1), _dense(new_len, "new_len", i32, d, 1),
+        _dense(seq_pt, "seq_pt", i32, d, 2), seq_pt.shape[1], _dense(free_pages, "free_pages", i32, d, 1),
+        free_pages.shape[0], _dense(free_count, "free_count", i32, d, 1), num_pages,
+        _dense(seq_len_out, "seq_len_out", i32, d, 1), _dense(free_count_out, "free_count_out", i32, d, 1),
+        _dense(cu, "cu", i32, d, 1), _dense(tok_slot, "tok_slot", torch.int64, d, 1),
+        _dense(tok_pos, "tok_pos", i32, d, 1), None if tok_seq is None else _dense(tok_seq, "tok_seq", i32, d, 1),
+        _err_ptr(dev_err, d))
+    _on(d, stream, "msa_plan_step", a)
+
+
+def msa_release_pages(seq_len: torch.Tensor, done: torch.Tensor, seq_pt: torch.Tensor, free_pages: torch.Tensor,
+                      free_count: torch.Tensor, seq_len_out: torch.Tensor, free_count_out: torch.Tensor, *,
+                      dev_err: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Returns the pages of every request with done[b] != 0 to the stack (see msa.h, msa_release_pages).
+
+    seq_len, done [B] int32, seq_pt [B,max_pages] int32 (left as it is), free_pages [F] int32 (written above
+    free_count), free_count [1]; seq_len_out [B] and free_count_out [1] may be the inputs.
+    """
+    d, i32 = seq_len.device, torch.int32
+    B = seq_len.shape[0]
+    if done.shape[0] != B or seq_pt.shape[0] != B or seq_len_out.shape[0] != B:
+        raise ValueError(f"B = {B}: done, seq_pt and seq_len_out need B rows")
+    if free_count.numel() != 1 or free_count_out.numel() != 1:
+        raise ValueError("free_count and free_count_out hold one value")
+    a = _abi.ReleaseArgs(
+        B, Bk, _dense(seq_len, "seq_len", i32, d, 1), _dense(done, "done", i32, d, 1),
+        _dense(seq_pt, "seq_pt", i32, d, 2), seq_pt.shape[1], _dense(free_pages, "free_pages", i32, d, 1),
+        free_pages.shape[0], _dense(free_count, "free_count", i32, d, 1),
+        _dense(seq_len_out, "seq_len_out", i32, d, 1), _dense(free_count_out, "free_count_out", i32, d, 1),
+        _err_ptr(dev_err, d))
+    _on(d, stream, "msa_release_pages", a)
+
+
+def msa_qk_norm_rope(Q: torch.Tensor, K: Optional[torch.Tensor], pos: torch.Tensor, inv_freq: Optional[torch.Tensor],
+                     Q_out: torch.Tensor, K_out: Optional[torch.Tensor], *, V: Optional[torch.Tensor] = None,
+                     V_out: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
+                     q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                     eps: float = 1e-6, interleaved: bool = False, dev_err: Optional[torch.Tensor] = None,
+                     stream=None) -> None:
+    """RMS norm of every query and key head and the position rotation, in one pass (see msa.h).
+
+    Q [N,Hq,D], K and V [N,Hkv,D] bf16 (any token and head strides, innermost contiguous; D = 64 or 128), pos [N] int32,
+    inv_freq [rot/2] fp32 (None: no rotation), q_weight and k_weight [D] bf16 or fp32 (None: no norm).  Q_out [N,Hq,D];
+    K_out [N,Hkv,D], or with ``slots`` [N] int64 the page pool [P,Hkv,Bk,D] that K goes into, and V into V_out.
+    Q_out may be Q and K_out may be K.  Rows with pos < 0 are left out.
+    """
+    d, bf16 = Q.device, torch.bfloat16
+    N, Hq, D_ = Q.shape
+    Hkv = 0 if K is None else K.shape[1]
+    if (K is None) != (K_out is None) or (K is None and (V is not None or slots is not None)):
+        raise ValueError("K, K_out, V and slots: K and K_out go together, V and slots need them")
+    if Q_out.shape != Q.shape or pos.shape[0] != N or (K is not None and K.shape != (N, Hkv, D_)) or (
+            V is not None and V.shape != K.shape):
+        raise ValueError("Q and Q_out [N,Hq,D], K and V [N,Hkv,D] and pos [N] must agree")
+    pools = [x for x in (K_out, V_out) if x is not None]
+    for x in pools:
+        if slots is None and x.shape != (N, Hkv, D_):
+            raise ValueError("K_out must be [N,Hkv,D] without slots")
+        if slots is not None and (x.dim() != 4 or x.shape != (K_out.shape[0], Hkv, Bk, D_)):
+            raise ValueError(f"K_out and V_out must be pools [P,Hkv,{Bk},D] with slots")
+    if slots is not None and slots.shape[0] != N:
+        raise ValueError("slots must be [N]")
+    fp32 = False
+    for w, nm in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            if w.shape != (D_,) or w.dtype not in (bf16, torch.float32):
+                raise ValueError(f"{nm} must be [{D_}], bf16 or fp32")
+            fp32 = w.dtype == torch.float32
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise ValueError("q_weight and k_weight must have one type")
+    for x, nm in ((Q, "Q"), (K, "K"), (V, "V"), (Q_out, "Q_out"), (K_out, "K_out"), (V_out, "V_out")):
+        if x is not None and x.numel() > 0:
+            _inner_contig(x, nm)
+    wt = torch.float32 if fp32 else bf16
+    kd = 3 if slots is None else 4
+    a = _abi.NormRopeArgs(
+        N, Hq, Hkv, D_, Bk, 0 if inv_freq is None else 2 * inv_freq.shape[0], int(interleaved), int(fp32), eps,
+        _cuda(Q, "Q", bf16, d, 3), Q.stride()[:2],
+        *((None, (0, 0)) if K is None else (_cuda(K, "K", bf16, d, 3), K.stride()[:2])),
+        *((None, (0, 0)) if V is None else (_cuda(V, "V", bf16, d, 3), V.stride()[:2])),
+        _dense(pos, "pos", torch.int32, d, 1),
+        None if inv_freq is None else _dense(inv_freq, "inv_freq", torch.float32, d, 1),
+        None if q_weight is None else _dense(q_weight, "q_weight", wt, d, 1),
+        None if k_weight is None else _dense(k_weight, "k_weight", wt, d, 1),
+        _cuda(Q_out, "Q_out", bf16, d, 3), Q_out.stride()[:2],
+        *((None, (0, 0, 0)) if K_out is None else (_cuda(K_out, "K_out", bf16, d, kd), K_out.stride()[:kd - 1])),
+        *((None, (0, 0, 0)) if V_out is None else (_cuda(V_out, "V_out", bf16, d, kd), V_out.stride()[:kd - 1])),
+        None if slots is None else _dense(slots, "slots", torch.int64, d, 1),
+        0 if slots is None else K_out.shape[0], _err_ptr(dev_err, d))
+    _on(d, stream, "msa_qk_norm_rope", a)
+
+
+class Q4Cache(NamedTuple):
+    """A paged K/V cache in 4 bits (see msa.h): codes [P,Hkv,Bk,D/2] and scales [P,Hkv,Bk,D/16], uint8, and one
+    power of two for each of K and V."""
+    K_codes: torch.Tensor
+    K_scales: torch.Tensor
+    V_codes: torch.Tensor
+    V_scales: torch.Tensor
+    k_scale: float = 1.0
+    v_scale: float = 1.0
+
+
+def q4_cache(num_pages: int, Hkv: int, device, k_scale: float = 1.0, v_scale: float = 1.0) -> Q4Cache:
+    """A 4-bit cache of zeros."""
+    def pool(last):
+        return torch.zeros(num_pages, Hkv, Bk, last, dtype=torch.uint8, device=torch.device(device))
+    return Q4Cache(pool(D // 2), pool(D // 16), pool(D // 2), pool(D // 16), k_scale, v_scale)
+
+
+def _q4_args(c: Q4Cache, d: torch.device) -> _abi.Q4CacheArgs:
+    P, Hkv = c.K_codes.shape[:2]
+    u8, cs, ss = torch.uint8, c.K_codes.stride(), c.K_scales.stride()
+    if c.K_codes.shape != (P, Hkv, Bk, D // 2) or c.V_codes.shape != c.K_codes.shape or c.K_scales.shape != (
+            P, Hkv, Bk, D // 16) or c.V_scales.shape != c.K_scales.shape:
+        raise ValueError(f"a 4-bit cache has codes [P,Hkv,{Bk},{D // 2}] and scales [P,Hkv,{Bk},{D // 16}]")
+    if c.V_codes.stride() != cs or c.V_scales.stride() != ss or cs[2:] != (D // 2, 1) or ss[2:] != (D // 16, 1):
+        raise ValueError("a 4-bit cache's K and V must share strides, and a block's rows be contiguous")
+    return _abi.Q4CacheArgs(_cuda(c.K_codes, "K_codes", u8, d, 4), _cuda(c.K_scales, "K_scales", u8, d, 4),
+                            _cuda(c.V_codes, "V_codes", u8, d, 4), _cuda(c.V_scales, "V_scales", u8, d, 4),
+                            cs[:2], ss[:2], P, c.k_scale, c.v_scale)
+
+
+def msa_cache_append_q4(K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, cache: Q4Cache, *,
+                        dev_err: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Stores K, V [N,Hkv,D] bf16 in 4 bits at slots [N] int64 (page * Bk + row; < 0: not stored) (see msa.h)."""
+    d, bf16 = K.device, torch.bfloat16
+    N, Hkv, D_ = K.shape
+    if V.shape != K.shape or slots.shape[0] != N or cache.K_codes.shape[1] != Hkv:
+        raise ValueError("K and V [N,Hkv,D], slots [N] and the cache's heads must agree")
+    if N > 0:
+        _inner_contig(K, "K")
+        _inner_contig(V, "V")
+    a = _abi.AppendQ4Args(N, Hkv, D_, Bk, _cuda(K, "K", bf16, d, 3), K.stride()[:2], _cuda(V, "V", bf16, d, 3),
+                          V.stride()[:2], _dense(slots, "slots", torch.int64, d, 1), _q4_args(cache, d),
+                          _err_ptr(dev_err, d))
+    _on(d, stream, "msa_cache_append_q4", a)
+
+
+def msa_cache_expand_q4(cache: Q4Cache, pages: torch.Tensor, K_out: torch.Tensor, V_out: torch.Tensor, *,
+                        dev_err: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The bf16 values of pages [n] int32 into K_out, V_out [n,Hkv,Bk,D] (see msa.h)."""
+    d, bf16 = cache.K_codes.device, torch.bfloat16
+    n, Hkv = pages.shape[0], cache.K_codes.shape[1]
+    if K_out.shape != (n, Hkv, Bk, D) or V_out.shape != K_out.shape:
+        raise ValueError(f"K_out and V_out must be [n,Hkv,{Bk},{D}]")
+    a = _abi.ExpandQ4Args(n, Hkv, D, Bk, _dense(pages, "pages", torch.int32, d, 1), _q4_args(cache, d),
+                          _dense(K_out, "K_out", bf16, d, 4), _dense(V_out, "V_out", bf16, d, 4), _err_ptr(dev_err, d))
+    _on(d, stream, "msa_cache_expand_q4", a)
+
+
+def msa_attn_decode_q4_workspace_size(B: int, Hkv: int) -> int:
+    return int(lib().msa_attn_decode_q4_workspace_size(B, Hkv))
+
+
+def _attn_q4_outputs(Q, O, LSE, ws, d):
+    B, Hq, D_ = Q.shape
+    if O.shape != Q.shape or (LSE is not None and LSE.shape != (B, Hq)):
+        raise ValueError("O must be [B,Hq,D] and LSE [B,Hq]")
+    if not ws.is_contiguous() or ws.device != d:
+        raise ValueError(f"ws must be a contiguous tensor on {d}")
+    return _dense(O, "O", torch.bfloat16, d, 3), None if LSE is None else _dense(LSE, "LSE", torch.float32, d, 2)
+
+
+def msa_sparse_attn_decode_q4(Q: torch.Tensor, cache: Q4Cache, pt: torch.Tensor, n: torch.Tensor,
+                              last_len: torch.Tensor, O: torch.Tensor, LSE: Optional[torch.Tensor], ws: torch.Tensor,
+                              *, softmax_scale: float = 0.0, dev_err: Optional[torch.Tensor] = None, stream=None,
+                              scratch_zeroed: bool = False) -> None:
+    """``msa_sparse_attn_decode`` over a 4-bit cache (see msa.h): Q [B,Hq,D] bf16, pt [B*Hkv,k], n, last_len [B*Hkv]
+    int32; O [B,Hq,D] bf16, LSE [B,Hq] fp32; ws of ``msa_attn_decode_q4_workspace_size`` bytes."""
+    d, i32 = Q.device, torch.int32
+    B, Hq, D_ = Q.shape
+    Hkv = cache.K_codes.shape[1]
+    rows = B * Hkv
+    if pt.shape[0] != rows or n.shape[0] != rows or last_len.shape[0] != rows:
+        raise ValueError(f"pt, n and last_len need B * Hkv = {rows} rows")
+    if B > 0:
+        _inner_contig(Q, "Q")
+    o, lse = _attn_q4_outputs(Q, O, LSE, ws, d)
+    a = _abi.DecodeQ4Args(B, Hq, Hkv, D_, Bk, pt.shape[1], softmax_scale, _cuda(Q, "Q", torch.bfloat16, d, 3),
+                          Q.stride()[:2], _q4_args(cache, d), _dense(pt, "pt", i32, d, 2), _dense(n, "n", i32, d, 1),
+                          _dense(last_len, "last_len", i32, d, 1), o, lse, _err_ptr(dev_err, d), int(scratch_zeroed))
+    _on(d, stream, "msa_sparse_attn_decode_q4", a, ws.data_ptr(), ws.numel() * ws.element_size())
+
+
+def msa_dense_attn_decode_q4(Q: torch.Tensor, cache: Q4Cache, seq_pt: torch.Tensor, seq_len: torch.Tensor,
+                             O: torch.Tensor, LSE: Optional[torch.Tensor], ws: torch.Tensor, *,
+                             softmax_scale: float = 0.0, dev_err: Optional[torch.Tensor] = None, stream=None,
+                             scratch_zeroed: bool = False) -> None:
+    """``msa_dense_attn_decode`` over a 4-bit cache (see msa.h): Q [B,Hq,D] bf16, seq_pt [B,max_pages], seq_len [B]
+    int32 (0: an empty sequence); O [B,Hq,D] bf16, LSE [B,Hq] fp32; ws as for ``msa_sparse_attn_decode_q4``."""
+    d, i32 = Q.device, torch.int32
+    B, Hq, D_ = Q.shape
+    Hkv = cache.K_codes.shape[1]
+    if seq_pt.shape[0] != B or seq_len.shape[0] != B:
+        raise ValueError(f"seq_pt and seq_len need B = {B} rows")
+    if B > 0:
+        _inner_contig(Q, "Q")
+    o, lse = _attn_q4_outputs(Q, O, LSE, ws, d)
+    a = _abi.DenseDecodeQ4Args(B, Hq, Hkv, D_, Bk, softmax_scale, _cuda(Q, "Q", torch.bfloat16, d, 3), Q.stride()[:2],
+                               _q4_args(cache, d), _dense(seq_pt, "seq_pt", i32, d, 2), seq_pt.shape[1],
+                               _dense(seq_len, "seq_len", i32, d, 1), o, lse, _err_ptr(dev_err, d), int(scratch_zeroed))
+    _on(d, stream, "msa_dense_attn_decode_q4", a, ws.data_ptr(), ws.numel() * ws.element_size())
+
+
+# ---------------------------------------------------------------------------
 # pipelines (hot-path order; marshalling and buffer allocation only)
 # ---------------------------------------------------------------------------
 
@@ -504,6 +784,34 @@ def decode_step(inp: Dict[str, torch.Tensor], k: int, bufs: Optional[Dict[str, t
     msa_sparse_attn_decode(inp["Q"], inp["K_pool"], inp["V_pool"], bufs["pt"], bufs["n"], bufs["last_len"],
                            bufs["O"], bufs["LSE"], bufs["ws"], softmax_scale=softmax_scale, dev_err=e,
                            stream=stream, scratch_zeroed=scratch_zeroed)
+    return bufs
+
+
+def decode_q4_buffers(B: int, Hq: int, Hkv: int, k: int, nb_stride: int, device) -> Dict[str, torch.Tensor]:
+    """``decode_buffers`` with the workspace of the 4-bit attention."""
+    dev = torch.device(device)
+    bufs = {n: t for n, t in decode_buffers(B, Hq, Hkv, k, nb_stride, dev).items() if n != "ws"}
+    bufs["ws"] = torch.zeros(msa_attn_decode_q4_workspace_size(B, Hkv), dtype=torch.uint8, device=dev)
+    return bufs
+
+
+def decode_step_q4(inp: Dict[str, torch.Tensor], cache: Q4Cache, k: int,
+                   bufs: Optional[Dict[str, torch.Tensor]] = None, softmax_scale: float = 0.0, stream=None,
+                   scratch_zeroed: bool = False) -> Dict[str, torch.Tensor]:
+    """``decode_step`` with K and V in a 4-bit cache: the index branch and selection are the same (``inp`` holds Q,
+    q_idx, w, kidx_pool, seq_pt, seq_len), the attention reads ``cache``."""
+    B, Hq, _ = inp["Q"].shape
+    Hkv = cache.K_codes.shape[1]
+    if bufs is None:
+        bufs = decode_q4_buffers(B, Hq, Hkv, k, inp["seq_pt"].shape[1], inp["Q"].device)
+    e = bufs["dev_err"]
+    msa_index_score(MSA_MODE_DECODE, inp["q_idx"], inp["w"], inp["kidx_pool"], bufs["C"], seq_pt=inp["seq_pt"],
+                    seq_len=inp["seq_len"], dev_err=e, stream=stream, k=k, sel=bufs["sel"], count=bufs["count"],
+                    pt=bufs["pt"], n=bufs["n"], last_len=bufs["last_len"], row_scratch=bufs["row_scratch"],
+                    scratch_zeroed=scratch_zeroed)
+    msa_sparse_attn_decode_q4(inp["Q"], cache, bufs["pt"], bufs["n"], bufs["last_len"], bufs["O"], bufs["LSE"],
+                              bufs["ws"], softmax_scale=softmax_scale, dev_err=e, stream=stream,
+                              scratch_zeroed=scratch_zeroed)
     return bufs
 
 

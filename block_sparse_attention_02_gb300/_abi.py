@@ -24,6 +24,7 @@ MSA_DEVERR_TIMEOUT = 0x1
 MSA_DEVERR_BAD_PAGE = 0x2
 MSA_DEVERR_BAD_SEL = 0x4
 MSA_DEVERR_BAD_LEN = 0x8
+MSA_DEVERR_NO_PAGES = 0x10
 
 MSA_MODE_PREFILL = 0
 MSA_MODE_DECODE = 1
@@ -110,6 +111,75 @@ class DensePrefillArgs(C.Structure):
     ]
 
 
+class PlanArgs(C.Structure):
+    _fields_ = [
+        ("B", C.c_int), ("Bk", C.c_int), ("N", C.c_int64),
+        ("seq_len", _p), ("new_len", _p), ("seq_pt", _p), ("max_pages", C.c_int64),
+        ("free_pages", _p), ("free_cap", C.c_int64), ("free_count", _p), ("num_pages", C.c_int64),
+        ("seq_len_out", _p), ("free_count_out", _p), ("cu", _p),
+        ("tok_slot", _p), ("tok_pos", _p), ("tok_seq", _p), ("dev_err", _p),
+    ]
+
+
+class ReleaseArgs(C.Structure):
+    _fields_ = [
+        ("B", C.c_int), ("Bk", C.c_int), ("seq_len", _p), ("done", _p), ("seq_pt", _p), ("max_pages", C.c_int64),
+        ("free_pages", _p), ("free_cap", C.c_int64), ("free_count", _p),
+        ("seq_len_out", _p), ("free_count_out", _p), ("dev_err", _p),
+    ]
+
+
+class NormRopeArgs(C.Structure):
+    _fields_ = [
+        ("N", C.c_int64), ("Hq", C.c_int), ("Hkv", C.c_int), ("D", C.c_int), ("Bk", C.c_int), ("rot", C.c_int),
+        ("interleaved", C.c_int), ("weight_fp32", C.c_int), ("eps", C.c_float),
+        ("Q", _p), ("Q_stride", _i64x2), ("K", _p), ("K_stride", _i64x2), ("V", _p), ("V_stride", _i64x2),
+        ("pos", _p), ("inv_freq", _p), ("q_weight", _p), ("k_weight", _p),
+        ("Q_out", _p), ("Q_out_stride", _i64x2), ("K_out", _p), ("K_out_stride", _i64x3),
+        ("V_out", _p), ("V_out_stride", _i64x3), ("slots", _p), ("num_pages", C.c_int64), ("dev_err", _p),
+    ]
+
+
+class Q4CacheArgs(C.Structure):
+    _fields_ = [
+        ("K_codes", _p), ("K_scales", _p), ("V_codes", _p), ("V_scales", _p),
+        ("code_stride", _i64x2), ("scale_stride", _i64x2), ("num_pages", C.c_int64),
+        ("k_scale", C.c_float), ("v_scale", C.c_float),
+    ]
+
+
+class AppendQ4Args(C.Structure):
+    _fields_ = [
+        ("N", C.c_int64), ("Hkv", C.c_int), ("D", C.c_int), ("Bk", C.c_int),
+        ("K", _p), ("K_stride", _i64x2), ("V", _p), ("V_stride", _i64x2), ("slots", _p),
+        ("cache", Q4CacheArgs), ("dev_err", _p),
+    ]
+
+
+class ExpandQ4Args(C.Structure):
+    _fields_ = [
+        ("n", C.c_int64), ("Hkv", C.c_int), ("D", C.c_int), ("Bk", C.c_int), ("pages", _p),
+        ("cache", Q4CacheArgs), ("K_out", _p), ("V_out", _p), ("dev_err", _p),
+    ]
+
+
+class DecodeQ4Args(C.Structure):
+    _fields_ = [
+        ("B", C.c_int), ("Hq", C.c_int), ("Hkv", C.c_int), ("D", C.c_int), ("Bk", C.c_int), ("k", C.c_int),
+        ("softmax_scale", C.c_float), ("Q", _p), ("Q_stride", _i64x2), ("cache", Q4CacheArgs),
+        ("pt", _p), ("n", _p), ("last_len", _p), ("O", _p), ("LSE", _p), ("dev_err", _p), ("scratch_zeroed", C.c_int),
+    ]
+
+
+class DenseDecodeQ4Args(C.Structure):
+    _fields_ = [
+        ("B", C.c_int), ("Hq", C.c_int), ("Hkv", C.c_int), ("D", C.c_int), ("Bk", C.c_int),
+        ("softmax_scale", C.c_float), ("Q", _p), ("Q_stride", _i64x2), ("cache", Q4CacheArgs),
+        ("seq_pt", _p), ("max_pages", C.c_int64), ("seq_len", _p),
+        ("O", _p), ("LSE", _p), ("dev_err", _p), ("scratch_zeroed", C.c_int),
+    ]
+
+
 # exported function name -> (restype, argtypes)
 SIGNATURES = {
     "msa_version": (C.c_int, []),
@@ -129,6 +199,14 @@ SIGNATURES = {
     "msa_dense_attn_decode_workspace_size": (C.c_size_t, [C.POINTER(DenseDecodeArgs)]),
     "msa_dense_attn_decode": (C.c_int, [C.POINTER(DenseDecodeArgs), _p, C.c_size_t, _p]),
     "msa_dense_attn_prefill": (C.c_int, [C.POINTER(DensePrefillArgs), _p]),
+    "msa_plan_step": (C.c_int, [C.POINTER(PlanArgs), _p]),
+    "msa_release_pages": (C.c_int, [C.POINTER(ReleaseArgs), _p]),
+    "msa_qk_norm_rope": (C.c_int, [C.POINTER(NormRopeArgs), _p]),
+    "msa_cache_append_q4": (C.c_int, [C.POINTER(AppendQ4Args), _p]),
+    "msa_cache_expand_q4": (C.c_int, [C.POINTER(ExpandQ4Args), _p]),
+    "msa_attn_decode_q4_workspace_size": (C.c_size_t, [C.c_int, C.c_int]),
+    "msa_sparse_attn_decode_q4": (C.c_int, [C.POINTER(DecodeQ4Args), _p, C.c_size_t, _p]),
+    "msa_dense_attn_decode_q4": (C.c_int, [C.POINTER(DenseDecodeQ4Args), _p, C.c_size_t, _p]),
 }
 
 _lock = threading.Lock()

@@ -458,4 +458,184 @@ msa_status msa_cache_append(const msa_append_args* a, msa_stream_t stream) {
   return launch_cache_append(*a, reinterpret_cast<cudaStream_t>(stream));
 }
 
+// ---------------------------------------------------------------------------
+static msa_status check_tables(int B, int Bk, int64_t max_pages, int64_t free_cap) {
+  MSA_REQUIRE(B >= 0 && B <= kMaxDecodeBatch, MSA_ERR_UNSUPPORTED, "B = %d, supported 0..%d", B, kMaxDecodeBatch);
+  MSA_REQUIRE(Bk == kBk, MSA_ERR_UNSUPPORTED, "Bk = %d, only %d is supported", Bk, kBk);
+  MSA_REQUIRE(max_pages >= 1 && max_pages < (int64_t(1) << 31) / Bk, MSA_ERR_INVALID_ARG, "max_pages = %" PRId64,
+              max_pages);
+  MSA_REQUIRE(free_cap >= 0 && free_cap < (int64_t(1) << 31) - 1, MSA_ERR_INVALID_ARG, "free_cap = %" PRId64, free_cap);
+  return MSA_OK;
+}
+
+msa_status msa_plan_step(const msa_plan_args* a, msa_stream_t stream) {
+  g_last_error.clear();
+  MSA_REQUIRE(a != nullptr, MSA_ERR_INVALID_ARG, "args is NULL");
+  if (msa_status st = check_tables(a->B, a->Bk, a->max_pages, a->free_cap); st != MSA_OK) return st;
+  MSA_REQUIRE(a->N >= 0 && a->N < (int64_t(1) << 31) - 1, MSA_ERR_INVALID_ARG, "N = %" PRId64, a->N);
+  MSA_REQUIRE(a->num_pages >= 1 && a->num_pages < (int64_t(1) << 31), MSA_ERR_INVALID_ARG, "num_pages = %" PRId64,
+              a->num_pages);
+  MSA_REQUIRE(a->B == 0 || (a->seq_len && a->new_len && a->seq_pt && a->seq_len_out), MSA_ERR_INVALID_ARG,
+              "seq_len, new_len, seq_pt and seq_len_out must be non-NULL");
+  MSA_REQUIRE(a->free_count && a->free_count_out && a->cu && (a->free_cap == 0 || a->free_pages), MSA_ERR_INVALID_ARG,
+              "free_pages, free_count, free_count_out and cu must be non-NULL");
+  MSA_REQUIRE(a->N == 0 || (a->tok_slot && a->tok_pos), MSA_ERR_INVALID_ARG, "tok_slot and tok_pos must be non-NULL");
+  return launch_plan_step(*a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+msa_status msa_release_pages(const msa_release_args* a, msa_stream_t stream) {
+  g_last_error.clear();
+  MSA_REQUIRE(a != nullptr, MSA_ERR_INVALID_ARG, "args is NULL");
+  if (msa_status st = check_tables(a->B, a->Bk, a->max_pages, a->free_cap); st != MSA_OK) return st;
+  MSA_REQUIRE(a->B == 0 || (a->seq_len && a->done && a->seq_pt && a->seq_len_out), MSA_ERR_INVALID_ARG,
+              "seq_len, done, seq_pt and seq_len_out must be non-NULL");
+  MSA_REQUIRE(a->free_count && a->free_count_out && (a->free_cap == 0 || a->free_pages), MSA_ERR_INVALID_ARG,
+              "free_pages, free_count and free_count_out must be non-NULL");
+  return launch_release_pages(*a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ---------------------------------------------------------------------------
+msa_status msa_qk_norm_rope(const msa_norm_rope_args* a, msa_stream_t stream) {
+  g_last_error.clear();
+  MSA_REQUIRE(a != nullptr, MSA_ERR_INVALID_ARG, "args is NULL");
+  MSA_REQUIRE(a->N >= 0 && a->N < (int64_t(1) << 31) && a->Hq >= 1 && a->Hkv >= 0, MSA_ERR_INVALID_ARG,
+              "N = %" PRId64 ", Hq = %d, Hkv = %d", a->N, a->Hq, a->Hkv);
+  MSA_REQUIRE(a->D == 64 || a->D == 128, MSA_ERR_UNSUPPORTED, "D = %d, supported 64 and 128", a->D);
+  MSA_REQUIRE(a->rot >= 0 && a->rot <= a->D && a->rot % 16 == 0, MSA_ERR_UNSUPPORTED,
+              "rot = %d, supported multiples of 16 up to D = %d", a->rot, a->D);
+  MSA_REQUIRE(a->eps >= 0.f && std::isfinite(a->eps), MSA_ERR_INVALID_ARG, "eps = %g", static_cast<double>(a->eps));
+  MSA_REQUIRE(a->pos && a->Q && a->Q_out && (a->rot == 0 || a->inv_freq), MSA_ERR_INVALID_ARG,
+              "pos, inv_freq, Q and Q_out must be non-NULL");
+  MSA_REQUIRE(a->Hkv == 0 || (a->K && a->K_out), MSA_ERR_INVALID_ARG, "K and K_out must be non-NULL");
+  MSA_REQUIRE((a->V == nullptr) == (a->V_out == nullptr), MSA_ERR_INVALID_ARG, "V and V_out go together");
+  MSA_REQUIRE(a->V == nullptr || (a->slots != nullptr && a->Hkv > 0), MSA_ERR_INVALID_ARG,
+              "V is stored by slots only, with Hkv >= 1");
+  MSA_REQUIRE(aligned16(a->Q) && aligned16(a->K) && aligned16(a->V) && aligned16(a->Q_out) && aligned16(a->K_out) &&
+                  aligned16(a->V_out),
+              MSA_ERR_INVALID_ARG, "Q, K, V and their outputs must be 16-byte aligned");
+  for (int i = 0; i < 2; ++i) {
+    MSA_REQUIRE(vec_stride_ok(a->Q_stride[i], 2) && vec_stride_ok(a->Q_out_stride[i], 2), MSA_ERR_INVALID_ARG,
+                "Q strides must be positive multiples of 8 elements");
+    MSA_REQUIRE(a->Hkv == 0 || vec_stride_ok(a->K_stride[i], 2), MSA_ERR_INVALID_ARG,
+                "K strides must be positive multiples of 8 elements");
+    MSA_REQUIRE(a->V == nullptr || vec_stride_ok(a->V_stride[i], 2), MSA_ERR_INVALID_ARG,
+                "V strides must be positive multiples of 8 elements");
+  }
+  for (int i = 0; i < (a->slots != nullptr ? 3 : 2); ++i)
+    MSA_REQUIRE(a->Hkv == 0 || (vec_stride_ok(a->K_out_stride[i], 2) &&
+                                (a->V == nullptr || vec_stride_ok(a->V_out_stride[i], 2))),
+                MSA_ERR_INVALID_ARG, "K_out and V_out strides must be positive multiples of 8 elements");
+  if (a->slots != nullptr) {
+    MSA_REQUIRE(a->Bk == kBk, MSA_ERR_UNSUPPORTED, "Bk = %d, only %d is supported", a->Bk, kBk);
+    MSA_REQUIRE(a->num_pages >= 1 && a->num_pages < (int64_t(1) << 31), MSA_ERR_INVALID_ARG, "num_pages = %" PRId64,
+                a->num_pages);
+  }
+  if (a->N == 0) return MSA_OK;
+  return launch_qk_norm_rope(*a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ---------------------------------------------------------------------------
+static bool power_of_two(float x) {
+  int e = 0;
+  return std::isfinite(x) && x > 0.f && std::frexp(x, &e) == 0.5f && e >= -63 && e <= 65;
+}
+
+static msa_status check_q4(const msa_q4_cache& c, int Hkv, int D, int Bk) {
+  MSA_REQUIRE(Hkv >= 1, MSA_ERR_INVALID_ARG, "Hkv = %d", Hkv);
+  if (msa_status st = check_common_shape(Bk, D, kD, "D"); st != MSA_OK) return st;
+  MSA_REQUIRE(c.K_codes && c.K_scales && c.V_codes && c.V_scales, MSA_ERR_INVALID_ARG,
+              "the cache's codes and scales must be non-NULL");
+  MSA_REQUIRE(aligned16(c.K_codes) && aligned16(c.K_scales) && aligned16(c.V_codes) && aligned16(c.V_scales),
+              MSA_ERR_INVALID_ARG, "the cache's codes and scales must be 16-byte aligned");
+  for (int i = 0; i < 2; ++i)
+    MSA_REQUIRE(vec_stride_ok(c.code_stride[i], 1) && vec_stride_ok(c.scale_stride[i], 1), MSA_ERR_INVALID_ARG,
+                "the cache's strides must be positive multiples of 16 bytes");
+  MSA_REQUIRE(c.num_pages >= 1 && c.num_pages < (int64_t(1) << 31), MSA_ERR_INVALID_ARG, "num_pages = %" PRId64,
+              c.num_pages);
+  MSA_REQUIRE(power_of_two(c.k_scale) && power_of_two(c.v_scale), MSA_ERR_INVALID_ARG,
+              "k_scale = %g, v_scale = %g: need powers of two in [2^-64, 2^64]", static_cast<double>(c.k_scale),
+              static_cast<double>(c.v_scale));
+  return MSA_OK;
+}
+
+msa_status msa_cache_append_q4(const msa_append_q4_args* a, msa_stream_t stream) {
+  g_last_error.clear();
+  MSA_REQUIRE(a != nullptr, MSA_ERR_INVALID_ARG, "args is NULL");
+  MSA_REQUIRE(a->N >= 0 && a->N < (int64_t(1) << 31), MSA_ERR_INVALID_ARG, "N = %" PRId64, a->N);
+  if (msa_status st = check_q4(a->cache, a->Hkv, a->D, a->Bk); st != MSA_OK) return st;
+  if (a->N == 0) return MSA_OK;
+  MSA_REQUIRE(a->K && a->V && a->slots, MSA_ERR_INVALID_ARG, "K, V and slots must be non-NULL");
+  MSA_REQUIRE(aligned16(a->K) && aligned16(a->V), MSA_ERR_INVALID_ARG, "K and V must be 16-byte aligned");
+  for (int i = 0; i < 2; ++i)
+    MSA_REQUIRE(vec_stride_ok(a->K_stride[i], 2) && vec_stride_ok(a->V_stride[i], 2), MSA_ERR_INVALID_ARG,
+                "K and V strides must be positive multiples of 8 elements");
+  return launch_append_q4(*a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+msa_status msa_cache_expand_q4(const msa_expand_q4_args* a, msa_stream_t stream) {
+  g_last_error.clear();
+  MSA_REQUIRE(a != nullptr, MSA_ERR_INVALID_ARG, "args is NULL");
+  MSA_REQUIRE(a->n >= 0 && a->n < (int64_t(1) << 31), MSA_ERR_INVALID_ARG, "n = %" PRId64, a->n);
+  if (msa_status st = check_q4(a->cache, a->Hkv, a->D, a->Bk); st != MSA_OK) return st;
+  if (a->n == 0) return MSA_OK;
+  MSA_REQUIRE(a->pages && a->K_out && a->V_out, MSA_ERR_INVALID_ARG, "pages, K_out and V_out must be non-NULL");
+  MSA_REQUIRE(aligned16(a->K_out) && aligned16(a->V_out), MSA_ERR_INVALID_ARG, "K_out and V_out must be 16-byte aligned");
+  return launch_expand_q4(*a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ---------------------------------------------------------------------------
+static msa_status check_attn_q4(int B, int max_B, int Hq, int Hkv, int D, int Bk, const void* Q, const int64_t* Q_stride,
+                                const msa_q4_cache& cache, const void* O) {
+  MSA_REQUIRE(B >= 0 && B <= max_B && Hq >= 1 && Hkv >= 1, MSA_ERR_INVALID_ARG, "B = %d (at most %d), Hq = %d, Hkv = %d",
+              B, max_B, Hq, Hkv);
+  MSA_REQUIRE(Hq % Hkv == 0 && Hq / Hkv <= kMaxG, MSA_ERR_UNSUPPORTED, "GQA ratio Hq/Hkv = %d/%d not in 1..%d", Hq, Hkv,
+              kMaxG);
+  if (msa_status st = check_q4(cache, Hkv, D, Bk); st != MSA_OK) return st;
+  MSA_REQUIRE(B == 0 || (Q && O), MSA_ERR_INVALID_ARG, "Q and O must be non-NULL");
+  MSA_REQUIRE(aligned16(Q) && aligned16(O), MSA_ERR_INVALID_ARG, "Q and O must be 16-byte aligned");
+  for (int i = 0; i < 2; ++i)
+    MSA_REQUIRE(vec_stride_ok(Q_stride[i], 2), MSA_ERR_INVALID_ARG,
+                "Q_stride[%d] = %" PRId64 " must be a positive multiple of 8 elements", i, Q_stride[i]);
+  return MSA_OK;
+}
+
+static msa_status check_q4_ws(int B, int Hkv, const void* ws, size_t ws_bytes) {
+  const size_t need = attn_decode_q4_workspace_size(B, Hkv);
+  MSA_REQUIRE(ws != nullptr && ws_bytes >= need, MSA_ERR_WORKSPACE, "workspace %zu bytes, need %zu", ws_bytes, need);
+  MSA_REQUIRE(aligned16(ws), MSA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  return MSA_OK;
+}
+
+size_t msa_attn_decode_q4_workspace_size(int B, int Hkv) {
+  return B < 0 || Hkv < 1 ? 0 : attn_decode_q4_workspace_size(B, Hkv);
+}
+
+msa_status msa_sparse_attn_decode_q4(const msa_decode_q4_args* a, void* ws, size_t ws_bytes, msa_stream_t stream) {
+  g_last_error.clear();
+  MSA_REQUIRE(a != nullptr, MSA_ERR_INVALID_ARG, "args is NULL");
+  if (msa_status st = check_attn_q4(a->B, kMaxDecodeBatch, a->Hq, a->Hkv, a->D, a->Bk, a->Q, a->Q_stride, a->cache, a->O);
+      st != MSA_OK)
+    return st;
+  MSA_REQUIRE(a->k >= 1 && a->k <= kMaxK, MSA_ERR_UNSUPPORTED, "k = %d, supported 1..%d", a->k, kMaxK);
+  if (a->B == 0) return MSA_OK;
+  MSA_REQUIRE(a->pt && a->n && a->last_len, MSA_ERR_INVALID_ARG, "pt, n and last_len must be non-NULL");
+  if (msa_status st = check_q4_ws(a->B, a->Hkv, ws, ws_bytes); st != MSA_OK) return st;
+  return launch_sparse_decode_q4(*a, ws, reinterpret_cast<cudaStream_t>(stream));
+}
+
+msa_status msa_dense_attn_decode_q4(const msa_dense_decode_q4_args* a, void* ws, size_t ws_bytes, msa_stream_t stream) {
+  g_last_error.clear();
+  MSA_REQUIRE(a != nullptr, MSA_ERR_INVALID_ARG, "args is NULL");
+  if (msa_status st = check_attn_q4(a->B, kDenseMaxBatch, a->Hq, a->Hkv, a->D, a->Bk, a->Q, a->Q_stride, a->cache, a->O);
+      st != MSA_OK)
+    return st;
+  if (a->B == 0) return MSA_OK;
+  MSA_REQUIRE(a->seq_pt && a->seq_len, MSA_ERR_INVALID_ARG, "seq_pt and seq_len must be non-NULL");
+  MSA_REQUIRE(a->max_pages >= 1 && a->max_pages < (int64_t(1) << 31) / kBk &&
+                  static_cast<int64_t>(a->B) * a->Hkv * a->max_pages < (int64_t(1) << 30),
+              MSA_ERR_INVALID_ARG, "max_pages = %" PRId64 ": B * Hkv * max_pages must be below 2^30", a->max_pages);
+  if (msa_status st = check_q4_ws(a->B, a->Hkv, ws, ws_bytes); st != MSA_OK) return st;
+  return launch_dense_decode_q4(*a, ws, reinterpret_cast<cudaStream_t>(stream));
+}
+
 }  // extern "C"

@@ -1,0 +1,498 @@
+// attn_decode_q4.cu -- decode attention over the paged cache in 4 bits, over the
+// selected pages (sparse) or every cached token (dense).
+//
+//     z[h][t] = scale * Q[h] . K[t],  O[h] = sum_t softmax_t(z[h]) V[t],  LSE[h] = ln sum_t e^z
+// for the G query heads that share a KV head.  A token costs 144 bytes (two rows
+// of 64 code and 8 scale bytes), so HBM is the floor and the work beside the
+// loads is turning codes into matrix operands.
+//
+// Products.  mma.m16n8k16 in fp16 with fp32 sums, straight from registers:
+//   S^T[t][h]: A = 16 tokens x 16 channels of K, B = Q (8 heads: G padded)
+//   O^T[d][h]: A = 16 channels x 16 tokens of V, B = P
+// The eight columns fit the heads exactly, where a 128-row tensor-memory tile would
+// need the dequantised block written to shared memory first (64 KiB a page) and read
+// back.  The order of the channels in S's sum and of the rows in O is free, so
+// each lane takes 16 bytes (32 channels) of a token's K row and 8 bytes (one
+// scale group) of a V row as they lie in the page.
+//
+// Exactness.  code * sf has 6 bits and lies in [2^-10, 2688]: exact in fp16, so
+// the cached values enter the products unrounded; the pools' powers of two and the
+// softmax scale multiply the fp32 sums.  Q is brought to [1, 2) per head by a power
+// of two; P = 2^(z - m + 8) with m the running maximum or up to 6 below it, at most
+// 2^14, is rounded to fp16 (2^-12 of the value down to 2^-22 of the largest).
+//
+// Work.  The (row, page) units of all rows form one list; each CTA takes an equal
+// run of it, its eight warps 16 tokens of every page each, with a softmax
+// of their own that is joined in shared memory at the end of a row's part.  Rows
+// cut by a run's end go through the workspace; the CTA that arrives last joins them.
+#include <cuda_fp16.h>
+
+#include "msa_internal.h"
+#include "msa_ptx.cuh"
+#include "q4.cuh"
+
+namespace msa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kCtasPerSm = 2;
+constexpr int kMaxGrid = 512;                           // CTAs per launch at most (sizes the workspace)
+constexpr int kPart = kMaxG * kD + 2 * kMaxG;           // floats of a partial: O [8][128], m [8], l [8]
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kPShift = 8.f;                          // P is held as 2^(z - m + 8)
+constexpr float kSlack = 6.f;                           // m follows a maximum more than this above it
+
+struct Params {
+  int B, Hq, Hkv, G, k;
+  float scale_log2, v_scale;
+  const uint8_t* Q;
+  int64_t q0, q1;                       // byte strides (b, h)
+  const uint8_t *K_codes, *K_scales, *V_codes, *V_scales;
+  int64_t c0, c1, s0, s1;               // byte strides (page, g)
+  int64_t num_pages;
+  const int32_t *pt, *n, *last_len;     // sparse
+  const int32_t *seq_pt, *seq_len;      // dense
+  int64_t max_pages;
+  int32_t* counter;                     // [B * Hkv] parts of a row that have arrived, zero on entry
+  float* part;                          // [grid][2][kPart]
+  __nv_bfloat16* O;
+  float* LSE;
+  int32_t* dev_err;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// Streaming loads: the cache is read once per step.
+__device__ __forceinline__ uint4 ldg16(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ldg8(const uint8_t* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+
+// A warp's 16 tokens of a page as loaded.
+struct Tile {
+  uint4 k[2];            // tokens g and g + 8, channels 32t .. 32t + 31
+  uint2 v[4];            // tokens 2t, 2t + 1, 2t + 8, 2t + 9, channels 16g .. 16g + 15
+  uint32_t ks[2], vs[4]; // their scale bytes (two groups, one group)
+};
+
+__device__ __forceinline__ void load_tile(const Params& p, int64_t page, int head, int tok0, int g, int t, Tile* x) {
+  const uint8_t* kc = p.K_codes + page * p.c0 + head * p.c1 + tok0 * 64;
+  const uint8_t* vc = p.V_codes + page * p.c0 + head * p.c1 + tok0 * 64;
+  const uint8_t* ks = p.K_scales + page * p.s0 + head * p.s1 + tok0 * 8;
+  const uint8_t* vs = p.V_scales + page * p.s0 + head * p.s1 + tok0 * 8;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    x->k[i] = ldg16(kc + (g + 8 * i) * 64 + t * 16);
+    x->ks[i] = __ldg(reinterpret_cast<const uint16_t*>(ks + (g + 8 * i) * 8 + t * 2));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int tok = 2 * t + (i & 1) + 8 * (i >> 1);
+    x->v[i] = ldg8(vc + tok * 64 + g * 8);
+    x->vs[i] = __ldg(vs + tok * 8 + g);
+  }
+}
+
+// The softmax state of a warp: lane (g, t) holds heads 2t and 2t + 1, of which
+// acc[i] are channels 16g + 2i (elements 0, 1) and 16g + 2i + 1 (elements 2, 3).
+struct State {
+  float acc[8][4];
+  float m[2], l[2];      // m the same in every g; l this lane's share
+};
+
+__device__ __forceinline__ void attend_tile(const uint32_t (&q)[16], const float (&coef)[2], Tile& x, int valid, int g,
+                                            int t, State* st) {
+  if (valid < 16) {      // slots past the last token may hold anything, a NaN scale too: they count as zeros
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (2 * t + (i & 1) + 8 * (i >> 1) >= valid) x.vs[i] = 0;
+  }
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  {
+    const __half2 sa = e4m3x2_to_half2(x.ks[0]), sb = e4m3x2_to_half2(x.ks[1]);
+    const uint32_t wa[4] = {x.k[0].x, x.k[0].y, x.k[0].z, x.k[0].w};
+    const uint32_t wb[4] = {x.k[1].x, x.k[1].y, x.k[1].z, x.k[1].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 fa = i < 2 ? __low2half2(sa) : __high2half2(sa), fb = i < 2 ? __low2half2(sb) : __high2half2(sb);
+      __half2 a[4], b[4];
+      e2m1x8_to_half2(wa[i], a);
+      e2m1x8_to_half2(wb[i], b);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        a[e] = __hmul2(a[e], fa);
+        b[e] = __hmul2(b[e], fb);
+      }
+      mma16816(s, h2u(a[0]), h2u(b[0]), h2u(a[1]), h2u(b[1]), q[4 * i], q[4 * i + 1]);
+      mma16816(s, h2u(a[2]), h2u(b[2]), h2u(a[3]), h2u(b[3]), q[4 * i + 2], q[4 * i + 3]);
+    }
+  }
+  const bool on0 = g < valid, on1 = g + 8 < valid;
+  float z[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) z[i] = (i < 2 ? on0 : on1) ? s[i] * coef[i & 1] : -INFINITY;
+  const float top0 = fmaxf(z[0], z[2]), top1 = fmaxf(z[1], z[3]);
+  if (__any_sync(0xffffffffu, top0 > st->m[0] + kSlack || top1 > st->m[1] + kSlack)) {
+    float top[2] = {top0, top1};
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], o));
+      const float m = fmaxf(st->m[c], top[c]);
+      const float f = m == -INFINITY ? 1.f : ex2(st->m[c] - m);
+      st->m[c] = m;
+      st->l[c] *= f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        st->acc[i][c] *= f;
+        st->acc[i][c + 2] *= f;
+      }
+    }
+  }
+  float pr[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) pr[i] = (i < 2 ? on0 : on1) ? ex2(z[i] - st->m[i & 1] + kPShift) : 0.f;
+  st->l[0] += pr[0] + pr[2];
+  st->l[1] += pr[1] + pr[3];
+  // P^T: from (token g, heads 2t, 2t + 1) to (head g, tokens 2t, 2t + 1)
+  const uint32_t b0 = transpose8x8(h2u(__floats2half2_rn(pr[0], pr[1])));
+  const uint32_t b1 = transpose8x8(h2u(__floats2half2_rn(pr[2], pr[3])));
+  __half2 sv[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sv[i] = e4m3_to_half2(x.vs[i]);
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    __half2 v[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      e2m1x8_to_half2(w ? x.v[i].y : x.v[i].x, v[i]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[i][e] = __hmul2(v[i][e], sv[i]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      mma16816(st->acc[w * 4 + e], h2u(__lows2half2(v[0][e], v[1][e])), h2u(__highs2half2(v[0][e], v[1][e])),
+               h2u(__lows2half2(v[2][e], v[3][e])), h2u(__highs2half2(v[2][e], v[3][e])), b0, b1);
+  }
+}
+
+template <bool DENSE>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_q4_kernel(const Params p) {
+  __shared__ __align__(16) float s_o[kWarps][kMaxG][kD];
+  __shared__ float s_m[kWarps][kMaxG], s_l[kWarps][kMaxG];
+  __shared__ int s_pre[DENSE ? kDenseMaxBatch + 1 : 1];   // pages of the sequences before b
+  __shared__ int s_wsum[kWarps];
+  __shared__ int s_last;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int rows = p.B * p.Hkv;
+
+  int64_t units;
+  if (DENSE) {
+    constexpr int kPer = kDenseMaxBatch / kThreads;
+    int mine[kPer], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int b = tid * kPer + i;
+      mine[i] = 0;
+      if (b < p.B) {
+        const int L = p.seq_len[b];
+        if (L < 0 || L > p.max_pages * kBk) {
+          if (blockIdx.x == 0) report(p.dev_err, MSA_DEVERR_BAD_LEN);
+        } else {
+          mine[i] = (L + kBk - 1) / kBk;
+        }
+      }
+      sum += mine[i];
+    }
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) s_wsum[warp] = inc;
+    __syncthreads();
+    int before = inc - sum;
+    for (int w = 0; w < warp; ++w) before += s_wsum[w];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int b = tid * kPer + i;
+      if (b <= p.B) s_pre[b] = before;
+      before += mine[i];
+    }
+    if (tid == kThreads - 1 && p.B == kDenseMaxBatch) s_pre[p.B] = before;
+    __syncthreads();
+    units = static_cast<int64_t>(s_pre[p.B]) * p.Hkv;
+  } else {
+    units = static_cast<int64_t>(rows) * p.k;
+  }
+  const int64_t per = (units + gridDim.x - 1) / gridDim.x;
+  const int64_t lo = min(units, static_cast<int64_t>(blockIdx.x) * per), hi = min(units, lo + per);
+
+  for (int64_t u = lo; u < hi;) {
+    // the part of a row that starts at unit u: pages p0 .. p1 of its list
+    int b, head, p0, row_pages, tokens;
+    const int32_t* list;
+    if (DENSE) {
+      int x = 0, y = p.B;                   // last sequence whose units start at or before u
+      while (y - x > 1) {
+        const int mid = (x + y) >> 1;
+        if (static_cast<int64_t>(s_pre[mid]) * p.Hkv <= u) x = mid; else y = mid;
+      }
+      b = x;
+      row_pages = s_pre[b + 1] - s_pre[b];
+      const int rem = static_cast<int>(u - static_cast<int64_t>(s_pre[b]) * p.Hkv);
+      head = rem / row_pages;
+      p0 = rem - head * row_pages;
+      tokens = p.seq_len[b];
+      list = p.seq_pt + b * p.max_pages;
+    } else {
+      const int r = static_cast<int>(u / p.k);
+      b = r / p.Hkv;
+      head = r - b * p.Hkv;
+      p0 = static_cast<int>(u - static_cast<int64_t>(r) * p.k);
+      row_pages = p.k;
+      const int nr = min(max(p.n[r], 0), p.k);
+      tokens = nr == 0 ? 0 : (nr - 1) * kBk + min(max(p.last_len[r], 0), kBk);
+      list = p.pt + static_cast<int64_t>(r) * p.k;
+    }
+    const int row = b * p.Hkv + head;
+    const int p1 = static_cast<int>(min(static_cast<int64_t>(row_pages), p0 + hi - u));
+    const int64_t row_first = u - p0;
+    u += p1 - p0;
+
+    // Q of head g as fp16, scaled by a power of two: channels 32t + 2i, 32t + 2i + 1 in q[i]
+    uint32_t q[16];
+    float coef[2];
+    {
+      float f[32], top = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (g < p.G) v = *reinterpret_cast<const uint4*>(p.Q + b * p.q0 + (head * p.G + g) * p.q1 + t * 64 + i * 16);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          f[8 * i + 2 * e] = __uint_as_float(w[e] << 16);
+          f[8 * i + 2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) top = fmaxf(top, fabsf(f[i]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int ex = min(max(static_cast<int>(__float_as_uint(top) >> 23), 1), 253);
+      const float down = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);   // 2^(127 - ex)
+      const float up = __uint_as_float(static_cast<uint32_t>(ex) << 23);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) q[i] = h2u(__floats2half2_rn(f[2 * i] * down, f[2 * i + 1] * down));
+#pragma unroll
+      for (int c = 0; c < 2; ++c) coef[c] = __shfl_sync(0xffffffffu, up, 8 * t + 4 * c) * p.scale_log2;
+    }
+    State st;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) st.acc[i][e] = 0.f;
+    st.m[0] = st.m[1] = -INFINITY;
+    st.l[0] = st.l[1] = 0.f;
+
+    // this warp's 16 tokens of each page, the next page's loads in flight behind the present one's work
+    const int tok0 = warp * 16;
+    const int live = min(p1, (tokens - tok0 + kBk - 1) / kBk);   // pages with a token of this warp's
+    int32_t ids = 0;
+    Tile next;
+    bool next_ok = false;
+    auto fetch = [&](int j) {
+      if (((j - p0) & 31) == 0) ids = j + lane < live ? list[j + lane] : -1;
+      const int64_t page = __shfl_sync(0xffffffffu, ids, (j - p0) & 31);
+      next_ok = page >= 0 && page < p.num_pages;
+      if (next_ok) load_tile(p, page, head, tok0, g, t, &next);
+      else if (lane == 0) report(p.dev_err, MSA_DEVERR_BAD_PAGE);
+    };
+    if (p0 < live) fetch(p0);
+    for (int j = p0; j < live; ++j) {
+      Tile cur = next;
+      const bool ok = next_ok;
+      if (j + 1 < live) fetch(j + 1);
+      if (ok) attend_tile(q, coef, cur, min(16, tokens - j * kBk - tok0), g, t, &st);
+    }
+
+    // the eight warps' softmaxes joined
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) st.l[c] += __shfl_xor_sync(0xffffffffu, st.l[c], o);
+    if (g == 0) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        s_m[warp][2 * t + c] = st.m[c];
+        s_l[warp][2 * t + c] = st.l[c];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        *reinterpret_cast<float2*>(&s_o[warp][2 * t + c][16 * g + 2 * i]) = make_float2(st.acc[i][c], st.acc[i][c + 2]);
+    __syncthreads();
+    const int h = tid >> 5, d0 = (tid & 31) * 4;
+    float M = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][h]);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float mw = s_m[w][h];
+      const float f = mw == -INFINITY ? (s_l[w][h] == 0.f ? 0.f : 1.f) : ex2(mw - M);   // l != 0 there: a NaN that has to stay
+      const float4 v = *reinterpret_cast<const float4*>(&s_o[w][h][d0]);
+      o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y); o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
+      l = fmaf(f, s_l[w][h], l);
+    }
+    const int first = static_cast<int>(row_first / per), last = static_cast<int>((row_first + row_pages - 1) / per);
+    bool write = first == last;
+    if (!write) {
+      // slot 0: the part at the start of a CTA's run, slot 1: the one at its end
+      float* mine = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + (lo >= row_first ? 0 : 1)) * kPart;
+      *reinterpret_cast<float4*>(mine + h * kD + d0) = o;
+      if ((tid & 31) == 0) {
+        mine[kMaxG * kD + h] = M;
+        mine[kMaxG * kD + kMaxG + h] = l;
+      }
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) s_last = atomicAdd(&p.counter[row], 1) == last - first;
+      __syncthreads();
+      write = s_last != 0;
+      if (write) {
+        __threadfence();
+        auto part_of = [&](int c) { return p.part + (static_cast<int64_t>(c) * 2 + (c * per >= row_first ? 0 : 1)) * kPart; };
+        M = -INFINITY;
+        for (int c = first; c <= last; ++c) M = fmaxf(M, __ldcg(part_of(c) + kMaxG * kD + h));
+        o = make_float4(0.f, 0.f, 0.f, 0.f);
+        l = 0.f;
+        for (int c = first; c <= last; ++c) {
+          const float* x = part_of(c);
+          const float mc = __ldcg(x + kMaxG * kD + h), lc = __ldcg(x + kMaxG * kD + kMaxG + h);
+          const float f = mc == -INFINITY ? (lc == 0.f ? 0.f : 1.f) : ex2(mc - M);
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(x + h * kD + d0));
+          o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y); o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
+          l = fmaf(f, lc, l);
+        }
+        if (tid == 0) p.counter[row] = 0;
+      }
+    }
+    if (write && h < p.G) {
+      const int64_t at = static_cast<int64_t>(b) * p.Hq + head * p.G + h;
+      const float r = l == 0.f ? 0.f : p.v_scale / l;
+      const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * r, o.y * r), y = __floats2bfloat162_rn(o.z * r, o.w * r);
+      uint2 w;
+      w.x = *reinterpret_cast<const uint32_t*>(&x);
+      w.y = *reinterpret_cast<const uint32_t*>(&y);
+      *reinterpret_cast<uint2*>(p.O + at * kD + d0) = w;
+      if (p.LSE != nullptr && (tid & 31) == 0) p.LSE[at] = l == 0.f ? -INFINITY : (M - kPShift + log2f(l)) * kLn2;
+    }
+    __syncthreads();
+  }
+
+  if (DENSE) {             // sequences without a token have no units
+    for (int r = blockIdx.x; r < rows; r += gridDim.x) {
+      const int b = r / p.Hkv, head = r - b * p.Hkv;
+      if (s_pre[b + 1] != s_pre[b]) continue;
+      const int h = tid >> 5;
+      if (h >= p.G) continue;
+      const int64_t at = static_cast<int64_t>(b) * p.Hq + head * p.G + h;
+      *reinterpret_cast<uint2*>(p.O + at * kD + (tid & 31) * 4) = make_uint2(0, 0);
+      if (p.LSE != nullptr && (tid & 31) == 0) p.LSE[at] = -INFINITY;
+    }
+  }
+}
+
+size_t counter_bytes(int B, int Hkv) { return (static_cast<size_t>(B) * Hkv * sizeof(int32_t) + 255) / 256 * 256; }
+
+template <class Args>
+Params common_params(const Args& a, void* ws) {
+  Params p = {};
+  p.B = a.B; p.Hq = a.Hq; p.Hkv = a.Hkv; p.G = a.Hq / a.Hkv;
+  const float scale = a.softmax_scale > 0.f ? a.softmax_scale : 1.0f / sqrtf(static_cast<float>(a.D));
+  p.scale_log2 = scale * kLog2e * a.cache.k_scale;
+  p.v_scale = a.cache.v_scale;
+  p.Q = static_cast<const uint8_t*>(a.Q);
+  p.q0 = a.Q_stride[0] * 2; p.q1 = a.Q_stride[1] * 2;
+  p.K_codes = static_cast<const uint8_t*>(a.cache.K_codes);
+  p.K_scales = static_cast<const uint8_t*>(a.cache.K_scales);
+  p.V_codes = static_cast<const uint8_t*>(a.cache.V_codes);
+  p.V_scales = static_cast<const uint8_t*>(a.cache.V_scales);
+  p.c0 = a.cache.code_stride[0]; p.c1 = a.cache.code_stride[1];
+  p.s0 = a.cache.scale_stride[0]; p.s1 = a.cache.scale_stride[1];
+  p.num_pages = a.cache.num_pages;
+  p.counter = static_cast<int32_t*>(ws);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + counter_bytes(a.B, a.Hkv));
+  p.O = static_cast<__nv_bfloat16*>(a.O);
+  p.LSE = a.LSE;
+  p.dev_err = a.dev_err;
+  return p;
+}
+
+template <bool DENSE>
+msa_status launch(const Params& p, int64_t most_units, int scratch_zeroed, cudaStream_t stream) {
+  DeviceInfo dev;
+  if (msa_status st = current_device(&dev); st != MSA_OK) return st;
+  if (!scratch_zeroed) {   // otherwise zero by contract (every error-free call leaves them zero)
+    const cudaError_t e = cudaMemsetAsync(p.counter, 0, static_cast<size_t>(p.B) * p.Hkv * sizeof(int32_t), stream);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(4-bit decode row counters)");
+  }
+  const int64_t room = std::min<int64_t>(static_cast<int64_t>(dev.num_sms) * kCtasPerSm, kMaxGrid);
+  const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(room, most_units)));
+  attn_q4_kernel<DENSE><<<grid, kThreads, 0, stream>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "attn_q4_kernel launch");
+  return MSA_OK;
+}
+
+}  // namespace
+
+size_t attn_decode_q4_workspace_size(int B, int Hkv) {
+  return counter_bytes(B, Hkv) + static_cast<size_t>(kMaxGrid) * 2 * kPart * sizeof(float);
+}
+
+msa_status launch_sparse_decode_q4(const msa_decode_q4_args& a, void* ws, cudaStream_t stream) {
+  Params p = common_params(a, ws);
+  p.k = a.k;
+  p.pt = a.pt; p.n = a.n; p.last_len = a.last_len;
+  return launch<false>(p, static_cast<int64_t>(a.B) * a.Hkv * a.k, a.scratch_zeroed, stream);
+}
+
+msa_status launch_dense_decode_q4(const msa_dense_decode_q4_args& a, void* ws, cudaStream_t stream) {
+  Params p = common_params(a, ws);
+  p.seq_pt = a.seq_pt; p.seq_len = a.seq_len; p.max_pages = a.max_pages;
+  return launch<true>(p, static_cast<int64_t>(a.B) * a.Hkv * a.max_pages, a.scratch_zeroed, stream);
+}
+
+}  // namespace msa

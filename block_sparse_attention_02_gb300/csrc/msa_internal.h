@@ -55,6 +55,14 @@ msa_status launch_cache_append(const msa_append_args& a, cudaStream_t stream);
 msa_status launch_dense_decode(const msa_dense_decode_args& a, void* ws, size_t ws_bytes, cudaStream_t stream);
 size_t dense_decode_workspace_size(const msa_dense_decode_args& a);
 msa_status launch_dense_prefill(const msa_dense_prefill_args& a, cudaStream_t stream);
+msa_status launch_plan_step(const msa_plan_args& a, cudaStream_t stream);
+msa_status launch_release_pages(const msa_release_args& a, cudaStream_t stream);
+msa_status launch_qk_norm_rope(const msa_norm_rope_args& a, cudaStream_t stream);
+msa_status launch_append_q4(const msa_append_q4_args& a, cudaStream_t stream);
+msa_status launch_expand_q4(const msa_expand_q4_args& a, cudaStream_t stream);
+msa_status launch_sparse_decode_q4(const msa_decode_q4_args& a, void* ws, cudaStream_t stream);
+msa_status launch_dense_decode_q4(const msa_dense_decode_q4_args& a, void* ws, cudaStream_t stream);
+size_t attn_decode_q4_workspace_size(int B, int Hkv);
 // Host-side argument checks of msa_sparse_attn_decode (no CUDA call).
 msa_status check_decode_args(const msa_decode_args* a);
 size_t attn_prefill_workspace_size(const msa_prefill_args& a, int64_t chunk_queries);

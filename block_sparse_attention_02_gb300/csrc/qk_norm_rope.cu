@@ -1,0 +1,230 @@
+// qk_norm_rope.cu -- RMS norm of every query and key head and the position
+// rotation in one pass, the keys and values written straight into their pages.
+//
+// Per token and head of D values:  y = x * rsqrt(mean(x^2) + eps) * w, then the
+// first rot values turned in pairs (a, b) -> (a cos t - b sin t, b cos t + a sin t)
+// with t = pos * inv_freq[i].  All of it in fp32 with one rounding at the end.
+//
+// The angle.  A position of a million times a frequency near 1 needs more than
+// fp32's 24 bits.  Only the fraction of a turn matters, so each lane keeps its
+// frequencies as turns per token in 64-bit fixed point (2^64 = one turn) and
+// pos * that, modulo 2^64, is the angle: one integer product, exact but for the
+// 53 bits of the frequency itself (2^-33 turns at 2^20 tokens).
+//
+// Layout: D / 16 lanes hold a head, 16 values each as two 16-byte chunks that
+// contain both members of every pair (chunks i and i + rot / 16 for split pairs,
+// any chunk for adjacent ones), so the rotation needs no exchange and the norm
+// log2(D / 16) shuffles.  A warp takes one token and walks its heads, which
+// share the token's sines; with few tokens the heads are split over warps.
+// Bound: HBM, every value read and written once.
+#include "msa_internal.h"
+#include "msa_ptx.cuh"
+
+namespace msa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+struct NormRopeParams {
+  int64_t N, num_pages;
+  int Hq, Hkv, rot, interleaved, weight_fp32, parts, Bk;
+  float eps;
+  const uint8_t *Q, *K, *V;
+  int64_t q0, q1, k0, k1, v0, v1;             // byte strides (n, h)
+  const int32_t* pos;
+  const float* inv_freq;
+  const void *q_weight, *k_weight;
+  uint8_t *Q_out, *K_out, *V_out;
+  int64_t qo0, qo1;                           // byte strides (n, h)
+  int64_t ko0, ko1, ko2, vo0, vo1, vo2;       // (n, h, -), or (page, g, t) with slots
+  const int64_t* slots;
+  int32_t* dev_err;
+};
+
+__device__ __forceinline__ void unpack8(const uint4 u, float* x) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float* x) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void load_weight8(const void* w, int fp32, int at, float* x) {
+  if (fp32) {
+    const float* f = static_cast<const float*>(w) + at;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = f[i];
+  } else {
+    const __nv_bfloat16* h = static_cast<const __nv_bfloat16*>(w) + at;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __bfloat162float(h[i]);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParams p) {
+  constexpr int kLanes = D / 16;              // lanes per head
+  constexpr int kHeads = 32 / kLanes;         // heads per warp and step
+  const int lane = threadIdx.x & 31;
+  const int sub = lane % kLanes, hl = lane / kLanes;
+  const int half = p.rot >> 4;                // chunks in each half of the rotated values
+  int c0, c1;                                 // this lane's chunks of 8 values
+  bool turn0, turn1;
+  if (p.interleaved) {
+    c0 = sub;
+    c1 = sub + kLanes;
+    turn0 = c0 < 2 * half;
+    turn1 = c1 < 2 * half;
+  } else {
+    c0 = sub < half ? sub : 2 * half + 2 * (sub - half);
+    c1 = sub < half ? sub + half : c0 + 1;
+    turn0 = turn1 = sub < half;
+  }
+  // turns per token in units of 2^-64 turns: pairs 8 sub + e, or 4 c0 + e and 4 c1 + e
+  uint64_t turns[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int i = p.interleaved ? 4 * (e < 4 ? c0 : c1) + (e & 3) : 8 * sub + e;
+    turns[e] = 0;
+    if (e < 4 ? turn0 : turn1) {
+      double t = static_cast<double>(p.inv_freq[i]) * 0.15915494309189533577;   // 1 / (2 pi)
+      t -= floor(t);
+      turns[e] = __double2ull_rz(t * 18446744073709551616.0);
+    }
+  }
+  const int q_steps = (p.Hq + kHeads - 1) / kHeads, k_steps = (p.Hkv + kHeads - 1) / kHeads;
+  const int steps = q_steps + k_steps + (p.V != nullptr ? k_steps : 0);
+  const int64_t items = p.N * p.parts;
+  bool bad = false;
+  for (int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); item < items;
+       item += static_cast<int64_t>(gridDim.x) * kWarps) {
+    const int64_t n = item / p.parts;
+    const int pos = p.pos[n];
+    if (pos < 0) continue;
+    // where this token's key and value rows go
+    int64_t k_row = n * p.ko0, v_row = 0;
+    bool store_kv = true;
+    if (p.slots != nullptr) {
+      const int64_t slot = p.slots[n], page = slot / p.Bk;
+      const int t = static_cast<int>(slot % p.Bk);
+      store_kv = slot >= 0 && page < p.num_pages;
+      bad |= slot >= 0 && !store_kv;
+      k_row = page * p.ko0 + t * p.ko2;
+      v_row = page * p.vo0 + t * p.vo2;
+    }
+    float cs[8], sn[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int32_t a = static_cast<int32_t>((turns[e] * static_cast<uint64_t>(pos)) >> 32);
+      sincospif(static_cast<float>(a) * 4.656612873077393e-10f, &sn[e], &cs[e]);   // 2^-31: half turns
+    }
+    for (int step = static_cast<int>(item % p.parts); step < steps; step += p.parts) {
+      const bool is_q = step < q_steps, is_v = step >= q_steps + k_steps;
+      const int head = (is_q ? step : is_v ? step - q_steps - k_steps : step - q_steps) * kHeads + hl;
+      const bool live = head < (is_q ? p.Hq : p.Hkv) && (is_q || store_kv);
+      if (is_v) {
+        if (live) {
+          const uint8_t* src = p.V + n * p.v0 + head * p.v1;
+          uint8_t* dst = p.V_out + v_row + head * p.vo1;
+          *reinterpret_cast<uint4*>(dst + c0 * 16) = *reinterpret_cast<const uint4*>(src + c0 * 16);
+          *reinterpret_cast<uint4*>(dst + c1 * 16) = *reinterpret_cast<const uint4*>(src + c1 * 16);
+        }
+        continue;
+      }
+      const uint8_t* src = is_q ? p.Q + n * p.q0 + head * p.q1 : p.K + n * p.k0 + head * p.k1;
+      float x[16];
+      uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
+      if (live) {
+        u0 = *reinterpret_cast<const uint4*>(src + c0 * 16);
+        u1 = *reinterpret_cast<const uint4*>(src + c1 * 16);
+      }
+      unpack8(u0, x);
+      unpack8(u1, x + 8);
+      const void* weight = is_q ? p.q_weight : p.k_weight;
+      if (weight != nullptr) {
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float r = rsqrtf(ss * (1.0f / D) + p.eps);
+        float w[16];
+        load_weight8(weight, p.weight_fp32, c0 * 8, w);
+        load_weight8(weight, p.weight_fp32, c1 * 8, w + 8);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = x[i] * r * w[i];
+      }
+      if (p.interleaved) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (e < 4 ? turn0 : turn1) {
+            const float a = x[2 * e], b = x[2 * e + 1];
+            x[2 * e] = a * cs[e] - b * sn[e];
+            x[2 * e + 1] = b * cs[e] + a * sn[e];
+          }
+        }
+      } else if (turn0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float a = x[e], b = x[8 + e];
+          x[e] = a * cs[e] - b * sn[e];
+          x[8 + e] = b * cs[e] + a * sn[e];
+        }
+      }
+      if (live) {
+        uint8_t* dst = is_q ? p.Q_out + n * p.qo0 + head * p.qo1 : p.K_out + k_row + head * p.ko1;
+        *reinterpret_cast<uint4*>(dst + c0 * 16) = pack8(x);
+        *reinterpret_cast<uint4*>(dst + c1 * 16) = pack8(x + 8);
+      }
+    }
+  }
+  if (bad && lane == 0) report(p.dev_err, MSA_DEVERR_BAD_PAGE);
+}
+
+}  // namespace
+
+msa_status launch_qk_norm_rope(const msa_norm_rope_args& a, cudaStream_t stream) {
+  DeviceInfo dev;
+  if (msa_status st = current_device(&dev); st != MSA_OK) return st;
+  NormRopeParams p;
+  p.N = a.N; p.num_pages = a.num_pages; p.Hq = a.Hq; p.Hkv = a.Hkv; p.rot = a.rot; p.Bk = a.Bk;
+  p.interleaved = a.interleaved; p.weight_fp32 = a.weight_fp32; p.eps = a.eps;
+  p.Q = static_cast<const uint8_t*>(a.Q);
+  p.K = static_cast<const uint8_t*>(a.K);
+  p.V = static_cast<const uint8_t*>(a.V);
+  p.q0 = a.Q_stride[0] * 2; p.q1 = a.Q_stride[1] * 2;
+  p.k0 = a.K_stride[0] * 2; p.k1 = a.K_stride[1] * 2;
+  p.v0 = a.V_stride[0] * 2; p.v1 = a.V_stride[1] * 2;
+  p.pos = a.pos; p.inv_freq = a.inv_freq; p.q_weight = a.q_weight; p.k_weight = a.k_weight;
+  p.Q_out = static_cast<uint8_t*>(a.Q_out);
+  p.K_out = static_cast<uint8_t*>(a.K_out);
+  p.V_out = static_cast<uint8_t*>(a.V_out);
+  p.qo0 = a.Q_out_stride[0] * 2; p.qo1 = a.Q_out_stride[1] * 2;
+  p.ko0 = a.K_out_stride[0] * 2; p.ko1 = a.K_out_stride[1] * 2; p.ko2 = a.K_out_stride[2] * 2;
+  p.vo0 = a.V_out_stride[0] * 2; p.vo1 = a.V_out_stride[1] * 2; p.vo2 = a.V_out_stride[2] * 2;
+  p.slots = a.slots; p.dev_err = a.dev_err;
+  const int heads = a.D == 128 ? 4 : 8;       // per warp and step
+  const int steps = (a.Hq + heads - 1) / heads + (a.V != nullptr ? 2 : 1) * ((a.Hkv + heads - 1) / heads);
+  // few tokens: their heads spread over enough warps to fill the SMs
+  const int64_t want = static_cast<int64_t>(dev.num_sms) * 32;
+  p.parts = static_cast<int>(std::min<int64_t>(std::max<int64_t>((want + a.N - 1) / a.N, 1), std::max(steps, 1)));
+  const int64_t items = a.N * p.parts;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>((items + kWarps - 1) / kWarps, dev.num_sms * 8));
+  if (a.D == 128) norm_rope_kernel<128><<<grid, kThreads, 0, stream>>>(p);
+  else norm_rope_kernel<64><<<grid, kThreads, 0, stream>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "norm_rope_kernel launch");
+  return MSA_OK;
+}
+
+}  // namespace msa

@@ -68,6 +68,7 @@ typedef enum msa_status {
 #define MSA_DEVERR_BAD_PAGE 0x2  /* a page id outside [0, num_pages) */
 #define MSA_DEVERR_BAD_SEL 0x4   /* a selected block outside the causal range */
 #define MSA_DEVERR_BAD_LEN 0x8   /* seq_len[b] (or a chunk's q_pos[b]) outside the pages or past nb_stride */
+#define MSA_DEVERR_NO_PAGES 0x10 /* the stack of free pages ran out, or holds no room for returned pages */
 
 /* PREFILL: a causal prefill over contiguous K/V/k_idx tensors.
  * DECODE:  one query per sequence over a paged cache.
@@ -533,6 +534,243 @@ typedef struct msa_append_args {
 } msa_append_args;
 
 msa_status msa_cache_append(const msa_append_args *args, msa_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * Page tables and token slots from request lengths
+ *
+ * The step before the cache append, on the GPU: which pages each request's new
+ * tokens need and where every token row goes ([serving], "MSA con paged
+ * attention": fixed-size pages).  Request b holds seq_len[b] cached tokens and
+ * brings new_len[b] (0 allowed: it sits the step out).  With have = ceil(seq_len / Bk),
+ * need = ceil((seq_len + new_len) / Bk) - have and off_b = sum of need over the
+ * requests before b:
+ *     seq_pt[b][have + i]  = free_pages[free_count - 1 - (off_b + i)],  i < need
+ *     cu[b]                = min(N, sum of new_len over the requests before b)
+ *     row r = cu[b] + i, i < new_len[b]:  tok_seq[r] = b, tok_pos[r] = seq_len[b] + i,
+ *                          tok_slot[r] = seq_pt[b][tok_pos[r] / Bk] * Bk + tok_pos[r] % Bk
+ *     seq_len_out[b]       = seq_len[b] + new_len[b]
+ *     free_count_out       = free_count - (pages taken)
+ * Rows from cu[B] to N (the padding of a captured graph) and the rows of a
+ * request that is not served get tok_seq = tok_pos = tok_slot = -1, which the
+ * calls that take slots and positions leave alone.
+ *   - A request whose pages go past the stack (off_b + need > free_count) is not
+ *     served: its length stays, its rows are -1, MSA_DEVERR_NO_PAGES.  Every
+ *     later request that needs a page is then refused too.
+ *   - seq_len < 0, seq_len + new_len > max_pages * Bk, or rows past N: not
+ *     served, needs no page, MSA_DEVERR_BAD_LEN.  new_len < 0 counts as 0
+ *     rows, with MSA_DEVERR_BAD_LEN.
+ *   - A page id outside [0, num_pages): the row's slot is -1 (its position
+ *     stays), MSA_DEVERR_BAD_PAGE.
+ * seq_len_out may be seq_len and free_count_out may be free_count.  The other
+ * outputs overlap nothing.  seq_pt entries other than the ones given stay.
+ * B <= 4096, N < 2^31, max_pages * Bk < 2^31.  tok_seq may be NULL.
+ * ------------------------------------------------------------------------ */
+typedef struct msa_plan_args {
+    int B, Bk;
+    int64_t N;                    /* token rows */
+    const int32_t *seq_len;       /* [B] */
+    const int32_t *new_len;       /* [B] */
+    int32_t *seq_pt;              /* [B, max_pages] */
+    int64_t max_pages;
+    const int32_t *free_pages;    /* [free_cap], a stack of page ids */
+    int64_t free_cap;
+    const int32_t *free_count;    /* [1] */
+    int64_t num_pages;
+    int32_t *seq_len_out;         /* [B] */
+    int32_t *free_count_out;      /* [1] */
+    int32_t *cu;                  /* [B + 1] */
+    int64_t *tok_slot;            /* [N] */
+    int32_t *tok_pos;             /* [N] */
+    int32_t *tok_seq;             /* [N] or NULL */
+    int32_t *dev_err;
+} msa_plan_args;
+
+msa_status msa_plan_step(const msa_plan_args *args, msa_stream_t stream);
+
+/* The pages of ended requests go back on the stack: for every b with done[b] != 0,
+ * in order, free_pages[free_count + ..] = seq_pt[b][0 .. ceil(seq_len[b] / Bk)), and
+ * seq_len_out[b] = 0 (the others keep their length); free_count_out is the new
+ * height.  seq_pt is left as it is.  A length outside [0, max_pages * Bk] of an
+ * ended request is not returned and keeps its length (MSA_DEVERR_BAD_LEN);
+ * pages past free_cap are dropped (MSA_DEVERR_NO_PAGES), and so is the part of a
+ * free_count outside [0, free_cap].  seq_len_out may be seq_len and
+ * free_count_out may be free_count.  B <= 4096. */
+typedef struct msa_release_args {
+    int B, Bk;
+    const int32_t *seq_len;       /* [B] */
+    const int32_t *done;          /* [B] */
+    const int32_t *seq_pt;        /* [B, max_pages] */
+    int64_t max_pages;
+    int32_t *free_pages;          /* [free_cap] */
+    int64_t free_cap;
+    const int32_t *free_count;    /* [1] */
+    int32_t *seq_len_out;         /* [B] */
+    int32_t *free_count_out;      /* [1] */
+    int32_t *dev_err;
+} msa_release_args;
+
+msa_status msa_release_pages(const msa_release_args *args, msa_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * Norm of queries and keys for each head, with the position rotation
+ *
+ * One pass from a projection's output to attention's inputs.  For every token
+ * row r and head x of Q and K (D values):
+ *     y = x * rsqrt(mean(x^2) + eps) * weight          (weight NULL: y = x)
+ *     the first rot values of y are turned in pairs (a, b) by the angle
+ *     pos[r] * inv_freq[i], i < rot / 2:  (a cos - b sin, b cos + a sin);
+ *     pair i is (i, i + rot / 2), or (2i, 2i + 1) with interleaved = 1
+ * fp32 throughout, the angle reduced in 64 bits, one rounding to bf16 at the end.
+ *     Q [N, Hq, D], K and V [N, Hkv, D] bf16, strides (n, h); Q_out [N, Hq, D]
+ *     q_weight, k_weight [D], bf16 or (weight_fp32 = 1) fp32; pos [N] int32;
+ *     inv_freq [rot / 2] fp32; rot a multiple of 16 up to D, 0: no rotation
+ * slots NULL: K_out [N, Hkv, D] with strides (n, h) in K_out_stride[0..1]; no V.
+ * slots given (tok_slot of msa_plan_step): K_out and V_out are page pools
+ *   [num_pages, Hkv, Bk, D] with strides (page, g, t), and token r goes to row
+ *   slots[r] % Bk of page slots[r] / Bk; V (copied as it is) and V_out may both be NULL.
+ * A row with pos < 0 is left out (Q_out, K_out and V_out untouched).  With
+ * slots, a row with slots[r] < 0 writes Q_out alone; one at or past
+ * num_pages * Bk does too and raises MSA_DEVERR_BAD_PAGE.  Two rows with the
+ * same slot leave either one's value.  K may be NULL with Hkv = 0.  Q_out may be
+ * Q and K_out may be K (same pointer and strides).  D = 64 or 128; pointers and
+ * strides 16-byte aligned (inv_freq and the weights: 4-byte).
+ * ------------------------------------------------------------------------ */
+typedef struct msa_norm_rope_args {
+    int64_t N;
+    int Hq, Hkv, D, Bk, rot, interleaved, weight_fp32;
+    float eps;
+    const void *Q;
+    int64_t Q_stride[2];
+    const void *K;
+    int64_t K_stride[2];
+    const void *V;
+    int64_t V_stride[2];
+    const int32_t *pos;
+    const float *inv_freq;
+    const void *q_weight;
+    const void *k_weight;
+    void *Q_out;
+    int64_t Q_out_stride[2];
+    void *K_out;
+    int64_t K_out_stride[3];
+    void *V_out;
+    int64_t V_out_stride[3];
+    const int64_t *slots;
+    int64_t num_pages;
+    int32_t *dev_err;
+} msa_norm_rope_args;
+
+msa_status msa_qk_norm_rope(const msa_norm_rope_args *args, msa_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * Paged cache held in 4 bits
+ *
+ * K and V as 4-bit floats (1 sign, 2 exponent, 1 mantissa bit: 0, 0.5, 1, 1.5, 2,
+ * 3, 4, 6) with one 8-bit scale (E4M3) for each 16 channels and one power-of-two
+ * scale for the whole pool: 72 bytes per token and head where bf16 takes 256.
+ *     sf   = e4m3(min(amax / (6 * scale), 448))      amax over the 16 channels
+ *     code = e2m1(x / (sf * scale))                  0 where sf = 0
+ *     the block stands for code * sf * scale
+ * with round to nearest even throughout; a value past the range (an infinity
+ * too) becomes the largest, a group that holds a NaN reads as NaN.
+ * Pools: codes [num_pages, Hkv, Bk, D / 2] bytes, element 2i in the low half of
+ * byte i; scales [num_pages, Hkv, Bk, D / 16] bytes; K's and V's share strides
+ * (page, g), multiples of 16 bytes; a block's Bk rows are contiguous.
+ * k_scale and v_scale are powers of two in [2^-64, 2^64] (a quotient is then exact
+ * enough in fp32 that codes never depend on its rounding); D = 128.
+ * ------------------------------------------------------------------------ */
+typedef struct msa_q4_cache {
+    void *K_codes, *K_scales, *V_codes, *V_scales;
+    int64_t code_stride[2];       /* bytes: (page, g) */
+    int64_t scale_stride[2];      /* bytes: (page, g) */
+    int64_t num_pages;
+    float k_scale, v_scale;
+} msa_q4_cache;
+
+/* Token r's K and V [N, Hkv, D] bf16 (strides (n, h)) into slot slots[r] (page * Bk +
+ * row, as msa_plan_step writes).  slots[r] < 0: nothing is stored; at or past
+ * num_pages * Bk: nothing, and MSA_DEVERR_BAD_PAGE.  Two rows with the same slot
+ * leave a mixture of both. */
+typedef struct msa_append_q4_args {
+    int64_t N;
+    int Hkv, D, Bk;
+    const void *K;
+    int64_t K_stride[2];
+    const void *V;
+    int64_t V_stride[2];
+    const int64_t *slots;
+    msa_q4_cache cache;
+    int32_t *dev_err;
+} msa_append_q4_args;
+
+msa_status msa_cache_append_q4(const msa_append_q4_args *args, msa_stream_t stream);
+
+/* The bf16 values of n pages: K_out, V_out [n, Hkv, Bk, D] (dense) from pages
+ * pages[i], for the calls that read bf16 pools (chunk prefill over a 4-bit
+ * prefix).  A page id outside [0, num_pages) leaves its block of the outputs
+ * untouched and raises MSA_DEVERR_BAD_PAGE.  Values past bf16's range become infinite. */
+typedef struct msa_expand_q4_args {
+    int64_t n;
+    int Hkv, D, Bk;
+    const int32_t *pages;
+    msa_q4_cache cache;
+    void *K_out;
+    void *V_out;
+    int32_t *dev_err;
+} msa_expand_q4_args;
+
+msa_status msa_cache_expand_q4(const msa_expand_q4_args *args, msa_stream_t stream);
+
+/* msa_sparse_attn_decode over a 4-bit cache: the same rows, page table, outputs
+ * and empty rows (n[r] = 0: O = 0, LSE = -inf).  n is taken within [0, k] and
+ * last_len within [0, Bk].  Cached values are exact in the products' fp16
+ * operands; Q is scaled by a power of two per head into fp16's range
+ * (subnormal parts below 2^-24 of the head's largest value round), P is rounded to fp16.
+ * Slots past a row's last token may hold anything.  Page ids outside
+ * [0, num_pages): left out, MSA_DEVERR_BAD_PAGE.  LSE may be NULL.
+ * Workspace: msa_attn_decode_q4_workspace_size(B, Hkv) bytes, 16-byte aligned,
+ * the row counters first.  scratch_zeroed works as in msa_sparse_attn_decode.
+ * Calls that overlap on the GPU need workspaces of their own.  B <= 4096. */
+typedef struct msa_decode_q4_args {
+    int B, Hq, Hkv, D, Bk, k;
+    float softmax_scale;
+    const void *Q;
+    int64_t Q_stride[2];
+    msa_q4_cache cache;
+    const int32_t *pt;
+    const int32_t *n;
+    const int32_t *last_len;
+    void *O;
+    float *LSE;
+    int32_t *dev_err;
+    int scratch_zeroed;
+} msa_decode_q4_args;
+
+size_t msa_attn_decode_q4_workspace_size(int B, int Hkv);
+msa_status msa_sparse_attn_decode_q4(const msa_decode_q4_args *args, void *ws, size_t ws_bytes, msa_stream_t stream);
+
+/* msa_dense_attn_decode over a 4-bit cache: every cached token of each sequence.
+ * A length of 0 is an empty sequence (O = 0, LSE = -inf, no error); one outside
+ * [0, max_pages * Bk] gives the same and raises MSA_DEVERR_BAD_LEN.  Workspace
+ * and page ids as in msa_sparse_attn_decode_q4; B <= 1024 and
+ * B * Hkv * max_pages < 2^30. */
+typedef struct msa_dense_decode_q4_args {
+    int B, Hq, Hkv, D, Bk;
+    float softmax_scale;
+    const void *Q;
+    int64_t Q_stride[2];
+    msa_q4_cache cache;
+    const int32_t *seq_pt;
+    int64_t max_pages;
+    const int32_t *seq_len;
+    void *O;
+    float *LSE;
+    int32_t *dev_err;
+    int scratch_zeroed;
+} msa_dense_decode_q4_args;
+
+msa_status msa_dense_attn_decode_q4(const msa_dense_decode_q4_args *args, void *ws, size_t ws_bytes,
+                                    msa_stream_t stream);
 
 #ifdef __cplusplus
 }
