@@ -452,45 +452,13 @@ def msa_cache_append(K_new: torch.Tensor, V_new: torch.Tensor, kidx_new: torch.T
 
 # ---------------------------------------------------------------------------
 # the serving step around the cache: page tables and slots, norm with rotation,
-# and the cache held in 4 bits
+# and the cache held in 4 bits.  The tensors are checked and marshalled in
+# _msa_binding (csrc/binding.cpp), which raises ValueError where one does not fit.
 # ---------------------------------------------------------------------------
 
-def _cuda(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device, dim: int) -> int:
-    """The pointer of a tensor that has to be of this type, device and number of dimensions."""
-    if t.dtype != dtype or t.dim() != dim or t.device != device:
-        raise ValueError(f"{name}: need a {dim}-dimensional {dtype} tensor on {device}, got {t.dim()} dimensions of "
-                         f"{t.dtype} on {t.device}")
-    return t.data_ptr()
-
-
-def _dense(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device, dim: int) -> int:
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return _cuda(t, name, dtype, device, dim)
-
-
-def _err_ptr(dev_err: Optional[torch.Tensor], device: torch.device):
-    if dev_err is None:
-        return None
-    if dev_err.numel() < 1:
-        raise ValueError("dev_err: need an int32 tensor of one value")
-    return _dense(dev_err, "dev_err", torch.int32, device, dev_err.dim())
-
-
-def _on(device: torch.device, stream, name: str, *args) -> None:
-    """Calls the entry point with the tensors' device current, on ``stream`` or on that device's current stream."""
-    if device.type != "cuda":
-        raise ValueError(f"{name}: tensors must be on a CUDA device, got {device}")
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif isinstance(stream, torch.cuda.Stream) and stream.device != device:
-        raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on {device}")
-    raw = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-    if torch.cuda.current_device() == device.index:
-        _abi.check(getattr(lib(), name)(*args, raw), name)
-    else:
-        with torch.cuda.device(device):
-            _abi.check(getattr(lib(), name)(*args, raw), name)
+def _call(name: str, status: int) -> None:
+    if status:
+        _abi.check(status, name)
 
 
 def plan_buffers(B: int, N: int, device) -> Dict[str, torch.Tensor]:
@@ -513,23 +481,9 @@ def msa_plan_step(seq_len: torch.Tensor, new_len: torch.Tensor, seq_pt: torch.Te
     free_count_out [1] (may be free_count), cu [B+1], and for N token rows tok_slot [N] int64, tok_pos and tok_seq [N]
     int32 (-1 in rows past the last token and in those of requests that were not served).
     """
-    d, i32 = seq_len.device, torch.int32
-    B, N = seq_len.shape[0], tok_slot.shape[0]
-    if new_len.shape[0] != B or seq_pt.shape[0] != B or seq_len_out.shape[0] != B or cu.shape[0] != B + 1:
-        raise ValueError(f"B = {B}: new_len, seq_pt and seq_len_out need B rows, cu B + 1")
-    if tok_pos.shape[0] != N or (tok_seq is not None and tok_seq.shape[0] != N):
-        raise ValueError(f"tok_slot, tok_pos and tok_seq need the same number of rows, got {N}, {tok_pos.shape[0]}")
-    if free_count.numel() != 1 or free_count_out.numel() != 1:
-        raise ValueError("free_count and free_count_out hold one value")
-    a = _abi.PlanArgs(
-        B, Bk, N, _dense(seq_len, "seq_len", i32, d, 1), _dense(new_len, "new_len", i32, d, 1),
-        _dense(seq_pt, "seq_pt", i32, d, 2), seq_pt.shape[1], _dense(free_pages, "free_pages", i32, d, 1),
-        free_pages.shape[0], _dense(free_count, "free_count", i32, d, 1), num_pages,
-        _dense(seq_len_out, "seq_len_out", i32, d, 1), _dense(free_count_out, "free_count_out", i32, d, 1),
-        _dense(cu, "cu", i32, d, 1), _dense(tok_slot, "tok_slot", torch.int64, d, 1),
-        _dense(tok_pos, "tok_pos", i32, d, 1), None if tok_seq is None else _dense(tok_seq, "tok_seq", i32, d, 1),
-        _err_ptr(dev_err, d))
-    _on(d, stream, "msa_plan_step", a)
+    _call("msa_plan_step", _abi.binding().plan_step(
+        seq_len, new_len, seq_pt, free_pages, free_count, seq_len_out, free_count_out, cu, tok_slot, tok_pos, tok_seq,
+        num_pages, dev_err, stream))
 
 
 def msa_release_pages(seq_len: torch.Tensor, done: torch.Tensor, seq_pt: torch.Tensor, free_pages: torch.Tensor,
@@ -540,19 +494,8 @@ def msa_release_pages(seq_len: torch.Tensor, done: torch.Tensor, seq_pt: torch.T
     seq_len, done [B] int32, seq_pt [B,max_pages] int32 (left as it is), free_pages [F] int32 (written above
     free_count), free_count [1]; seq_len_out [B] and free_count_out [1] may be the inputs.
     """
-    d, i32 = seq_len.device, torch.int32
-    B = seq_len.shape[0]
-    if done.shape[0] != B or seq_pt.shape[0] != B or seq_len_out.shape[0] != B:
-        raise ValueError(f"B = {B}: done, seq_pt and seq_len_out need B rows")
-    if free_count.numel() != 1 or free_count_out.numel() != 1:
-        raise ValueError("free_count and free_count_out hold one value")
-    a = _abi.ReleaseArgs(
-        B, Bk, _dense(seq_len, "seq_len", i32, d, 1), _dense(done, "done", i32, d, 1),
-        _dense(seq_pt, "seq_pt", i32, d, 2), seq_pt.shape[1], _dense(free_pages, "free_pages", i32, d, 1),
-        free_pages.shape[0], _dense(free_count, "free_count", i32, d, 1),
-        _dense(seq_len_out, "seq_len_out", i32, d, 1), _dense(free_count_out, "free_count_out", i32, d, 1),
-        _err_ptr(dev_err, d))
-    _on(d, stream, "msa_release_pages", a)
+    _call("msa_release_pages", _abi.binding().release_pages(
+        seq_len, done, seq_pt, free_pages, free_count, seq_len_out, free_count_out, dev_err, stream))
 
 
 def msa_qk_norm_rope(Q: torch.Tensor, K: Optional[torch.Tensor], pos: torch.Tensor, inv_freq: Optional[torch.Tensor],
@@ -568,50 +511,8 @@ def msa_qk_norm_rope(Q: torch.Tensor, K: Optional[torch.Tensor], pos: torch.Tens
     K_out [N,Hkv,D], or with ``slots`` [N] int64 the page pool [P,Hkv,Bk,D] that K goes into, and V into V_out.
     Q_out may be Q and K_out may be K.  Rows with pos < 0 are left out.
     """
-    d, bf16 = Q.device, torch.bfloat16
-    N, Hq, D_ = Q.shape
-    Hkv = 0 if K is None else K.shape[1]
-    if (K is None) != (K_out is None) or (K is None and (V is not None or slots is not None)):
-        raise ValueError("K, K_out, V and slots: K and K_out go together, V and slots need them")
-    if Q_out.shape != Q.shape or pos.shape[0] != N or (K is not None and K.shape != (N, Hkv, D_)) or (
-            V is not None and V.shape != K.shape):
-        raise ValueError("Q and Q_out [N,Hq,D], K and V [N,Hkv,D] and pos [N] must agree")
-    pools = [x for x in (K_out, V_out) if x is not None]
-    for x in pools:
-        if slots is None and x.shape != (N, Hkv, D_):
-            raise ValueError("K_out must be [N,Hkv,D] without slots")
-        if slots is not None and (x.dim() != 4 or x.shape != (K_out.shape[0], Hkv, Bk, D_)):
-            raise ValueError(f"K_out and V_out must be pools [P,Hkv,{Bk},D] with slots")
-    if slots is not None and slots.shape[0] != N:
-        raise ValueError("slots must be [N]")
-    fp32 = False
-    for w, nm in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            if w.shape != (D_,) or w.dtype not in (bf16, torch.float32):
-                raise ValueError(f"{nm} must be [{D_}], bf16 or fp32")
-            fp32 = w.dtype == torch.float32
-    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
-        raise ValueError("q_weight and k_weight must have one type")
-    for x, nm in ((Q, "Q"), (K, "K"), (V, "V"), (Q_out, "Q_out"), (K_out, "K_out"), (V_out, "V_out")):
-        if x is not None and x.numel() > 0:
-            _inner_contig(x, nm)
-    wt = torch.float32 if fp32 else bf16
-    kd = 3 if slots is None else 4
-    a = _abi.NormRopeArgs(
-        N, Hq, Hkv, D_, Bk, 0 if inv_freq is None else 2 * inv_freq.shape[0], int(interleaved), int(fp32), eps,
-        _cuda(Q, "Q", bf16, d, 3), Q.stride()[:2],
-        *((None, (0, 0)) if K is None else (_cuda(K, "K", bf16, d, 3), K.stride()[:2])),
-        *((None, (0, 0)) if V is None else (_cuda(V, "V", bf16, d, 3), V.stride()[:2])),
-        _dense(pos, "pos", torch.int32, d, 1),
-        None if inv_freq is None else _dense(inv_freq, "inv_freq", torch.float32, d, 1),
-        None if q_weight is None else _dense(q_weight, "q_weight", wt, d, 1),
-        None if k_weight is None else _dense(k_weight, "k_weight", wt, d, 1),
-        _cuda(Q_out, "Q_out", bf16, d, 3), Q_out.stride()[:2],
-        *((None, (0, 0, 0)) if K_out is None else (_cuda(K_out, "K_out", bf16, d, kd), K_out.stride()[:kd - 1])),
-        *((None, (0, 0, 0)) if V_out is None else (_cuda(V_out, "V_out", bf16, d, kd), V_out.stride()[:kd - 1])),
-        None if slots is None else _dense(slots, "slots", torch.int64, d, 1),
-        0 if slots is None else K_out.shape[0], _err_ptr(dev_err, d))
-    _on(d, stream, "msa_qk_norm_rope", a)
+    _call("msa_qk_norm_rope", _abi.binding().qk_norm_rope(
+        Q, K, pos, inv_freq, Q_out, K_out, V, V_out, slots, q_weight, k_weight, eps, interleaved, dev_err, stream))
 
 
 class Q4Cache(NamedTuple):
@@ -632,58 +533,20 @@ def q4_cache(num_pages: int, Hkv: int, device, k_scale: float = 1.0, v_scale: fl
     return Q4Cache(pool(D // 2), pool(D // 16), pool(D // 2), pool(D // 16), k_scale, v_scale)
 
 
-def _q4_args(c: Q4Cache, d: torch.device) -> _abi.Q4CacheArgs:
-    P, Hkv = c.K_codes.shape[:2]
-    u8, cs, ss = torch.uint8, c.K_codes.stride(), c.K_scales.stride()
-    if c.K_codes.shape != (P, Hkv, Bk, D // 2) or c.V_codes.shape != c.K_codes.shape or c.K_scales.shape != (
-            P, Hkv, Bk, D // 16) or c.V_scales.shape != c.K_scales.shape:
-        raise ValueError(f"a 4-bit cache has codes [P,Hkv,{Bk},{D // 2}] and scales [P,Hkv,{Bk},{D // 16}]")
-    if c.V_codes.stride() != cs or c.V_scales.stride() != ss or cs[2:] != (D // 2, 1) or ss[2:] != (D // 16, 1):
-        raise ValueError("a 4-bit cache's K and V must share strides, and a block's rows be contiguous")
-    return _abi.Q4CacheArgs(_cuda(c.K_codes, "K_codes", u8, d, 4), _cuda(c.K_scales, "K_scales", u8, d, 4),
-                            _cuda(c.V_codes, "V_codes", u8, d, 4), _cuda(c.V_scales, "V_scales", u8, d, 4),
-                            cs[:2], ss[:2], P, c.k_scale, c.v_scale)
-
-
 def msa_cache_append_q4(K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, cache: Q4Cache, *,
                         dev_err: Optional[torch.Tensor] = None, stream=None) -> None:
     """Stores K, V [N,Hkv,D] bf16 in 4 bits at slots [N] int64 (page * Bk + row; < 0: not stored) (see msa.h)."""
-    d, bf16 = K.device, torch.bfloat16
-    N, Hkv, D_ = K.shape
-    if V.shape != K.shape or slots.shape[0] != N or cache.K_codes.shape[1] != Hkv:
-        raise ValueError("K and V [N,Hkv,D], slots [N] and the cache's heads must agree")
-    if N > 0:
-        _inner_contig(K, "K")
-        _inner_contig(V, "V")
-    a = _abi.AppendQ4Args(N, Hkv, D_, Bk, _cuda(K, "K", bf16, d, 3), K.stride()[:2], _cuda(V, "V", bf16, d, 3),
-                          V.stride()[:2], _dense(slots, "slots", torch.int64, d, 1), _q4_args(cache, d),
-                          _err_ptr(dev_err, d))
-    _on(d, stream, "msa_cache_append_q4", a)
+    _call("msa_cache_append_q4", _abi.binding().cache_append_q4(K, V, slots, cache, dev_err, stream))
 
 
 def msa_cache_expand_q4(cache: Q4Cache, pages: torch.Tensor, K_out: torch.Tensor, V_out: torch.Tensor, *,
                         dev_err: Optional[torch.Tensor] = None, stream=None) -> None:
     """The bf16 values of pages [n] int32 into K_out, V_out [n,Hkv,Bk,D] (see msa.h)."""
-    d, bf16 = cache.K_codes.device, torch.bfloat16
-    n, Hkv = pages.shape[0], cache.K_codes.shape[1]
-    if K_out.shape != (n, Hkv, Bk, D) or V_out.shape != K_out.shape:
-        raise ValueError(f"K_out and V_out must be [n,Hkv,{Bk},{D}]")
-    a = _abi.ExpandQ4Args(n, Hkv, D, Bk, _dense(pages, "pages", torch.int32, d, 1), _q4_args(cache, d),
-                          _dense(K_out, "K_out", bf16, d, 4), _dense(V_out, "V_out", bf16, d, 4), _err_ptr(dev_err, d))
-    _on(d, stream, "msa_cache_expand_q4", a)
+    _call("msa_cache_expand_q4", _abi.binding().cache_expand_q4(cache, pages, K_out, V_out, dev_err, stream))
 
 
 def msa_attn_decode_q4_workspace_size(B: int, Hkv: int) -> int:
     return int(lib().msa_attn_decode_q4_workspace_size(B, Hkv))
-
-
-def _attn_q4_outputs(Q, O, LSE, ws, d):
-    B, Hq, D_ = Q.shape
-    if O.shape != Q.shape or (LSE is not None and LSE.shape != (B, Hq)):
-        raise ValueError("O must be [B,Hq,D] and LSE [B,Hq]")
-    if not ws.is_contiguous() or ws.device != d:
-        raise ValueError(f"ws must be a contiguous tensor on {d}")
-    return _dense(O, "O", torch.bfloat16, d, 3), None if LSE is None else _dense(LSE, "LSE", torch.float32, d, 2)
 
 
 def msa_sparse_attn_decode_q4(Q: torch.Tensor, cache: Q4Cache, pt: torch.Tensor, n: torch.Tensor,
@@ -692,19 +555,8 @@ def msa_sparse_attn_decode_q4(Q: torch.Tensor, cache: Q4Cache, pt: torch.Tensor,
                               scratch_zeroed: bool = False) -> None:
     """``msa_sparse_attn_decode`` over a 4-bit cache (see msa.h): Q [B,Hq,D] bf16, pt [B*Hkv,k], n, last_len [B*Hkv]
     int32; O [B,Hq,D] bf16, LSE [B,Hq] fp32; ws of ``msa_attn_decode_q4_workspace_size`` bytes."""
-    d, i32 = Q.device, torch.int32
-    B, Hq, D_ = Q.shape
-    Hkv = cache.K_codes.shape[1]
-    rows = B * Hkv
-    if pt.shape[0] != rows or n.shape[0] != rows or last_len.shape[0] != rows:
-        raise ValueError(f"pt, n and last_len need B * Hkv = {rows} rows")
-    if B > 0:
-        _inner_contig(Q, "Q")
-    o, lse = _attn_q4_outputs(Q, O, LSE, ws, d)
-    a = _abi.DecodeQ4Args(B, Hq, Hkv, D_, Bk, pt.shape[1], softmax_scale, _cuda(Q, "Q", torch.bfloat16, d, 3),
-                          Q.stride()[:2], _q4_args(cache, d), _dense(pt, "pt", i32, d, 2), _dense(n, "n", i32, d, 1),
-                          _dense(last_len, "last_len", i32, d, 1), o, lse, _err_ptr(dev_err, d), int(scratch_zeroed))
-    _on(d, stream, "msa_sparse_attn_decode_q4", a, ws.data_ptr(), ws.numel() * ws.element_size())
+    _call("msa_sparse_attn_decode_q4", _abi.binding().sparse_attn_decode_q4(
+        Q, cache, pt, n, last_len, O, LSE, ws, softmax_scale, dev_err, stream, scratch_zeroed))
 
 
 def msa_dense_attn_decode_q4(Q: torch.Tensor, cache: Q4Cache, seq_pt: torch.Tensor, seq_len: torch.Tensor,
@@ -713,18 +565,8 @@ def msa_dense_attn_decode_q4(Q: torch.Tensor, cache: Q4Cache, seq_pt: torch.Tens
                              scratch_zeroed: bool = False) -> None:
     """``msa_dense_attn_decode`` over a 4-bit cache (see msa.h): Q [B,Hq,D] bf16, seq_pt [B,max_pages], seq_len [B]
     int32 (0: an empty sequence); O [B,Hq,D] bf16, LSE [B,Hq] fp32; ws as for ``msa_sparse_attn_decode_q4``."""
-    d, i32 = Q.device, torch.int32
-    B, Hq, D_ = Q.shape
-    Hkv = cache.K_codes.shape[1]
-    if seq_pt.shape[0] != B or seq_len.shape[0] != B:
-        raise ValueError(f"seq_pt and seq_len need B = {B} rows")
-    if B > 0:
-        _inner_contig(Q, "Q")
-    o, lse = _attn_q4_outputs(Q, O, LSE, ws, d)
-    a = _abi.DenseDecodeQ4Args(B, Hq, Hkv, D_, Bk, softmax_scale, _cuda(Q, "Q", torch.bfloat16, d, 3), Q.stride()[:2],
-                               _q4_args(cache, d), _dense(seq_pt, "seq_pt", i32, d, 2), seq_pt.shape[1],
-                               _dense(seq_len, "seq_len", i32, d, 1), o, lse, _err_ptr(dev_err, d), int(scratch_zeroed))
-    _on(d, stream, "msa_dense_attn_decode_q4", a, ws.data_ptr(), ws.numel() * ws.element_size())
+    _call("msa_dense_attn_decode_q4", _abi.binding().dense_attn_decode_q4(
+        Q, cache, seq_pt, seq_len, O, LSE, ws, softmax_scale, dev_err, stream, scratch_zeroed))
 
 
 # ---------------------------------------------------------------------------

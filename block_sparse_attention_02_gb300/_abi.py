@@ -211,6 +211,7 @@ SIGNATURES = {
 
 _lock = threading.Lock()
 _lib = None
+_binding = None
 
 
 def load(path: str = LIB_PATH):
@@ -228,6 +229,20 @@ def load(path: str = LIB_PATH):
                 f.argtypes = args
             _lib = lib
     return _lib
+
+
+def binding():
+    """The module that marshals torch tensors for the serving-step calls (built in-tree beside libmsa.so)."""
+    global _binding
+    if _binding is None:
+        load()
+        try:
+            from . import _msa_binding
+        except ImportError as e:
+            raise RuntimeError("_msa_binding is missing: build it with "
+                               "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+        _binding = _msa_binding
+    return _binding
 
 
 class MSAError(RuntimeError):

@@ -3,7 +3,9 @@
 Each ``csrc/*.cu`` is compiled in parallel to an object under ``_build/`` and
 the objects are linked into ``libmsa.so`` next to this file (CUDA runtime
 linked statically, so the library needs only the driver at run time).
-Objects are rebuilt when their source or any header is newer.
+``csrc/binding.cpp`` becomes ``_msa_binding.so``, the Python module that checks
+and marshals torch tensors for the serving-step calls; it finds ``libmsa.so``
+beside itself.  Objects are rebuilt when their source or any header is newer.
 """
 from __future__ import annotations
 
@@ -20,6 +22,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmsa.so")
+BINDING = os.path.join(HERE, "_msa_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
@@ -47,8 +50,38 @@ def _compile(src: str, obj: str, extra) -> str:
     return r.stderr
 
 
+def _compile_binding(src: str, obj: str, extra) -> str:
+    """binding.cpp against torch's and this interpreter's headers."""
+    import sysconfig
+
+    import torch
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    at = os.path.join(os.path.dirname(torch.__file__), "include")
+    inc = [at, os.path.join(at, "torch", "csrc", "api", "include"), sysconfig.get_path("include"),
+           os.path.join(cuda, "include"), os.path.join(cuda, "targets", f"{os.uname().machine}-linux", "include")]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           *[x for d in inc for x in ("-isystem", d)], "-c", src, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {os.path.basename(src)}:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    return ""
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, f"-L{HERE}", "-l:libmsa.so", f"-L{libs}", "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile every CUDA source for sm_103a and link libmsa.so; returns its path."""
+    """Compile every CUDA source for sm_103a and link libmsa.so and the Python module; returns the library's path."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     hdr = _headers_mtime()
@@ -56,11 +89,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     for s in srcs:
         o = os.path.join(BUILD, os.path.splitext(os.path.basename(s))[0] + ".o")
         if force or not os.path.exists(o) or os.path.getmtime(o) < max(os.path.getmtime(s), hdr):
-            jobs.append((s, o))
+            jobs.append((_compile, s, o))
+    bind_src, bind_obj = os.path.join(CSRC, "binding.cpp"), os.path.join(BUILD, "binding.o")
+    if force or not os.path.exists(bind_obj) or os.path.getmtime(bind_obj) < max(os.path.getmtime(bind_src), hdr):
+        jobs.append((_compile_binding, bind_src, bind_obj))
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
-            futs = {ex.submit(_compile, s, o, list(extra_flags) + (["-Xptxas", "-v"] if verbose else [])): s
-                    for s, o in jobs}
+            futs = {ex.submit(f, s, o, list(extra_flags) + (["-Xptxas", "-v"] if verbose else [])): s
+                    for f, s, o in jobs}
             for f in cf.as_completed(futs):
                 log = f.result()
                 if verbose and log:
@@ -73,6 +109,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    if force or jobs or not os.path.exists(BINDING):
+        _link_binding(bind_obj)
     return LIB
 
 

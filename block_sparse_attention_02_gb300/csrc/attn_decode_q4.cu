@@ -22,10 +22,12 @@
 // 2^14, is rounded to fp16 (2^-12 of the value down to 2^-22 of the largest).
 //
 // Work.  The (row, page) units of all rows form one list; each CTA takes an equal
-// run of it, its eight warps 16 tokens of every page each, with a softmax
+// run of it, its eight warps 32 tokens of every other page each, with a softmax
 // of their own that is joined in shared memory at the end of a row's part.  Rows
 // cut by a run's end go through the workspace; the CTA that arrives last joins them.
 #include <cuda_fp16.h>
+
+#include <cfloat>
 
 #include "msa_internal.h"
 #include "msa_ptx.cuh"
@@ -94,28 +96,30 @@ __device__ __forceinline__ uint2 ldg8(const uint8_t* p) {
   return v;
 }
 
-// A warp's 16 tokens of a page as loaded.
+// 16 tokens of a page as a lane loads them.  Row m of S^T is token
+// 2m - (m & 1) for m < 8 and that + 2 for m - 8, so that the four rows whose
+// probabilities a lane holds after the transposition are tokens 4t .. 4t + 3.
 struct Tile {
-  uint4 k[2];            // tokens g and g + 8, channels 32t .. 32t + 31
-  uint2 v[4];            // tokens 2t, 2t + 1, 2t + 8, 2t + 9, channels 16g .. 16g + 15
+  uint4 k[2];            // tokens 2g - (g & 1) and + 2, channels 32t .. 32t + 31
+  uint2 v[4];            // tokens 4t .. 4t + 3, channels 16g .. 16g + 15
   uint32_t ks[2], vs[4]; // their scale bytes (two groups, one group)
 };
 
-__device__ __forceinline__ void load_tile(const Params& p, int64_t page, int head, int tok0, int g, int t, Tile* x) {
-  const uint8_t* kc = p.K_codes + page * p.c0 + head * p.c1 + tok0 * 64;
-  const uint8_t* vc = p.V_codes + page * p.c0 + head * p.c1 + tok0 * 64;
-  const uint8_t* ks = p.K_scales + page * p.s0 + head * p.s1 + tok0 * 8;
-  const uint8_t* vs = p.V_scales + page * p.s0 + head * p.s1 + tok0 * 8;
+// Where a lane's share of a page's tokens starts, within page 0.
+struct Bases {
+  const uint8_t *kc, *vc, *ks, *vs;
+};
+
+__device__ __forceinline__ void load_tile(const Bases& at, int64_t code_off, int64_t scale_off, int tok, Tile* x) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    x->k[i] = ldg16(kc + (g + 8 * i) * 64 + t * 16);
-    x->ks[i] = __ldg(reinterpret_cast<const uint16_t*>(ks + (g + 8 * i) * 8 + t * 2));
+    x->k[i] = ldg16(at.kc + code_off + (tok + 2 * i) * 64);
+    x->ks[i] = __ldg(reinterpret_cast<const uint16_t*>(at.ks + scale_off + (tok + 2 * i) * 8));
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int tok = 2 * t + (i & 1) + 8 * (i >> 1);
-    x->v[i] = ldg8(vc + tok * 64 + g * 8);
-    x->vs[i] = __ldg(vs + tok * 8 + g);
+    x->v[i] = ldg8(at.vc + code_off + (tok + i) * 64);
+    x->vs[i] = __ldg(at.vs + scale_off + (tok + i) * 8);
   }
 }
 
@@ -128,11 +132,6 @@ struct State {
 
 __device__ __forceinline__ void attend_tile(const uint32_t (&q)[16], const float (&coef)[2], Tile& x, int valid, int g,
                                             int t, State* st) {
-  if (valid < 16) {      // slots past the last token may hold anything, a NaN scale too: they count as zeros
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (2 * t + (i & 1) + 8 * (i >> 1) >= valid) x.vs[i] = 0;
-  }
   float s[4] = {0.f, 0.f, 0.f, 0.f};
   {
     const __half2 sa = e4m3x2_to_half2(x.ks[0]), sb = e4m3x2_to_half2(x.ks[1]);
@@ -153,18 +152,25 @@ __device__ __forceinline__ void attend_tile(const uint32_t (&q)[16], const float
       mma16816(s, h2u(a[2]), h2u(b[2]), h2u(a[3]), h2u(b[3]), q[4 * i + 2], q[4 * i + 3]);
     }
   }
-  const bool on0 = g < valid, on1 = g + 8 < valid;
-  float z[4];
+  const int tok = 2 * g - (g & 1);
+  if (valid < 16) {      // slots past the last token may hold anything, a NaN scale too
 #pragma unroll
-  for (int i = 0; i < 4; ++i) z[i] = (i < 2 ? on0 : on1) ? s[i] * coef[i & 1] : -INFINITY;
-  const float top0 = fmaxf(z[0], z[2]), top1 = fmaxf(z[1], z[3]);
-  if (__any_sync(0xffffffffu, top0 > st->m[0] + kSlack || top1 > st->m[1] + kSlack)) {
-    float top[2] = {top0, top1};
+    for (int i = 0; i < 4; ++i) {
+      if (tok + (i < 2 ? 0 : 2) >= valid) s[i] = -INFINITY;
+      if (4 * t + i >= valid) x.vs[i] = 0;
+    }
+  }
+  // exponents of P relative to m - 8: infinite until a first maximum is known
+  float e[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) e[i] = fmaf(s[i], coef[i & 1], kPShift - st->m[i & 1]);
+  if (__any_sync(0xffffffffu, fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])) > kPShift + kSlack)) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
+      float top = fmaxf(s[c] * coef[c], s[c + 2] * coef[c]);
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], o));
-      const float m = fmaxf(st->m[c], top[c]);
+      for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float m = fmaxf(st->m[c], top);
       const float f = m == -INFINITY ? 1.f : ex2(st->m[c] - m);
       st->m[c] = m;
       st->l[c] *= f;
@@ -174,31 +180,32 @@ __device__ __forceinline__ void attend_tile(const uint32_t (&q)[16], const float
         st->acc[i][c + 2] *= f;
       }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e[i] = fmaf(s[i], coef[i & 1], kPShift - st->m[i & 1]);
   }
-  float pr[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) pr[i] = (i < 2 ? on0 : on1) ? ex2(z[i] - st->m[i & 1] + kPShift) : 0.f;
-  st->l[0] += pr[0] + pr[2];
-  st->l[1] += pr[1] + pr[3];
-  // P^T: from (token g, heads 2t, 2t + 1) to (head g, tokens 2t, 2t + 1)
-  const uint32_t b0 = transpose8x8(h2u(__floats2half2_rn(pr[0], pr[1])));
-  const uint32_t b1 = transpose8x8(h2u(__floats2half2_rn(pr[2], pr[3])));
-  __half2 sv[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) sv[i] = e4m3_to_half2(x.vs[i]);
+  for (int i = 0; i < 4; ++i) e[i] = ex2(e[i]);
+  st->l[0] += e[0] + e[2];
+  st->l[1] += e[1] + e[3];
+  // P^T: from (row g, heads 2t, 2t + 1) to (head g, rows 2t, 2t + 1)
+  const uint32_t b0 = transpose8x8(h2u(__floats2half2_rn(e[0], e[1])));
+  const uint32_t b1 = transpose8x8(h2u(__floats2half2_rn(e[2], e[3])));
+  const __half2 s01 = e4m3x2_to_half2(x.vs[0] | x.vs[1] << 8), s23 = e4m3x2_to_half2(x.vs[2] | x.vs[3] << 8);
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
-    __half2 v[4][4];
+    // the codes of two tokens side by side: even and odd channels' bytes (token, next token)
+    const uint32_t a = w ? x.v[0].y : x.v[0].x, b = w ? x.v[1].y : x.v[1].x;
+    const uint32_t c = w ? x.v[2].y : x.v[2].x, d = w ? x.v[3].y : x.v[3].x;
+    constexpr uint32_t kLow = 0x0f0f0f0fu;
+    __half2 even01[4], odd01[4], even23[4], odd23[4];
+    e2m1x8_to_half2((a & kLow) | ((b << 4) & ~kLow), even01);
+    e2m1x8_to_half2(((a >> 4) & kLow) | (b & ~kLow), odd01);
+    e2m1x8_to_half2((c & kLow) | ((d << 4) & ~kLow), even23);
+    e2m1x8_to_half2(((c >> 4) & kLow) | (d & ~kLow), odd23);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      e2m1x8_to_half2(w ? x.v[i].y : x.v[i].x, v[i]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[i][e] = __hmul2(v[i][e], sv[i]);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      mma16816(st->acc[w * 4 + e], h2u(__lows2half2(v[0][e], v[1][e])), h2u(__highs2half2(v[0][e], v[1][e])),
-               h2u(__lows2half2(v[2][e], v[3][e])), h2u(__highs2half2(v[2][e], v[3][e])), b0, b1);
+    for (int i = 0; i < 4; ++i)
+      mma16816(st->acc[w * 4 + i], h2u(__hmul2(even01[i], s01)), h2u(__hmul2(odd01[i], s01)),
+               h2u(__hmul2(even23[i], s23)), h2u(__hmul2(odd23[i], s23)), b0, b1);
   }
 }
 
@@ -313,7 +320,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_q4_kernel(const Par
 #pragma unroll
       for (int i = 0; i < 16; ++i) q[i] = h2u(__floats2half2_rn(f[2 * i] * down, f[2 * i + 1] * down));
 #pragma unroll
-      for (int c = 0; c < 2; ++c) coef[c] = __shfl_sync(0xffffffffu, up, 8 * t + 4 * c) * p.scale_log2;
+      for (int c = 0; c < 2; ++c) 
+        coef[c] = fmaxf(__shfl_sync(0xffffffffu, up, 8 * t + 4 * c) * p.scale_log2, FLT_MIN);   // > 0: -inf stays so
     }
     State st;
 #pragma unroll
@@ -323,25 +331,42 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_q4_kernel(const Par
     st.m[0] = st.m[1] = -INFINITY;
     st.l[0] = st.l[1] = 0.f;
 
-    // this warp's 16 tokens of each page, the next page's loads in flight behind the present one's work
-    const int tok0 = warp * 16;
+    // this warp's 32 tokens of every other page: two tiles, each loaded again for the next page as soon as it is used
+    const int tok0 = (warp & 3) * 32;
+    const int j0 = p0 + (warp >> 2);
     const int live = min(p1, (tokens - tok0 + kBk - 1) / kBk);   // pages with a token of this warp's
-    int32_t ids = 0;
-    Tile next;
-    bool next_ok = false;
-    auto fetch = [&](int j) {
-      if (((j - p0) & 31) == 0) ids = j + lane < live ? list[j + lane] : -1;
-      const int64_t page = __shfl_sync(0xffffffffu, ids, (j - p0) & 31);
-      next_ok = page >= 0 && page < p.num_pages;
-      if (next_ok) load_tile(p, page, head, tok0, g, t, &next);
-      else if (lane == 0) report(p.dev_err, MSA_DEVERR_BAD_PAGE);
+    const Bases at = {p.K_codes + head * p.c1 + (tok0 + 2 * g - (g & 1)) * 64 + t * 16,
+                      p.V_codes + head * p.c1 + (tok0 + 4 * t) * 64 + g * 8,
+                      p.K_scales + head * p.s1 + (tok0 + 2 * g - (g & 1)) * 8 + t * 2,
+                      p.V_scales + head * p.s1 + (tok0 + 4 * t) * 8 + g};
+    int32_t ids = 0;                        // lane i: page of iteration (n & ~31) + i
+    int64_t code_off = 0, scale_off = 0;
+    auto find = [&](int n) {                // the page of iteration n; false: a bad id
+      if ((n & 31) == 0) ids = j0 + 2 * (n + lane) < live ? list[j0 + 2 * (n + lane)] : -1;
+      const int64_t page = __shfl_sync(0xffffffffu, ids, n & 31);
+      const bool ok = page >= 0 && page < p.num_pages;
+      if (!ok && lane == 0) report(p.dev_err, MSA_DEVERR_BAD_PAGE);
+      code_off = page * p.c0;
+      scale_off = page * p.s0;
+      return ok;
     };
-    if (p0 < live) fetch(p0);
-    for (int j = p0; j < live; ++j) {
-      Tile cur = next;
-      const bool ok = next_ok;
-      if (j + 1 < live) fetch(j + 1);
-      if (ok) attend_tile(q, coef, cur, min(16, tokens - j * kBk - tok0), g, t, &st);
+    Tile x, y;
+    bool ok = false;
+    if (j0 < live) {
+      ok = find(0);
+      if (ok) {
+        load_tile(at, code_off, scale_off, 0, &x);
+        load_tile(at, code_off, scale_off, 16, &y);
+      }
+    }
+    for (int j = j0, n = 1; j < live; j += 2, ++n) {
+      const int left = tokens - j * kBk - tok0;
+      const bool now = ok;
+      ok = j + 2 < live && find(n);
+      if (now) attend_tile(q, coef, x, left, g, t, &st);
+      if (ok) load_tile(at, code_off, scale_off, 0, &x);
+      if (now) attend_tile(q, coef, y, left - 16, g, t, &st);
+      if (ok) load_tile(at, code_off, scale_off, 16, &y);
     }
 
     // the eight warps' softmaxes joined

@@ -25,10 +25,11 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kCtasPerSm = 3;
 
 struct NormRopeParams {
   int64_t N, num_pages;
-  int Hq, Hkv, rot, interleaved, weight_fp32, parts, Bk;
+  int Hq, Hkv, rot, weight_fp32, parts;
   float eps;
   const uint8_t *Q, *K, *V;
   int64_t q0, q1, k0, k1, v0, v1;             // byte strides (n, h)
@@ -59,28 +60,25 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void load_weight8(const void* w, int fp32, int at, float* x) {
-  if (fp32) {
-    const float* f = static_cast<const float*>(w) + at;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = f[i];
-  } else {
-    const __nv_bfloat16* h = static_cast<const __nv_bfloat16*>(w) + at;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __bfloat162float(h[i]);
-  }
-}
-
-template <int D>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParams p) {
+template <int D, bool PAIRS>   // PAIRS: the rotated pairs are neighbours (2i, 2i + 1)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const NormRopeParams p) {
   constexpr int kLanes = D / 16;              // lanes per head
   constexpr int kHeads = 32 / kLanes;         // heads per warp and step
-  const int lane = threadIdx.x & 31;
+  __shared__ __align__(16) float s_weight[2][D];
+  __shared__ float2 s_turn[kWarps][D / 2];    // cosine and sine of every pair of a warp's token
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane % kLanes, hl = lane / kLanes;
-  const int half = p.rot >> 4;                // chunks in each half of the rotated values
-  int c0, c1;                                 // this lane's chunks of 8 values
+  for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+    const void* w = i < D ? p.q_weight : p.k_weight;
+    float x = 1.f;
+    if (w != nullptr)
+      x = p.weight_fp32 ? static_cast<const float*>(w)[i % D] : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i % D]);
+    s_weight[i / D][i % D] = x;
+  }
+  const int half = p.rot >> 4;                // chunks of 8 values in each half of the rotated ones
+  int c0, c1;                                 // this lane's chunks
   bool turn0, turn1;
-  if (p.interleaved) {
+  if (PAIRS) {
     c0 = sub;
     c1 = sub + kLanes;
     turn0 = c0 < 2 * half;
@@ -90,81 +88,108 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParam
     c1 = sub < half ? sub + half : c0 + 1;
     turn0 = turn1 = sub < half;
   }
-  // turns per token in units of 2^-64 turns: pairs 8 sub + e, or 4 c0 + e and 4 c1 + e
-  uint64_t turns[8];
+  // turns per token, in units of 2^-64 turns, of pairs lane and lane + 32
+  uint64_t turns[D / 64];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int i = p.interleaved ? 4 * (e < 4 ? c0 : c1) + (e & 3) : 8 * sub + e;
+  for (int e = 0; e < D / 64; ++e) {
     turns[e] = 0;
-    if (e < 4 ? turn0 : turn1) {
-      double t = static_cast<double>(p.inv_freq[i]) * 0.15915494309189533577;   // 1 / (2 pi)
+    if (lane + 32 * e < p.rot / 2) {
+      double t = static_cast<double>(p.inv_freq[lane + 32 * e]) * 0.15915494309189533577;   // 1 / (2 pi)
       t -= floor(t);
       turns[e] = __double2ull_rz(t * 18446744073709551616.0);
     }
   }
+  __syncthreads();
   const int q_steps = (p.Hq + kHeads - 1) / kHeads, k_steps = (p.Hkv + kHeads - 1) / kHeads;
   const int steps = q_steps + k_steps + (p.V != nullptr ? k_steps : 0);
   const int64_t items = p.N * p.parts;
   bool bad = false;
-  for (int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); item < items;
+  for (int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + warp; item < items;
        item += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const int64_t n = item / p.parts;
+    const int64_t n = p.parts == 1 ? item : item / p.parts;
+    const int first = p.parts == 1 ? 0 : static_cast<int>(item - n * p.parts);
     const int pos = p.pos[n];
     if (pos < 0) continue;
     // where this token's key and value rows go
     int64_t k_row = n * p.ko0, v_row = 0;
     bool store_kv = true;
     if (p.slots != nullptr) {
-      const int64_t slot = p.slots[n], page = slot / p.Bk;
-      const int t = static_cast<int>(slot % p.Bk);
+      const int64_t slot = p.slots[n], page = slot / kBk;
+      const int t = static_cast<int>(slot & (kBk - 1));
       store_kv = slot >= 0 && page < p.num_pages;
       bad |= slot >= 0 && !store_kv;
       k_row = page * p.ko0 + t * p.ko2;
       v_row = page * p.vo0 + t * p.vo2;
     }
+    auto head_of = [&](int step) {            // of this lane; -1: nothing to do
+      const bool is_q = step < q_steps;
+      const int head = (is_q ? step : step < q_steps + k_steps ? step - q_steps : step - q_steps - k_steps) * kHeads + hl;
+      return head < (is_q ? p.Hq : p.Hkv) && (is_q || store_kv) ? head : -1;
+    };
+    uint4 next0 = make_uint4(0, 0, 0, 0), next1 = next0;
+    auto fetch = [&](int step) {
+      const int head = head_of(step);
+      if (head < 0) return;
+      const uint8_t* src = step < q_steps             ? p.Q + n * p.q0 + head * p.q1
+                           : step < q_steps + k_steps ? p.K + n * p.k0 + head * p.k1
+                                                      : p.V + n * p.v0 + head * p.v1;
+      next0 = *reinterpret_cast<const uint4*>(src + c0 * 16);
+      next1 = *reinterpret_cast<const uint4*>(src + c1 * 16);
+    };
+    if (first < steps) fetch(first);
+    __syncwarp();                             // the last token's turns are read
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e) {
+      if (lane + 32 * e < p.rot / 2) {
+        const int32_t a = static_cast<int32_t>((turns[e] * static_cast<uint64_t>(pos)) >> 32);
+        float2 cs;
+        sincospif(static_cast<float>(a) * 4.656612873077393e-10f, &cs.y, &cs.x);   // 2^-31: half turns
+        s_turn[warp][lane + 32 * e] = cs;
+      }
+    }
+    __syncwarp();
     float cs[8], sn[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int32_t a = static_cast<int32_t>((turns[e] * static_cast<uint64_t>(pos)) >> 32);
-      sincospif(static_cast<float>(a) * 4.656612873077393e-10f, &sn[e], &cs[e]);   // 2^-31: half turns
+      const int i = PAIRS ? 4 * (e < 4 ? c0 : c1) + (e & 3) : 8 * sub + e;
+      const float2 v = (e < 4 ? turn0 : turn1) ? s_turn[warp][i] : make_float2(1.f, 0.f);
+      cs[e] = v.x;
+      sn[e] = v.y;
     }
-    for (int step = static_cast<int>(item % p.parts); step < steps; step += p.parts) {
-      const bool is_q = step < q_steps, is_v = step >= q_steps + k_steps;
-      const int head = (is_q ? step : is_v ? step - q_steps - k_steps : step - q_steps) * kHeads + hl;
-      const bool live = head < (is_q ? p.Hq : p.Hkv) && (is_q || store_kv);
-      if (is_v) {
-        if (live) {
-          const uint8_t* src = p.V + n * p.v0 + head * p.v1;
+    for (int step = first; step < steps; step += p.parts) {
+      const uint4 u0 = next0, u1 = next1;
+      if (step + p.parts < steps) fetch(step + p.parts);
+      const bool is_q = step < q_steps;
+      const int head = head_of(step);
+      if (step >= q_steps + k_steps) {        // values go as they are
+        if (head >= 0) {
           uint8_t* dst = p.V_out + v_row + head * p.vo1;
-          *reinterpret_cast<uint4*>(dst + c0 * 16) = *reinterpret_cast<const uint4*>(src + c0 * 16);
-          *reinterpret_cast<uint4*>(dst + c1 * 16) = *reinterpret_cast<const uint4*>(src + c1 * 16);
+          *reinterpret_cast<uint4*>(dst + c0 * 16) = u0;
+          *reinterpret_cast<uint4*>(dst + c1 * 16) = u1;
         }
         continue;
       }
-      const uint8_t* src = is_q ? p.Q + n * p.q0 + head * p.q1 : p.K + n * p.k0 + head * p.k1;
       float x[16];
-      uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
-      if (live) {
-        u0 = *reinterpret_cast<const uint4*>(src + c0 * 16);
-        u1 = *reinterpret_cast<const uint4*>(src + c1 * 16);
-      }
       unpack8(u0, x);
       unpack8(u1, x + 8);
-      const void* weight = is_q ? p.q_weight : p.k_weight;
-      if (weight != nullptr) {
+      if ((is_q ? p.q_weight : p.k_weight) != nullptr) {
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
         for (int o = 1; o < kLanes; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         const float r = rsqrtf(ss * (1.0f / D) + p.eps);
-        float w[16];
-        load_weight8(weight, p.weight_fp32, c0 * 8, w);
-        load_weight8(weight, p.weight_fp32, c1 * 8, w + 8);
+        const float* w = s_weight[is_q ? 0 : 1];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = x[i] * r * w[i];
+        for (int i = 0; i < 16; i += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(w + (i < 8 ? c0 * 8 + i : c1 * 8 + i - 8));
+          x[i] *= r * f.x;
+          x[i + 1] *= r * f.y;
+          x[i + 2] *= r * f.z;
+          x[i + 3] *= r * f.w;
+        }
       }
-      if (p.interleaved) {
+      if (PAIRS) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           if (e < 4 ? turn0 : turn1) {
@@ -181,7 +206,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParam
           x[8 + e] = b * cs[e] + a * sn[e];
         }
       }
-      if (live) {
+      if (head >= 0) {
         uint8_t* dst = is_q ? p.Q_out + n * p.qo0 + head * p.qo1 : p.K_out + k_row + head * p.ko1;
         *reinterpret_cast<uint4*>(dst + c0 * 16) = pack8(x);
         *reinterpret_cast<uint4*>(dst + c1 * 16) = pack8(x + 8);
@@ -197,8 +222,8 @@ msa_status launch_qk_norm_rope(const msa_norm_rope_args& a, cudaStream_t stream)
   DeviceInfo dev;
   if (msa_status st = current_device(&dev); st != MSA_OK) return st;
   NormRopeParams p;
-  p.N = a.N; p.num_pages = a.num_pages; p.Hq = a.Hq; p.Hkv = a.Hkv; p.rot = a.rot; p.Bk = a.Bk;
-  p.interleaved = a.interleaved; p.weight_fp32 = a.weight_fp32; p.eps = a.eps;
+  p.N = a.N; p.num_pages = a.num_pages; p.Hq = a.Hq; p.Hkv = a.Hkv; p.rot = a.rot;
+  p.weight_fp32 = a.weight_fp32; p.eps = a.eps;
   p.Q = static_cast<const uint8_t*>(a.Q);
   p.K = static_cast<const uint8_t*>(a.K);
   p.V = static_cast<const uint8_t*>(a.V);
@@ -216,12 +241,18 @@ msa_status launch_qk_norm_rope(const msa_norm_rope_args& a, cudaStream_t stream)
   const int heads = a.D == 128 ? 4 : 8;       // per warp and step
   const int steps = (a.Hq + heads - 1) / heads + (a.V != nullptr ? 2 : 1) * ((a.Hkv + heads - 1) / heads);
   // few tokens: their heads spread over enough warps to fill the SMs
-  const int64_t want = static_cast<int64_t>(dev.num_sms) * 32;
+  const int64_t want = static_cast<int64_t>(dev.num_sms) * kCtasPerSm * kWarps;
   p.parts = static_cast<int>(std::min<int64_t>(std::max<int64_t>((want + a.N - 1) / a.N, 1), std::max(steps, 1)));
   const int64_t items = a.N * p.parts;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>((items + kWarps - 1) / kWarps, dev.num_sms * 8));
-  if (a.D == 128) norm_rope_kernel<128><<<grid, kThreads, 0, stream>>>(p);
-  else norm_rope_kernel<64><<<grid, kThreads, 0, stream>>>(p);
+  const unsigned grid =
+      static_cast<unsigned>(std::min<int64_t>((items + kWarps - 1) / kWarps, static_cast<int64_t>(dev.num_sms) * kCtasPerSm));
+  if (a.D == 128) {
+    if (a.interleaved) norm_rope_kernel<128, true><<<grid, kThreads, 0, stream>>>(p);
+    else norm_rope_kernel<128, false><<<grid, kThreads, 0, stream>>>(p);
+  } else {
+    if (a.interleaved) norm_rope_kernel<64, true><<<grid, kThreads, 0, stream>>>(p);
+    else norm_rope_kernel<64, false><<<grid, kThreads, 0, stream>>>(p);
+  }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "norm_rope_kernel launch");
   return MSA_OK;

@@ -172,11 +172,12 @@ def test_empty_calls_enqueue_nothing(abi):
 # the Python wrappers
 # ---------------------------------------------------------------------------
 
-def test_wrappers_refuse(abi):
+def wrapper_refusals(device):
+    """Calls that the wrappers have to refuse, on tensors of this device."""
     import block_sparse_attention_02_gb300 as msa
-    z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt)  # noqa: E731
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt, device=device)  # noqa: E731
     i32, i64 = torch.int32, torch.int64
-    c = msa.q4_cache(3, 2, "cpu")
+    c = msa.q4_cache(3, 2, device)
     Q, K, pos = z(4, 6, 128), z(4, 2, 128), z(4, dt=i32)
     L, pt, free, one = z(4, dt=i32), z(4, 2, dt=i32), z(9, dt=i32), z(1, dt=i32)
     rows, rows32 = z(5, dt=i64), z(5, dt=i32)
@@ -186,27 +187,37 @@ def test_wrappers_refuse(abi):
         cu=rows32, tok_slot=rows, tok_pos=rows32, num_pages=9), **k})
     rope = lambda **k: msa.msa_qk_norm_rope(**{**dict(Q=Q, K=K, pos=pos, inv_freq=f, Q_out=Q, K_out=K), **k})  # noqa: E731
     bad = [
-        plan,                                                        # not on a CUDA device
         lambda: plan(new_len=z(3, dt=i32)), lambda: plan(cu=L), lambda: plan(tok_pos=L), lambda: plan(seq_len=z(4, dt=i64)),
         lambda: plan(seq_pt=z(2, 4, dt=i32).T), lambda: plan(free_count=z(2, dt=i32)), lambda: plan(tok_seq=z(6, dt=i32)),
         lambda: plan(dev_err=z(0, dt=i32)), lambda: plan(dev_err=z(1, dt=i64)),
         lambda: msa.msa_release_pages(L, L[:3], pt, free, one, L, one), lambda: msa.msa_release_pages(L, L.bool(), pt, free, one, L, one),
-        lambda: msa.msa_release_pages(L, L, pt, free, one, L, one),
-        rope, lambda: rope(Q_out=z(4, 5, 128)), lambda: rope(K=None), lambda: rope(K_out=z(3, 2, 128, 128)), lambda: rope(pos=pos[:3]),
+        lambda: rope(Q_out=z(4, 5, 128)), lambda: rope(K=None), lambda: rope(K_out=z(3, 2, 128, 128)), lambda: rope(pos=pos[:3]),
         lambda: rope(V=K), lambda: rope(slots=z(4, dt=i64)), lambda: rope(q_weight=z(64)), lambda: rope(q_weight=z(128, dt=torch.float16)),
         lambda: rope(q_weight=z(128), k_weight=z(128, dt=torch.float32)), lambda: rope(Q=z(4, 6, 256)[..., ::2], Q_out=Q),
         lambda: rope(inv_freq=f.double()), lambda: rope(Q=Q.float()), lambda: rope(K_out=z(3, 2, 64, 128), slots=z(4, dt=i64)),
-        lambda: msa.msa_cache_append_q4(K, K, z(4, dt=i64), c), lambda: msa.msa_cache_append_q4(K, K, z(4, dt=i32), c),
+        lambda: msa.msa_cache_append_q4(K, K, z(4, dt=i32), c),
         lambda: msa.msa_cache_append_q4(z(4, 3, 128), z(4, 3, 128), z(4, dt=i64), c), lambda: msa.msa_cache_append_q4(K, K[:3], z(4, dt=i64), c),
         lambda: msa.msa_cache_append_q4(K, K, z(4, dt=i64), c._replace(V_codes=c.V_codes[:2])),
         lambda: msa.msa_cache_append_q4(K, K, z(4, dt=i64), c._replace(K_codes=z(3, 128, 2, 64, dt=torch.uint8).transpose(1, 2))),
-        lambda: msa.msa_cache_expand_q4(c, one, z(1, 2, 128, 128), z(2, 2, 128, 128)), lambda: msa.msa_cache_expand_q4(c, one, z(1, 2, 128, 128), z(1, 2, 128, 128)),
-        lambda: msa.msa_sparse_attn_decode_q4(O, c, pt, L, L, O, LSE, ws), lambda: msa.msa_sparse_attn_decode_q4(O, c, pt[:3], L, L, O, LSE, ws),
+        lambda: msa.msa_cache_expand_q4(c, one, z(1, 2, 128, 128), z(2, 2, 128, 128)),
+        lambda: msa.msa_sparse_attn_decode_q4(O, c, pt[:3], L, L, O, LSE, ws),
         lambda: msa.msa_sparse_attn_decode_q4(O, c, pt, L, L, O[:1], LSE, ws), lambda: msa.msa_sparse_attn_decode_q4(O, c, pt, L, L, O, LSE[:1], ws),
-        lambda: msa.msa_dense_attn_decode_q4(O, c, pt[:2], L[:2], O, LSE, ws), lambda: msa.msa_dense_attn_decode_q4(O, c, pt, L, O, LSE, ws),
+        lambda: msa.msa_dense_attn_decode_q4(O, c, pt, L, O, LSE, ws),
         lambda: msa.msa_dense_attn_decode_q4(O, c, pt[:2], L[:2], O, LSE, ws[::2]),
+        lambda: rope(inv_freq=z(68, dt=torch.float32)[::2]), lambda: plan(stream="s"), lambda: plan(num_pages=2.5),
+        lambda: msa.msa_cache_append_q4(K, K, z(4, dt=i64), c[:4]), lambda: msa.msa_cache_append_q4([], K, z(4, dt=i64), c),
+        lambda: msa.msa_cache_append_q4(K, K, z(4, dt=i64), c._replace(k_scale="x")),
     ]
-    for i, refused in enumerate(bad):
+    on_host_only = [plan, lambda: msa.msa_release_pages(L, L, pt, free, one, L, one), rope,
+                    lambda: msa.msa_cache_append_q4(K, K, z(4, dt=i64), c),
+                    lambda: msa.msa_cache_expand_q4(c, one, z(1, 2, 128, 128), z(1, 2, 128, 128)),
+                    lambda: msa.msa_sparse_attn_decode_q4(O, c, pt, L, L, O, LSE, ws),
+                    lambda: msa.msa_dense_attn_decode_q4(O, c, pt[:2], L[:2], O, LSE, ws)]
+    return bad + (on_host_only if device == "cpu" else [])
+
+
+def test_wrappers_refuse(abi):
+    for i, refused in enumerate(wrapper_refusals("cpu")):
         with pytest.raises(ValueError):
             refused()
             raise AssertionError(f"call {i} was accepted")

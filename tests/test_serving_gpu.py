@@ -502,6 +502,35 @@ def test_decode_q4_far_pages(msa):
 
 
 # ---------------------------------------------------------------------------
+# refusals, streams
+# ---------------------------------------------------------------------------
+
+def test_wrappers_refuse_on_the_gpu(msa):
+    from test_serving_abi import wrapper_refusals
+    for i, refused in enumerate(wrapper_refusals("cuda")):
+        with pytest.raises(ValueError):
+            refused()
+            raise AssertionError(f"call {i} was accepted")
+    L, pt = i32([3]), i32([[0]])
+    with pytest.raises(msa.MSAError):                            # a workspace that is too small: the entry point's refusal
+        msa.msa_dense_attn_decode_q4(queries(1, 2, 0), msa.q4_cache(3, 2, "cuda"), pt, L, *outputs(1, 2), err_word())
+
+
+def test_stream_arguments(msa):
+    """A torch stream, its raw pointer and the current stream: work goes where it is sent."""
+    c = PLANS["edges"]()
+    want = ref.plan(*c)
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream, None):
+        t = [i32(x) for x in (c[0], c[1], c[2], c[3], [c[4]])]
+        o = msa.plan_buffers(len(c[0]), c[5], "cuda")
+        torch.cuda.synchronize()
+        msa.msa_plan_step(*t, *o.values(), num_pages=c[6], stream=stream)
+        (torch.cuda.current_stream() if stream is None else side).synchronize()
+        assert np.array_equal(o["tok_slot"].cpu(), want["tok_slot"]) and np.array_equal(o["cu"].cpu(), want["cu"])
+
+
+# ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
 
