@@ -22,7 +22,7 @@
 // 2^14, is rounded to fp16 (2^-12 of the value down to 2^-22 of the largest).
 //
 // Work.  The (row, page) units of all rows form one list; each CTA takes an equal
-// run of it, its eight warps 32 tokens of every other page each, with a softmax
+// run of it, its eight warps 16 tokens of every page each, with a softmax
 // of their own that is joined in shared memory at the end of a row's part.  Rows
 // cut by a run's end go through the workspace; the CTA that arrives last joins them.
 #include <cuda_fp16.h>
@@ -39,6 +39,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCtasPerSm = 2;
+constexpr int kStages = 4;                              // tiles of 16 tokens per warp in shared memory
 constexpr int kMaxGrid = 512;                           // CTAs per launch at most (sizes the workspace)
 constexpr int kPart = kMaxG * kD + 2 * kMaxG;           // floats of a partial: O [8][128], m [8], l [8]
 constexpr float kLog2e = 1.4426950408889634f;
@@ -82,44 +83,60 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-// Streaming loads: the cache is read once per step.
-__device__ __forceinline__ uint4 ldg16(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+// 16 bytes from the cache to shared memory, asynchronously and past L1: the cache is read once per step.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ uint2 ldg8(const uint8_t* p) {
-  uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// 16 tokens of a page as a lane loads them.  Row m of S^T is token
-// 2m - (m & 1) for m < 8 and that + 2 for m - 8, so that the four rows whose
-// probabilities a lane holds after the transposition are tokens 4t .. 4t + 3.
-struct Tile {
-  uint4 k[2];            // tokens 2g - (g & 1) and + 2, channels 32t .. 32t + 31
-  uint2 v[4];            // tokens 4t .. 4t + 3, channels 16g .. 16g + 15
-  uint32_t ks[2], vs[4]; // their scale bytes (two groups, one group)
-};
+// A warp's tile of 16 tokens in shared memory: K codes, V codes, K scales, V
+// scales, rows as in the page but for V's 16-byte chunks, of which rows 4-7 and 12-15 hold
+// them in the order 2, 3, 0, 1.  A lane's rows: row m of S^T is token
+// m ^ (m >> 1 & 1), so that the rows whose probabilities lane t holds after the
+// transposition are tokens 2t and 2t + 1 (swapped for odd t) and these + 8.  With
+// both, eight lanes that read 16 bytes of K, or sixteen that read 8 of V, meet every bank once.
+constexpr int kVAt = 1024, kKsAt = 2048, kVsAt = 2176, kTileBytes = 2304;
 
-// Where a lane's share of a page's tokens starts, within page 0.
+__device__ __forceinline__ int token_of_row(int m) { return m ^ ((m >> 1) & 1); }
+
+// Where a warp's tile of page 0 starts in the four pools.
 struct Bases {
   const uint8_t *kc, *vc, *ks, *vs;
 };
 
-__device__ __forceinline__ void load_tile(const Bases& at, int64_t code_off, int64_t scale_off, int tok, Tile* x) {
+__device__ __forceinline__ void fetch_tile(const Bases& at, int64_t code_off, int64_t scale_off, uint32_t dst, int lane) {
+  const int v_chunk = lane ^ ((lane >> 4) << 1);       // row lane / 4, chunk lane % 4 (^ 2 in rows 4-7)
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    x->k[i] = ldg16(at.kc + code_off + (tok + 2 * i) * 64);
-    x->ks[i] = __ldg(reinterpret_cast<const uint16_t*>(at.ks + scale_off + (tok + 2 * i) * 8));
+    copy16(dst + i * 512 + lane * 16, at.kc + code_off + i * 512 + lane * 16);
+    copy16(dst + kVAt + i * 512 + v_chunk * 16, at.vc + code_off + i * 512 + lane * 16);
+  }
+  if (lane < 16) copy16(dst + kKsAt + lane * 16, (lane < 8 ? at.ks : at.vs - 128) + scale_off + lane * 16);
+}
+
+// What a lane takes of a tile.
+struct Tile {
+  uint4 k[2];            // tokens token_of_row(g) and + 8, channels 32t .. 32t + 31
+  uint2 v[4];            // the tokens of rows 2t, 2t + 1 and these + 8, channels 16g .. 16g + 15
+  uint32_t ks[2], vs[4]; // their scale bytes (two groups, one group)
+};
+
+__device__ __forceinline__ void read_tile(const uint8_t* s, int g, int t, Tile* x) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int tok = token_of_row(g) + 8 * i;
+    x->k[i] = *reinterpret_cast<const uint4*>(s + tok * 64 + t * 16);
+    x->ks[i] = *reinterpret_cast<const uint16_t*>(s + kKsAt + tok * 8 + t * 2);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x->v[i] = ldg8(at.vc + code_off + (tok + i) * 64);
-    x->vs[i] = __ldg(at.vs + scale_off + (tok + i) * 8);
+    const int tok = token_of_row(2 * t + (i & 1)) + 8 * (i >> 1);
+    x->v[i] = *reinterpret_cast<const uint2*>(s + kVAt + tok * 64 + ((g * 8) ^ ((tok & 4) << 3)));
+    x->vs[i] = s[kVsAt + tok * 8 + g];
   }
 }
 
@@ -152,12 +169,11 @@ __device__ __forceinline__ void attend_tile(const uint32_t (&q)[16], const float
       mma16816(s, h2u(a[2]), h2u(b[2]), h2u(a[3]), h2u(b[3]), q[4 * i + 2], q[4 * i + 3]);
     }
   }
-  const int tok = 2 * g - (g & 1);
   if (valid < 16) {      // slots past the last token may hold anything, a NaN scale too
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (tok + (i < 2 ? 0 : 2) >= valid) s[i] = -INFINITY;
-      if (4 * t + i >= valid) x.vs[i] = 0;
+      if (token_of_row(g) + (i < 2 ? 0 : 8) >= valid) s[i] = -INFINITY;
+      if (token_of_row(2 * t + (i & 1)) + 8 * (i >> 1) >= valid) x.vs[i] = 0;
     }
   }
   // exponents of P relative to m - 8: infinite until a first maximum is known
@@ -211,7 +227,8 @@ __device__ __forceinline__ void attend_tile(const uint32_t (&q)[16], const float
 
 template <bool DENSE>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_q4_kernel(const Params p) {
-  __shared__ __align__(16) float s_o[kWarps][kMaxG][kD];
+  extern __shared__ __align__(128) uint8_t s_ring[];
+  float(*s_o)[kMaxG][kD] = reinterpret_cast<float(*)[kMaxG][kD]>(s_ring);   // after a row's part: [warp][head][channel]
   __shared__ float s_m[kWarps][kMaxG], s_l[kWarps][kMaxG];
   __shared__ int s_pre[DENSE ? kDenseMaxBatch + 1 : 1];   // pages of the sequences before b
   __shared__ int s_wsum[kWarps];
@@ -331,43 +348,43 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_q4_kernel(const Par
     st.m[0] = st.m[1] = -INFINITY;
     st.l[0] = st.l[1] = 0.f;
 
-    // this warp's 32 tokens of every other page: two tiles, each loaded again for the next page as soon as it is used
-    const int tok0 = (warp & 3) * 32;
-    const int j0 = p0 + (warp >> 2);
-    const int live = min(p1, (tokens - tok0 + kBk - 1) / kBk);   // pages with a token of this warp's
-    const Bases at = {p.K_codes + head * p.c1 + (tok0 + 2 * g - (g & 1)) * 64 + t * 16,
-                      p.V_codes + head * p.c1 + (tok0 + 4 * t) * 64 + g * 8,
-                      p.K_scales + head * p.s1 + (tok0 + 2 * g - (g & 1)) * 8 + t * 2,
-                      p.V_scales + head * p.s1 + (tok0 + 4 * t) * 8 + g};
-    int32_t ids = 0;                        // lane i: page of iteration (n & ~31) + i
-    int64_t code_off = 0, scale_off = 0;
-    auto find = [&](int n) {                // the page of iteration n; false: a bad id
-      if ((n & 31) == 0) ids = j0 + 2 * (n + lane) < live ? list[j0 + 2 * (n + lane)] : -1;
-      const int64_t page = __shfl_sync(0xffffffffu, ids, n & 31);
-      const bool ok = page >= 0 && page < p.num_pages;
-      if (!ok && lane == 0) report(p.dev_err, MSA_DEVERR_BAD_PAGE);
-      code_off = page * p.c0;
-      scale_off = page * p.s0;
-      return ok;
+    // this warp's 16 tokens of each page, kStages - 1 pages in flight
+    const int tok0 = warp * 16;
+    const int pages = min(p1, (tokens - tok0 + kBk - 1) / kBk) - p0;   // those with a token of this warp's
+    const Bases at = {p.K_codes + head * p.c1 + tok0 * 64, p.V_codes + head * p.c1 + tok0 * 64,
+                      p.K_scales + head * p.s1 + tok0 * 8, p.V_scales + head * p.s1 + tok0 * 8};
+    uint8_t* ring = s_ring + warp * (kStages * kTileBytes);
+    int32_t ids = 0;                        // lane i: page of the present run of 32
+    uint32_t good = 0;                      // bit n % 32: page n has a valid id
+    auto fetch = [&](int n) {
+      if (n < pages) {
+        if ((n & 31) == 0) ids = n + lane < pages ? list[p0 + n + lane] : -1;
+        const int64_t page = __shfl_sync(0xffffffffu, ids, n & 31);
+        const uint32_t bit = 1u << (n & 31);
+        if (page >= 0 && page < p.num_pages) {
+          good |= bit;
+          fetch_tile(at, page * p.c0, page * p.s0, smem_u32(ring + (n % kStages) * kTileBytes), lane);
+        } else {
+          good &= ~bit;
+          if (lane == 0) report(p.dev_err, MSA_DEVERR_BAD_PAGE);
+        }
+      }
+      copies_commit();
     };
-    Tile x, y;
-    bool ok = false;
-    if (j0 < live) {
-      ok = find(0);
-      if (ok) {
-        load_tile(at, code_off, scale_off, 0, &x);
-        load_tile(at, code_off, scale_off, 16, &y);
+#pragma unroll
+    for (int n = 0; n < kStages - 1; ++n) fetch(n);
+    for (int n = 0; n < pages; ++n) {
+      copies_wait<kStages - 2>();
+      __syncwarp();                         // every lane's share of page n is there, and page n - 1 is read
+      fetch(n + kStages - 1);
+      if (good >> (n & 31) & 1) {
+        Tile x;
+        read_tile(ring + (n % kStages) * kTileBytes, g, t, &x);
+        attend_tile(q, coef, x, tokens - (p0 + n) * kBk - tok0, g, t, &st);
       }
     }
-    for (int j = j0, n = 1; j < live; j += 2, ++n) {
-      const int left = tokens - j * kBk - tok0;
-      const bool now = ok;
-      ok = j + 2 < live && find(n);
-      if (now) attend_tile(q, coef, x, left, g, t, &st);
-      if (ok) load_tile(at, code_off, scale_off, 0, &x);
-      if (now) attend_tile(q, coef, y, left - 16, g, t, &st);
-      if (ok) load_tile(at, code_off, scale_off, 16, &y);
-    }
+    copies_wait<0>();
+    __syncthreads();                        // the rings give way to the joined outputs
 
     // the eight warps' softmaxes joined
 #pragma unroll
@@ -495,8 +512,11 @@ msa_status launch(const Params& p, int64_t most_units, int scratch_zeroed, cudaS
   }
   const int64_t room = std::min<int64_t>(static_cast<int64_t>(dev.num_sms) * kCtasPerSm, kMaxGrid);
   const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(room, most_units)));
-  attn_q4_kernel<DENSE><<<grid, kThreads, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  constexpr int smem = kWarps * std::max<int>(kStages * kTileBytes, kMaxG * kD * sizeof(float));
+  cudaError_t e = cudaFuncSetAttribute(attn_q4_kernel<DENSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(attn_q4)");
+  attn_q4_kernel<DENSE><<<grid, kThreads, smem, stream>>>(p);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "attn_q4_kernel launch");
   return MSA_OK;
 }
