@@ -22,7 +22,7 @@
 // 2^14, is rounded to fp16 (2^-12 of the value down to 2^-22 of the largest).
 //
 // Work.  The (row, page) units of all rows form one list; each CTA takes an equal
-// run of it, its eight warps 16 tokens of every page each, with a softmax
+// run of it, its eight warps 32 tokens of every other page each, with a softmax
 // of their own that is joined in shared memory at the end of a row's part.  Rows
 // cut by a run's end go through the workspace; the CTA that arrives last joins them.
 #include <cuda_fp16.h>
@@ -39,7 +39,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCtasPerSm = 2;
-constexpr int kStages = 4;                              // tiles of 16 tokens per warp in shared memory
+constexpr int kStages = 3;                              // tiles of 32 tokens per warp in shared memory
 constexpr int kMaxGrid = 512;                           // CTAs per launch at most (sizes the workspace)
 constexpr int kPart = kMaxG * kD + 2 * kMaxG;           // floats of a partial: O [8][128], m [8], l [8]
 constexpr float kLog2e = 1.4426950408889634f;
@@ -73,14 +73,14 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 // 16 bytes from the cache to shared memory, asynchronously and past L1: the cache is read once per step.
@@ -93,51 +93,34 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A warp's tile of 16 tokens in shared memory: K codes, V codes, K scales, V
-// scales, rows as in the page but for V's 16-byte chunks, of which rows 4-7 and 12-15 hold
-// them in the order 2, 3, 0, 1.  A lane's rows: row m of S^T is token
-// m ^ (m >> 1 & 1), so that the rows whose probabilities lane t holds after the
-// transposition are tokens 2t and 2t + 1 (swapped for odd t) and these + 8.  With
-// both, eight lanes that read 16 bytes of K, or sixteen that read 8 of V, meet every bank once.
-constexpr int kVAt = 1024, kKsAt = 2048, kVsAt = 2176, kTileBytes = 2304;
+// A warp's tile of 32 tokens in shared memory: K codes, V codes, K scales, V
+// scales, rows as in the page but for V's 16-byte chunks, of which rows with bit 2 set hold
+// them in the order 2, 3, 0, 1.  It is worked on as two halves of 16 rows.
+// Row m of a half of S^T is token m ^ (m >> 1 & 1), so that the rows whose
+// probabilities lane t holds after the transposition are tokens 2t and 2t + 1 (swapped
+// for odd t) and these + 8.  With both, eight lanes that read 16 bytes of K, or
+// sixteen that read 8 of V, meet every bank once.
+constexpr int kTile = 32;
+constexpr int kVAt = kTile * 64, kKsAt = 2 * kVAt, kVsAt = kKsAt + kTile * 8, kTileBytes = kVsAt + kTile * 8;
 
 __device__ __forceinline__ int token_of_row(int m) { return m ^ ((m >> 1) & 1); }
 
-// Where a warp's tile of page 0 starts in the four pools.
+// Where a warp's tile of page 0 starts in the four pools, plus a lane's 16 bytes.
 struct Bases {
-  const uint8_t *kc, *vc, *ks, *vs;
+  const uint8_t *kc, *vc, *scales;   // scales: K's in lanes 0-15, V's in lanes 16-31
 };
 
 __device__ __forceinline__ void fetch_tile(const Bases& at, int64_t code_off, int64_t scale_off, uint32_t dst, int lane) {
-  const int v_chunk = lane ^ ((lane >> 4) << 1);       // row lane / 4, chunk lane % 4 (^ 2 in rows 4-7)
+  const uint32_t dk = dst + lane * 16;                                  // row lane / 4, chunk lane % 4
+  const uint32_t dv = dst + kVAt + (lane ^ ((lane >> 4) << 1)) * 16;    // chunk ^ 2 in rows 4-7 of 8
+  const uint8_t* kc = at.kc + code_off;
+  const uint8_t* vc = at.vc + code_off;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    copy16(dst + i * 512 + lane * 16, at.kc + code_off + i * 512 + lane * 16);
-    copy16(dst + kVAt + i * 512 + v_chunk * 16, at.vc + code_off + i * 512 + lane * 16);
+  for (int i = 0; i < kTile / 8; ++i) {
+    copy16(dk + i * 512, kc + i * 512);
+    copy16(dv + i * 512, vc + i * 512);
   }
-  if (lane < 16) copy16(dst + kKsAt + lane * 16, (lane < 8 ? at.ks : at.vs - 128) + scale_off + lane * 16);
-}
-
-// What a lane takes of a tile.
-struct Tile {
-  uint4 k[2];            // tokens token_of_row(g) and + 8, channels 32t .. 32t + 31
-  uint2 v[4];            // the tokens of rows 2t, 2t + 1 and these + 8, channels 16g .. 16g + 15
-  uint32_t ks[2], vs[4]; // their scale bytes (two groups, one group)
-};
-
-__device__ __forceinline__ void read_tile(const uint8_t* s, int g, int t, Tile* x) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int tok = token_of_row(g) + 8 * i;
-    x->k[i] = *reinterpret_cast<const uint4*>(s + tok * 64 + t * 16);
-    x->ks[i] = *reinterpret_cast<const uint16_t*>(s + kKsAt + tok * 8 + t * 2);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int tok = token_of_row(2 * t + (i & 1)) + 8 * (i >> 1);
-    x->v[i] = *reinterpret_cast<const uint2*>(s + kVAt + tok * 64 + ((g * 8) ^ ((tok & 4) << 3)));
-    x->vs[i] = s[kVsAt + tok * 8 + g];
-  }
+  copy16(dk + kKsAt, at.scales + scale_off);
 }
 
 // The softmax state of a warp: lane (g, t) holds heads 2t and 2t + 1, of which
@@ -147,13 +130,20 @@ struct State {
   float m[2], l[2];      // m the same in every g; l this lane's share
 };
 
-__device__ __forceinline__ void attend_tile(const uint32_t (&q)[16], const float (&coef)[2], Tile& x, int valid, int g,
-                                            int t, State* st) {
-  float s[4] = {0.f, 0.f, 0.f, 0.f};
-  {
-    const __half2 sa = e4m3x2_to_half2(x.ks[0]), sb = e4m3x2_to_half2(x.ks[1]);
-    const uint32_t wa[4] = {x.k[0].x, x.k[0].y, x.k[0].z, x.k[0].w};
-    const uint32_t wb[4] = {x.k[1].x, x.k[1].y, x.k[1].z, x.k[1].w};
+// valid: live tokens of the tile, from its start (any number, 32 and more: all).
+__device__ __forceinline__ void attend_tile(const uint32_t (&q)[16], const float (&coef)[2], const uint8_t* tile, int valid,
+                                            int g, int t, State* st) {
+  float s[2][4];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const uint8_t* row = tile + (u * 16 + token_of_row(g)) * 64 + t * 16;
+    const uint8_t* sf = tile + kKsAt + (u * 16 + token_of_row(g)) * 8 + t * 2;
+    const uint4 ka = *reinterpret_cast<const uint4*>(row), kb = *reinterpret_cast<const uint4*>(row + 8 * 64);
+    const __half2 sa = e4m3x2_to_half2(*reinterpret_cast<const uint16_t*>(sf));
+    const __half2 sb = e4m3x2_to_half2(*reinterpret_cast<const uint16_t*>(sf + 8 * 8));
+    const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[u][i] = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const __half2 fa = i < 2 ? __low2half2(sa) : __high2half2(sa), fb = i < 2 ? __low2half2(sb) : __high2half2(sb);
@@ -165,28 +155,33 @@ __device__ __forceinline__ void attend_tile(const uint32_t (&q)[16], const float
         a[e] = __hmul2(a[e], fa);
         b[e] = __hmul2(b[e], fb);
       }
-      mma16816(s, h2u(a[0]), h2u(b[0]), h2u(a[1]), h2u(b[1]), q[4 * i], q[4 * i + 1]);
-      mma16816(s, h2u(a[2]), h2u(b[2]), h2u(a[3]), h2u(b[3]), q[4 * i + 2], q[4 * i + 3]);
+      mma16816(s[u], h2u(a[0]), h2u(b[0]), h2u(a[1]), h2u(b[1]), q[4 * i], q[4 * i + 1]);
+      mma16816(s[u], h2u(a[2]), h2u(b[2]), h2u(a[3]), h2u(b[3]), q[4 * i + 2], q[4 * i + 3]);
     }
   }
-  if (valid < 16) {      // slots past the last token may hold anything, a NaN scale too
+  if (valid < kTile) {   // slots past the last token may hold anything, a NaN scale too
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (token_of_row(g) + (i < 2 ? 0 : 8) >= valid) s[i] = -INFINITY;
-      if (token_of_row(2 * t + (i & 1)) + 8 * (i >> 1) >= valid) x.vs[i] = 0;
-    }
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (u * 16 + token_of_row(g) + (i < 2 ? 0 : 8) >= valid) s[u][i] = -INFINITY;
   }
   // exponents of P relative to m - 8: infinite until a first maximum is known
-  float e[4];
+  float e[2][4], top = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) e[i] = fmaf(s[i], coef[i & 1], kPShift - st->m[i & 1]);
-  if (__any_sync(0xffffffffu, fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])) > kPShift + kSlack)) {
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      e[u][i] = fmaf(s[u][i], coef[i & 1], kPShift - st->m[i & 1]);
+      top = fmaxf(top, e[u][i]);
+    }
+  if (__any_sync(0xffffffffu, top > kPShift + kSlack)) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      float top = fmaxf(s[c] * coef[c], s[c + 2] * coef[c]);
+      float z = fmaxf(fmaxf(s[0][c], s[0][c + 2]), fmaxf(s[1][c], s[1][c + 2])) * coef[c];
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float m = fmaxf(st->m[c], top);
+      for (int o = 4; o < 32; o <<= 1) z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, o));
+      const float m = fmaxf(st->m[c], z);
       const float f = m == -INFINITY ? 1.f : ex2(st->m[c] - m);
       st->m[c] = m;
       st->l[c] *= f;
@@ -197,31 +192,45 @@ __device__ __forceinline__ void attend_tile(const uint32_t (&q)[16], const float
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) e[i] = fmaf(s[i], coef[i & 1], kPShift - st->m[i & 1]);
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) e[u][i] = fmaf(s[u][i], coef[i & 1], kPShift - st->m[i & 1]);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) e[i] = ex2(e[i]);
-  st->l[0] += e[0] + e[2];
-  st->l[1] += e[1] + e[3];
-  // P^T: from (row g, heads 2t, 2t + 1) to (head g, rows 2t, 2t + 1)
-  const uint32_t b0 = transpose8x8(h2u(__floats2half2_rn(e[0], e[1])));
-  const uint32_t b1 = transpose8x8(h2u(__floats2half2_rn(e[2], e[3])));
-  const __half2 s01 = e4m3x2_to_half2(x.vs[0] | x.vs[1] << 8), s23 = e4m3x2_to_half2(x.vs[2] | x.vs[3] << 8);
+  for (int u = 0; u < 2; ++u) {
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    // the codes of two tokens side by side: even and odd channels' bytes (token, next token)
-    const uint32_t a = w ? x.v[0].y : x.v[0].x, b = w ? x.v[1].y : x.v[1].x;
-    const uint32_t c = w ? x.v[2].y : x.v[2].x, d = w ? x.v[3].y : x.v[3].x;
-    constexpr uint32_t kLow = 0x0f0f0f0fu;
-    __half2 even01[4], odd01[4], even23[4], odd23[4];
-    e2m1x8_to_half2((a & kLow) | ((b << 4) & ~kLow), even01);
-    e2m1x8_to_half2(((a >> 4) & kLow) | (b & ~kLow), odd01);
-    e2m1x8_to_half2((c & kLow) | ((d << 4) & ~kLow), even23);
-    e2m1x8_to_half2(((c >> 4) & kLow) | (d & ~kLow), odd23);
+    for (int i = 0; i < 4; ++i) e[u][i] = ex2(e[u][i]);
+    st->l[0] += e[u][0] + e[u][2];
+    st->l[1] += e[u][1] + e[u][3];
+    // P^T: from (row g, heads 2t, 2t + 1) to (head g, rows 2t, 2t + 1)
+    const uint32_t b0 = transpose8x8(h2u(__floats2half2_rn(e[u][0], e[u][1])));
+    const uint32_t b1 = transpose8x8(h2u(__floats2half2_rn(e[u][2], e[u][3])));
+    uint2 v[4];          // the tokens of rows 2t, 2t + 1 and these + 8, channels 16g .. 16g + 15
+    uint32_t sf[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      mma16816(st->acc[w * 4 + i], h2u(__hmul2(even01[i], s01)), h2u(__hmul2(odd01[i], s01)),
-               h2u(__hmul2(even23[i], s23)), h2u(__hmul2(odd23[i], s23)), b0, b1);
+    for (int i = 0; i < 4; ++i) {
+      const int tok = u * 16 + token_of_row(2 * t + (i & 1)) + 8 * (i >> 1);
+      v[i] = *reinterpret_cast<const uint2*>(tile + kVAt + tok * 64 + ((g * 8) ^ ((tok & 4) << 3)));
+      sf[i] = tile[kVsAt + tok * 8 + g];
+      if (valid < kTile && tok >= valid) sf[i] = 0;
+    }
+    const __half2 s01 = e4m3x2_to_half2(sf[0] | sf[1] << 8), s23 = e4m3x2_to_half2(sf[2] | sf[3] << 8);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      // the codes of two tokens side by side: even and odd channels' bytes (token, next token)
+      const uint32_t a = w ? v[0].y : v[0].x, b = w ? v[1].y : v[1].x;
+      const uint32_t c = w ? v[2].y : v[2].x, d = w ? v[3].y : v[3].x;
+      constexpr uint32_t kLow = 0x0f0f0f0fu;
+      __half2 even01[4], odd01[4], even23[4], odd23[4];
+      e2m1x8_to_half2((a & kLow) | ((b << 4) & ~kLow), even01);
+      e2m1x8_to_half2(((a >> 4) & kLow) | (b & ~kLow), odd01);
+      e2m1x8_to_half2((c & kLow) | ((d << 4) & ~kLow), even23);
+      e2m1x8_to_half2(((c >> 4) & kLow) | (d & ~kLow), odd23);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        mma16816(st->acc[w * 4 + i], h2u(__hmul2(even01[i], s01)), h2u(__hmul2(odd01[i], s01)),
+                 h2u(__hmul2(even23[i], s23)), h2u(__hmul2(odd23[i], s23)), b0, b1);
+    }
   }
 }
 
@@ -348,40 +357,41 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_q4_kernel(const Par
     st.m[0] = st.m[1] = -INFINITY;
     st.l[0] = st.l[1] = 0.f;
 
-    // this warp's 16 tokens of each page, kStages - 1 pages in flight
-    const int tok0 = warp * 16;
-    const int pages = min(p1, (tokens - tok0 + kBk - 1) / kBk) - p0;   // those with a token of this warp's
-    const Bases at = {p.K_codes + head * p.c1 + tok0 * 64, p.V_codes + head * p.c1 + tok0 * 64,
-                      p.K_scales + head * p.s1 + tok0 * 8, p.V_scales + head * p.s1 + tok0 * 8};
+    // this warp's 32 tokens of every other page, kStages - 1 of them in flight
+    const int tok0 = (warp & 3) * kTile, j0 = p0 + (warp >> 2);
+    const int live = min(p1, (tokens - tok0 + kBk - 1) / kBk);   // pages before here have a token of this warp's
+    const int count = (live - j0 + 1) / 2;
+    const Bases at = {p.K_codes + head * p.c1 + tok0 * 64 + lane * 16, p.V_codes + head * p.c1 + tok0 * 64 + lane * 16,
+                      (lane < 16 ? p.K_scales : p.V_scales) + head * p.s1 + tok0 * 8 + (lane & 15) * 16};
     uint8_t* ring = s_ring + warp * (kStages * kTileBytes);
-    int32_t ids = 0;                        // lane i: page of the present run of 32
-    uint32_t good = 0;                      // bit n % 32: page n has a valid id
+    int32_t ids = 0;                        // lane i: page of the i-th of the present run of 32
+    uint32_t good = 0;                      // bit n % 32: the n-th page has a valid id
+    int into = 0, from = 0;                 // stages of the ring
     auto fetch = [&](int n) {
-      if (n < pages) {
-        if ((n & 31) == 0) ids = n + lane < pages ? list[p0 + n + lane] : -1;
-        const int64_t page = __shfl_sync(0xffffffffu, ids, n & 31);
+      if (n < count) {
+        if ((n & 31) == 0) ids = j0 + 2 * (n + lane) < live ? list[j0 + 2 * (n + lane)] : -1;
+        const int32_t page = __shfl_sync(0xffffffffu, ids, n & 31);
         const uint32_t bit = 1u << (n & 31);
         if (page >= 0 && page < p.num_pages) {
           good |= bit;
-          fetch_tile(at, page * p.c0, page * p.s0, smem_u32(ring + (n % kStages) * kTileBytes), lane);
+          fetch_tile(at, page * p.c0, page * p.s0, smem_u32(ring + into * kTileBytes), lane);
         } else {
           good &= ~bit;
           if (lane == 0) report(p.dev_err, MSA_DEVERR_BAD_PAGE);
         }
       }
+      into = into + 1 == kStages ? 0 : into + 1;
       copies_commit();
     };
 #pragma unroll
     for (int n = 0; n < kStages - 1; ++n) fetch(n);
-    for (int n = 0; n < pages; ++n) {
+    for (int n = 0; n < count; ++n) {
       copies_wait<kStages - 2>();
-      __syncwarp();                         // every lane's share of page n is there, and page n - 1 is read
+      __syncwarp();                         // every lane's share of tile n is there, and tile n - 1 is read
       fetch(n + kStages - 1);
-      if (good >> (n & 31) & 1) {
-        Tile x;
-        read_tile(ring + (n % kStages) * kTileBytes, g, t, &x);
-        attend_tile(q, coef, x, tokens - (p0 + n) * kBk - tok0, g, t, &st);
-      }
+      if (good >> (n & 31) & 1)
+        attend_tile(q, coef, ring + from * kTileBytes, tokens - (j0 + 2 * n) * kBk - tok0, g, t, &st);
+      from = from + 1 == kStages ? 0 : from + 1;
     }
     copies_wait<0>();
     __syncthreads();                        // the rings give way to the joined outputs

@@ -126,16 +126,17 @@ def norm_rope(x, weight, pos, inv_freq, eps, interleaved):
 
 
 def attend(q, K, V, scale):
-    """(O, LSE, A, Z) of q [G, D] over K, V [T, D] (float64): A = sum_t p |v|, Z = max_t scale * sum |q k|."""
+    """(O, LSE, A, Z, S) of q [G, D] over K, V [T, D] (float64): A = sum_t p |v|, Z = max_t scale * sum |q k|,
+    S = sum_t |v|."""
     if len(K) == 0:
-        return np.zeros_like(q), np.full(len(q), -np.inf), np.zeros_like(q), np.zeros(len(q))
+        return np.zeros_like(q), np.full(len(q), -np.inf), np.zeros_like(q), np.zeros(len(q)), 0.0
     z = q @ K.T * scale
     m = z.max(-1, keepdims=True)
     p = np.exp(z - m)
     l = p.sum(-1, keepdims=True)
     p /= l
     Z = (np.abs(q) @ np.abs(K).T).max(-1) * scale
-    return p @ V, (m + np.log(l))[:, 0], p @ np.abs(V), Z
+    return p @ V, (m + np.log(l))[:, 0], p @ np.abs(V), Z, np.abs(V).sum(0)
 
 
 def check_attend(O, LSE, ref):
@@ -144,12 +145,14 @@ def check_attend(O, LSE, ref):
     Scores: 128 exact products summed in fp32 with at most one step (2^-23) lost per
     addition, 128 * 2^-23 of Z at worst, and a few roundings of z and of 2^x (2^-20 of
     1 + Z): dz = 2^-16 (1 + Z).  The probabilities then err by 2 dz, and fp16 rounds
-    each by 2^-11 (below 2^-22 of the largest by 2^-33 in absolute terms); fp32 sums
-    over the tokens add less than 2^-14.  bf16 rounds the result by 2^-8 of it.
+    each by 2^-11; fp32 sums over the tokens add less than 2^-14.  A probability below
+    2^-22 of the largest rounds by an absolute amount instead: fp16's subnormal
+    steps are 2^-24, half of one 2^-25, and the largest is held as 2^8 at least, so by
+    2^-33 of the largest (at most 1) for each token, 2^-33 S in all.  bf16 rounds the result by 2^-8 of it.
     """
-    Oe, Le, A, Z = ref
+    Oe, Le, A, Z, S = ref
     dz = 2.0 ** -16 * (1 + Z)
-    lim = 2.0 ** -8 * np.abs(Oe) + (2.0 ** -11 + 2.0 ** -14 + 2 * dz[:, None]) * A + 1e-30
+    lim = 2.0 ** -8 * np.abs(Oe) + (2.0 ** -11 + 2.0 ** -14 + 2 * dz[:, None]) * A + 2.0 ** -33 * S + 1e-30
     bad = ~(np.abs(O - Oe) <= lim)
     assert not bad.any(), f"O off at {np.argwhere(bad)[:3]}, worst {np.nanmax(np.abs(O - Oe) / lim):.3f} of the bound"
     same_inf = np.isneginf(LSE) == np.isneginf(Le)
