@@ -12,9 +12,11 @@
 // and the second within 2^-22, so the code is that of the real quotient.  The
 // same holds for amax / 6 against the scale's halfway points.
 //
-// One thread per group: 32 bytes in, 8 codes bytes and a scale byte out; eight
-// neighbouring threads share a row, so every access fills its sectors.
-// Bound: HBM.
+// Bound: HBM.  A block takes one head, so that the tokens of a prompt, whose slots
+// follow one another, write whole runs of a page.  Store: a thread takes a group (32 bytes in,
+// 8 code bytes and a scale byte out) of four tokens, all of whose loads are issued
+// first.  Expand: a thread takes half groups, 16 bytes out, so that a warp's store is one
+// run of 512 bytes, eight of them loaded ahead.
 #include <cuda_fp16.h>
 
 #include "msa_internal.h"
@@ -25,10 +27,14 @@ namespace msa {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kStoreUnroll = 4;                             // tokens per thread
+constexpr int kStoreTokens = kThreads / 16 * kStoreUnroll;  // and per block
+constexpr int kExpandUnroll = 8;                            // half groups per thread and run
+constexpr unsigned kMaxGridY = 65535;
 
 struct StoreParams {
   int64_t N, num_pages;
-  int Hkv, Bk;
+  int Hkv;
   const uint8_t *K, *V;
   int64_t k0, k1, v0, v1;       // byte strides (n, h)
   const int64_t* slots;
@@ -74,37 +80,54 @@ __device__ __forceinline__ void quantise16(const uint32_t (&u)[8], float inv, ui
 }
 
 __global__ void __launch_bounds__(kThreads) append_q4_kernel(const StoreParams p) {
-  const int64_t total = p.N * p.Hkv * 16;               // (token, head, K or V, group)
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int group = static_cast<int>(i & 7);
-    const bool is_v = (i >> 3) & 1;
-    const int64_t nh = i >> 4;
-    const int64_t n = nh / p.Hkv;
-    const int h = static_cast<int>(nh - n * p.Hkv);
-    const int64_t slot = p.slots[n];
-    if (slot < 0) continue;
-    const int64_t page = slot / p.Bk;
-    const int t = static_cast<int>(slot - page * p.Bk);
-    if (page >= p.num_pages) {
-      if (group == 0 && h == 0 && !is_v) report(p.dev_err, MSA_DEVERR_BAD_PAGE);
-      continue;
-    }
-    const uint4* src = reinterpret_cast<const uint4*>((is_v ? p.V + n * p.v0 + h * p.v1 : p.K + n * p.k0 + h * p.k1) +
-                                                      group * 32);
-    const uint4 a = src[0], b = src[1];
-    const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    uint2 codes;
-    uint32_t scale;
-    quantise16(u, is_v ? p.v_inv : p.k_inv, &codes, &scale);
-    *reinterpret_cast<uint2*>((is_v ? p.V_codes : p.K_codes) + page * p.c0 + h * p.c1 + t * 64 + group * 8) = codes;
-    (is_v ? p.V_scales : p.K_scales)[page * p.s0 + h * p.s1 + t * 8 + group] = static_cast<uint8_t>(scale);
+  const int group = threadIdx.x & 7;
+  const bool is_v = threadIdx.x >> 3 & 1;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kStoreTokens + (threadIdx.x >> 4);
+  const int64_t n_stride = is_v ? p.v0 : p.k0;
+  const float inv = is_v ? p.v_inv : p.k_inv;
+  int64_t slot[kStoreUnroll];
+#pragma unroll
+  for (int i = 0; i < kStoreUnroll; ++i) {
+    const int64_t n = first + i * (kThreads / 16);
+    slot[i] = n < p.N ? p.slots[n] : -1;
   }
+  bool bad = false;
+  for (int h = blockIdx.y; h < p.Hkv; h += gridDim.y) {
+    const uint8_t* src = (is_v ? p.V + h * p.v1 : p.K + h * p.k1) + first * n_stride + group * 32;
+    uint8_t* codes = (is_v ? p.V_codes : p.K_codes) + h * p.c1 + group * 8;
+    uint8_t* scales = (is_v ? p.V_scales : p.K_scales) + h * p.s1 + group;
+    uint4 a[kStoreUnroll], b[kStoreUnroll];
+#pragma unroll
+    for (int i = 0; i < kStoreUnroll; ++i) {
+      a[i] = b[i] = make_uint4(0, 0, 0, 0);
+      if (slot[i] < 0) continue;
+      const uint4* x = reinterpret_cast<const uint4*>(src + i * (kThreads / 16) * n_stride);
+      a[i] = x[0];
+      b[i] = x[1];
+    }
+#pragma unroll
+    for (int i = 0; i < kStoreUnroll; ++i) {
+      if (slot[i] < 0) continue;
+      const int64_t page = slot[i] / kBk;
+      const int t = static_cast<int>(slot[i] & (kBk - 1));
+      if (page >= p.num_pages) {
+        bad = true;
+        continue;
+      }
+      const uint32_t u[8] = {a[i].x, a[i].y, a[i].z, a[i].w, b[i].x, b[i].y, b[i].z, b[i].w};
+      uint2 c;
+      uint32_t sf;
+      quantise16(u, inv, &c, &sf);
+      *reinterpret_cast<uint2*>(codes + page * p.c0 + t * 64) = c;
+      scales[page * p.s0 + t * 8] = static_cast<uint8_t>(sf);
+    }
+  }
+  if (bad && group == 0 && !is_v) report(p.dev_err, MSA_DEVERR_BAD_PAGE);
 }
 
 struct ExpandParams {
   int64_t n, num_pages;
-  int Hkv, Bk;
+  int Hkv;
   const int32_t* pages;
   const uint8_t *K_codes, *K_scales, *V_codes, *V_scales;
   int64_t c0, c1, s0, s1;
@@ -114,57 +137,53 @@ struct ExpandParams {
 };
 
 __global__ void __launch_bounds__(kThreads) expand_q4_kernel(const ExpandParams p) {
-  const int64_t rows = p.n * p.Hkv * p.Bk;              // output rows of K, as many of V
-  const int64_t total = rows * 16;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const bool is_v = i >= rows * 8;
-    const int64_t at = is_v ? i - rows * 8 : i;
-    const int group = static_cast<int>(at & 7);
-    const int64_t row = at >> 3;
-    const int t = static_cast<int>(row % p.Bk);
-    const int64_t xh = row / p.Bk;
-    const int h = static_cast<int>(xh % p.Hkv);
-    const int64_t x = xh / p.Hkv;
-    const int64_t page = p.pages[x];
-    if (page < 0 || page >= p.num_pages) {
-      if (group == 0 && t == 0 && h == 0 && !is_v) report(p.dev_err, MSA_DEVERR_BAD_PAGE);
-      continue;
-    }
-    const uint2 c = *reinterpret_cast<const uint2*>((is_v ? p.V_codes : p.K_codes) + page * p.c0 + h * p.c1 + t * 64 +
-                                                    group * 8);
-    const uint32_t sf = (is_v ? p.V_scales : p.K_scales)[page * p.s0 + h * p.s1 + t * 8 + group];
-    const __half2 s = e4m3_to_half2(sf);
-    const float gs = is_v ? p.v_scale : p.k_scale;
-    uint32_t out[8];
+  const int64_t page = p.pages[blockIdx.x];
+  if (page < 0 || page >= p.num_pages) {
+    if (blockIdx.y == 0 && threadIdx.x == 0) report(p.dev_err, MSA_DEVERR_BAD_PAGE);
+    return;
+  }
+  constexpr int kHalves = kBk * kD / 8;                 // half groups of a block of K, as many of V
+  static_assert(kHalves % (kThreads * kExpandUnroll) == 0, "whole runs");
+  for (int h = blockIdx.y; h < p.Hkv; h += gridDim.y) {
+#pragma unroll 1
+    for (int part = 0; part < 2 * kHalves / (kThreads * kExpandUnroll); ++part) {
+      const bool is_v = part >= kHalves / (kThreads * kExpandUnroll);
+      const int first = part * kThreads * kExpandUnroll - (is_v ? kHalves : 0) + threadIdx.x;
+      const uint8_t* codes = (is_v ? p.V_codes : p.K_codes) + page * p.c0 + h * p.c1;
+      const uint8_t* scales = (is_v ? p.V_scales : p.K_scales) + page * p.s0 + h * p.s1;
+      uint4* out = reinterpret_cast<uint4*>(is_v ? p.V_out : p.K_out) +
+                   (static_cast<int64_t>(blockIdx.x) * p.Hkv + h) * kHalves;
+      const float gs = is_v ? p.v_scale : p.k_scale;
+      uint32_t c[kExpandUnroll], sf[kExpandUnroll];
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      __half2 v[4];
-      e2m1x8_to_half2(w ? c.y : c.x, v);
+      for (int i = 0; i < kExpandUnroll; ++i) {
+        const int x = first + i * kThreads;
+        c[i] = reinterpret_cast<const uint32_t*>(codes)[x];
+        sf[i] = scales[x >> 1];
+      }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = __half22float2(__hmul2(v[e], s));   // exact: 2 bits times 4 bits, at least 2^-10
-        const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * gs, f.y * gs);
-        out[w * 4 + e] = *reinterpret_cast<const uint32_t*>(&b);
+      for (int i = 0; i < kExpandUnroll; ++i) {
+        const __half2 s = e4m3_to_half2(sf[i]);
+        __half2 v[4];
+        e2m1x8_to_half2(c[i], v);
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = __half22float2(__hmul2(v[e], s));   // exact: 2 bits times 4 bits, at least 2^-10
+          const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * gs, f.y * gs);
+          w[e] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        out[first + i * kThreads] = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
-    uint4* dst = reinterpret_cast<uint4*>((is_v ? p.V_out : p.K_out) + row * 256 + group * 32);
-    dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
-    dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
   }
-}
-
-unsigned grid_for(int64_t threads, int sms) {
-  return static_cast<unsigned>(std::min<int64_t>((threads + kThreads - 1) / kThreads, static_cast<int64_t>(sms) * 32));
 }
 
 }  // namespace
 
 msa_status launch_append_q4(const msa_append_q4_args& a, cudaStream_t stream) {
-  DeviceInfo dev;
-  if (msa_status st = current_device(&dev); st != MSA_OK) return st;
   StoreParams p;
-  p.N = a.N; p.num_pages = a.cache.num_pages; p.Hkv = a.Hkv; p.Bk = a.Bk;
+  p.N = a.N; p.num_pages = a.cache.num_pages; p.Hkv = a.Hkv;
   p.K = static_cast<const uint8_t*>(a.K);
   p.V = static_cast<const uint8_t*>(a.V);
   p.k0 = a.K_stride[0] * 2; p.k1 = a.K_stride[1] * 2;
@@ -178,17 +197,17 @@ msa_status launch_append_q4(const msa_append_q4_args& a, cudaStream_t stream) {
   p.s0 = a.cache.scale_stride[0]; p.s1 = a.cache.scale_stride[1];
   p.k_inv = 1.0f / a.cache.k_scale; p.v_inv = 1.0f / a.cache.v_scale;
   p.dev_err = a.dev_err;
-  append_q4_kernel<<<grid_for(a.N * a.Hkv * 16, dev.num_sms), kThreads, 0, stream>>>(p);
+  const dim3 grid(static_cast<unsigned>((a.N + kStoreTokens - 1) / kStoreTokens),
+                  std::min<unsigned>(static_cast<unsigned>(a.Hkv), kMaxGridY));
+  append_q4_kernel<<<grid, kThreads, 0, stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "append_q4_kernel launch");
   return MSA_OK;
 }
 
 msa_status launch_expand_q4(const msa_expand_q4_args& a, cudaStream_t stream) {
-  DeviceInfo dev;
-  if (msa_status st = current_device(&dev); st != MSA_OK) return st;
   ExpandParams p;
-  p.n = a.n; p.num_pages = a.cache.num_pages; p.Hkv = a.Hkv; p.Bk = a.Bk;
+  p.n = a.n; p.num_pages = a.cache.num_pages; p.Hkv = a.Hkv;
   p.pages = a.pages;
   p.K_codes = static_cast<const uint8_t*>(a.cache.K_codes);
   p.K_scales = static_cast<const uint8_t*>(a.cache.K_scales);
@@ -200,7 +219,8 @@ msa_status launch_expand_q4(const msa_expand_q4_args& a, cudaStream_t stream) {
   p.V_out = static_cast<uint8_t*>(a.V_out);
   p.k_scale = a.cache.k_scale; p.v_scale = a.cache.v_scale;
   p.dev_err = a.dev_err;
-  expand_q4_kernel<<<grid_for(a.n * a.Hkv * a.Bk * 16, dev.num_sms), kThreads, 0, stream>>>(p);
+  const dim3 grid(static_cast<unsigned>(a.n), std::min<unsigned>(static_cast<unsigned>(a.Hkv), kMaxGridY));
+  expand_q4_kernel<<<grid, kThreads, 0, stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "expand_q4_kernel launch");
   return MSA_OK;

@@ -8,12 +8,13 @@
 // sums of need its pages on the free stack.  The sums run over at most 4096
 // requests, so every CTA forms them for itself in shared memory and then fills its
 // share of the token rows and table entries by binary search in the sums: no
-// second launch and no scratch.  The CTAs form one thread-block cluster; all of
-// them have read the lengths and the stack's height once its barrier is passed,
-// so both may be updated in place.
+// second launch and no scratch.  Lengths and the stack's height may be updated
+// in place; the CTAs then form one thread-block cluster, whose barrier tells that all
+// of them have read the old values.  With outputs of their own there is nothing to
+// wait for and the grid is as large as the rows ask for.
 //
-// Bound: launch latency for the few rows of a decode step; for a prompt batch
-// the 16 bytes written per token row by the cluster's few SMs.
+// Bound: latency (the lengths, the sums, one page id per row, the stores); the
+// 16 bytes written per token row are far below it.
 #include <cooperative_groups.h>
 
 #include <climits>
@@ -26,10 +27,9 @@ namespace cg = cooperative_groups;
 namespace msa {
 namespace {
 
-constexpr int kPlanThreads = 1024;
-constexpr int kPerThread = kMaxDecodeBatch / kPlanThreads;   // requests per thread in the prefix sums
-constexpr int kPlanCluster = 8;                              // CTAs per cluster for large steps (portable maximum)
-constexpr int kRowsPerCta = 4096;                            // token rows worth a CTA of their own
+constexpr int kPlanThreads = 512;
+constexpr int kPerThread = kMaxDecodeBatch / kPlanThreads;   // requests per thread in the prefix sums, at most
+constexpr int kPlanCluster = 8;                              // CTAs of an update in place (portable maximum)
 
 // Exclusive prefix sums of (a, b) over the CTA's threads; returns the totals.
 struct Sum2 {
@@ -72,82 +72,84 @@ __device__ __forceinline__ int last_at_most(const int* first, int n, int x) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const msa_plan_args p) {
+__global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const msa_plan_args p, const bool in_place) {
   extern __shared__ int s_plan[];
   int* s_cu = s_plan;                       // [B + 1] first token row, at most N
   int* s_off = s_cu + p.B + 1;              // [B + 1] pages given to the requests before b
   int* s_len = s_off + p.B + 1;             // [B] cached tokens; -1: not served
-  cg::cluster_group cluster = cg::this_cluster();
-  const int tid = threadIdx.x, B = p.B;
-  const int rank = static_cast<int>(cluster.block_rank()), ctas = static_cast<int>(cluster.num_blocks());
+  const int tid = threadIdx.x, B = p.B, rank = blockIdx.x, ctas = gridDim.x;
   const int per = (B + blockDim.x - 1) / blockDim.x;   // <= kPerThread
-  const int64_t cap = p.max_pages * p.Bk;
+  const int64_t cap = p.max_pages * kBk;
   const int raw = *p.free_count;
   const int count = static_cast<int>(min(max(static_cast<int64_t>(raw), int64_t(0)), p.free_cap));
   int32_t err = raw == count ? 0 : MSA_DEVERR_NO_PAGES;
 
-  int L[kPerThread], n[kPerThread], rows[kPerThread], need[kPerThread];
+  int L[kPerThread], n[kPerThread], need[kPerThread];
   Sum2 own{0, 0};
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i) {
     const int b = tid * per + i;
-    L[i] = n[i] = rows[i] = need[i] = 0;
+    L[i] = n[i] = need[i] = 0;
     if (i < per && b < B) {
       L[i] = p.seq_len[b];
       n[i] = p.new_len[b];
-      rows[i] = max(n[i], 0);
-      own.a += rows[i];
     }
   }
-  // token rows first: a request whose rows pass N needs no pages
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) {
+    const int64_t end = static_cast<int64_t>(L[i]) + n[i];
+    if (L[i] >= 0 && n[i] >= 0 && end <= cap)
+      need[i] = static_cast<int>((end + kBk - 1) / kBk) - static_cast<int>((static_cast<int64_t>(L[i]) + kBk - 1) / kBk);
+    own.a += max(n[i], 0);
+    own.b += need[i];
+  }
   Sum2 total;
   Sum2 before = block_exclusive(own, &total);
-  const int64_t all_rows = total.a;
-  int64_t row = before.a;
-  own = Sum2{0, 0};
+  if (total.a > p.N) {                      // rare: a request whose rows pass N needs no pages, so the sums change
+    int64_t row = before.a;
+    own.b = 0;
 #pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int b = tid * per + i;
-    if (i < per && b < B) {
-      s_cu[b] = static_cast<int>(min(row, p.N));
-      const int64_t end = static_cast<int64_t>(L[i]) + n[i];
-      if (L[i] < 0 || n[i] < 0 || end > cap || row + rows[i] > p.N) {
-        n[i] = -1;                          // not served
-        err |= MSA_DEVERR_BAD_LEN;
-      } else {
-        need[i] = static_cast<int>((end + p.Bk - 1) / p.Bk) - static_cast<int>((static_cast<int64_t>(L[i]) + p.Bk - 1) / p.Bk);
-      }
-      row += rows[i];
+    for (int i = 0; i < kPerThread; ++i) {
+      row += max(n[i], 0);
+      if (row > p.N) need[i] = 0;
       own.b += need[i];
     }
+    __syncthreads();                        // the first sums are read
+    before = block_exclusive(own, &total);
   }
-  __syncthreads();                          // block_exclusive's shared sums are read
-  before = block_exclusive(own, &total);
-  int64_t off = before.b;
+  {
+    int64_t row = before.a, off = before.b;
 #pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int b = tid * per + i;
-    if (i < per && b < B) {
-      const bool served = n[i] >= 0 && (need[i] == 0 || off + need[i] <= count);
-      if (n[i] >= 0 && !served) err |= MSA_DEVERR_NO_PAGES;
-      // past the first refusal nothing that needs a page is served, so the sums
-      // clamped to the stack's height stay exact for every served request
-      s_off[b] = static_cast<int>(min(off, static_cast<int64_t>(count) + 1));
-      s_len[b] = served ? L[i] : -1;
-      off += need[i];
+    for (int i = 0; i < kPerThread; ++i) {
+      const int b = tid * per + i;
+      if (i < per && b < B) {
+        const int64_t end = static_cast<int64_t>(L[i]) + n[i];
+        const bool fits = L[i] >= 0 && n[i] >= 0 && end <= cap && row + n[i] <= p.N;
+        const bool served = fits && (need[i] == 0 || off + need[i] <= count);
+        if (!fits) err |= MSA_DEVERR_BAD_LEN;
+        else if (!served) err |= MSA_DEVERR_NO_PAGES;
+        s_cu[b] = static_cast<int>(min(row, p.N));
+        // past the first refusal nothing that needs a page is served, so the sums
+        // clamped to the stack's height stay exact for every served request
+        s_off[b] = static_cast<int>(min(off, static_cast<int64_t>(count) + 1));
+        s_len[b] = served ? L[i] : -1;
+        row += max(n[i], 0);
+        off += need[i];
+      }
     }
   }
+  const int64_t all_rows = total.a;
   if (tid == 0) {
     s_cu[B] = static_cast<int>(min(all_rows, p.N));
     s_off[B] = static_cast<int>(min(total.b, static_cast<int64_t>(count) + 1));
   }
   if (rank == 0 && err != 0) report(p.dev_err, err);
   __syncthreads();
-  if (ctas > 1) cluster.sync();             // every CTA has read the lengths and the stack's height
+  if (in_place && ctas > 1) cg::this_cluster().sync();   // every CTA has read the lengths and the stack's height
 
   const int stride = ctas * blockDim.x, first = rank * blockDim.x + tid;
-  // lengths and offsets out
-  if (rank == 0) {
+  // lengths and offsets out, by the last CTA, which has the fewest rows
+  if (rank == ctas - 1) {
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
       const int b = tid * per + i;
@@ -162,10 +164,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const msa_plan_
   for (int x = first; x < min(entries, count); x += stride) {
     const int b = last_at_most(s_off, B, x);
     if (s_len[b] < 0) continue;             // the request that did not fit
-    const int have = (s_len[b] + p.Bk - 1) / p.Bk;
+    const int have = (s_len[b] + kBk - 1) / kBk;
     p.seq_pt[b * p.max_pages + have + (x - s_off[b])] = p.free_pages[count - 1 - x];
   }
-  if (rank == 0 && tid == 0) {
+  if (rank == ctas - 1 && tid == 0) {
     given = min(entries, count);
     if (entries > count) given = s_off[last_at_most(s_off, B, count)];   // pages before the first refusal
     *p.free_count_out = count - given;
@@ -181,9 +183,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const msa_plan_
       if (s_len[b] >= 0) {
         seq = b;
         pos = s_len[b] + static_cast<int>(r) - s_cu[b];
-        const int have = (s_len[b] + p.Bk - 1) / p.Bk, j = pos / p.Bk;
+        const int have = (s_len[b] + kBk - 1) / kBk, j = pos / kBk;
         const int page = j >= have ? p.free_pages[count - 1 - (s_off[b] + j - have)] : p.seq_pt[b * p.max_pages + j];
-        if (page >= 0 && page < p.num_pages) slot = static_cast<int64_t>(page) * p.Bk + pos % p.Bk;
+        if (page >= 0 && page < p.num_pages) slot = static_cast<int64_t>(page) * kBk + pos % kBk;
         else bad = true;
       }
     }
@@ -194,13 +196,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const msa_plan_
   if (bad) report(p.dev_err, MSA_DEVERR_BAD_PAGE);
 }
 
-__global__ void __launch_bounds__(kPlanThreads) release_kernel(const msa_release_args p) {
+__global__ void __launch_bounds__(kPlanThreads) release_kernel(const msa_release_args p, const bool in_place) {
   extern __shared__ int s_off[];            // [B + 1] pages returned by the requests before b
-  cg::cluster_group cluster = cg::this_cluster();
-  const int tid = threadIdx.x, B = p.B;
-  const int rank = static_cast<int>(cluster.block_rank()), ctas = static_cast<int>(cluster.num_blocks());
+  const int tid = threadIdx.x, B = p.B, rank = blockIdx.x, ctas = gridDim.x;
   const int per = (B + blockDim.x - 1) / blockDim.x;
-  const int64_t cap = p.max_pages * p.Bk;
+  const int64_t cap = p.max_pages * kBk;
   const int raw = *p.free_count;
   const int64_t count = min(max(static_cast<int64_t>(raw), int64_t(0)), p.free_cap);
   int32_t err = raw == count ? 0 : MSA_DEVERR_NO_PAGES;
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kPlanThreads) release_kernel(const msa_release
         if (out_len[i] < 0 || out_len[i] > cap) {
           err |= MSA_DEVERR_BAD_LEN;
         } else {
-          gone[i] = static_cast<int>((static_cast<int64_t>(out_len[i]) + p.Bk - 1) / p.Bk);
+          gone[i] = static_cast<int>((static_cast<int64_t>(out_len[i]) + kBk - 1) / kBk);
           out_len[i] = 0;
         }
       }
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kPlanThreads) release_kernel(const msa_release
   if (total.a > room) err |= MSA_DEVERR_NO_PAGES;
   if (rank == 0 && err != 0) report(p.dev_err, err);
   __syncthreads();
-  if (ctas > 1) cluster.sync();
+  if (in_place && ctas > 1) cg::this_cluster().sync();
   if (rank == 0) {
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
@@ -252,9 +252,16 @@ __global__ void __launch_bounds__(kPlanThreads) release_kernel(const msa_release
   }
 }
 
+// One CTA, a plain grid, or (an update in place with more than one CTA's rows) one cluster.
 template <class Args>
-msa_status launch_cluster(void (*kernel)(const Args), const Args& a, int ctas, int threads, size_t smem,
-                          cudaStream_t stream, const char* what) {
+msa_status launch_rows(void (*kernel)(const Args, const bool), const Args& a, int64_t items, bool in_place, size_t smem,
+                       cudaStream_t stream, const char* what) {
+  DeviceInfo dev;
+  if (msa_status st = current_device(&dev); st != MSA_OK) return st;
+  // enough threads for the sums (8 requests each at most), few for the small steps that come once a token
+  const int threads = a.B > 512 ? kPlanThreads : a.B > 128 ? 256 : 128;
+  const int64_t want = std::max<int64_t>((items + threads - 1) / threads, 1);
+  const int ctas = static_cast<int>(std::min<int64_t>(want, in_place ? kPlanCluster : 2 * dev.num_sms));
   if (smem > (40u << 10)) {   // with the prefix sums' own shared memory past the 48 KiB default
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return cuda_fail(e, what);
@@ -270,31 +277,26 @@ msa_status launch_cluster(void (*kernel)(const Args), const Args& a, int ctas, i
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+  cfg.numAttrs = in_place && ctas > 1 ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, in_place);
   if (e != cudaSuccess) return cuda_fail(e, what);
   return MSA_OK;
-}
-
-// Threads for B requests and `items` rows or pages in one CTA: a multiple of 32.
-int plan_threads(int B, int64_t items) {
-  const int64_t want = std::max<int64_t>(B, items);
-  return static_cast<int>(std::min<int64_t>(kPlanThreads, std::max<int64_t>(128, (want + 31) / 32 * 32)));
 }
 
 }  // namespace
 
 msa_status launch_plan_step(const msa_plan_args& a, cudaStream_t stream) {
-  const int ctas = a.N > kRowsPerCta ? kPlanCluster : 1;
+  const bool in_place = a.seq_len_out == a.seq_len || a.free_count_out == a.free_count;
   const size_t smem = (3 * static_cast<size_t>(a.B) + 2) * sizeof(int);
-  return launch_cluster(plan_step_kernel, a, ctas, plan_threads(a.B, a.N), smem, stream, "plan_step_kernel launch");
+  return launch_rows(plan_step_kernel, a, a.N, in_place, smem, stream, "plan_step_kernel launch");
 }
 
 msa_status launch_release_pages(const msa_release_args& a, cudaStream_t stream) {
-  const int64_t most = static_cast<int64_t>(a.B) * a.max_pages;   // pages that can come back
-  const int ctas = most > kRowsPerCta ? kPlanCluster : 1;
+  const bool in_place = a.seq_len_out == a.seq_len || a.free_count_out == a.free_count;
   const size_t smem = (static_cast<size_t>(a.B) + 1) * sizeof(int);
-  return launch_cluster(release_kernel, a, ctas, plan_threads(a.B, most), smem, stream, "release_kernel launch");
+  // at most B * max_pages pages come back, a few of the requests' as a rule
+  return launch_rows(release_kernel, a, static_cast<int64_t>(a.B) * a.max_pages / 8, in_place, smem, stream,
+                     "release_kernel launch");
 }
 
 }  // namespace msa

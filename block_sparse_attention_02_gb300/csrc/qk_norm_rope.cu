@@ -26,6 +26,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCtasPerSm = 3;
+constexpr int kRounds = 6;                    // items per warp below which a token's heads are split (the last round's tail)
 
 struct NormRopeParams {
   int64_t N, num_pages;
@@ -242,7 +243,7 @@ msa_status launch_qk_norm_rope(const msa_norm_rope_args& a, cudaStream_t stream)
   const int steps = (a.Hq + heads - 1) / heads + (a.V != nullptr ? 2 : 1) * ((a.Hkv + heads - 1) / heads);
   // few tokens: their heads spread over enough warps to fill the SMs
   const int64_t want = static_cast<int64_t>(dev.num_sms) * kCtasPerSm * kWarps;
-  p.parts = static_cast<int>(std::min<int64_t>(std::max<int64_t>((want + a.N - 1) / a.N, 1), std::max(steps, 1)));
+  p.parts = static_cast<int>(std::min<int64_t>(std::max<int64_t>((kRounds * want + a.N - 1) / a.N, 1), std::max(steps, 1)));
   const int64_t items = a.N * p.parts;
   const unsigned grid =
       static_cast<unsigned>(std::min<int64_t>((items + kWarps - 1) / kWarps, static_cast<int64_t>(dev.num_sms) * kCtasPerSm));
