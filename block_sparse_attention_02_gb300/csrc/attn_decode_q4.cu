@@ -244,6 +244,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_q4_kernel(const Par
   __shared__ int s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int rows = p.B * p.Hkv;
+  wait_for_stream();
 
   int64_t units;
   if (DENSE) {
@@ -525,8 +526,7 @@ msa_status launch(const Params& p, int64_t most_units, int scratch_zeroed, cudaS
   constexpr int smem = kWarps * std::max<int>(kStages * kTileBytes, kMaxG * kD * sizeof(float));
   cudaError_t e = cudaFuncSetAttribute(attn_q4_kernel<DENSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(attn_q4)");
-  attn_q4_kernel<DENSE><<<grid, kThreads, smem, stream>>>(p);
-  e = cudaGetLastError();
+  e = launch_early(attn_q4_kernel<DENSE>, grid, kThreads, smem, stream, p);
   if (e != cudaSuccess) return cuda_fail(e, "attn_q4_kernel launch");
   return MSA_OK;
 }

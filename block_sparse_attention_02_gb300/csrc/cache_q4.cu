@@ -5,12 +5,14 @@
 //     sf = e4m3(amax / (6 gs)),  code = e2m1(x / (sf gs)),  value = code * sf * gs.
 // 72 bytes per token and head instead of 256.
 //
-// Rounding.  x is bf16 (8 bits), sf has 4 bits and gs is a power of two, so an
-// exact quotient x / (sf gs) that lies halfway between two codes has at most 8 bits,
-// and one that does not differs from a halfway point by more than 2^-13 of
-// itself.  q = x r + (x - (x r) sf) r with r = 1 / sf in fp32 returns the first kind exactly
-// and the second within 2^-22, so the code is that of the real quotient.  The
-// same holds for amax / 6 against the scale's halfway points.
+// Rounding.  x is bf16 (8 bits), sf has at most 4 bits and gs is a power of two.  A
+// quotient x / (sf gs) that lies halfway between two codes is a multiple of 1/4 up
+// to 5; one that does not is at least 2^-10 away from every halfway point.  With r =
+// 1 / (sf gs) rounded to fp32, x r + 1536 in one rounding is a multiple of 2^-13: the first kind comes
+// out exact, the second stays on its side, so the code is that of the real
+// quotient, at two instructions a value where a division takes ten.  (In the
+// same way amax / 6 against the scale's halfway points: a product with 1 / 6 that has
+// at most 7 bits rounds to itself.)  Values past the range end at the largest code.
 //
 // Bound: HBM.  A block takes one head, so that the tokens of a prompt, whose slots
 // follow one another, write whole runs of a page.  Store: a thread takes a group (32 bytes in,
@@ -46,40 +48,34 @@ struct StoreParams {
 
 __device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b) { return __vmaxu2(a & 0x7fff7fffu, b & 0x7fff7fffu); }
 
-// Codes and scale byte of the 16 bf16 values in u[0..7] (two per word).
+// Codes and scale byte of the 16 bf16 values in u[0..7] (two per word); inv = 1 / gs.
 __device__ __forceinline__ void quantise16(const uint32_t (&u)[8], float inv, uint2* codes, uint32_t* scale) {
   uint32_t m = abs_max2(u[0], u[1]);
 #pragma unroll
   for (int i = 2; i < 8; ++i) m = abs_max2(m, u[i]);
   const uint32_t top = max(m & 0xffffu, m >> 16);      // bf16 bits order as magnitudes, NaN above infinity
-  const float amax = __uint_as_float(top << 16);
-  const uint32_t sf = top > 0x7f80u ? 0x7fu : e4m3_from_float(fminf(amax * inv, 2688.f) * (1.0f / 6.0f));
+  const float amax = __uint_as_float(top << 16) * inv;
+  const uint32_t sf = top > 0x7f80u ? 0x7fu : e4m3_from_float(fminf(amax, 2688.f) * (1.0f / 6.0f));
   const float s = e4m3_to_float(sf);
-  const float r = s > 0.f ? __fdiv_rn(1.0f, s) : 0.f;   // a group of zeros, or of NaN scale: codes 0
+  const bool some = s > 0.f;                            // not a group of zeros, nor of NaN scale: their codes are 0
+  const float r = some ? __frcp_rn(s) * inv : 0.f;
   uint32_t out[2];
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
-    uint32_t c = 0;
+    float q[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t v = u[w * 4 + i];
-      float q[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float raw = __uint_as_float(e ? v & 0xffff0000u : v << 16) * inv;
-        const float x = fminf(fmaxf(raw, -2688.f), 2688.f);
-        const float q0 = x * r;
-        q[e] = fmaf(fmaf(-q0, s, x), r, q0);
-      }
-      c |= e2m1x2_from_floats(q[0], q[1]) << (8 * i);
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t v = u[w * 4 + (i >> 1)];
+      q[i] = __fadd_rn(__fmaf_rn(__uint_as_float(i & 1 ? v & 0xffff0000u : v << 16), r, 1536.f), -1536.f);
     }
-    out[w] = s > 0.f ? c : 0u;
+    out[w] = some ? e2m1x8_from_floats(q) : 0u;
   }
   *codes = make_uint2(out[0], out[1]);
   *scale = sf;
 }
 
 __global__ void __launch_bounds__(kThreads) append_q4_kernel(const StoreParams p) {
+  wait_for_stream();
   const int group = threadIdx.x & 7;
   const bool is_v = threadIdx.x >> 3 & 1;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * kStoreTokens + (threadIdx.x >> 4);
@@ -98,9 +94,9 @@ __global__ void __launch_bounds__(kThreads) append_q4_kernel(const StoreParams p
     uint8_t* scales = (is_v ? p.V_scales : p.K_scales) + h * p.s1 + group;
     uint4 a[kStoreUnroll], b[kStoreUnroll];
 #pragma unroll
-    for (int i = 0; i < kStoreUnroll; ++i) {
+    for (int i = 0; i < kStoreUnroll; ++i) {   // rows without a slot too: nothing waits for the slots
       a[i] = b[i] = make_uint4(0, 0, 0, 0);
-      if (slot[i] < 0) continue;
+      if (first + i * (kThreads / 16) >= p.N) continue;
       const uint4* x = reinterpret_cast<const uint4*>(src + i * (kThreads / 16) * n_stride);
       a[i] = x[0];
       b[i] = x[1];
@@ -137,6 +133,7 @@ struct ExpandParams {
 };
 
 __global__ void __launch_bounds__(kThreads) expand_q4_kernel(const ExpandParams p) {
+  wait_for_stream();
   const int64_t page = p.pages[blockIdx.x];
   if (page < 0 || page >= p.num_pages) {
     if (blockIdx.y == 0 && threadIdx.x == 0) report(p.dev_err, MSA_DEVERR_BAD_PAGE);
@@ -199,8 +196,7 @@ msa_status launch_append_q4(const msa_append_q4_args& a, cudaStream_t stream) {
   p.dev_err = a.dev_err;
   const dim3 grid(static_cast<unsigned>((a.N + kStoreTokens - 1) / kStoreTokens),
                   std::min<unsigned>(static_cast<unsigned>(a.Hkv), kMaxGridY));
-  append_q4_kernel<<<grid, kThreads, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_early(append_q4_kernel, grid, kThreads, 0, stream, p);
   if (e != cudaSuccess) return cuda_fail(e, "append_q4_kernel launch");
   return MSA_OK;
 }
@@ -220,8 +216,7 @@ msa_status launch_expand_q4(const msa_expand_q4_args& a, cudaStream_t stream) {
   p.k_scale = a.cache.k_scale; p.v_scale = a.cache.v_scale;
   p.dev_err = a.dev_err;
   const dim3 grid(static_cast<unsigned>(a.n), std::min<unsigned>(static_cast<unsigned>(a.Hkv), kMaxGridY));
-  expand_q4_kernel<<<grid, kThreads, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_early(expand_q4_kernel, grid, kThreads, 0, stream, p);
   if (e != cudaSuccess) return cuda_fail(e, "expand_q4_kernel launch");
   return MSA_OK;
 }

@@ -73,6 +73,7 @@ __device__ __forceinline__ int last_at_most(const int* first, int n, int x) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const msa_plan_args p, const bool in_place) {
+  wait_for_stream();
   extern __shared__ int s_plan[];
   int* s_cu = s_plan;                       // [B + 1] first token row, at most N
   int* s_off = s_cu + p.B + 1;              // [B + 1] pages given to the requests before b
@@ -197,6 +198,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const msa_plan_
 }
 
 __global__ void __launch_bounds__(kPlanThreads) release_kernel(const msa_release_args p, const bool in_place) {
+  wait_for_stream();
   extern __shared__ int s_off[];            // [B + 1] pages returned by the requests before b
   const int tid = threadIdx.x, B = p.B, rank = blockIdx.x, ctas = gridDim.x;
   const int per = (B + blockDim.x - 1) / blockDim.x;
@@ -266,19 +268,24 @@ msa_status launch_rows(void (*kernel)(const Args, const bool), const Args& a, in
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return cuda_fail(e, what);
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = in_place && ctas > 1 ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, in_place);
+  cudaError_t e;
+  if (in_place && ctas > 1) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, a, true);
+  } else {
+    e = launch_early(kernel, ctas, threads, smem, stream, a, false);
+  }
   if (e != cudaSuccess) return cuda_fail(e, what);
   return MSA_OK;
 }

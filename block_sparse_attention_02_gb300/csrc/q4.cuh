@@ -7,15 +7,17 @@
 
 namespace msa {
 
-// The two values a, b rounded to E2M1 (nearest even, past the range to +-6):
-// a in the low half of the byte.
-__device__ __forceinline__ uint32_t e2m1x2_from_floats(float a, float b) {
+// Eight values rounded to E2M1 (nearest even, past the range to +-6), element i in bits 4i .. 4i + 3.
+__device__ __forceinline__ uint32_t e2m1x8_from_floats(const float (&q)[8]) {
   uint32_t r;
-  asm("{\n\t.reg .b8 c;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 c, %2, %1;\n\t"
-      "mov.b32 %0, {c, 0, 0, 0};\n\t}"
+  asm("{\n\t.reg .b8 c0, c1, c2, c3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c3, %8, %7;\n\t"
+      "mov.b32 %0, {c0, c1, c2, c3};\n\t}"
       : "=r"(r)
-      : "f"(a), "f"(b));
+      : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
   return r;
 }
 // E4M3 of x (nearest even, past the range to 448; NaN stays NaN).

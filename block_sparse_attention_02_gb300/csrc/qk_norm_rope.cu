@@ -26,7 +26,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCtasPerSm = 3;
-constexpr int kRounds = 6;                    // items per warp below which a token's heads are split (the last round's tail)
+constexpr int kAhead = 4;                     // steps of 1 KiB per warp in shared memory
 
 struct NormRopeParams {
   int64_t N, num_pages;
@@ -44,6 +44,9 @@ struct NormRopeParams {
   int32_t* dev_err;
 };
 
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void unpack8(const uint4 u, float* x) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -67,6 +70,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const N
   constexpr int kHeads = 32 / kLanes;         // heads per warp and step
   __shared__ __align__(16) float s_weight[2][D];
   __shared__ float2 s_turn[kWarps][D / 2];    // cosine and sine of every pair of a warp's token
+  __shared__ __align__(16) uint8_t s_ring[kWarps][kAhead * 1024];
+  wait_for_stream();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane % kLanes, hl = lane / kLanes;
   for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
@@ -103,46 +108,64 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const N
   __syncthreads();
   const int q_steps = (p.Hq + kHeads - 1) / kHeads, k_steps = (p.Hkv + kHeads - 1) / kHeads;
   const int steps = q_steps + k_steps + (p.V != nullptr ? k_steps : 0);
-  const int64_t items = p.N * p.parts;
+  const int64_t items = p.N * p.parts, stride = static_cast<int64_t>(gridDim.x) * kWarps;
+  const int64_t item0 = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+
+  // The loads run kAhead steps before the work, across tokens (they need no position): each lane
+  // copies its two chunks into shared memory places that it alone reads.
+  const uint32_t ring = smem_u32(s_ring[warp]) + lane * 16;
+  int64_t load_item = item0, load_n = 0;
+  int load_step = 0;
+  uint32_t load_at = 0, read_at = 0;
+  auto load_token = [&] {
+    load_n = p.parts == 1 ? load_item : load_item / p.parts;
+    load_step = p.parts == 1 ? 0 : static_cast<int>(load_item - load_n * p.parts);
+  };
+  auto fetch = [&] {
+    if (load_item < items) {
+      const bool is_q = load_step < q_steps, is_v = load_step >= q_steps + k_steps;
+      const int head = (load_step - (is_q ? 0 : is_v ? q_steps + k_steps : q_steps)) * kHeads + hl;
+      if (head < (is_q ? p.Hq : p.Hkv)) {
+        const uint8_t* src = is_q   ? p.Q + load_n * p.q0 + head * p.q1
+                             : is_v ? p.V + load_n * p.v0 + head * p.v1
+                                    : p.K + load_n * p.k0 + head * p.k1;
+        copy16(ring + load_at, src + c0 * 16);
+        copy16(ring + load_at + 512, src + c1 * 16);
+      }
+      load_at = load_at + 1024 == kAhead * 1024 ? 0 : load_at + 1024;
+      load_step += p.parts;
+      if (load_step >= steps) {
+        load_item += stride;
+        if (load_item < items) load_token();
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (load_item < items) load_token();
+#pragma unroll
+  for (int i = 0; i < kAhead - 1; ++i) fetch();
+
   bool bad = false;
-  for (int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + warp; item < items;
-       item += static_cast<int64_t>(gridDim.x) * kWarps) {
+  for (int64_t item = item0; item < items; item += stride) {
     const int64_t n = p.parts == 1 ? item : item / p.parts;
     const int first = p.parts == 1 ? 0 : static_cast<int>(item - n * p.parts);
     const int pos = p.pos[n];
-    if (pos < 0) continue;
     // where this token's key and value rows go
     int64_t k_row = n * p.ko0, v_row = 0;
-    bool store_kv = true;
+    bool store_kv = pos >= 0;
     if (p.slots != nullptr) {
       const int64_t slot = p.slots[n], page = slot / kBk;
       const int t = static_cast<int>(slot & (kBk - 1));
-      store_kv = slot >= 0 && page < p.num_pages;
-      bad |= slot >= 0 && !store_kv;
+      store_kv = pos >= 0 && slot >= 0 && page < p.num_pages;
+      bad |= pos >= 0 && slot >= 0 && page >= p.num_pages;
       k_row = page * p.ko0 + t * p.ko2;
       v_row = page * p.vo0 + t * p.vo2;
     }
-    auto head_of = [&](int step) {            // of this lane; -1: nothing to do
-      const bool is_q = step < q_steps;
-      const int head = (is_q ? step : step < q_steps + k_steps ? step - q_steps : step - q_steps - k_steps) * kHeads + hl;
-      return head < (is_q ? p.Hq : p.Hkv) && (is_q || store_kv) ? head : -1;
-    };
-    uint4 next0 = make_uint4(0, 0, 0, 0), next1 = next0;
-    auto fetch = [&](int step) {
-      const int head = head_of(step);
-      if (head < 0) return;
-      const uint8_t* src = step < q_steps             ? p.Q + n * p.q0 + head * p.q1
-                           : step < q_steps + k_steps ? p.K + n * p.k0 + head * p.k1
-                                                      : p.V + n * p.v0 + head * p.v1;
-      next0 = *reinterpret_cast<const uint4*>(src + c0 * 16);
-      next1 = *reinterpret_cast<const uint4*>(src + c1 * 16);
-    };
-    if (first < steps) fetch(first);
     __syncwarp();                             // the last token's turns are read
 #pragma unroll
     for (int e = 0; e < D / 64; ++e) {
       if (lane + 32 * e < p.rot / 2) {
-        const int32_t a = static_cast<int32_t>((turns[e] * static_cast<uint64_t>(pos)) >> 32);
+        const int32_t a = static_cast<int32_t>((turns[e] * static_cast<uint64_t>(max(pos, 0))) >> 32);
         float2 cs;
         sincospif(static_cast<float>(a) * 4.656612873077393e-10f, &cs.y, &cs.x);   // 2^-31: half turns
         s_turn[warp][lane + 32 * e] = cs;
@@ -158,12 +181,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const N
       sn[e] = v.y;
     }
     for (int step = first; step < steps; step += p.parts) {
-      const uint4 u0 = next0, u1 = next1;
-      if (step + p.parts < steps) fetch(step + p.parts);
-      const bool is_q = step < q_steps;
-      const int head = head_of(step);
-      if (step >= q_steps + k_steps) {        // values go as they are
-        if (head >= 0) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 2) : "memory");
+      const uint4 u0 = *reinterpret_cast<const uint4*>(s_ring[warp] + read_at + lane * 16);
+      const uint4 u1 = *reinterpret_cast<const uint4*>(s_ring[warp] + read_at + 512 + lane * 16);
+      read_at = read_at + 1024 == kAhead * 1024 ? 0 : read_at + 1024;
+      fetch();
+      const bool is_q = step < q_steps, is_v = step >= q_steps + k_steps;
+      const int head = (step - (is_q ? 0 : is_v ? q_steps + k_steps : q_steps)) * kHeads + hl;
+      const bool live = head < (is_q ? p.Hq : p.Hkv) && (is_q ? pos >= 0 : store_kv);
+      if (is_v) {                             // values go as they are
+        if (live) {
           uint8_t* dst = p.V_out + v_row + head * p.vo1;
           *reinterpret_cast<uint4*>(dst + c0 * 16) = u0;
           *reinterpret_cast<uint4*>(dst + c1 * 16) = u1;
@@ -207,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const N
           x[8 + e] = b * cs[e] + a * sn[e];
         }
       }
-      if (head >= 0) {
+      if (live) {
         uint8_t* dst = is_q ? p.Q_out + n * p.qo0 + head * p.qo1 : p.K_out + k_row + head * p.ko1;
         *reinterpret_cast<uint4*>(dst + c0 * 16) = pack8(x);
         *reinterpret_cast<uint4*>(dst + c1 * 16) = pack8(x + 8);
@@ -243,18 +270,18 @@ msa_status launch_qk_norm_rope(const msa_norm_rope_args& a, cudaStream_t stream)
   const int steps = (a.Hq + heads - 1) / heads + (a.V != nullptr ? 2 : 1) * ((a.Hkv + heads - 1) / heads);
   // few tokens: their heads spread over enough warps to fill the SMs
   const int64_t want = static_cast<int64_t>(dev.num_sms) * kCtasPerSm * kWarps;
-  p.parts = static_cast<int>(std::min<int64_t>(std::max<int64_t>((kRounds * want + a.N - 1) / a.N, 1), std::max(steps, 1)));
+  p.parts = static_cast<int>(std::min<int64_t>(std::max<int64_t>((want + a.N - 1) / a.N, 1), std::max(steps, 1)));
   const int64_t items = a.N * p.parts;
   const unsigned grid =
       static_cast<unsigned>(std::min<int64_t>((items + kWarps - 1) / kWarps, static_cast<int64_t>(dev.num_sms) * kCtasPerSm));
+  cudaError_t e;
   if (a.D == 128) {
-    if (a.interleaved) norm_rope_kernel<128, true><<<grid, kThreads, 0, stream>>>(p);
-    else norm_rope_kernel<128, false><<<grid, kThreads, 0, stream>>>(p);
+    if (a.interleaved) e = launch_early(norm_rope_kernel<128, true>, grid, kThreads, 0, stream, p);
+    else e = launch_early(norm_rope_kernel<128, false>, grid, kThreads, 0, stream, p);
   } else {
-    if (a.interleaved) norm_rope_kernel<64, true><<<grid, kThreads, 0, stream>>>(p);
-    else norm_rope_kernel<64, false><<<grid, kThreads, 0, stream>>>(p);
+    if (a.interleaved) e = launch_early(norm_rope_kernel<64, true>, grid, kThreads, 0, stream, p);
+    else e = launch_early(norm_rope_kernel<64, false>, grid, kThreads, 0, stream, p);
   }
-  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "norm_rope_kernel launch");
   return MSA_OK;
 }
