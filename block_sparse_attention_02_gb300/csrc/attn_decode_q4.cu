@@ -45,7 +45,8 @@ constexpr int kPart = kMaxG * kD + 2 * kMaxG;           // floats of a partial: 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPShift = 8.f;                          // P is held as 2^(z - m + 8)
-constexpr float kSlack = 6.f;                           // m follows a maximum more than this above it
+constexpr float kNoMax = -1e30f;                        // m before a first score: finite, so that no difference is NaN
+constexpr float kPMost = 32768.f;                       // most of a lane's sum of P (fp16 ends at 65504)
 
 struct Params {
   int B, Hq, Hkv, G, k;
@@ -166,23 +167,26 @@ __device__ __forceinline__ void attend_tile(const uint32_t (&q)[16], const float
       for (int i = 0; i < 4; ++i)
         if (u * 16 + token_of_row(g) + (i < 2 ? 0 : 8) >= valid) s[u][i] = -INFINITY;
   }
-  // exponents of P relative to m - 8: infinite until a first maximum is known
-  float e[2][4], top = -INFINITY;
+  // P as 2^(z - m + 8): infinite against kNoMax, and 0 where z is -inf.  A sum above 2^15
+  // means that some score passed m by more than 5: m follows and P is formed again.
+  float e[2][4], sum[2];
+  auto form = [&] {
 #pragma unroll
-  for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      e[u][i] = fmaf(s[u][i], coef[i & 1], kPShift - st->m[i & 1]);
-      top = fmaxf(top, e[u][i]);
-    }
-  if (__any_sync(0xffffffffu, top > kPShift + kSlack)) {
+      for (int i = 0; i < 4; ++i) e[u][i] = ex2(fmaf(s[u][i], coef[i & 1], kPShift - st->m[i & 1]));
+#pragma unroll
+    for (int c = 0; c < 2; ++c) sum[c] = (e[0][c] + e[0][c + 2]) + (e[1][c] + e[1][c + 2]);
+  };
+  form();
+  if (__any_sync(0xffffffffu, fmaxf(sum[0], sum[1]) > kPMost)) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       float z = fmaxf(fmaxf(s[0][c], s[0][c + 2]), fmaxf(s[1][c], s[1][c + 2])) * coef[c];
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, o));
       const float m = fmaxf(st->m[c], z);
-      const float f = m == -INFINITY ? 1.f : ex2(st->m[c] - m);
+      const float f = ex2(st->m[c] - m);
       st->m[c] = m;
       st->l[c] *= f;
 #pragma unroll
@@ -191,17 +195,12 @@ __device__ __forceinline__ void attend_tile(const uint32_t (&q)[16], const float
         st->acc[i][c + 2] *= f;
       }
     }
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) e[u][i] = fmaf(s[u][i], coef[i & 1], kPShift - st->m[i & 1]);
+    form();
   }
+  st->l[0] += sum[0];
+  st->l[1] += sum[1];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) e[u][i] = ex2(e[u][i]);
-    st->l[0] += e[u][0] + e[u][2];
-    st->l[1] += e[u][1] + e[u][3];
     // P^T: from (row g, heads 2t, 2t + 1) to (head g, rows 2t, 2t + 1)
     const uint32_t b0 = transpose8x8(h2u(__floats2half2_rn(e[u][0], e[u][1])));
     const uint32_t b1 = transpose8x8(h2u(__floats2half2_rn(e[u][2], e[u][3])));
@@ -212,7 +211,11 @@ __device__ __forceinline__ void attend_tile(const uint32_t (&q)[16], const float
       const int tok = u * 16 + token_of_row(2 * t + (i & 1)) + 8 * (i >> 1);
       v[i] = *reinterpret_cast<const uint2*>(tile + kVAt + tok * 64 + ((g * 8) ^ ((tok & 4) << 3)));
       sf[i] = tile[kVsAt + tok * 8 + g];
-      if (valid < kTile && tok >= valid) sf[i] = 0;
+    }
+    if (valid < kTile) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (u * 16 + token_of_row(2 * t + (i & 1)) + 8 * (i >> 1) >= valid) sf[i] = 0;
     }
     const __half2 s01 = e4m3x2_to_half2(sf[0] | sf[1] << 8), s23 = e4m3x2_to_half2(sf[2] | sf[3] << 8);
 #pragma unroll
@@ -355,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_q4_kernel(const Par
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) st.acc[i][e] = 0.f;
-    st.m[0] = st.m[1] = -INFINITY;
+    st.m[0] = st.m[1] = kNoMax;
     st.l[0] = st.l[1] = 0.f;
 
     // this warp's 32 tokens of every other page, kStages - 1 of them in flight
@@ -416,14 +419,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_q4_kernel(const Par
         *reinterpret_cast<float2*>(&s_o[warp][2 * t + c][16 * g + 2 * i]) = make_float2(st.acc[i][c], st.acc[i][c + 2]);
     __syncthreads();
     const int h = tid >> 5, d0 = (tid & 31) * 4;
-    float M = -INFINITY, l = 0.f;
+    float M = kNoMax, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][h]);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float mw = s_m[w][h];
-      const float f = mw == -INFINITY ? (s_l[w][h] == 0.f ? 0.f : 1.f) : ex2(mw - M);   // l != 0 there: a NaN that has to stay
+      const float f = ex2(s_m[w][h] - M);
       const float4 v = *reinterpret_cast<const float4*>(&s_o[w][h][d0]);
       o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y); o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
       l = fmaf(f, s_l[w][h], l);
@@ -446,14 +448,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_q4_kernel(const Par
       if (write) {
         __threadfence();
         auto part_of = [&](int c) { return p.part + (static_cast<int64_t>(c) * 2 + (c * per >= row_first ? 0 : 1)) * kPart; };
-        M = -INFINITY;
-        for (int c = first; c <= last; ++c) M = fmaxf(M, __ldcg(part_of(c) + kMaxG * kD + h));
+        M = kNoMax;
+        for (int c = first + lane; c <= last; c += 32) M = fmaxf(M, __ldcg(part_of(c) + kMaxG * kD + h));
+#pragma unroll
+        for (int i = 1; i < 32; i <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, i));
         o = make_float4(0.f, 0.f, 0.f, 0.f);
         l = 0.f;
+#pragma unroll 8
         for (int c = first; c <= last; ++c) {
           const float* x = part_of(c);
-          const float mc = __ldcg(x + kMaxG * kD + h), lc = __ldcg(x + kMaxG * kD + kMaxG + h);
-          const float f = mc == -INFINITY ? (lc == 0.f ? 0.f : 1.f) : ex2(mc - M);
+          const float f = ex2(__ldcg(x + kMaxG * kD + h) - M), lc = __ldcg(x + kMaxG * kD + kMaxG + h);
           const float4 v = __ldcg(reinterpret_cast<const float4*>(x + h * kD + d0));
           o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y); o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
           l = fmaf(f, lc, l);
