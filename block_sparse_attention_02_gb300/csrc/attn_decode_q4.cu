@@ -36,12 +36,15 @@
 namespace msa {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kCtasPerSm = 2;
+// Warps of a CTA: eight for long rows; four for rows of few pages, where twice as many CTAs leave an SM
+// less idle while one of them ends a row and waits for the next one's first pages.
+constexpr int kDenseWarps = 8, kSparseWarps = 4;
+constexpr int kSmWarps = 16;                            // that the registers of an SM hold
 constexpr int kStages = 3;                              // tiles of 32 tokens per warp in shared memory
-constexpr int kMaxGrid = 512;                           // CTAs per launch at most (sizes the workspace)
-constexpr int kPart = kMaxG * kD + 2 * kMaxG;           // floats of a partial: O [8][128], m [8], l [8]
+constexpr int kDenseBins = kDenseMaxBatch, kSparseBins = 256;   // that the pages are counted by
+constexpr int kRowCost = 3;                             // pages' time that a row's end and the next one's start take
+constexpr int kMaxGrid = 1024;                           // CTAs per launch at most (sizes the workspace)
+constexpr int kPart = kMaxG * kD + 2 * kMaxG;           // floats of a partial: O, m, l of eight heads
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPShift = 8.f;                          // P is held as 2^(z - m + 8)
@@ -50,6 +53,9 @@ constexpr float kPMost = 32768.f;                       // most of a lane's sum 
 
 struct Params {
   int B, Hq, Hkv, G, k;
+  // sparse: units of a row (k or a few more, the last ones without a page), or 0: each row has its own pages
+  // and kRowCost more for units, counted by bins of bin_rows rows
+  int row_units, bin_rows;
   float scale_log2, v_scale;
   const uint8_t* Q;
   int64_t q0, q1;                       // byte strides (b, h)
@@ -238,31 +244,45 @@ __device__ __forceinline__ void attend_tile(const uint32_t (&q)[16], const float
 }
 
 template <bool DENSE>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_q4_kernel(const Params p) {
+__global__ void __launch_bounds__(32 * (DENSE ? kDenseWarps : kSparseWarps), kSmWarps / (DENSE ? kDenseWarps : kSparseWarps))
+    attn_q4_kernel(const Params p) {
+  constexpr int kWarps = DENSE ? kDenseWarps : kSparseWarps, kThreads = 32 * kWarps;
+  constexpr int kBins = DENSE ? kDenseBins : kSparseBins;
+  constexpr int kTeams = kWarps / 4;        // four warps share a page, 32 tokens each; the teams alternate pages
+  constexpr int kRep = 8 / kWarps;          // of the joined outputs' eight parts, those of a warp
   extern __shared__ __align__(128) uint8_t s_ring[];
-  float(*s_o)[kMaxG][kD] = reinterpret_cast<float(*)[kMaxG][kD]>(s_ring);   // after a row's part: [warp][head][channel]
+  float4(*s_o)[8][32] = reinterpret_cast<float4(*)[8][32]>(s_ring);   // after a row's part: [warp][i][lane]
   __shared__ float s_m[kWarps][kMaxG], s_l[kWarps][kMaxG];
-  __shared__ int s_pre[DENSE ? kDenseMaxBatch + 1 : 1];   // pages of the sequences before b
+  __shared__ int s_pre[kBins + 1];          // pages before a bin: a sequence (of one head; dense) or bin_rows rows
   __shared__ int s_wsum[kWarps];
   __shared__ int s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int rows = p.B * p.Hkv;
   wait_for_stream();
 
-  int64_t units;
-  if (DENSE) {
-    constexpr int kPer = kDenseMaxBatch / kThreads;
+  auto row_live = [&](int r) { return min(max(p.n[r], 0), p.k); };   // sparse: pages of a row
+  auto row_units = [&](int r) {             // and its units where rows are counted
+    const int live = row_live(r);
+    return live > 0 ? live + kRowCost : 0;
+  };
+  const int bins = DENSE ? p.B : p.bin_rows > 0 ? (rows + p.bin_rows - 1) / p.bin_rows : 0;
+  if (bins > 0) {
+    constexpr int kPer = kBins / kThreads;
     int mine[kPer], sum = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int b = tid * kPer + i;
       mine[i] = 0;
-      if (b < p.B) {
-        const int L = p.seq_len[b];
-        if (L < 0 || L > p.max_pages * kBk) {
-          if (blockIdx.x == 0) report(p.dev_err, MSA_DEVERR_BAD_LEN);
+      if (b < bins) {
+        if (DENSE) {
+          const int L = p.seq_len[b];
+          if (L < 0 || L > p.max_pages * kBk) {
+            if (blockIdx.x == 0) report(p.dev_err, MSA_DEVERR_BAD_LEN);
+          } else {
+            mine[i] = (L + kBk - 1) / kBk;
+          }
         } else {
-          mine[i] = (L + kBk - 1) / kBk;
+          for (int r = b * p.bin_rows; r < min(rows, (b + 1) * p.bin_rows); ++r) mine[i] += row_units(r);
         }
       }
       sum += mine[i];
@@ -280,15 +300,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_q4_kernel(const Par
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int b = tid * kPer + i;
-      if (b <= p.B) s_pre[b] = before;
+      if (b <= bins) s_pre[b] = before;
       before += mine[i];
     }
-    if (tid == kThreads - 1 && p.B == kDenseMaxBatch) s_pre[p.B] = before;
+    if (tid == kThreads - 1 && bins == kBins) s_pre[bins] = before;
     __syncthreads();
-    units = static_cast<int64_t>(s_pre[p.B]) * p.Hkv;
-  } else {
-    units = static_cast<int64_t>(rows) * p.k;
   }
+  auto bin_of = [&](int64_t u, int heads) {   // last bin whose units start at or before u
+    int x = 0, y = bins;
+    while (y - x > 1) {
+      const int mid = (x + y) >> 1;
+      if (static_cast<int64_t>(s_pre[mid]) * heads <= u) x = mid; else y = mid;
+    }
+    return x;
+  };
+  const int64_t units = DENSE      ? static_cast<int64_t>(s_pre[bins]) * p.Hkv
+                        : bins > 0 ? s_pre[bins]
+                                   : static_cast<int64_t>(rows) * p.row_units;
   const int64_t per = (units + gridDim.x - 1) / gridDim.x;
   const int64_t lo = min(units, static_cast<int64_t>(blockIdx.x) * per), hi = min(units, lo + per);
 
@@ -297,12 +325,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_q4_kernel(const Par
     int b, head, p0, row_pages, tokens;
     const int32_t* list;
     if (DENSE) {
-      int x = 0, y = p.B;                   // last sequence whose units start at or before u
-      while (y - x > 1) {
-        const int mid = (x + y) >> 1;
-        if (static_cast<int64_t>(s_pre[mid]) * p.Hkv <= u) x = mid; else y = mid;
-      }
-      b = x;
+      b = bin_of(u, p.Hkv);
       row_pages = s_pre[b + 1] - s_pre[b];
       const int rem = static_cast<int>(u - static_cast<int64_t>(s_pre[b]) * p.Hkv);
       head = rem / row_pages;
@@ -310,12 +333,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_q4_kernel(const Par
       tokens = p.seq_len[b];
       list = p.seq_pt + b * p.max_pages;
     } else {
-      const int r = static_cast<int>(u / p.k);
+      int r;
+      if (bins > 0) {
+        const int x = bin_of(u, 1);
+        r = x * p.bin_rows;
+        p0 = static_cast<int>(u - s_pre[x]);
+        for (row_pages = row_units(r); p0 >= row_pages; row_pages = row_units(++r)) p0 -= row_pages;
+      } else {
+        r = static_cast<int>(u / p.row_units);
+        p0 = static_cast<int>(u - static_cast<int64_t>(r) * p.row_units);
+        row_pages = p.row_units;
+      }
       b = r / p.Hkv;
       head = r - b * p.Hkv;
-      p0 = static_cast<int>(u - static_cast<int64_t>(r) * p.k);
-      row_pages = p.k;
-      const int nr = min(max(p.n[r], 0), p.k);
+      const int nr = row_live(r);
       tokens = nr == 0 ? 0 : (nr - 1) * kBk + min(max(p.last_len[r], 0), kBk);
       list = p.pt + static_cast<int64_t>(r) * p.k;
     }
@@ -324,56 +355,27 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_q4_kernel(const Par
     const int64_t row_first = u - p0;
     u += p1 - p0;
 
-    // Q of head g as fp16, scaled by a power of two: channels 32t + 2i, 32t + 2i + 1 in q[i]
-    uint32_t q[16];
-    float coef[2];
-    {
-      float f[32], top = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (g < p.G) v = *reinterpret_cast<const uint4*>(p.Q + b * p.q0 + (head * p.G + g) * p.q1 + t * 64 + i * 16);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          f[8 * i + 2 * e] = __uint_as_float(w[e] << 16);
-          f[8 * i + 2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 32; ++i) top = fmaxf(top, fabsf(f[i]));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int ex = min(max(static_cast<int>(__float_as_uint(top) >> 23), 1), 253);
-      const float down = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);   // 2^(127 - ex)
-      const float up = __uint_as_float(static_cast<uint32_t>(ex) << 23);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) q[i] = h2u(__floats2half2_rn(f[2 * i] * down, f[2 * i + 1] * down));
-#pragma unroll
-      for (int c = 0; c < 2; ++c) 
-        coef[c] = fmaxf(__shfl_sync(0xffffffffu, up, 8 * t + 4 * c) * p.scale_log2, FLT_MIN);   // > 0: -inf stays so
-    }
-    State st;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) st.acc[i][e] = 0.f;
-    st.m[0] = st.m[1] = kNoMax;
-    st.l[0] = st.l[1] = 0.f;
-
-    // this warp's 32 tokens of every other page, kStages - 1 of them in flight
+    // this warp's 32 tokens of its team's pages, kStages - 1 of them in flight
     const int tok0 = (warp & 3) * kTile, j0 = p0 + (warp >> 2);
     const int live = min(p1, (tokens - tok0 + kBk - 1) / kBk);   // pages before here have a token of this warp's
-    const int count = (live - j0 + 1) / 2;
+    const int count = (live - j0 + kTeams - 1) / kTeams;
     const Bases at = {p.K_codes + head * p.c1 + tok0 * 64 + lane * 16, p.V_codes + head * p.c1 + tok0 * 64 + lane * 16,
                       (lane < 16 ? p.K_scales : p.V_scales) + head * p.s1 + tok0 * 8 + (lane & 15) * 16};
     uint8_t* ring = s_ring + warp * (kStages * kTileBytes);
-    int32_t ids = 0;                        // lane i: page of the i-th of the present run of 32
+    // lane i: page of the i-th of the present run of 32 (known before the row's length, so both loads go together)
+    const int listed = DENSE ? p1 : min(p1, p.k);
+    int32_t ids = j0 + kTeams * lane < listed ? list[j0 + kTeams * lane] : -1;
+    uint4 raw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if (g < p.G) raw[i] = *reinterpret_cast<const uint4*>(p.Q + b * p.q0 + (head * p.G + g) * p.q1 + t * 64 + i * 16);
+    }
     uint32_t good = 0;                      // bit n % 32: the n-th page has a valid id
     int into = 0, from = 0;                 // stages of the ring
     auto fetch = [&](int n) {
       if (n < count) {
-        if ((n & 31) == 0) ids = j0 + 2 * (n + lane) < live ? list[j0 + 2 * (n + lane)] : -1;
+        if ((n & 31) == 0 && n > 0) ids = j0 + kTeams * (n + lane) < listed ? list[j0 + kTeams * (n + lane)] : -1;
         const int32_t page = __shfl_sync(0xffffffffu, ids, n & 31);
         const uint32_t bit = 1u << (n & 31);
         if (page >= 0 && page < p.num_pages) {
@@ -389,18 +391,55 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_q4_kernel(const Par
     };
 #pragma unroll
     for (int n = 0; n < kStages - 1; ++n) fetch(n);
+    // Q of head g as fp16, scaled by a power of two: channels 32t + 2i, 32t + 2i + 1 in q[i]
+    uint32_t q[16];
+    float coef[2];
+    {
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int ex = min(max(static_cast<int>(__float_as_uint(top) >> 23), 1), 253);
+      const float down = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);   // 2^(127 - ex)
+      const float up = __uint_as_float(static_cast<uint32_t>(ex) << 23);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          q[4 * i + e] = h2u(__floats2half2_rn(__uint_as_float(w[e] << 16) * down, __uint_as_float(w[e] & 0xffff0000u) * down));
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        coef[c] = fmaxf(__shfl_sync(0xffffffffu, up, 8 * t + 4 * c) * p.scale_log2, FLT_MIN);   // > 0: -inf stays so
+    }
+    State st;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) st.acc[i][e] = 0.f;
+    st.m[0] = st.m[1] = kNoMax;
+    st.l[0] = st.l[1] = 0.f;
+
     for (int n = 0; n < count; ++n) {
       copies_wait<kStages - 2>();
       __syncwarp();                         // every lane's share of tile n is there, and tile n - 1 is read
       fetch(n + kStages - 1);
       if (good >> (n & 31) & 1)
-        attend_tile(q, coef, ring + from * kTileBytes, tokens - (j0 + 2 * n) * kBk - tok0, g, t, &st);
+        attend_tile(q, coef, ring + from * kTileBytes, tokens - (j0 + kTeams * n) * kBk - tok0, g, t, &st);
       from = from + 1 == kStages ? 0 : from + 1;
     }
     copies_wait<0>();
     __syncthreads();                        // the rings give way to the joined outputs
 
-    // the eight warps' softmaxes joined
+    // the warps' softmaxes joined, in the order the products left them: element [i][lane] of
+    // a warp's outputs is its lane's acc[i], and a warp joins elements i = warp (and + 4) of all
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -413,32 +452,45 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_q4_kernel(const Par
       }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-        *reinterpret_cast<float2*>(&s_o[warp][2 * t + c][16 * g + 2 * i]) = make_float2(st.acc[i][c], st.acc[i][c + 2]);
+    for (int i = 0; i < 8; ++i) s_o[warp][i][lane] = make_float4(st.acc[i][0], st.acc[i][1], st.acc[i][2], st.acc[i][3]);
     __syncthreads();
-    const int h = tid >> 5, d0 = (tid & 31) * 4;
-    float M = kNoMax, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float M[2] = {kNoMax, kNoMax}, l[2] = {0.f, 0.f};    // of heads 2t, 2t + 1
+    float4 o[kRep];                                      // their channel 16g + 2i (x, y) and the next (z, w)
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][h]);
+    for (int i = 0; i < kRep; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float4& x, float f0, float f1, float4 v) {
+      x.x = fmaf(f0, v.x, x.x); x.y = fmaf(f1, v.y, x.y); x.z = fmaf(f0, v.z, x.z); x.w = fmaf(f1, v.w, x.w);
+    };
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) M[c] = fmaxf(M[c], s_m[w][2 * t + c]);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float f = ex2(s_m[w][h] - M);
-      const float4 v = *reinterpret_cast<const float4*>(&s_o[w][h][d0]);
-      o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y); o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
-      l = fmaf(f, s_l[w][h], l);
+      float f[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        f[c] = ex2(s_m[w][2 * t + c] - M[c]);
+        l[c] = fmaf(f[c], s_l[w][2 * t + c], l[c]);
+      }
+#pragma unroll
+      for (int i = 0; i < kRep; ++i) add(o[i], f[0], f[1], s_o[w][warp + i * kWarps][lane]);
     }
     const int first = static_cast<int>(row_first / per), last = static_cast<int>((row_first + row_pages - 1) / per);
     bool write = first == last;
     if (!write) {
-      // slot 0: the part at the start of a CTA's run, slot 1: the one at its end
-      float* mine = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + (lo >= row_first ? 0 : 1)) * kPart;
-      *reinterpret_cast<float4*>(mine + h * kD + d0) = o;
-      if ((tid & 31) == 0) {
-        mine[kMaxG * kD + h] = M;
-        mine[kMaxG * kD + kMaxG + h] = l;
+      // a part in the workspace: O as [8][32] float4, m [8], l [8]; slot 0: the one at the start
+      // of a CTA's run, slot 1: the one at its end
+      auto part_of = [&](int c) { return p.part + (static_cast<int64_t>(c) * 2 + (c * per >= row_first ? 0 : 1)) * kPart; };
+      float* mine = part_of(blockIdx.x);
+#pragma unroll
+      for (int i = 0; i < kRep; ++i) reinterpret_cast<float4*>(mine)[tid + i * kThreads] = o[i];
+      if (warp == 0 && g == 0) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          mine[kMaxG * kD + 2 * t + c] = M[c];
+          mine[kMaxG * kD + kMaxG + 2 * t + c] = l[c];
+        }
       }
       __threadfence();
       __syncthreads();
@@ -447,46 +499,60 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_q4_kernel(const Par
       write = s_last != 0;
       if (write) {
         __threadfence();
-        auto part_of = [&](int c) { return p.part + (static_cast<int64_t>(c) * 2 + (c * per >= row_first ? 0 : 1)) * kPart; };
-        M = kNoMax;
-        for (int c = first + lane; c <= last; c += 32) M = fmaxf(M, __ldcg(part_of(c) + kMaxG * kD + h));
+        M[0] = M[1] = kNoMax;
+        for (int c = first + g; c <= last; c += 8) {     // eight parts at a time, by g
+          const float2 m = __ldcg(reinterpret_cast<const float2*>(part_of(c) + kMaxG * kD) + t);
+          M[0] = fmaxf(M[0], m.x);
+          M[1] = fmaxf(M[1], m.y);
+        }
 #pragma unroll
-        for (int i = 1; i < 32; i <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, i));
-        o = make_float4(0.f, 0.f, 0.f, 0.f);
-        l = 0.f;
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int i = 4; i < 32; i <<= 1) M[c] = fmaxf(M[c], __shfl_xor_sync(0xffffffffu, M[c], i));
+        l[0] = l[1] = 0.f;
+#pragma unroll
+        for (int i = 0; i < kRep; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
         for (int c = first; c <= last; ++c) {
           const float* x = part_of(c);
-          const float f = ex2(__ldcg(x + kMaxG * kD + h) - M), lc = __ldcg(x + kMaxG * kD + kMaxG + h);
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(x + h * kD + d0));
-          o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y); o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
-          l = fmaf(f, lc, l);
+          const float2 m = __ldcg(reinterpret_cast<const float2*>(x + kMaxG * kD) + t);
+          const float2 lc = __ldcg(reinterpret_cast<const float2*>(x + kMaxG * kD + kMaxG) + t);
+          const float f0 = ex2(m.x - M[0]), f1 = ex2(m.y - M[1]);
+          l[0] = fmaf(f0, lc.x, l[0]);
+          l[1] = fmaf(f1, lc.y, l[1]);
+#pragma unroll
+          for (int i = 0; i < kRep; ++i) add(o[i], f0, f1, __ldcg(reinterpret_cast<const float4*>(x) + tid + i * kThreads));
         }
         if (tid == 0) p.counter[row] = 0;
       }
     }
-    if (write && h < p.G) {
-      const int64_t at = static_cast<int64_t>(b) * p.Hq + head * p.G + h;
-      const float r = l == 0.f ? 0.f : p.v_scale / l;
-      const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * r, o.y * r), y = __floats2bfloat162_rn(o.z * r, o.w * r);
-      uint2 w;
-      w.x = *reinterpret_cast<const uint32_t*>(&x);
-      w.y = *reinterpret_cast<const uint32_t*>(&y);
-      *reinterpret_cast<uint2*>(p.O + at * kD + d0) = w;
-      if (p.LSE != nullptr && (tid & 31) == 0) p.LSE[at] = l == 0.f ? -INFINITY : (M - kPShift + log2f(l)) * kLn2;
+    if (write) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int h = 2 * t + c;
+        if (h >= p.G) break;
+        const int64_t at = static_cast<int64_t>(b) * p.Hq + head * p.G + h;
+        const float r = l[c] == 0.f ? 0.f : p.v_scale / l[c];
+#pragma unroll
+        for (int i = 0; i < kRep; ++i)
+          *reinterpret_cast<__nv_bfloat162*>(p.O + at * kD + 16 * g + 2 * (warp + i * kWarps)) =
+              c ? __floats2bfloat162_rn(o[i].y * r, o[i].w * r) : __floats2bfloat162_rn(o[i].x * r, o[i].z * r);
+        if (p.LSE != nullptr && warp == 0 && g == 0)
+          p.LSE[at] = l[c] == 0.f ? -INFINITY : (M[c] - kPShift + log2f(l[c])) * kLn2;
+      }
     }
     __syncthreads();
   }
 
-  if (DENSE) {             // sequences without a token have no units
+  if (bins > 0) {          // rows without a page have no units
     for (int r = blockIdx.x; r < rows; r += gridDim.x) {
       const int b = r / p.Hkv, head = r - b * p.Hkv;
-      if (s_pre[b + 1] != s_pre[b]) continue;
-      const int h = tid >> 5;
-      if (h >= p.G) continue;
-      const int64_t at = static_cast<int64_t>(b) * p.Hq + head * p.G + h;
-      *reinterpret_cast<uint2*>(p.O + at * kD + (tid & 31) * 4) = make_uint2(0, 0);
-      if (p.LSE != nullptr && (tid & 31) == 0) p.LSE[at] = -INFINITY;
+      if ((DENSE ? s_pre[b + 1] - s_pre[b] : row_live(r)) != 0) continue;
+      for (int h = warp; h < p.G; h += kWarps) {
+        const int64_t at = static_cast<int64_t>(b) * p.Hq + head * p.G + h;
+        *reinterpret_cast<uint2*>(p.O + at * kD + lane * 4) = make_uint2(0, 0);
+        if (p.LSE != nullptr && lane == 0) p.LSE[at] = -INFINITY;
+      }
     }
   }
 }
@@ -518,20 +584,25 @@ Params common_params(const Args& a, void* ws) {
 }
 
 template <bool DENSE>
-msa_status launch(const Params& p, int64_t most_units, int scratch_zeroed, cudaStream_t stream) {
-  DeviceInfo dev;
-  if (msa_status st = current_device(&dev); st != MSA_OK) return st;
+msa_status launch(const Params& p, int grid, int scratch_zeroed, cudaStream_t stream) {
   if (!scratch_zeroed) {   // otherwise zero by contract (every error-free call leaves them zero)
     const cudaError_t e = cudaMemsetAsync(p.counter, 0, static_cast<size_t>(p.B) * p.Hkv * sizeof(int32_t), stream);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(4-bit decode row counters)");
   }
-  const int64_t room = std::min<int64_t>(static_cast<int64_t>(dev.num_sms) * kCtasPerSm, kMaxGrid);
-  const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(room, most_units)));
-  constexpr int smem = kWarps * std::max<int>(kStages * kTileBytes, kMaxG * kD * sizeof(float));
+  constexpr int warps = DENSE ? kDenseWarps : kSparseWarps;
+  constexpr int smem = warps * std::max<int>(kStages * kTileBytes, kMaxG * kD * sizeof(float));
   cudaError_t e = cudaFuncSetAttribute(attn_q4_kernel<DENSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(attn_q4)");
-  e = launch_early(attn_q4_kernel<DENSE>, grid, kThreads, smem, stream, p);
+  e = launch_early(attn_q4_kernel<DENSE>, grid, 32 * warps, smem, stream, p);
   if (e != cudaSuccess) return cuda_fail(e, "attn_q4_kernel launch");
+  return MSA_OK;
+}
+
+// CTAs of this many warps that run at once.
+msa_status room_for(int warps, int* room) {
+  DeviceInfo dev;
+  if (msa_status st = current_device(&dev); st != MSA_OK) return st;
+  *room = std::min(dev.num_sms * (kSmWarps / warps), kMaxGrid);
   return MSA_OK;
 }
 
@@ -542,16 +613,35 @@ size_t attn_decode_q4_workspace_size(int B, int Hkv) {
 }
 
 msa_status launch_sparse_decode_q4(const msa_decode_q4_args& a, void* ws, cudaStream_t stream) {
+  int room;
+  if (msa_status st = room_for(kSparseWarps, &room); st != MSA_OK) return st;
   Params p = common_params(a, ws);
   p.k = a.k;
   p.pt = a.pt; p.n = a.n; p.last_len = a.last_len;
-  return launch<false>(p, static_cast<int64_t>(a.B) * a.Hkv * a.k, a.scratch_zeroed, stream);
+  const int rows = a.B * a.Hkv;
+  int grid = room;
+  if (rows <= room) {
+    // Few rows: each is cut into equal parts, as many as there are CTAs for, so that no CTA has pages of two
+    // rows (32 pages of 64 rows in runs of 7 units, most of them across two rows: 20.6 us; in equal parts: 16.2).
+    const int per = (a.k + room / rows - 1) / (room / rows);
+    const int parts = (a.k + per - 1) / per;
+    p.row_units = parts * per;
+    grid = rows * parts;
+  } else {
+    // Many rows: equal runs over the pages that the rows have, each row's change of pages counted as kRowCost
+    // more (192 sequences, a fifth of them short: 97.5 us with none, 84.0 with 2, 83.0 with 3, 84.7 with 4).
+    p.bin_rows = (rows + kSparseBins - 1) / kSparseBins;
+  }
+  return launch<false>(p, grid, a.scratch_zeroed, stream);
 }
 
 msa_status launch_dense_decode_q4(const msa_dense_decode_q4_args& a, void* ws, cudaStream_t stream) {
+  int room;
+  if (msa_status st = room_for(kDenseWarps, &room); st != MSA_OK) return st;
   Params p = common_params(a, ws);
   p.seq_pt = a.seq_pt; p.seq_len = a.seq_len; p.max_pages = a.max_pages;
-  return launch<true>(p, static_cast<int64_t>(a.B) * a.Hkv * a.max_pages, a.scratch_zeroed, stream);
+  const int64_t most = static_cast<int64_t>(a.B) * a.Hkv * a.max_pages;
+  return launch<true>(p, static_cast<int>(std::min<int64_t>(room, most)), a.scratch_zeroed, stream);
 }
 
 }  // namespace msa
