@@ -29,7 +29,8 @@ namespace msa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kStoreUnroll = 4;                             // tokens per thread
+constexpr int kStoreUnroll = 2;                             // tokens per thread
+constexpr int kStoreCtas = 6;                               // per SM
 constexpr int kStoreTokens = kThreads / 16 * kStoreUnroll;  // and per block
 constexpr int kExpandUnroll = 8;                            // half groups per thread and run
 constexpr unsigned kMaxGridY = 65535;
@@ -74,7 +75,7 @@ __device__ __forceinline__ void quantise16(const uint32_t (&u)[8], float inv, ui
   *scale = sf;
 }
 
-__global__ void __launch_bounds__(kThreads) append_q4_kernel(const StoreParams p) {
+__global__ void __launch_bounds__(kThreads, kStoreCtas) append_q4_kernel(const StoreParams p) {
   wait_for_stream();
   const int group = threadIdx.x & 7;
   const bool is_v = threadIdx.x >> 3 & 1;

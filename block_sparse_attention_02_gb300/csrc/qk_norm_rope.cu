@@ -26,7 +26,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCtasPerSm = 3;
-constexpr int kAhead = 4;                     // steps of 1 KiB per warp in shared memory
+constexpr int kAhead = 3;                     // steps of 1 KiB per warp in shared memory
 
 struct NormRopeParams {
   int64_t N, num_pages;
@@ -74,13 +74,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const N
   wait_for_stream();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane % kLanes, hl = lane / kLanes;
-  for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
-    const void* w = i < D ? p.q_weight : p.k_weight;
-    float x = 1.f;
-    if (w != nullptr)
-      x = p.weight_fp32 ? static_cast<const float*>(w)[i % D] : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i % D]);
-    s_weight[i / D][i % D] = x;
-  }
   const int half = p.rot >> 4;                // chunks of 8 values in each half of the rotated ones
   int c0, c1;                                 // this lane's chunks
   bool turn0, turn1;
@@ -94,18 +87,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const N
     c1 = sub < half ? sub + half : c0 + 1;
     turn0 = turn1 = sub < half;
   }
-  // turns per token, in units of 2^-64 turns, of pairs lane and lane + 32
-  uint64_t turns[D / 64];
-#pragma unroll
-  for (int e = 0; e < D / 64; ++e) {
-    turns[e] = 0;
-    if (lane + 32 * e < p.rot / 2) {
-      double t = static_cast<double>(p.inv_freq[lane + 32 * e]) * 0.15915494309189533577;   // 1 / (2 pi)
-      t -= floor(t);
-      turns[e] = __double2ull_rz(t * 18446744073709551616.0);
-    }
-  }
-  __syncthreads();
   const int q_steps = (p.Hq + kHeads - 1) / kHeads, k_steps = (p.Hkv + kHeads - 1) / kHeads;
   const int steps = q_steps + k_steps + (p.V != nullptr ? k_steps : 0);
   const int64_t items = p.N * p.parts, stride = static_cast<int64_t>(gridDim.x) * kWarps;
@@ -144,20 +125,40 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const N
   if (load_item < items) load_token();
 #pragma unroll
   for (int i = 0; i < kAhead - 1; ++i) fetch();
+  for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+    const void* w = i < D ? p.q_weight : p.k_weight;
+    float x = 1.f;
+    if (w != nullptr)
+      x = p.weight_fp32 ? static_cast<const float*>(w)[i % D] : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i % D]);
+    s_weight[i / D][i % D] = x;
+  }
+  // turns per token, in units of 2^-64 turns, of pairs lane and lane + 32
+  uint64_t turns[D / 64];
+#pragma unroll
+  for (int e = 0; e < D / 64; ++e) {
+    turns[e] = 0;
+    if (lane + 32 * e < p.rot / 2) {
+      double t = static_cast<double>(p.inv_freq[lane + 32 * e]) * 0.15915494309189533577;   // 1 / (2 pi)
+      t -= floor(t);
+      turns[e] = __double2ull_rz(t * 18446744073709551616.0);
+    }
+  }
+  __syncthreads();
 
   bool bad = false;
   for (int64_t item = item0; item < items; item += stride) {
     const int64_t n = p.parts == 1 ? item : item / p.parts;
     const int first = p.parts == 1 ? 0 : static_cast<int>(item - n * p.parts);
     const int pos = p.pos[n];
+    const bool store_q = pos >= 0;
     // where this token's key and value rows go
     int64_t k_row = n * p.ko0, v_row = 0;
-    bool store_kv = pos >= 0;
+    bool store_kv = store_q;
     if (p.slots != nullptr) {
       const int64_t slot = p.slots[n], page = slot / kBk;
       const int t = static_cast<int>(slot & (kBk - 1));
-      store_kv = pos >= 0 && slot >= 0 && page < p.num_pages;
-      bad |= pos >= 0 && slot >= 0 && page >= p.num_pages;
+      store_kv = store_q && slot >= 0 && page < p.num_pages;
+      bad |= store_q && slot >= 0 && page >= p.num_pages;
       k_row = page * p.ko0 + t * p.ko2;
       v_row = page * p.vo0 + t * p.vo2;
     }
@@ -188,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const N
       fetch();
       const bool is_q = step < q_steps, is_v = step >= q_steps + k_steps;
       const int head = (step - (is_q ? 0 : is_v ? q_steps + k_steps : q_steps)) * kHeads + hl;
-      const bool live = head < (is_q ? p.Hq : p.Hkv) && (is_q ? pos >= 0 : store_kv);
+      const bool live = head < (is_q ? p.Hq : p.Hkv) && (is_q ? store_q : store_kv);
       if (is_v) {                             // values go as they are
         if (live) {
           uint8_t* dst = p.V_out + v_row + head * p.vo1;
