@@ -25,6 +25,7 @@
 // run of it, its eight warps 32 tokens of every other page each, with a softmax
 // of their own that is joined in shared memory at the end of a row's part.  Rows
 // cut by a run's end go through the workspace; the CTA that arrives last joins them.
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
 #include <cfloat>
@@ -32,6 +33,8 @@
 #include "msa_internal.h"
 #include "msa_ptx.cuh"
 #include "q4.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace msa {
 namespace {
@@ -43,6 +46,7 @@ constexpr int kSmWarps = 16;                            // that the registers of
 constexpr int kStages = 3;                              // tiles of 32 tokens per warp in shared memory
 constexpr int kDenseBins = kDenseMaxBatch, kSparseBins = 256;   // that the pages are counted by
 constexpr int kRowCost = 3;                             // pages' time that a row's end and the next one's start take
+constexpr int kMaxParts = 4;                            // CTAs of a row up to which they form a cluster
 constexpr int kMaxGrid = 1024;                           // CTAs per launch at most (sizes the workspace)
 constexpr int kPart = kMaxG * kD + 2 * kMaxG;           // floats of a partial: O, m, l of eight heads
 constexpr float kLog2e = 1.4426950408889634f;
@@ -56,6 +60,7 @@ struct Params {
   // sparse: units of a row (k or a few more, the last ones without a page), or 0: each row has its own pages
   // and kRowCost more for units, counted by bins of bin_rows rows
   int row_units, bin_rows;
+  int parts;                            // sparse: CTAs of a row that form a cluster (0 or 1: none)
   float scale_log2, v_scale;
   const uint8_t* Q;
   int64_t q0, q1;                       // byte strides (b, h)
@@ -252,7 +257,7 @@ __global__ void __launch_bounds__(32 * (DENSE ? kDenseWarps : kSparseWarps), kSm
   constexpr int kRep = 8 / kWarps;          // of the joined outputs' eight parts, those of a warp
   extern __shared__ __align__(128) uint8_t s_ring[];
   float4(*s_o)[8][32] = reinterpret_cast<float4(*)[8][32]>(s_ring);   // after a row's part: [warp][i][lane]
-  __shared__ float s_m[kWarps][kMaxG], s_l[kWarps][kMaxG];
+  __shared__ __align__(8) float s_m[kWarps][kMaxG], s_l[kWarps][kMaxG];
   __shared__ int s_pre[kBins + 1];          // pages before a bin: a sequence (of one head; dense) or bin_rows rows
   __shared__ int s_wsum[kWarps];
   __shared__ int s_last;
@@ -476,6 +481,64 @@ __global__ void __launch_bounds__(32 * (DENSE ? kDenseWarps : kSparseWarps), kSm
 #pragma unroll
       for (int i = 0; i < kRep; ++i) add(o[i], f[0], f[1], s_o[w][warp + i * kWarps][lane]);
     }
+    // element [i][lane] of the row's outputs, of heads 2t, 2t + 1 for lane (g, t)
+    auto put = [&](int i, int ln, float4 v, const float* sum, const float* top) {
+      const float out[2][2] = {{v.x, v.z}, {v.y, v.w}};
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int h = 2 * (ln & 3) + c;
+        if (h >= p.G) break;
+        const int64_t at = static_cast<int64_t>(b) * p.Hq + head * p.G + h;
+        const float r = sum[c] == 0.f ? 0.f : p.v_scale / sum[c];
+        *reinterpret_cast<__nv_bfloat162*>(p.O + at * kD + 16 * (ln >> 2) + 2 * i) = __floats2bfloat162_rn(out[c][0] * r, out[c][1] * r);
+        if (p.LSE != nullptr && i == 0 && ln < 4)
+          p.LSE[at] = sum[c] == 0.f ? -INFINITY : (top[c] - kPShift + log2f(sum[c])) * kLn2;
+      }
+    };
+    if (!DENSE && p.parts > 1) {
+      // the row's parts are the CTAs of this cluster: joined through their shared memory, an equal share by each
+      cg::cluster_group cluster = cg::this_cluster();
+      const int parts = p.parts, rank = static_cast<int>(cluster.block_rank());
+      float4* mine = reinterpret_cast<float4*>(s_ring);
+      __syncthreads();                                   // the warps' outputs are read
+#pragma unroll
+      for (int i = 0; i < kRep; ++i) mine[tid + i * kThreads] = o[i];
+      if (warp == 0 && g == 0) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          s_m[0][2 * t + c] = M[c];
+          s_l[0][2 * t + c] = l[c];
+        }
+      }
+      cluster.sync();
+      const int item = tid * parts + rank;
+      if (item < 256) {
+        const int h0 = 2 * (item & 3);
+        float m[kMaxParts][2], top[2] = {kNoMax, kNoMax}, sum[2] = {0.f, 0.f};
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < kMaxParts; ++c) {
+          if (c >= parts) break;
+          const float2 x = *reinterpret_cast<const float2*>(cluster.map_shared_rank(&s_m[0][h0], c));
+          m[c][0] = x.x;
+          m[c][1] = x.y;
+          top[0] = fmaxf(top[0], x.x);
+          top[1] = fmaxf(top[1], x.y);
+        }
+#pragma unroll
+        for (int c = 0; c < kMaxParts; ++c) {
+          if (c >= parts) break;
+          const float f0 = ex2(m[c][0] - top[0]), f1 = ex2(m[c][1] - top[1]);
+          const float2 x = *reinterpret_cast<const float2*>(cluster.map_shared_rank(&s_l[0][h0], c));
+          sum[0] = fmaf(f0, x.x, sum[0]);
+          sum[1] = fmaf(f1, x.y, sum[1]);
+          add(v, f0, f1, *cluster.map_shared_rank(mine + item, c));
+        }
+        put(item >> 5, item & 31, v, sum, top);
+      }
+      cluster.sync();                                    // no CTA leaves while another reads its memory
+      return;
+    }
     const int first = static_cast<int>(row_first / per), last = static_cast<int>((row_first + row_pages - 1) / per);
     bool write = first == last;
     if (!write) {
@@ -528,18 +591,7 @@ __global__ void __launch_bounds__(32 * (DENSE ? kDenseWarps : kSparseWarps), kSm
     }
     if (write) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int h = 2 * t + c;
-        if (h >= p.G) break;
-        const int64_t at = static_cast<int64_t>(b) * p.Hq + head * p.G + h;
-        const float r = l[c] == 0.f ? 0.f : p.v_scale / l[c];
-#pragma unroll
-        for (int i = 0; i < kRep; ++i)
-          *reinterpret_cast<__nv_bfloat162*>(p.O + at * kD + 16 * g + 2 * (warp + i * kWarps)) =
-              c ? __floats2bfloat162_rn(o[i].y * r, o[i].w * r) : __floats2bfloat162_rn(o[i].x * r, o[i].z * r);
-        if (p.LSE != nullptr && warp == 0 && g == 0)
-          p.LSE[at] = l[c] == 0.f ? -INFINITY : (M[c] - kPShift + log2f(l[c])) * kLn2;
-      }
+      for (int i = 0; i < kRep; ++i) put(warp + i * kWarps, lane, o[i], l, M);
     }
     __syncthreads();
   }
@@ -593,7 +645,7 @@ msa_status launch(const Params& p, int grid, int scratch_zeroed, cudaStream_t st
   constexpr int smem = warps * std::max<int>(kStages * kTileBytes, kMaxG * kD * sizeof(float));
   cudaError_t e = cudaFuncSetAttribute(attn_q4_kernel<DENSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(attn_q4)");
-  e = launch_early(attn_q4_kernel<DENSE>, grid, 32 * warps, smem, stream, p);
+  e = launch_early(attn_q4_kernel<DENSE>, grid, 32 * warps, smem, stream, std::max(p.parts, 1), p);
   if (e != cudaSuccess) return cuda_fail(e, "attn_q4_kernel launch");
   return MSA_OK;
 }
@@ -621,11 +673,15 @@ msa_status launch_sparse_decode_q4(const msa_decode_q4_args& a, void* ws, cudaSt
   const int rows = a.B * a.Hkv;
   int grid = room;
   if (rows <= room) {
-    // Few rows: each is cut into equal parts, as many as there are CTAs for, so that no CTA has pages of two
-    // rows (32 pages of 64 rows in runs of 7 units, most of them across two rows: 20.6 us; in equal parts: 16.2).
-    const int per = (a.k + room / rows - 1) / (room / rows);
+    // Few rows: each is cut into equal parts, as many as there are CTAs for, so that no CTA has pages of two rows
+    // (32 pages of 64 rows in runs of 7 units, most of them across two rows: 20.6 us; in equal parts: 16.2).  Up
+    // to four parts are a cluster, which joins its row without the workspace (8 rows of 4 pages: 5.8 us
+    // for 6.4); a cluster's barrier grows with it, and at eight (6.8 us for 6.4) the workspace is as fast.
+    const int most = room / rows;
+    const int per = (a.k + most - 1) / most;
     const int parts = (a.k + per - 1) / per;
     p.row_units = parts * per;
+    p.parts = parts <= kMaxParts ? parts : 1;
     grid = rows * parts;
   } else {
     // Many rows: equal runs over the pages that the rows have, each row's change of pages counted as kRowCost

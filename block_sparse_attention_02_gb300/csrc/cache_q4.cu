@@ -197,7 +197,7 @@ msa_status launch_append_q4(const msa_append_q4_args& a, cudaStream_t stream) {
   p.dev_err = a.dev_err;
   const dim3 grid(static_cast<unsigned>((a.N + kStoreTokens - 1) / kStoreTokens),
                   std::min<unsigned>(static_cast<unsigned>(a.Hkv), kMaxGridY));
-  const cudaError_t e = launch_early(append_q4_kernel, grid, kThreads, 0, stream, p);
+  const cudaError_t e = launch_early(append_q4_kernel, grid, kThreads, 0, stream, 1, p);
   if (e != cudaSuccess) return cuda_fail(e, "append_q4_kernel launch");
   return MSA_OK;
 }
@@ -217,7 +217,7 @@ msa_status launch_expand_q4(const msa_expand_q4_args& a, cudaStream_t stream) {
   p.k_scale = a.cache.k_scale; p.v_scale = a.cache.v_scale;
   p.dev_err = a.dev_err;
   const dim3 grid(static_cast<unsigned>(a.n), std::min<unsigned>(static_cast<unsigned>(a.Hkv), kMaxGridY));
-  const cudaError_t e = launch_early(expand_q4_kernel, grid, kThreads, 0, stream, p);
+  const cudaError_t e = launch_early(expand_q4_kernel, grid, kThreads, 0, stream, 1, p);
   if (e != cudaSuccess) return cuda_fail(e, "expand_q4_kernel launch");
   return MSA_OK;
 }

@@ -268,24 +268,7 @@ msa_status launch_rows(void (*kernel)(const Args, const bool), const Args& a, in
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return cuda_fail(e, what);
   }
-  cudaError_t e;
-  if (in_place && ctas > 1) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ctas;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kernel, a, true);
-  } else {
-    e = launch_early(kernel, ctas, threads, smem, stream, a, false);
-  }
+  const cudaError_t e = launch_early(kernel, ctas, threads, smem, stream, in_place ? ctas : 1, a, in_place);
   if (e != cudaSuccess) return cuda_fail(e, what);
   return MSA_OK;
 }

@@ -277,11 +277,11 @@ msa_status launch_qk_norm_rope(const msa_norm_rope_args& a, cudaStream_t stream)
       static_cast<unsigned>(std::min<int64_t>((items + kWarps - 1) / kWarps, static_cast<int64_t>(dev.num_sms) * kCtasPerSm));
   cudaError_t e;
   if (a.D == 128) {
-    if (a.interleaved) e = launch_early(norm_rope_kernel<128, true>, grid, kThreads, 0, stream, p);
-    else e = launch_early(norm_rope_kernel<128, false>, grid, kThreads, 0, stream, p);
+    if (a.interleaved) e = launch_early(norm_rope_kernel<128, true>, grid, kThreads, 0, stream, 1, p);
+    else e = launch_early(norm_rope_kernel<128, false>, grid, kThreads, 0, stream, 1, p);
   } else {
-    if (a.interleaved) e = launch_early(norm_rope_kernel<64, true>, grid, kThreads, 0, stream, p);
-    else e = launch_early(norm_rope_kernel<64, false>, grid, kThreads, 0, stream, p);
+    if (a.interleaved) e = launch_early(norm_rope_kernel<64, true>, grid, kThreads, 0, stream, 1, p);
+    else e = launch_early(norm_rope_kernel<64, false>, grid, kThreads, 0, stream, 1, p);
   }
   if (e != cudaSuccess) return cuda_fail(e, "norm_rope_kernel launch");
   return MSA_OK;
