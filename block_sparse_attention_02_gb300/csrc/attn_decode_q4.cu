@@ -39,12 +39,13 @@ namespace cg = cooperative_groups;
 namespace msa {
 namespace {
 
-// Warps of a CTA: eight for long rows; four for rows of few pages, where twice as many CTAs leave an SM
-// less idle while one of them ends a row and waits for the next one's first pages.
-constexpr int kDenseWarps = 8, kSparseWarps = 4;
+// Warps of a CTA: four, and for few long rows eight.  With four, twice as many CTAs leave an SM less idle while one
+// of them ends a row and waits for the next one's first pages (64 sequences of 1 to 2,000 tokens 23.6 -> 15.8
+// us); with eight a row that many CTAs share has half as many parts (1,048,576 tokens 214 -> 202 us).
+constexpr int kFew = 4, kMany = 8;
 constexpr int kSmWarps = 16;                            // that the registers of an SM hold
 constexpr int kStages = 3;                              // tiles of 32 tokens per warp in shared memory
-constexpr int kDenseBins = kDenseMaxBatch, kSparseBins = 256;   // that the pages are counted by
+constexpr int kBins = 256;                              // that the units are counted by
 constexpr int kRowCost = 3;                             // pages' time that a row's end and the next one's start take
 constexpr int kMaxParts = 4;                            // CTAs of a row up to which they form a cluster
 constexpr int kMaxGrid = 1024;                           // CTAs per launch at most (sizes the workspace)
@@ -57,9 +58,9 @@ constexpr float kPMost = 32768.f;                       // most of a lane's sum 
 
 struct Params {
   int B, Hq, Hkv, G, k;
-  // sparse: units of a row (k or a few more, the last ones without a page), or 0: each row has its own pages
-  // and kRowCost more for units, counted by bins of bin_rows rows
-  int row_units, bin_rows;
+  // Units of a row: row_units for every one (sparse, few rows; k or a few more, the last ones without a page), or 0:
+  // each row's own pages and row_cost more, counted by bins of bin_size sequences (dense) or rows (sparse).
+  int row_units, bin_size, row_cost;
   int parts;                            // sparse: CTAs of a row that form a cluster (0 or 1: none)
   float scale_log2, v_scale;
   const uint8_t* Q;
@@ -248,11 +249,9 @@ __device__ __forceinline__ void attend_tile(const uint32_t (&q)[16], const float
   }
 }
 
-template <bool DENSE>
-__global__ void __launch_bounds__(32 * (DENSE ? kDenseWarps : kSparseWarps), kSmWarps / (DENSE ? kDenseWarps : kSparseWarps))
-    attn_q4_kernel(const Params p) {
-  constexpr int kWarps = DENSE ? kDenseWarps : kSparseWarps, kThreads = 32 * kWarps;
-  constexpr int kBins = DENSE ? kDenseBins : kSparseBins;
+template <bool DENSE, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, kSmWarps / kWarps) attn_q4_kernel(const Params p) {
+  constexpr int kThreads = 32 * kWarps;
   constexpr int kTeams = kWarps / 4;        // four warps share a page, 32 tokens each; the teams alternate pages
   constexpr int kRep = 8 / kWarps;          // of the joined outputs' eight parts, those of a warp
   extern __shared__ __align__(128) uint8_t s_ring[];
@@ -265,29 +264,30 @@ __global__ void __launch_bounds__(32 * (DENSE ? kDenseWarps : kSparseWarps), kSm
   const int rows = p.B * p.Hkv;
   wait_for_stream();
 
-  auto row_live = [&](int r) { return min(max(p.n[r], 0), p.k); };   // sparse: pages of a row
-  auto row_units = [&](int r) {             // and its units where rows are counted
-    const int live = row_live(r);
-    return live > 0 ? live + kRowCost : 0;
+  // pages of one head of sequence x (dense) or of row x (sparse), and its units where they are counted
+  auto pages_of = [&](int x) {
+    if (!DENSE) return min(max(p.n[x], 0), p.k);
+    const int L = p.seq_len[x];
+    return L < 0 || L > p.max_pages * kBk ? 0 : (L + kBk - 1) / kBk;
   };
-  const int bins = DENSE ? p.B : p.bin_rows > 0 ? (rows + p.bin_rows - 1) / p.bin_rows : 0;
+  auto units_of = [&](int x) {
+    const int pages = pages_of(x);
+    return pages > 0 ? pages + p.row_cost : 0;
+  };
+  const int counted = DENSE ? p.B : rows, per_item = DENSE ? p.Hkv : 1;
+  const int bins = p.row_units > 0 ? 0 : (counted + p.bin_size - 1) / p.bin_size;
   if (bins > 0) {
-    constexpr int kPer = kBins / kThreads;
+    constexpr int kPer = (kBins + kThreads - 1) / kThreads;
     int mine[kPer], sum = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int b = tid * kPer + i;
       mine[i] = 0;
       if (b < bins) {
-        if (DENSE) {
-          const int L = p.seq_len[b];
-          if (L < 0 || L > p.max_pages * kBk) {
-            if (blockIdx.x == 0) report(p.dev_err, MSA_DEVERR_BAD_LEN);
-          } else {
-            mine[i] = (L + kBk - 1) / kBk;
-          }
-        } else {
-          for (int r = b * p.bin_rows; r < min(rows, (b + 1) * p.bin_rows); ++r) mine[i] += row_units(r);
+        for (int x = b * p.bin_size; x < min(counted, (b + 1) * p.bin_size); ++x) {
+          mine[i] += units_of(x);
+          if (DENSE && blockIdx.x == 0 && (p.seq_len[x] < 0 || p.seq_len[x] > p.max_pages * kBk))
+            report(p.dev_err, MSA_DEVERR_BAD_LEN);
         }
       }
       sum += mine[i];
@@ -311,17 +311,7 @@ __global__ void __launch_bounds__(32 * (DENSE ? kDenseWarps : kSparseWarps), kSm
     if (tid == kThreads - 1 && bins == kBins) s_pre[bins] = before;
     __syncthreads();
   }
-  auto bin_of = [&](int64_t u, int heads) {   // last bin whose units start at or before u
-    int x = 0, y = bins;
-    while (y - x > 1) {
-      const int mid = (x + y) >> 1;
-      if (static_cast<int64_t>(s_pre[mid]) * heads <= u) x = mid; else y = mid;
-    }
-    return x;
-  };
-  const int64_t units = DENSE      ? static_cast<int64_t>(s_pre[bins]) * p.Hkv
-                        : bins > 0 ? s_pre[bins]
-                                   : static_cast<int64_t>(rows) * p.row_units;
+  const int64_t units = bins > 0 ? static_cast<int64_t>(s_pre[bins]) * per_item : static_cast<int64_t>(rows) * p.row_units;
   const int64_t per = (units + gridDim.x - 1) / gridDim.x;
   const int64_t lo = min(units, static_cast<int64_t>(blockIdx.x) * per), hi = min(units, lo + per);
 
@@ -329,31 +319,34 @@ __global__ void __launch_bounds__(32 * (DENSE ? kDenseWarps : kSparseWarps), kSm
     // the part of a row that starts at unit u: pages p0 .. p1 of its list
     int b, head, p0, row_pages, tokens;
     const int32_t* list;
+    int item, rem;                          // sequence (dense) or row (sparse), and the unit within it
+    if (bins > 0) {
+      int x = 0, y = bins;                  // the last bin whose units start at or before u
+      while (y - x > 1) {
+        const int mid = (x + y) >> 1;
+        if (static_cast<int64_t>(s_pre[mid]) * per_item <= u) x = mid; else y = mid;
+      }
+      item = x * p.bin_size;
+      rem = static_cast<int>(u - static_cast<int64_t>(s_pre[x]) * per_item);
+      for (row_pages = units_of(item); rem >= row_pages * per_item; row_pages = units_of(++item)) rem -= row_pages * per_item;
+    } else {
+      item = static_cast<int>(u / p.row_units);
+      rem = static_cast<int>(u - static_cast<int64_t>(item) * p.row_units);
+      row_pages = p.row_units;
+    }
     if (DENSE) {
-      b = bin_of(u, p.Hkv);
-      row_pages = s_pre[b + 1] - s_pre[b];
-      const int rem = static_cast<int>(u - static_cast<int64_t>(s_pre[b]) * p.Hkv);
+      b = item;
       head = rem / row_pages;
       p0 = rem - head * row_pages;
       tokens = p.seq_len[b];
       list = p.seq_pt + b * p.max_pages;
     } else {
-      int r;
-      if (bins > 0) {
-        const int x = bin_of(u, 1);
-        r = x * p.bin_rows;
-        p0 = static_cast<int>(u - s_pre[x]);
-        for (row_pages = row_units(r); p0 >= row_pages; row_pages = row_units(++r)) p0 -= row_pages;
-      } else {
-        r = static_cast<int>(u / p.row_units);
-        p0 = static_cast<int>(u - static_cast<int64_t>(r) * p.row_units);
-        row_pages = p.row_units;
-      }
-      b = r / p.Hkv;
-      head = r - b * p.Hkv;
-      const int nr = row_live(r);
-      tokens = nr == 0 ? 0 : (nr - 1) * kBk + min(max(p.last_len[r], 0), kBk);
-      list = p.pt + static_cast<int64_t>(r) * p.k;
+      b = item / p.Hkv;
+      head = item - b * p.Hkv;
+      p0 = rem;
+      const int live = pages_of(item);
+      tokens = live == 0 ? 0 : (live - 1) * kBk + min(max(p.last_len[item], 0), kBk);
+      list = p.pt + static_cast<int64_t>(item) * p.k;
     }
     const int row = b * p.Hkv + head;
     const int p1 = static_cast<int>(min(static_cast<int64_t>(row_pages), p0 + hi - u));
@@ -368,7 +361,7 @@ __global__ void __launch_bounds__(32 * (DENSE ? kDenseWarps : kSparseWarps), kSm
                       (lane < 16 ? p.K_scales : p.V_scales) + head * p.s1 + tok0 * 8 + (lane & 15) * 16};
     uint8_t* ring = s_ring + warp * (kStages * kTileBytes);
     // lane i: page of the i-th of the present run of 32 (known before the row's length, so both loads go together)
-    const int listed = DENSE ? p1 : min(p1, p.k);
+    const int listed = min(p1, DENSE ? static_cast<int>(p.max_pages) : p.k);
     int32_t ids = j0 + kTeams * lane < listed ? list[j0 + kTeams * lane] : -1;
     uint4 raw[4];
 #pragma unroll
@@ -562,29 +555,76 @@ __global__ void __launch_bounds__(32 * (DENSE ? kDenseWarps : kSparseWarps), kSm
       write = s_last != 0;
       if (write) {
         __threadfence();
+        // all parts of the row, 64 at a time: lane (g, t) takes m and l of parts g, g + 8, .. in one batch of
+        // loads, and each lane its share of O eight parts deep
         M[0] = M[1] = kNoMax;
-        for (int c = first + g; c <= last; c += 8) {     // eight parts at a time, by g
-          const float2 m = __ldcg(reinterpret_cast<const float2*>(part_of(c) + kMaxG * kD) + t);
-          M[0] = fmaxf(M[0], m.x);
-          M[1] = fmaxf(M[1], m.y);
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int i = 4; i < 32; i <<= 1) M[c] = fmaxf(M[c], __shfl_xor_sync(0xffffffffu, M[c], i));
         l[0] = l[1] = 0.f;
 #pragma unroll
         for (int i = 0; i < kRep; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int c = first; c <= last; ++c) {
-          const float* x = part_of(c);
-          const float2 m = __ldcg(reinterpret_cast<const float2*>(x + kMaxG * kD) + t);
-          const float2 lc = __ldcg(reinterpret_cast<const float2*>(x + kMaxG * kD + kMaxG) + t);
-          const float f0 = ex2(m.x - M[0]), f1 = ex2(m.y - M[1]);
-          l[0] = fmaf(f0, lc.x, l[0]);
-          l[1] = fmaf(f1, lc.y, l[1]);
+        for (int c0 = first; c0 <= last; c0 += 64) {
+          float2 m[8], sum[8];
+          float top[2] = {M[0], M[1]};
 #pragma unroll
-          for (int i = 0; i < kRep; ++i) add(o[i], f0, f1, __ldcg(reinterpret_cast<const float4*>(x) + tid + i * kThreads));
+          for (int k = 0; k < 8; ++k) {
+            const int c = c0 + g + 8 * k;
+            m[k] = make_float2(kNoMax, kNoMax);
+            sum[k] = make_float2(0.f, 0.f);
+            if (c <= last) {
+              m[k] = __ldcg(reinterpret_cast<const float2*>(part_of(c) + kMaxG * kD) + t);
+              sum[k] = __ldcg(reinterpret_cast<const float2*>(part_of(c) + kMaxG * kD + kMaxG) + t);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            top[0] = fmaxf(top[0], m[k].x);
+            top[1] = fmaxf(top[1], m[k].y);
+          }
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+#pragma unroll
+            for (int i = 4; i < 32; i <<= 1) top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], i));
+          }
+          const float s0 = ex2(M[0] - top[0]), s1 = ex2(M[1] - top[1]);
+          M[0] = top[0];
+          M[1] = top[1];
+          float part_l[2] = {0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {      // m becomes the part's factor
+            m[k].x = ex2(m[k].x - top[0]);
+            m[k].y = ex2(m[k].y - top[1]);
+            part_l[0] = fmaf(m[k].x, sum[k].x, part_l[0]);
+            part_l[1] = fmaf(m[k].y, sum[k].y, part_l[1]);
+          }
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+#pragma unroll
+            for (int i = 4; i < 32; i <<= 1) part_l[c] += __shfl_xor_sync(0xffffffffu, part_l[c], i);
+          }
+          l[0] = fmaf(l[0], s0, part_l[0]);
+          l[1] = fmaf(l[1], s1, part_l[1]);
+#pragma unroll
+          for (int i = 0; i < kRep; ++i) o[i] = make_float4(o[i].x * s0, o[i].y * s1, o[i].z * s0, o[i].w * s1);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            constexpr int kDeep = 8;
+            if (c0 + 8 * k > last) break;
+            float4 v[kDeep][kRep];
+#pragma unroll
+            for (int x = 0; x < kDeep; ++x)
+#pragma unroll
+              for (int i = 0; i < kRep; ++i) {
+                v[x][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (c0 + 8 * k + x <= last)
+                  v[x][i] = __ldcg(reinterpret_cast<const float4*>(part_of(c0 + 8 * k + x)) + tid + i * kThreads);
+              }
+#pragma unroll
+            for (int x = 0; x < kDeep; ++x) {
+              const int from = x * 4 + t;
+              const float f0 = __shfl_sync(0xffffffffu, m[k].x, from), f1 = __shfl_sync(0xffffffffu, m[k].y, from);
+#pragma unroll
+              for (int i = 0; i < kRep; ++i) add(o[i], f0, f1, v[x][i]);
+            }
+          }
         }
         if (tid == 0) p.counter[row] = 0;
       }
@@ -599,7 +639,7 @@ __global__ void __launch_bounds__(32 * (DENSE ? kDenseWarps : kSparseWarps), kSm
   if (bins > 0) {          // rows without a page have no units
     for (int r = blockIdx.x; r < rows; r += gridDim.x) {
       const int b = r / p.Hkv, head = r - b * p.Hkv;
-      if ((DENSE ? s_pre[b + 1] - s_pre[b] : row_live(r)) != 0) continue;
+      if (pages_of(DENSE ? b : r) != 0) continue;
       for (int h = warp; h < p.G; h += kWarps) {
         const int64_t at = static_cast<int64_t>(b) * p.Hq + head * p.G + h;
         *reinterpret_cast<uint2*>(p.O + at * kD + lane * 4) = make_uint2(0, 0);
@@ -635,17 +675,16 @@ Params common_params(const Args& a, void* ws) {
   return p;
 }
 
-template <bool DENSE>
+template <bool DENSE, int kWarps>
 msa_status launch(const Params& p, int grid, int scratch_zeroed, cudaStream_t stream) {
   if (!scratch_zeroed) {   // otherwise zero by contract (every error-free call leaves them zero)
     const cudaError_t e = cudaMemsetAsync(p.counter, 0, static_cast<size_t>(p.B) * p.Hkv * sizeof(int32_t), stream);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(4-bit decode row counters)");
   }
-  constexpr int warps = DENSE ? kDenseWarps : kSparseWarps;
-  constexpr int smem = warps * std::max<int>(kStages * kTileBytes, kMaxG * kD * sizeof(float));
-  cudaError_t e = cudaFuncSetAttribute(attn_q4_kernel<DENSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  constexpr int smem = kWarps * std::max<int>(kStages * kTileBytes, kMaxG * kD * sizeof(float));
+  cudaError_t e = cudaFuncSetAttribute(attn_q4_kernel<DENSE, kWarps>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(attn_q4)");
-  e = launch_early(attn_q4_kernel<DENSE>, grid, 32 * warps, smem, stream, std::max(p.parts, 1), p);
+  e = launch_early(attn_q4_kernel<DENSE, kWarps>, grid, 32 * kWarps, smem, stream, std::max(p.parts, 1), p);
   if (e != cudaSuccess) return cuda_fail(e, "attn_q4_kernel launch");
   return MSA_OK;
 }
@@ -666,7 +705,7 @@ size_t attn_decode_q4_workspace_size(int B, int Hkv) {
 
 msa_status launch_sparse_decode_q4(const msa_decode_q4_args& a, void* ws, cudaStream_t stream) {
   int room;
-  if (msa_status st = room_for(kSparseWarps, &room); st != MSA_OK) return st;
+  if (msa_status st = room_for(kFew, &room); st != MSA_OK) return st;
   Params p = common_params(a, ws);
   p.k = a.k;
   p.pt = a.pt; p.n = a.n; p.last_len = a.last_len;
@@ -686,18 +725,25 @@ msa_status launch_sparse_decode_q4(const msa_decode_q4_args& a, void* ws, cudaSt
   } else {
     // Many rows: equal runs over the pages that the rows have, each row's change of pages counted as kRowCost
     // more (192 sequences, a fifth of them short: 97.5 us with none, 84.0 with 2, 83.0 with 3, 84.7 with 4).
-    p.bin_rows = (rows + kSparseBins - 1) / kSparseBins;
+    p.bin_size = (rows + kBins - 1) / kBins;
+    p.row_cost = kRowCost;
   }
-  return launch<false>(p, grid, a.scratch_zeroed, stream);
+  return launch<false, kFew>(p, grid, a.scratch_zeroed, stream);
 }
 
 msa_status launch_dense_decode_q4(const msa_dense_decode_q4_args& a, void* ws, cudaStream_t stream) {
-  int room;
-  if (msa_status st = room_for(kDenseWarps, &room); st != MSA_OK) return st;
+  int few, many;
+  if (msa_status st = room_for(kFew, &few); st != MSA_OK) return st;
+  if (msa_status st = room_for(kMany, &many); st != MSA_OK) return st;
   Params p = common_params(a, ws);
   p.seq_pt = a.seq_pt; p.seq_len = a.seq_len; p.max_pages = a.max_pages;
-  const int64_t most = static_cast<int64_t>(a.B) * a.Hkv * a.max_pages;
-  return launch<true>(p, static_cast<int>(std::min<int64_t>(room, most)), a.scratch_zeroed, stream);
+  p.bin_size = (a.B + kBins - 1) / kBins;
+  const int64_t rows = static_cast<int64_t>(a.B) * a.Hkv;
+  if (rows > many) {       // rows enough for all CTAs: their ends count (the lengths are on the device)
+    p.row_cost = kRowCost;
+    return launch<true, kFew>(p, few, a.scratch_zeroed, stream);
+  }
+  return launch<true, kMany>(p, static_cast<int>(std::min<int64_t>(many, rows * a.max_pages)), a.scratch_zeroed, stream);
 }
 
 }  // namespace msa

@@ -343,7 +343,8 @@ def check_rows(Q, O, LSE, pages_of, tokens_of, c, scale=None):
 
 
 @pytest.mark.parametrize("B,Hq,Hkv,k", [(1, 8, 8, 16), (1, 1, 1, 1), (3, 12, 2, 16), (8, 48, 8, 16), (5, 6, 2, 64), (2, 10, 2, 7),
-                                        (70, 14, 2, 3), (40, 32, 4, 16)])
+                                        (70, 14, 2, 3), (40, 32, 4, 16), (700, 4, 2, 5), (1300, 3, 1, 2),
+                                        (300, 5, 1, 64), (1, 8, 1, 64), (2, 6, 6, 33)])
 def test_sparse_decode_q4(msa, B, Hq, Hkv, k):
     r = np.random.default_rng(B * 100 + k)
     P = max(2 * k, 40)
@@ -377,6 +378,11 @@ DENSE = {
     "gqa8": ([9000, 0, 640, 3], 16, 2),
     "gqa1": ([300, 4100, 777], 3, 3),
     "many": ([(37 * i) % 700 for i in range(150)], 8, 4),
+    "b600": ([(53 * i) % 401 for i in range(600)], 3, 1),
+    "b1024": ([(i % 3) * ((17 * i) % 260) for i in range(1024)], 2, 1),
+    "one_long_of_many": ([3] * 200 + [30000] + [0] * 50 + [129] * 100, 2, 1),
+    "all_empty": ([0] * 40, 6, 2),
+    "two_long": ([50000, 21], 4, 2),
 }
 
 
