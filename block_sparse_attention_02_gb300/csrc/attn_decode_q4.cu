@@ -91,6 +91,12 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The low half of each byte of a and the high half of b's, in one instruction (written out, it takes two).
+__device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xE4;" : "=r"(r) : "r"(a), "r"(b), "r"(0x0f0f0f0fu));
+  return r;
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -235,12 +241,11 @@ __device__ __forceinline__ void attend_tile(const uint32_t (&q)[16], const float
       // the codes of two tokens side by side: even and odd channels' bytes (token, next token)
       const uint32_t a = w ? v[0].y : v[0].x, b = w ? v[1].y : v[1].x;
       const uint32_t c = w ? v[2].y : v[2].x, d = w ? v[3].y : v[3].x;
-      constexpr uint32_t kLow = 0x0f0f0f0fu;
       __half2 even01[4], odd01[4], even23[4], odd23[4];
-      e2m1x8_to_half2((a & kLow) | ((b << 4) & ~kLow), even01);
-      e2m1x8_to_half2(((a >> 4) & kLow) | (b & ~kLow), odd01);
-      e2m1x8_to_half2((c & kLow) | ((d << 4) & ~kLow), even23);
-      e2m1x8_to_half2(((c >> 4) & kLow) | (d & ~kLow), odd23);
+      e2m1x8_to_half2(low_halves(a, b << 4), even01);
+      e2m1x8_to_half2(low_halves(a >> 4, b), odd01);
+      e2m1x8_to_half2(low_halves(c, d << 4), even23);
+      e2m1x8_to_half2(low_halves(c >> 4, d), odd23);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         mma16816(st->acc[w * 4 + i], h2u(__hmul2(even01[i], s01)), h2u(__hmul2(odd01[i], s01)),
