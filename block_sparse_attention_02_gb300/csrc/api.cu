@@ -548,8 +548,9 @@ static msa_status check_q4(const msa_q4_cache& c, int Hkv, int D, int Bk) {
   MSA_REQUIRE(aligned16(c.K_codes) && aligned16(c.K_scales) && aligned16(c.V_codes) && aligned16(c.V_scales),
               MSA_ERR_INVALID_ARG, "the cache's codes and scales must be 16-byte aligned");
   for (int i = 0; i < 2; ++i)
-    MSA_REQUIRE(vec_stride_ok(c.code_stride[i], 1) && vec_stride_ok(c.scale_stride[i], 1), MSA_ERR_INVALID_ARG,
-                "the cache's strides must be positive multiples of 16 bytes");
+    MSA_REQUIRE(vec_stride_ok(c.code_stride[i], 1) && vec_stride_ok(c.scale_stride[i], 1) &&
+                    c.code_stride[i] < (int64_t(1) << 32) && c.scale_stride[i] < (int64_t(1) << 32),
+                MSA_ERR_INVALID_ARG, "the cache's strides must be positive multiples of 16 bytes below 2^32");
   MSA_REQUIRE(c.num_pages >= 1 && c.num_pages < (int64_t(1) << 31), MSA_ERR_INVALID_ARG, "num_pages = %" PRId64,
               c.num_pages);
   MSA_REQUIRE(power_of_two(c.k_scale) && power_of_two(c.v_scale), MSA_ERR_INVALID_ARG,

@@ -129,17 +129,25 @@ struct Bases {
   const uint8_t *kc, *vc, *scales;   // scales: K's in lanes 0-15, V's in lanes 16-31
 };
 
-__device__ __forceinline__ void fetch_tile(const Bases& at, int64_t code_off, int64_t scale_off, uint32_t dst, int lane) {
+// base + page * stride in one instruction (page strides lie below 2^32 bytes).
+__device__ __forceinline__ const uint8_t* page_at(const uint8_t* base, uint32_t page, uint32_t stride) {
+  uint64_t r;
+  asm("mad.wide.u32 %0, %1, %2, %3;" : "=l"(r) : "r"(page), "r"(stride), "l"(reinterpret_cast<uint64_t>(base)));
+  return reinterpret_cast<const uint8_t*>(r);
+}
+
+__device__ __forceinline__ void fetch_tile(const Bases& at, uint32_t page, uint32_t code_stride, uint32_t scale_stride,
+                                           uint32_t dst, int lane) {
   const uint32_t dk = dst + lane * 16;                                  // row lane / 4, chunk lane % 4
   const uint32_t dv = dst + kVAt + (lane ^ ((lane >> 4) << 1)) * 16;    // chunk ^ 2 in rows 4-7 of 8
-  const uint8_t* kc = at.kc + code_off;
-  const uint8_t* vc = at.vc + code_off;
+  const uint8_t* kc = page_at(at.kc, page, code_stride);
+  const uint8_t* vc = page_at(at.vc, page, code_stride);
 #pragma unroll
   for (int i = 0; i < kTile / 8; ++i) {
     copy16(dk + i * 512, kc + i * 512);
     copy16(dv + i * 512, vc + i * 512);
   }
-  copy16(dk + kKsAt, at.scales + scale_off);
+  copy16(dk + kKsAt, page_at(at.scales, page, scale_stride));
 }
 
 // The softmax state of a warp: lane (g, t) holds heads 2t and 2t + 1, of which
@@ -317,6 +325,8 @@ __global__ void __launch_bounds__(32 * kWarps, kSmWarps / kWarps) attn_q4_kernel
     __syncthreads();
   }
   const int64_t units = bins > 0 ? static_cast<int64_t>(s_pre[bins]) * per_item : static_cast<int64_t>(rows) * p.row_units;
+  const uint32_t pool_pages = static_cast<uint32_t>(p.num_pages);
+  const uint32_t code_stride = static_cast<uint32_t>(p.c0), scale_stride = static_cast<uint32_t>(p.s0);
   const int64_t per = (units + gridDim.x - 1) / gridDim.x;
   const int64_t lo = min(units, static_cast<int64_t>(blockIdx.x) * per), hi = min(units, lo + per);
 
@@ -374,18 +384,17 @@ __global__ void __launch_bounds__(32 * kWarps, kSmWarps / kWarps) attn_q4_kernel
       raw[i] = make_uint4(0, 0, 0, 0);
       if (g < p.G) raw[i] = *reinterpret_cast<const uint4*>(p.Q + b * p.q0 + (head * p.G + g) * p.q1 + t * 64 + i * 16);
     }
-    uint32_t good = 0;                      // bit n % 32: the n-th page has a valid id
+    uint32_t bad = 0;                       // bit n % 32: the n-th page has no valid id
     int into = 0, from = 0;                 // stages of the ring
     auto fetch = [&](int n) {
       if (n < count) {
         if ((n & 31) == 0 && n > 0) ids = j0 + kTeams * (n + lane) < listed ? list[j0 + kTeams * (n + lane)] : -1;
-        const int32_t page = __shfl_sync(0xffffffffu, ids, n & 31);
-        const uint32_t bit = 1u << (n & 31);
-        if (page >= 0 && page < p.num_pages) {
-          good |= bit;
-          fetch_tile(at, page * p.c0, page * p.s0, smem_u32(ring + into * kTileBytes), lane);
+        const uint32_t page = __shfl_sync(0xffffffffu, ids, n & 31);
+        if (page < pool_pages) {
+          if (bad != 0) bad &= ~(1u << (n & 31));
+          fetch_tile(at, page, code_stride, scale_stride, smem_u32(ring + into * kTileBytes), lane);
         } else {
-          good &= ~bit;
+          bad |= 1u << (n & 31);
           if (lane == 0) report(p.dev_err, MSA_DEVERR_BAD_PAGE);
         }
       }
@@ -430,12 +439,13 @@ __global__ void __launch_bounds__(32 * kWarps, kSmWarps / kWarps) attn_q4_kernel
     st.m[0] = st.m[1] = kNoMax;
     st.l[0] = st.l[1] = 0.f;
 
+    int valid = tokens - j0 * kBk - tok0;   // live tokens from the next tile's start on
     for (int n = 0; n < count; ++n) {
       copies_wait<kStages - 2>();
       __syncwarp();                         // every lane's share of tile n is there, and tile n - 1 is read
       fetch(n + kStages - 1);
-      if (good >> (n & 31) & 1)
-        attend_tile(q, coef, ring + from * kTileBytes, tokens - (j0 + kTeams * n) * kBk - tok0, g, t, &st);
+      if (bad == 0 || (bad >> (n & 31) & 1) == 0) attend_tile(q, coef, ring + from * kTileBytes, valid, g, t, &st);
+      valid -= kTeams * kBk;
       from = from + 1 == kStages ? 0 : from + 1;
     }
     copies_wait<0>();

@@ -675,7 +675,7 @@ msa_status msa_qk_norm_rope(const msa_norm_rope_args *args, msa_stream_t stream)
  * too) becomes the largest, a group that holds a NaN reads as NaN.
  * Pools: codes [num_pages, Hkv, Bk, D / 2] bytes, element 2i in the low half of
  * byte i; scales [num_pages, Hkv, Bk, D / 16] bytes; K's and V's share strides
- * (page, g), multiples of 16 bytes; a block's Bk rows are contiguous.
+ * (page, g), multiples of 16 bytes below 2^32; a block's Bk rows are contiguous.
  * k_scale and v_scale are powers of two in [2^-64, 2^64] (a quotient is then exact
  * enough in fp32 that codes never depend on its rounding); D = 128.
  * ------------------------------------------------------------------------ */

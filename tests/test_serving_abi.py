@@ -142,7 +142,7 @@ def test_refused(abi, fn, build, kw, status):
                                       ("msa_sparse_attn_decode_q4", sparse_args), ("msa_dense_attn_decode_q4", dense_args)])
 def test_cache_refused(abi, fn, build):
     for kw in (dict(k_scale=0.0), dict(k_scale=3.0), dict(v_scale=-1.0), dict(v_scale=float("inf")), dict(k_scale=float("nan")),
-               dict(k_scale=2.0 ** 65), dict(v_scale=2.0 ** -65), dict(code_stride=(16384, 8)), dict(scale_stride=(0, 1024)),
+               dict(k_scale=2.0 ** 65), dict(v_scale=2.0 ** -65), dict(code_stride=(16384, 8)), dict(scale_stride=(0, 1024)), dict(code_stride=(1 << 32, 8192)),
                dict(num_pages=0), dict(K_codes=None), dict(V_scales=FAKE + 8)):
         assert call(abi, fn, build(abi, cache=q4(abi, **kw))) == INV, kw
 
