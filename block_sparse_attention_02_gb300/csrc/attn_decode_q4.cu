@@ -157,7 +157,8 @@ struct State {
   float m[2], l[2];      // m the same in every g; l this lane's share
 };
 
-// valid: live tokens of the tile, from its start (any number, 32 and more: all).
+// WHOLE: every token of the tile is live; else the first `valid` of them.
+template <bool WHOLE>
 __device__ __forceinline__ void attend_tile(const uint32_t (&q)[16], const float (&coef)[2], const uint8_t* tile, int valid,
                                             int g, int t, State* st) {
   float s[2][4];
@@ -186,7 +187,7 @@ __device__ __forceinline__ void attend_tile(const uint32_t (&q)[16], const float
       mma16816(s[u], h2u(a[2]), h2u(b[2]), h2u(a[3]), h2u(b[3]), q[4 * i + 2], q[4 * i + 3]);
     }
   }
-  if (valid < kTile) {   // slots past the last token may hold anything, a NaN scale too
+  if (!WHOLE) {          // slots past the last token may hold anything, a NaN scale too
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -238,7 +239,7 @@ __device__ __forceinline__ void attend_tile(const uint32_t (&q)[16], const float
       v[i] = *reinterpret_cast<const uint2*>(tile + kVAt + tok * 64 + ((g * 8) ^ ((tok & 4) << 3)));
       sf[i] = tile[kVsAt + tok * 8 + g];
     }
-    if (valid < kTile) {
+    if (!WHOLE) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (u * 16 + token_of_row(2 * t + (i & 1)) + 8 * (i >> 1) >= valid) sf[i] = 0;
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(32 * kWarps, kSmWarps / kWarps) attn_q4_kernel
   __shared__ int s_pre[kBins + 1];          // pages before a bin: a sequence (of one head; dense) or bin_rows rows
   __shared__ int s_wsum[kWarps];
   __shared__ int s_last;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int rows = p.B * p.Hkv;
   wait_for_stream();
 
@@ -371,7 +372,8 @@ __global__ void __launch_bounds__(32 * kWarps, kSmWarps / kWarps) attn_q4_kernel
     // this warp's 32 tokens of its team's pages, kStages - 1 of them in flight
     const int tok0 = (warp & 3) * kTile, j0 = p0 + (warp >> 2);
     const int live = min(p1, (tokens - tok0 + kBk - 1) / kBk);   // pages before here have a token of this warp's
-    const int count = (live - j0 + kTeams - 1) / kTeams;
+    // (from lane 0: the compiler then knows that the warp goes one way)
+    const int count = __shfl_sync(0xffffffffu, (live - j0 + kTeams - 1) / kTeams, 0);
     const Bases at = {p.K_codes + head * p.c1 + tok0 * 64 + lane * 16, p.V_codes + head * p.c1 + tok0 * 64 + lane * 16,
                       (lane < 16 ? p.K_scales : p.V_scales) + head * p.s1 + tok0 * 8 + (lane & 15) * 16};
     uint8_t* ring = s_ring + warp * (kStages * kTileBytes);
@@ -439,15 +441,20 @@ __global__ void __launch_bounds__(32 * kWarps, kSmWarps / kWarps) attn_q4_kernel
     st.m[0] = st.m[1] = kNoMax;
     st.l[0] = st.l[1] = 0.f;
 
-    int valid = tokens - j0 * kBk - tok0;   // live tokens from the next tile's start on
-    for (int n = 0; n < count; ++n) {
+    // all tiles but a warp's last one of a row are whole
+    const int valid = tokens - (j0 + kTeams * (count - 1)) * kBk - tok0;   // live tokens from the last one's start on
+    const int whole = count - (count > 0 && valid < kTile ? 1 : 0);
+    auto next_tile = [&](int n) {           // waits for tile n and sends for the one kStages - 1 ahead; false: a bad page
       copies_wait<kStages - 2>();
       __syncwarp();                         // every lane's share of tile n is there, and tile n - 1 is read
       fetch(n + kStages - 1);
-      if (bad == 0 || (bad >> (n & 31) & 1) == 0) attend_tile(q, coef, ring + from * kTileBytes, valid, g, t, &st);
-      valid -= kTeams * kBk;
+      return bad == 0 || (bad >> (n & 31) & 1) == 0;
+    };
+    for (int n = 0; n < whole; ++n) {
+      if (next_tile(n)) attend_tile<true>(q, coef, ring + from * kTileBytes, kTile, g, t, &st);
       from = from + 1 == kStages ? 0 : from + 1;
     }
+    if (whole < count && next_tile(whole)) attend_tile<false>(q, coef, ring + from * kTileBytes, valid, g, t, &st);
     copies_wait<0>();
     __syncthreads();                        // the rings give way to the joined outputs
 
