@@ -44,7 +44,7 @@ namespace {
 // us); with eight a row that many CTAs share has half as many parts (1,048,576 tokens 214 -> 202 us).
 constexpr int kFew = 4, kMany = 8;
 constexpr int kSmWarps = 16;                            // that the registers of an SM hold
-constexpr int kStages = 3;                              // tiles of 32 tokens per warp in shared memory
+constexpr int kStages = 2;                              // tiles of 32 tokens per warp in shared memory (three: 3 % slower)
 constexpr int kBins = 256;                              // that the units are counted by
 constexpr int kRowCost = 3;                             // pages' time that a row's end and the next one's start take
 constexpr int kMaxParts = 4;                            // CTAs of a row up to which they form a cluster
@@ -120,6 +120,7 @@ __device__ __forceinline__ void copies_wait() {
 // for odd t) and these + 8.  With both, eight lanes that read 16 bytes of K, or
 // sixteen that read 8 of V, meet every bank once.
 constexpr int kTile = 32;
+static_assert(kStages == 2, "the stages alternate");
 constexpr int kVAt = kTile * 64, kKsAt = 2 * kVAt, kVsAt = kKsAt + kTile * 8, kTileBytes = kVsAt + kTile * 8;
 
 __device__ __forceinline__ int token_of_row(int m) { return m ^ ((m >> 1) & 1); }
@@ -387,20 +388,20 @@ __global__ void __launch_bounds__(32 * kWarps, kSmWarps / kWarps) attn_q4_kernel
       if (g < p.G) raw[i] = *reinterpret_cast<const uint4*>(p.Q + b * p.q0 + (head * p.G + g) * p.q1 + t * 64 + i * 16);
     }
     uint32_t bad = 0;                       // bit n % 32: the n-th page has no valid id
-    int into = 0, from = 0;                 // stages of the ring
+    int into = 0, from = 0;                 // byte offsets of the ring's next stages
     auto fetch = [&](int n) {
       if (n < count) {
         if ((n & 31) == 0 && n > 0) ids = j0 + kTeams * (n + lane) < listed ? list[j0 + kTeams * (n + lane)] : -1;
         const uint32_t page = __shfl_sync(0xffffffffu, ids, n & 31);
         if (page < pool_pages) {
           if (bad != 0) bad &= ~(1u << (n & 31));
-          fetch_tile(at, page, code_stride, scale_stride, smem_u32(ring + into * kTileBytes), lane);
+          fetch_tile(at, page, code_stride, scale_stride, smem_u32(ring + into), lane);
         } else {
           bad |= 1u << (n & 31);
           if (lane == 0) report(p.dev_err, MSA_DEVERR_BAD_PAGE);
         }
       }
-      into = into + 1 == kStages ? 0 : into + 1;
+      into = kTileBytes - into;
       copies_commit();
     };
 #pragma unroll
@@ -451,10 +452,10 @@ __global__ void __launch_bounds__(32 * kWarps, kSmWarps / kWarps) attn_q4_kernel
       return bad == 0 || (bad >> (n & 31) & 1) == 0;
     };
     for (int n = 0; n < whole; ++n) {
-      if (next_tile(n)) attend_tile<true>(q, coef, ring + from * kTileBytes, kTile, g, t, &st);
-      from = from + 1 == kStages ? 0 : from + 1;
+      if (next_tile(n)) attend_tile<true>(q, coef, ring + from, kTile, g, t, &st);
+      from = kTileBytes - from;
     }
-    if (whole < count && next_tile(whole)) attend_tile<false>(q, coef, ring + from * kTileBytes, valid, g, t, &st);
+    if (whole < count && next_tile(whole)) attend_tile<false>(q, coef, ring + from, valid, g, t, &st);
     copies_wait<0>();
     __syncthreads();                        // the rings give way to the joined outputs
 
