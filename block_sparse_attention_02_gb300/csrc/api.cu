@@ -148,7 +148,7 @@ msa_status msa::check_decode_args(const msa_decode_args* a) {
 
 extern "C" {
 
-int msa_version(void) { return 100; }
+int msa_version(void) { return 200; }
 
 const char* msa_last_error_string(void) { return g_last_error.c_str(); }
 
@@ -591,6 +591,7 @@ static msa_status check_attn_q4(int B, int max_B, int Hq, int Hkv, int D, int Bk
               B, max_B, Hq, Hkv);
   MSA_REQUIRE(Hq % Hkv == 0 && Hq / Hkv <= kMaxG, MSA_ERR_UNSUPPORTED, "GQA ratio Hq/Hkv = %d/%d not in 1..%d", Hq, Hkv,
               kMaxG);
+  MSA_REQUIRE(static_cast<int64_t>(B) * Hq < (int64_t(1) << 24), MSA_ERR_UNSUPPORTED, "B * Hq = %d * %d too large", B, Hq);
   if (msa_status st = check_q4(cache, Hkv, D, Bk); st != MSA_OK) return st;
   MSA_REQUIRE(B == 0 || (Q && O), MSA_ERR_INVALID_ARG, "Q and O must be non-NULL");
   MSA_REQUIRE(aligned16(Q) && aligned16(O), MSA_ERR_INVALID_ARG, "Q and O must be 16-byte aligned");

@@ -730,7 +730,8 @@ msa_status msa_cache_expand_q4(const msa_expand_q4_args *args, msa_stream_t stre
  * [0, num_pages): left out, MSA_DEVERR_BAD_PAGE.  LSE may be NULL.
  * Workspace: msa_attn_decode_q4_workspace_size(B, Hkv) bytes, 16-byte aligned,
  * the row counters first.  scratch_zeroed works as in msa_sparse_attn_decode.
- * Calls that overlap on the GPU need workspaces of their own.  B <= 4096. */
+ * Calls that overlap on the GPU need workspaces of their own.  B <= 4096,
+ * B * Hq < 2^24. */
 typedef struct msa_decode_q4_args {
     int B, Hq, Hkv, D, Bk, k;
     float softmax_scale;

@@ -117,6 +117,7 @@ REFUSED = [
     ("msa_cache_expand_q4", expand_args, dict(n=-1), INV), ("msa_cache_expand_q4", expand_args, dict(pages=None), INV),
     ("msa_cache_expand_q4", expand_args, dict(V_out=FAKE + 8), INV),
     ("msa_sparse_attn_decode_q4", sparse_args, dict(B=4097), INV), ("msa_sparse_attn_decode_q4", sparse_args, dict(k=65), UNS),
+    ("msa_sparse_attn_decode_q4", sparse_args, dict(B=4096, Hq=1 << 15, Hkv=1 << 13), UNS),
     ("msa_sparse_attn_decode_q4", sparse_args, dict(k=0), UNS), ("msa_sparse_attn_decode_q4", sparse_args, dict(Hq=18), UNS),
     ("msa_sparse_attn_decode_q4", sparse_args, dict(Hq=13), UNS), ("msa_sparse_attn_decode_q4", sparse_args, dict(D=64), UNS),
     ("msa_sparse_attn_decode_q4", sparse_args, dict(pt=None), INV), ("msa_sparse_attn_decode_q4", sparse_args, dict(O=None), INV),
@@ -125,6 +126,22 @@ REFUSED = [
     ("msa_dense_attn_decode_q4", dense_args, dict(max_pages=1 << 28), INV), ("msa_dense_attn_decode_q4", dense_args, dict(seq_len=None), INV),
     ("msa_dense_attn_decode_q4", dense_args, dict(Q=FAKE + 4), INV),
 ]
+
+
+def test_store_rounding_of_every_value():
+    """The store's fp32 steps against the definition, for every bf16 magnitude up to past the range under every scale:
+    x r + 1536 in one rounding, less 1536, then the nearest code; and amax / 6 as a product."""
+    import numpy as np
+    import serving_ref as ref
+    x = (np.arange(1, 0x7F80, dtype=np.uint32) << 16).view(np.float32)
+    for step in ref.E4M3[1:].astype(np.float32):
+        v = x[x <= step * np.float32(7.5)].astype(np.float64)
+        q = (v * np.float64(np.float32(1) / step) + 1536.0).astype(np.float32) - np.float32(1536)
+        assert np.array_equal(ref.nearest(ref.GRID, np.minimum(q.astype(np.float64), 6.0)),
+                              ref.nearest(ref.GRID, np.minimum(v / np.float64(step), 6.0))), step
+    a = x[x <= 2688]
+    assert np.array_equal(ref.nearest(ref.E4M3, (a * np.float32(1 / 6)).astype(np.float64)),
+                          ref.nearest(ref.E4M3, a.astype(np.float64) / 6))
 
 
 def call(abi, fn, a, ws_bytes=1 << 40, ws=FAKE):

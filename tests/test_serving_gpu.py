@@ -483,6 +483,54 @@ def test_decode_q4_bad_pages_and_lengths(msa):
     check_rows(Q, O, LSE, lambda b, g: pt[b], lambda b, g: T[b * Hkv + g], c)
 
 
+def test_q4_strided_pools_and_queries(msa):
+    """One layer's K and V of a pool that interleaves layers and sides, and Q as a slice of a projection: what dense
+    tensors give."""
+    P, Hkv, Hq, L = 12, 2, 12, [700, 333]
+    c = q4_pool(msa, P, Hkv, 15)
+    codes = torch.full((P, 3, 2, Hkv, BK, 64), 0xFF, dtype=torch.uint8, device="cuda")
+    scales = torch.full((P, 3, 2, Hkv, BK, 8), 0x7F, dtype=torch.uint8, device="cuda")
+    s = msa.Q4Cache(codes[:, 1, 0], scales[:, 1, 0], codes[:, 1, 1], scales[:, 1, 1], c.k_scale, c.v_scale)
+    every = torch.arange(P, dtype=torch.int32, device="cuda")
+    for a, b in zip(s[:4], c[:4]):
+        a.copy_(b)
+    pt = np.random.default_rng(3).permutation(P).reshape(2, 6)
+    wide = queries(2, Hq + 5, 16)
+    Q, ws = wide[:, 3:3 + Hq], workspace(msa, 2, Hkv)
+    want, got = outputs(2, Hq), outputs(2, Hq)
+    msa.msa_dense_attn_decode_q4(Q.contiguous(), c, i32(pt), i32(L), *want, ws)
+    msa.msa_dense_attn_decode_q4(Q, s, i32(pt), i32(L), *got, ws)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    K = queries(40, Hkv, 17, 1.0)
+    slots = torch.randperm(P * BK, device="cuda")[:40]
+    out = [[torch.empty(P, Hkv, BK, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)] for _ in range(2)]
+    for x, o in ((c, out[0]), (s, out[1])):
+        msa.msa_cache_append_q4(K, K, slots, x)
+        msa.msa_cache_expand_q4(x, every, *o)
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
+    assert (codes[:, [0, 2]] == 0xFF).all() and (scales[:, [0, 2]] == 0x7F).all()
+
+
+def test_decode_q4_on_two_streams_at_once(msa):
+    """Two attentions in flight with workspaces of their own, many times over: the bits of calls one by one."""
+    c = q4_pool(msa, 30, 2, 18)
+    pt, L = i32(np.arange(30).reshape(3, 10)), i32([1280, 900, 77])
+    Qs, ws, want = [queries(3, 12, 20 + i) for i in range(2)], [workspace(msa, 3, 2) for _ in range(2)], []
+    for i in range(2):
+        want.append(outputs(3, 12))
+        msa.msa_dense_attn_decode_q4(Qs[i], c, pt, L, *want[i], ws[i])
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [[outputs(3, 12) for _ in range(20)] for _ in range(2)]
+    torch.cuda.synchronize()
+    for r in range(20):
+        for i in range(2):
+            msa.msa_dense_attn_decode_q4(Qs[i], c, pt, L, *got[i][r], ws[i], stream=streams[i], scratch_zeroed=True)
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o in got[i]:
+            assert torch.equal(o[0], want[i][0]) and torch.equal(o[1], want[i][1])
+
+
 def test_decode_q4_far_pages(msa):
     """A pool whose last page lies past 2^32 bytes."""
     Hkv, P = 8, 68000                                            # 8192 code bytes a block: 4.46e9
