@@ -504,6 +504,7 @@ msa_status msa_qk_norm_rope(const msa_norm_rope_args* a, msa_stream_t stream) {
   MSA_REQUIRE(a->rot >= 0 && a->rot <= a->D && a->rot % 16 == 0, MSA_ERR_UNSUPPORTED,
               "rot = %d, supported multiples of 16 up to D = %d", a->rot, a->D);
   MSA_REQUIRE(a->eps >= 0.f && std::isfinite(a->eps), MSA_ERR_INVALID_ARG, "eps = %g", static_cast<double>(a->eps));
+  if (a->N == 0) return MSA_OK;
   MSA_REQUIRE(a->pos && a->Q && a->Q_out && (a->rot == 0 || a->inv_freq), MSA_ERR_INVALID_ARG,
               "pos, inv_freq, Q and Q_out must be non-NULL");
   MSA_REQUIRE(a->Hkv == 0 || (a->K && a->K_out), MSA_ERR_INVALID_ARG, "K and K_out must be non-NULL");
@@ -530,7 +531,6 @@ msa_status msa_qk_norm_rope(const msa_norm_rope_args* a, msa_stream_t stream) {
     MSA_REQUIRE(a->num_pages >= 1 && a->num_pages < (int64_t(1) << 31), MSA_ERR_INVALID_ARG, "num_pages = %" PRId64,
                 a->num_pages);
   }
-  if (a->N == 0) return MSA_OK;
   return launch_qk_norm_rope(*a, reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -679,7 +679,9 @@ __global__ void __launch_bounds__(32 * kWarps, kSmWarps / kWarps) attn_q4_kernel
   }
 }
 
-size_t counter_bytes(int B, int Hkv) { return (static_cast<size_t>(B) * Hkv * sizeof(int32_t) + 255) / 256 * 256; }
+// The workspace: the parts, then a counter per row.  The counters start at the same byte for every B and Hkv, so
+// that a call of one shape leaves those of another zero.
+constexpr size_t kPartBytes = static_cast<size_t>(kMaxGrid) * 2 * kPart * sizeof(float);
 
 template <class Args>
 Params common_params(const Args& a, void* ws) {
@@ -697,8 +699,8 @@ Params common_params(const Args& a, void* ws) {
   p.c0 = a.cache.code_stride[0]; p.c1 = a.cache.code_stride[1];
   p.s0 = a.cache.scale_stride[0]; p.s1 = a.cache.scale_stride[1];
   p.num_pages = a.cache.num_pages;
-  p.counter = static_cast<int32_t*>(ws);
-  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + counter_bytes(a.B, a.Hkv));
+  p.part = static_cast<float*>(ws);
+  p.counter = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + kPartBytes);
   p.O = static_cast<__nv_bfloat16*>(a.O);
   p.LSE = a.LSE;
   p.dev_err = a.dev_err;
@@ -730,7 +732,7 @@ msa_status room_for(int warps, int* room) {
 }  // namespace
 
 size_t attn_decode_q4_workspace_size(int B, int Hkv) {
-  return counter_bytes(B, Hkv) + static_cast<size_t>(kMaxGrid) * 2 * kPart * sizeof(float);
+  return kPartBytes + (static_cast<size_t>(B) * Hkv * sizeof(int32_t) + 255) / 256 * 256;
 }
 
 msa_status launch_sparse_decode_q4(const msa_decode_q4_args& a, void* ws, cudaStream_t stream) {

@@ -185,6 +185,18 @@ def test_empty_calls_enqueue_nothing(abi):
         assert call(abi, fn, a) == 0, fn
 
 
+def test_empty_calls_need_no_rows(abi):
+    """The pointer of an empty tensor is NULL."""
+    for fn, a, names in (("msa_qk_norm_rope", rope_args(abi, N=0), ("pos", "Q", "K", "Q_out")),
+                         ("msa_cache_append_q4", append_args(abi, N=0), ("K", "V", "slots")),
+                         ("msa_cache_expand_q4", expand_args(abi, n=0), ("pages", "K_out", "V_out")),
+                         ("msa_sparse_attn_decode_q4", sparse_args(abi, B=0), ("Q", "pt", "n", "last_len", "O", "LSE")),
+                         ("msa_dense_attn_decode_q4", dense_args(abi, B=0), ("Q", "seq_pt", "seq_len", "O", "LSE"))):
+        for name in names:
+            setattr(a, name, None)
+        assert call(abi, fn, a) == 0, fn
+
+
 # ---------------------------------------------------------------------------
 # the Python wrappers
 # ---------------------------------------------------------------------------

@@ -531,6 +531,41 @@ def test_decode_q4_on_two_streams_at_once(msa):
             assert torch.equal(o[0], want[i][0]) and torch.equal(o[1], want[i][1])
 
 
+def test_decode_q4_workspace_of_several_shapes(msa):
+    """One zero-filled workspace of the largest size, calls of both kinds and several shapes in turn."""
+    c, ws = q4_pool(msa, 60, 4, 21), workspace(msa, 64, 4)
+    calls = []
+    for B, seed in ((3, 1), (1, 2), (6, 3), (64, 4)):
+        Q = queries(B, 16, 30 + seed)
+        pt = i32(np.arange(B * 16).reshape(B, 16) % 60)
+        L = i32(np.full(B, 2000) - np.arange(B))
+        rows = i32(np.arange(B * 4 * 16).reshape(B * 4, 16) % 60)
+        n, last = i32(np.full(B * 4, 16)), i32(np.full(B * 4, 100))
+        calls.append((msa.msa_dense_attn_decode_q4, (Q, c, pt, L), outputs(B, 16), workspace(msa, B, 4)))
+        calls.append((msa.msa_sparse_attn_decode_q4, (Q, c, rows, n, last), outputs(B, 16), workspace(msa, B, 4)))
+    for f, args, want, own in calls:
+        f(*args, *want, own)
+    for order in (calls, calls[::-1]):
+        for f, args, want, _ in order:
+            got = outputs(*want[1].shape)
+            f(*args, *got, ws, scratch_zeroed=True)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_serving_calls_without_rows(msa):
+    c, e = q4_pool(msa, 2, 2, 1), torch.empty
+    bf, i64, dev = torch.bfloat16, torch.int64, "cuda"
+    none, K = i32([]), e(0, 2, 128, dtype=bf, device=dev)
+    msa.msa_qk_norm_rope(e(0, 4, 128, dtype=bf, device=dev), K, none, None, e(0, 4, 128, dtype=bf, device=dev), K)
+    msa.msa_cache_append_q4(K, K, e(0, dtype=i64, device=dev), c)
+    blocks = e(0, 2, 128, 128, dtype=bf, device=dev)
+    msa.msa_cache_expand_q4(c, none, blocks, blocks)
+    Q, table, ws = e(0, 4, 128, dtype=bf, device=dev), e(0, 3, dtype=torch.int32, device=dev), workspace(msa, 1, 2)
+    msa.msa_sparse_attn_decode_q4(Q, c, table, none, none, Q, None, ws)
+    msa.msa_dense_attn_decode_q4(Q, c, table, none, Q, None, ws)
+    torch.cuda.synchronize()
+
+
 def test_decode_q4_far_pages(msa):
     """A pool whose last page lies past 2^32 bytes."""
     Hkv, P = 8, 68000                                            # 8192 code bytes a block: 4.46e9
