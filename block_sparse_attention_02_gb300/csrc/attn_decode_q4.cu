@@ -48,7 +48,7 @@ namespace {
 
 // Warps of a CTA: four, and for few long rows eight.  With four, twice as many CTAs leave an SM less idle while one
 // of them ends a row and waits for the next one's first pages (64 sequences of 1 to 2,000 tokens 23.6 -> 15.8
-// us); with eight a row that many CTAs share has half as many parts (1,048,576 tokens 214 -> 202 us).
+// us); with eight a row that many CTAs share has half as many parts (1,048,576 tokens 6 % faster).
 constexpr int kFew = 4, kMany = 8;
 constexpr int kSmWarps = 16;                            // that the registers of an SM hold
 constexpr int kStages = 2;                              // tiles of 32 tokens per warp in shared memory (three: 3 % slower)
@@ -745,7 +745,7 @@ msa_status launch_sparse_decode_q4(const msa_decode_q4_args& a, void* ws, cudaSt
   int grid = room;
   if (rows <= room) {
     // Few rows: each is cut into equal parts, as many as there are CTAs for, so that no CTA has pages of two rows
-    // (32 pages of 64 rows in runs of 7 units, most of them across two rows: 20.6 us; in equal parts: 16.2).  Up
+    // (32 pages of 64 rows, now 14.9 us, gained a fifth over runs of 7 units, most of them across two rows).  Up
     // to four parts are a cluster, which joins its row without the workspace (8 rows of 4 pages: 5.8 us
     // for 6.4); a cluster's barrier grows with it, and at eight (6.8 us for 6.4) the workspace is as fast.
     const int most = room / rows;
@@ -756,7 +756,7 @@ msa_status launch_sparse_decode_q4(const msa_decode_q4_args& a, void* ws, cudaSt
     grid = rows * parts;
   } else {
     // Many rows: equal runs over the pages that the rows have, each row's change of pages counted as kRowCost
-    // more (192 sequences, a fifth of them short: 97.5 us with none, 84.0 with 2, 83.0 with 3, 84.7 with 4).
+    // more (192 sequences, a fifth of them short, 78.7 us: 17 % slower with none, 1 to 2 % with 2 or 4).
     p.bin_size = (rows + kBins - 1) / kBins;
     p.row_cost = kRowCost;
   }

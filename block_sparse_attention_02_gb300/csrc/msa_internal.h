@@ -69,7 +69,7 @@ size_t attn_prefill_workspace_size(const msa_prefill_args& a, int64_t chunk_quer
 
 // A launch that the device may prepare while the kernel before it in the stream still runs; the kernel
 // calls wait_for_stream() before its first access to global memory.  Kernels of a few microseconds
-// follow one another in 3 us so, where a plain launch takes 6 (page tables of 8 requests).  cluster: CTAs of a
+// follow one another in 3 us so, where plain launches take 6 (page tables of 8 requests).  cluster: CTAs of a
 // thread-block cluster, 1 for none.
 template <class... P, class... A>
 cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, int cluster,
