@@ -37,6 +37,7 @@
 
 #include <cfloat>
 
+#include "launch_early.cuh"
 #include "msa_internal.h"
 #include "msa_ptx.cuh"
 #include "q4.cuh"

@@ -24,6 +24,7 @@
 // 12.8); of 8 sequences' last tokens and pages 5.1 us, two launches' latency.
 #include <cuda_fp16.h>
 
+#include "launch_early.cuh"
 #include "msa_internal.h"
 #include "msa_ptx.cuh"
 #include "q4.cuh"

@@ -67,30 +67,6 @@ size_t attn_decode_q4_workspace_size(int B, int Hkv);
 msa_status check_decode_args(const msa_decode_args* a);
 size_t attn_prefill_workspace_size(const msa_prefill_args& a, int64_t chunk_queries);
 
-// A launch that the device may prepare while the kernel before it in the stream still runs; the kernel
-// calls wait_for_stream() before its first access to global memory.  Kernels of a few microseconds
-// follow one another in 3 us so, where plain launches take 6 (page tables of 8 requests).  cluster: CTAs of a
-// thread-block cluster, 1 for none.
-template <class... P, class... A>
-cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, int cluster,
-                         A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 constexpr int kBk = 128;
 constexpr int kD = 128;
 constexpr int kDI = 64;

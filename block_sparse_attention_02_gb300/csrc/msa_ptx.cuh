@@ -33,13 +33,6 @@ __device__ __forceinline__ void report(int32_t* dev_err, int32_t bits) {
   if (dev_err != nullptr) atomicOr(dev_err, bits);
 }
 
-// In a kernel launched while the one before it in the stream may still run: waits until
-// everything before is complete and visible.  Called before the first access to global
-// memory, so stream order holds.  (No kernel here lets its successor start
-// earlier than its own end: with such a trigger at the start, the waiting CTAs cost the
-// running kernel more than they gain: a store and expand of 8,192 tokens became a fifth slower.)
-__device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // ---------------------------------------------------------------------------
 // mbarrier
 // ---------------------------------------------------------------------------

@@ -21,6 +21,7 @@
 
 #include <climits>
 
+#include "launch_early.cuh"
 #include "msa_internal.h"
 #include "msa_ptx.cuh"
 

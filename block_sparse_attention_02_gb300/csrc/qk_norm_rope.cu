@@ -22,6 +22,7 @@
 // steps (of four or eight heads) ahead, across tokens: 370 us with plain loads,
 // 352 with a ring of two steps, 333 to 339 with four to six.  4,097 tokens of 40 heads of
 // 64, which fit L2: 12.7 us, bound by issue (floor 6.2); 8 tokens: 3.9 us, a launch's latency.
+#include "launch_early.cuh"
 #include "msa_internal.h"
 #include "msa_ptx.cuh"
 
