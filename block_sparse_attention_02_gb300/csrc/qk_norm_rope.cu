@@ -14,7 +14,9 @@
 // Layout: D / 16 lanes hold a head, 16 values each as two 16-byte chunks that
 // contain both members of every pair (chunks i and i + rot / 16 for split pairs,
 // any chunk for adjacent ones), so the rotation needs no exchange and the norm
-// log2(D / 16) shuffles.  A warp takes one token and walks its heads, which
+// log2(D / 16) shuffles.  The chunks past the rotated ones are taken so that neighbouring lanes'
+// lie side by side (in twos per lane, each request had half of a 32-byte sector: 16,384 tokens
+// with half of each head rotated 106 us for 87).  A warp takes one token and walks its heads, which
 // share the token's sines; with few tokens the heads are split over warps.
 //
 // Bound: HBM, every value read and written once: 65,536 tokens of 48 + 8 + 8 heads of
@@ -89,8 +91,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const N
     turn0 = c0 < 2 * half;
     turn1 = c1 < 2 * half;
   } else {
-    c0 = sub < half ? sub : 2 * half + 2 * (sub - half);
-    c1 = sub < half ? sub + half : c0 + 1;
+    c0 = sub < half ? sub : sub + half;
+    c1 = sub < half ? sub + half : sub + kLanes;
     turn0 = turn1 = sub < half;
   }
   const int q_steps = (p.Hq + kHeads - 1) / kHeads, k_steps = (p.Hkv + kHeads - 1) / kHeads;
