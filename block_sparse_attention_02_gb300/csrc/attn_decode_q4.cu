@@ -748,13 +748,15 @@ msa_status launch_sparse_decode_q4(const msa_decode_q4_args& a, void* ws, cudaSt
     // Few rows: each is cut into equal parts, as many as there are CTAs for, so that no CTA has pages of two rows
     // (32 pages of 64 rows, now 14.9 us, gained a fifth over runs of 7 units, most of them across two rows).  Up
     // to four parts are a cluster, which joins its row without the workspace (8 rows of 4 pages: 5.8 us
-    // for 6.4); a cluster's barrier grows with it, and at eight (6.8 us for 6.4) the workspace is as fast.
+    // for 6.4); a cluster's barrier grows with it, and at eight (6.8 us for 6.4) the workspace is as fast.  Clusters
+    // of three and four that nearly fill the GPU do not all fit at once (200 rows in three parts: 22.4 us for
+    // 17.7 through the workspace); those of two do (300 rows: 20.4 us for 22.3).
     const int most = room / rows;
     const int per = (a.k + most - 1) / most;
     const int parts = (a.k + per - 1) / per;
     p.row_units = parts * per;
-    p.parts = parts <= kMaxParts ? parts : 1;
     grid = rows * parts;
+    p.parts = parts == 2 || (parts <= kMaxParts && 4 * grid <= 3 * room) ? parts : 1;
   } else {
     // Many rows: equal runs over the pages that the rows have, each row's change of pages counted as kRowCost
     // more (192 sequences, a fifth of them short, 78.7 us: 17 % slower with none, 1 to 2 % with 2 or 4).

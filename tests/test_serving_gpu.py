@@ -371,6 +371,12 @@ def test_sparse_decode_q4(msa, B, Hq, Hkv, k):
     assert torch.equal(O, O3)
 
 
+@pytest.mark.parametrize("B,Hq,Hkv,k", [(50, 8, 4, 16), (38, 4, 4, 16), (75, 4, 4, 4), (14, 8, 8, 4), (13, 8, 8, 3), (152, 1, 1, 9)])
+def test_sparse_decode_q4_in_parts(msa, B, Hq, Hkv, k):
+    """Rows in two, three and four parts, as clusters and through the workspace."""
+    test_sparse_decode_q4(msa, B, Hq, Hkv, k)
+
+
 DENSE = {
     "edges": ([0, 1, 2, 15, 16, 17, 127, 128, 129, 255, 256, 257, 1000], 12, 2),
     "one": ([1], 1, 1),
