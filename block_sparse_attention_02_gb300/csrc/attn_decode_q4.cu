@@ -56,6 +56,8 @@ constexpr int kStages = 2;                              // tiles of 32 tokens pe
 constexpr int kBins = 256;                              // that the units are counted by
 constexpr int kRowCost = 3;                             // pages' time that a row's end and the next one's start take
 constexpr int kMaxParts = 4;                            // CTAs of a row up to which they form a cluster
+constexpr int kGroup = 16, kMostFlat = 32;              // parts joined at a time where a row has more than kMostFlat
+constexpr int kMostParts = 80;                          // of a row, up to which a kernel without groups is used (1-2 % faster)
 constexpr int kMaxGrid = 1024;                          // CTAs per launch at most (sizes the workspace)
 constexpr int kPart = kMaxG * kD + 2 * kMaxG;           // floats of a partial: O, m, l of eight heads
 constexpr float kLog2e = 1.4426950408889634f;
@@ -79,7 +81,8 @@ struct Params {
   const int32_t *pt, *n, *last_len;     // sparse
   const int32_t *seq_pt, *seq_len;      // dense
   int64_t max_pages;
-  int32_t* counter;                     // [B * Hkv] parts of a row that have arrived, zero on entry
+  int32_t* counter;                     // [B * Hkv] parts (or groups of parts) of a row that have arrived, zero on entry
+  int32_t* group_counter;               // [kMaxGrid][2] parts of a group that have arrived, zero on entry
   float* part;                          // [grid][2][kPart]
   __nv_bfloat16* O;
   float* LSE;
@@ -272,11 +275,12 @@ __device__ __forceinline__ void attend_tile(const uint32_t (&q)[16], const float
   }
 }
 
-template <bool DENSE, int kWarps>
+template <bool DENSE, int kWarps, bool TREE>
 __global__ void __launch_bounds__(32 * kWarps, kSmWarps / kWarps) attn_q4_kernel(const Params p) {
   constexpr int kThreads = 32 * kWarps;
   constexpr int kTeams = kWarps / 4;        // four warps share a page, 32 tokens each; the teams alternate pages
   constexpr int kRep = 8 / kWarps;          // of the joined outputs' eight parts, those of a warp
+  constexpr int kDeep = 8;                  // parts of a row that a lane loads at a time
   extern __shared__ __align__(128) uint8_t s_ring[];
   float4(*s_o)[8][32] = reinterpret_cast<float4(*)[8][32]>(s_ring);   // after a row's part: [warp][i][lane]
   __shared__ __align__(8) float s_m[kWarps][kMaxG], s_l[kWarps][kMaxG];
@@ -569,30 +573,39 @@ __global__ void __launch_bounds__(32 * kWarps, kSmWarps / kWarps) attn_q4_kernel
       // a part in the workspace: O as [8][32] float4, m [8], l [8]; slot 0: the one at the start
       // of a CTA's run, slot 1: the one at its end
       auto part_of = [&](int c) { return p.part + (static_cast<int64_t>(c) * 2 + (c * per >= row_first ? 0 : 1)) * kPart; };
-      float* mine = part_of(blockIdx.x);
+      // The parts joined: CTAs base, base + step, .., `count` of them, by the last to arrive.  Many parts are joined
+      // in groups first, whose results take the place of their first part (a CTA that reads 300 parts waits
+      // for 38 rounds of loads: 1,000,000 tokens of one head 54 us for 36).
+      const int members = last - first + 1;
+      const bool tree = TREE && members > kMostFlat;
+      const int group = tree ? (static_cast<int>(blockIdx.x) - first) / kGroup : 0;
+      int own = blockIdx.x, base = first + group * kGroup, step = 1, count = tree ? min(kGroup, members - group * kGroup) : members;
+      // (a CTA is the first of at most one group that starts a row and of one that does not)
+      int32_t* counter = tree ? p.group_counter + 2 * base + (group == 0) : p.counter + row;
+      while (true) {
+        float* mine = part_of(own);
 #pragma unroll
-      for (int i = 0; i < kRep; ++i) reinterpret_cast<float4*>(mine)[tid + i * kThreads] = o[i];
-      if (warp == 0 && g == 0) {
+        for (int i = 0; i < kRep; ++i) reinterpret_cast<float4*>(mine)[tid + i * kThreads] = o[i];
+        if (warp == 0 && g == 0) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          mine[kMaxG * kD + 2 * t + c] = M[c];
-          mine[kMaxG * kD + kMaxG + 2 * t + c] = l[c];
+          for (int c = 0; c < 2; ++c) {
+            mine[kMaxG * kD + 2 * t + c] = M[c];
+            mine[kMaxG * kD + kMaxG + 2 * t + c] = l[c];
+          }
         }
-      }
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) s_last = atomicAdd(&p.counter[row], 1) == last - first;
-      __syncthreads();
-      write = s_last != 0;
-      if (write) {
         __threadfence();
-        // all parts of the row, 64 at a time: lane (g, t) takes m and l of parts g, g + 8, .. in one batch of
-        // loads, and each lane its share of O eight parts deep
+        __syncthreads();
+        if (tid == 0) s_last = atomicAdd(counter, 1) == count - 1;
+        __syncthreads();
+        if (s_last == 0) break;
+        __threadfence();
+        // 64 parts at a time: lane (g, t) takes m and l of parts g, g + 8, .. in one batch of
+        // loads, and each lane its share of O kDeep parts deep
         M[0] = M[1] = kNoMax;
         l[0] = l[1] = 0.f;
 #pragma unroll
         for (int i = 0; i < kRep; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c0 = first; c0 <= last; c0 += 64) {
+        for (int c0 = 0; c0 < count; c0 += 64) {
           float2 m[8], sum[8];
           float top[2] = {M[0], M[1]};
 #pragma unroll
@@ -600,9 +613,10 @@ __global__ void __launch_bounds__(32 * kWarps, kSmWarps / kWarps) attn_q4_kernel
             const int c = c0 + g + 8 * k;
             m[k] = make_float2(kNoMax, kNoMax);
             sum[k] = make_float2(0.f, 0.f);
-            if (c <= last) {
-              m[k] = __ldcg(reinterpret_cast<const float2*>(part_of(c) + kMaxG * kD) + t);
-              sum[k] = __ldcg(reinterpret_cast<const float2*>(part_of(c) + kMaxG * kD + kMaxG) + t);
+            if (c < count) {
+              const float2* x = reinterpret_cast<const float2*>(part_of(base + c * step) + kMaxG * kD);
+              m[k] = __ldcg(x + t);
+              sum[k] = __ldcg(x + kMaxG / 2 + t);
             }
           }
 #pragma unroll
@@ -636,28 +650,35 @@ __global__ void __launch_bounds__(32 * kWarps, kSmWarps / kWarps) attn_q4_kernel
 #pragma unroll
           for (int i = 0; i < kRep; ++i) o[i] = make_float4(o[i].x * s0, o[i].y * s1, o[i].z * s0, o[i].w * s1);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            constexpr int kDeep = 8;
-            if (c0 + 8 * k > last) break;
+          for (int k = 0; k < 8; k += kDeep / 8) {
+            if (c0 + 8 * k >= count) break;
             float4 v[kDeep][kRep];
 #pragma unroll
             for (int x = 0; x < kDeep; ++x)
 #pragma unroll
               for (int i = 0; i < kRep; ++i) {
                 v[x][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (c0 + 8 * k + x <= last)
-                  v[x][i] = __ldcg(reinterpret_cast<const float4*>(part_of(c0 + 8 * k + x)) + tid + i * kThreads);
+                if (c0 + 8 * k + x < count)
+                  v[x][i] = __ldcg(reinterpret_cast<const float4*>(part_of(base + (c0 + 8 * k + x) * step)) + tid + i * kThreads);
               }
 #pragma unroll
             for (int x = 0; x < kDeep; ++x) {
-              const int from = x * 4 + t;
-              const float f0 = __shfl_sync(0xffffffffu, m[k].x, from), f1 = __shfl_sync(0xffffffffu, m[k].y, from);
+              const int from = x % 8 * 4 + t;
+              const float f0 = __shfl_sync(0xffffffffu, m[k + x / 8].x, from), f1 = __shfl_sync(0xffffffffu, m[k + x / 8].y, from);
 #pragma unroll
               for (int i = 0; i < kRep; ++i) add(o[i], f0, f1, v[x][i]);
             }
           }
         }
-        if (tid == 0) p.counter[row] = 0;
+        if (tid == 0) *counter = 0;
+        write = !tree || step > 1;
+        if (write) break;
+        own = base;
+        base = first;
+        step = kGroup;
+        count = (members + kGroup - 1) / kGroup;
+        counter = p.counter + row;
+        __syncthreads();                    // the group's first part is read, and s_last
       }
     }
     if (write) {
@@ -680,9 +701,10 @@ __global__ void __launch_bounds__(32 * kWarps, kSmWarps / kWarps) attn_q4_kernel
   }
 }
 
-// The workspace: the parts, then a counter per row.  The counters start at the same byte for every B and Hkv, so
-// that a call of one shape leaves those of another zero.
+// The workspace: the parts, then the counters of groups and rows.  They start at the same bytes for every B and Hkv,
+// so that a call of one shape leaves those of another zero.
 constexpr size_t kPartBytes = static_cast<size_t>(kMaxGrid) * 2 * kPart * sizeof(float);
+constexpr size_t kGroupBytes = kMaxGrid * 2 * sizeof(int32_t);
 
 template <class Args>
 Params common_params(const Args& a, void* ws) {
@@ -701,23 +723,24 @@ Params common_params(const Args& a, void* ws) {
   p.s0 = a.cache.scale_stride[0]; p.s1 = a.cache.scale_stride[1];
   p.num_pages = a.cache.num_pages;
   p.part = static_cast<float*>(ws);
-  p.counter = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + kPartBytes);
+  p.group_counter = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + kPartBytes);
+  p.counter = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + kPartBytes + kGroupBytes);
   p.O = static_cast<__nv_bfloat16*>(a.O);
   p.LSE = a.LSE;
   p.dev_err = a.dev_err;
   return p;
 }
 
-template <bool DENSE, int kWarps>
+template <bool DENSE, int kWarps, bool TREE>
 msa_status launch(const Params& p, int grid, int scratch_zeroed, cudaStream_t stream) {
   if (!scratch_zeroed) {   // otherwise zero by contract (every error-free call leaves them zero)
-    const cudaError_t e = cudaMemsetAsync(p.counter, 0, static_cast<size_t>(p.B) * p.Hkv * sizeof(int32_t), stream);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(4-bit decode row counters)");
+    const cudaError_t e = cudaMemsetAsync(p.group_counter, 0, kGroupBytes + static_cast<size_t>(p.B) * p.Hkv * sizeof(int32_t), stream);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(4-bit decode counters)");
   }
   constexpr int smem = kWarps * std::max<int>(kStages * kTileBytes, kMaxG * kD * sizeof(float));
-  cudaError_t e = cudaFuncSetAttribute(attn_q4_kernel<DENSE, kWarps>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(attn_q4_kernel<DENSE, kWarps, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(attn_q4)");
-  e = launch_early(attn_q4_kernel<DENSE, kWarps>, grid, 32 * kWarps, smem, stream, std::max(p.parts, 1), p);
+  e = launch_early(attn_q4_kernel<DENSE, kWarps, TREE>, grid, 32 * kWarps, smem, stream, std::max(p.parts, 1), p);
   if (e != cudaSuccess) return cuda_fail(e, "attn_q4_kernel launch");
   return MSA_OK;
 }
@@ -733,7 +756,7 @@ msa_status room_for(int warps, int* room) {
 }  // namespace
 
 size_t attn_decode_q4_workspace_size(int B, int Hkv) {
-  return kPartBytes + (static_cast<size_t>(B) * Hkv * sizeof(int32_t) + 255) / 256 * 256;
+  return kPartBytes + kGroupBytes + (static_cast<size_t>(B) * Hkv * sizeof(int32_t) + 255) / 256 * 256;
 }
 
 msa_status launch_sparse_decode_q4(const msa_decode_q4_args& a, void* ws, cudaStream_t stream) {
@@ -763,7 +786,7 @@ msa_status launch_sparse_decode_q4(const msa_decode_q4_args& a, void* ws, cudaSt
     p.bin_size = (rows + kBins - 1) / kBins;
     p.row_cost = kRowCost;
   }
-  return launch<false, kFew>(p, grid, a.scratch_zeroed, stream);
+  return launch<false, kFew, false>(p, grid, a.scratch_zeroed, stream);
 }
 
 msa_status launch_dense_decode_q4(const msa_dense_decode_q4_args& a, void* ws, cudaStream_t stream) {
@@ -776,9 +799,13 @@ msa_status launch_dense_decode_q4(const msa_dense_decode_q4_args& a, void* ws, c
   const int64_t rows = static_cast<int64_t>(a.B) * a.Hkv;
   if (rows > many) {       // rows enough for all CTAs: their ends count (the lengths are on the device)
     p.row_cost = kRowCost;
-    return launch<true, kFew>(p, few, a.scratch_zeroed, stream);
+    if (few > kMostParts * a.Hkv) return launch<true, kFew, true>(p, few, a.scratch_zeroed, stream);
+    return launch<true, kFew, false>(p, few, a.scratch_zeroed, stream);
   }
-  return launch<true, kMany>(p, static_cast<int>(std::min<int64_t>(many, rows * a.max_pages)), a.scratch_zeroed, stream);
+  const int grid = static_cast<int>(std::min<int64_t>(many, rows * a.max_pages));
+  // (a sequence may be all that there is to do, and its Hkv heads are equally long)
+  if (grid > kMostParts * a.Hkv) return launch<true, kMany, true>(p, grid, a.scratch_zeroed, stream);
+  return launch<true, kMany, false>(p, grid, a.scratch_zeroed, stream);
 }
 
 }  // namespace msa

@@ -729,8 +729,8 @@ msa_status msa_cache_expand_q4(const msa_expand_q4_args *args, msa_stream_t stre
  * Slots past a row's last token may hold anything.  Page ids outside
  * [0, num_pages): left out, MSA_DEVERR_BAD_PAGE.  LSE may be NULL.
  * Workspace: msa_attn_decode_q4_workspace_size(B, Hkv) bytes, 16-byte aligned: the
- * parts of cut rows, then (from the same byte in every call) one int32 counter per
- * row.  scratch_zeroed works as in msa_sparse_attn_decode, but for any B and Hkv: a
+ * parts of cut rows, then (from the same byte in every call) the counters of groups of
+ * parts and of rows.  scratch_zeroed works as in msa_sparse_attn_decode, but for any B and Hkv: a
  * zero-filled workspace of the largest call's size serves calls of both kinds and all sizes.
  * Calls that overlap on the GPU need workspaces of their own.  B <= 4096,
  * B * Hq < 2^24. */

@@ -415,6 +415,24 @@ def test_dense_decode_q4(msa, name):
     assert torch.equal(O, O2) and torch.equal(LSE, L2)
 
 
+@pytest.mark.parametrize("L,Hq,Hkv", [([150 * BK], 2, 1), ([149 * BK + 5] * 2, 3, 1), ([190000] + [30 * BK] * 49, 2, 2), ([60 * BK + 1], 5, 1),
+                                      ([120000] + [7] * 400, 1, 1)])
+def test_dense_decode_q4_many_parts(msa, L, Hq, Hkv):
+    """Rows in so many parts that they are joined in groups; pages shared, so that the pool is small."""
+    r, P, B = np.random.default_rng(7), 50, len(L)
+    per = [-(-x // BK) for x in L]
+    pt = r.integers(0, P, (B, max(per) + 3))
+    c, Q = q4_pool(msa, P, Hkv, 5), queries(B, Hq, 3)
+    O, LSE = outputs(B, Hq)
+    ws = workspace(msa, B, Hkv)
+    msa.msa_dense_attn_decode_q4(Q, c, i32(pt), i32(L), O, LSE, ws)
+    check_rows(Q, O, LSE, lambda b, g: pt[b, :per[b]], lambda b, g: L[b], c)
+    for _ in range(3):
+        O2, L2 = outputs(B, Hq)
+        msa.msa_dense_attn_decode_q4(Q, c, i32(pt), i32(L), O2, L2, ws, scratch_zeroed=True)
+        assert torch.equal(O, O2) and torch.equal(LSE, L2)
+
+
 @pytest.mark.parametrize("amp,spread", [(40.0, 4.0), (1e-3, 1e-2), (2.0 ** 100, 2.0 ** -3), (0.0, 1.0)])
 def test_decode_q4_score_ranges(msa, amp, spread):
     """Scores that concentrate on one token, that are all alike, queries far outside fp16's range, and zeros."""
