@@ -22,7 +22,7 @@
 // 2^15, is rounded to fp16 (2^-11 of the value down to 2^-22 of the largest).
 //
 // Work.  The (row, page) units of all rows form one list; each CTA takes an equal
-// run of it.  Four warps share a page, a warp takes 32 tokens of it through two
+// run of it, or, where there are few pages, one part of one row.  Four warps share a page, a warp takes 32 tokens of it through two
 // stages in shared memory of its own (more bytes in flight serve HBM worse, see kStages)
 // with a softmax of its own; the warps' softmaxes are joined in shared memory at the
 // end of a row's part.  Rows cut by a run's end go through the workspace, where
@@ -71,6 +71,7 @@ struct Params {
   // Units of a row: row_units for every one (sparse, few rows; k or a few more, the last ones without a page), or 0:
   // each row's own pages and row_cost more, counted by bins of bin_size sequences (dense) or rows (sparse).
   int row_units, bin_size, row_cost;
+  bool whole_parts;                     // dense: the units may become parts of rows, one per CTA
   int parts;                            // sparse: CTAs of a row that form a cluster (0 or 1: none)
   float scale_log2, v_scale;
   const uint8_t* Q;
@@ -297,9 +298,11 @@ __global__ void __launch_bounds__(32 * kWarps, kSmWarps / kWarps) attn_q4_kernel
     const int L = p.seq_len[x];
     return L < 0 || L > p.max_pages * kBk ? 0 : (L + kBk - 1) / kBk;
   };
+  bool settled = !p.whole_parts;            // what a unit is
+  int chunk = 1, row_cost = settled ? p.row_cost : 0;   // pages of a unit, units that a row has more
   auto units_of = [&](int x) {
     const int pages = pages_of(x);
-    return pages > 0 ? pages + p.row_cost : 0;
+    return pages > 0 ? (DENSE && chunk > 1 ? (pages + chunk - 1) / chunk : pages) + row_cost : 0;
   };
   const int counted = DENSE ? p.B : rows, per_item = DENSE ? p.Hkv : 1;
   const int bins = p.row_units > 0 ? 0 : (counted + p.bin_size - 1) / p.bin_size;
@@ -319,24 +322,43 @@ __global__ void __launch_bounds__(32 * kWarps, kSmWarps / kWarps) attn_q4_kernel
       }
       sum += mine[i];
     }
-    int inc = sum;
+    while (true) {
+      int inc = sum;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
-    }
-    if (lane == 31) s_wsum[warp] = inc;
-    __syncthreads();
-    int before = inc - sum;
-    for (int w = 0; w < warp; ++w) before += s_wsum[w];
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      if (lane == 31) s_wsum[warp] = inc;
+      __syncthreads();
+      int before = inc - sum;
+      for (int w = 0; w < warp; ++w) before += s_wsum[w];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int b = tid * kPer + i;
-      if (b <= bins) s_pre[b] = before;
-      before += mine[i];
+      for (int i = 0; i < kPer; ++i) {
+        const int b = tid * kPer + i;
+        if (b <= bins) s_pre[b] = before;
+        before += mine[i];
+      }
+      if (tid == kThreads - 1 && bins == kBins) s_pre[bins] = before;
+      __syncthreads();
+      if (settled) break;
+      settled = true;
+      // Few pages: a unit becomes a part of a row that is all a CTA has, if that makes the longest one at most
+      // kRowCost pages longer (a row's end costs that much; 40 sequences of 437 to 1,825 tokens of one head 10.5 us
+      // for 14.5).  ceil(x / c) <= x / c + 1, so as many fit.
+      const int total = s_pre[bins] * per_item, ctas = gridDim.x;
+      const int pages = (total + ctas - rows - 1) / (ctas - rows);
+      if (pages <= (total + ctas - 1) / ctas + kRowCost) chunk = max(pages, 1);
+      else row_cost = p.row_cost;
+      if (chunk == 1 && row_cost == 0) break;
+      sum = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        mine[i] = chunk > 1 ? (mine[i] + chunk - 1) / chunk : mine[i] > 0 ? mine[i] + row_cost : 0;
+        sum += mine[i];
+      }
+      __syncthreads();                      // the pages' sums are read
     }
-    if (tid == kThreads - 1 && bins == kBins) s_pre[bins] = before;
-    __syncthreads();
   }
   const int64_t units = bins > 0 ? static_cast<int64_t>(s_pre[bins]) * per_item : static_cast<int64_t>(rows) * p.row_units;
   const uint32_t pool_pages = static_cast<uint32_t>(p.num_pages);
@@ -378,9 +400,13 @@ __global__ void __launch_bounds__(32 * kWarps, kSmWarps / kWarps) attn_q4_kernel
       list = p.pt + static_cast<int64_t>(item) * p.k;
     }
     const int row = b * p.Hkv + head;
-    const int p1 = static_cast<int>(min(static_cast<int64_t>(row_pages), p0 + hi - u));
     const int64_t row_first = u - p0;
+    int p1 = static_cast<int>(min(static_cast<int64_t>(row_pages), p0 + hi - u));
     u += p1 - p0;
+    if (DENSE) {
+      p0 *= chunk;
+      p1 *= chunk;
+    }
 
     // this warp's 32 tokens of its team's pages, the next one's in flight
     const int tok0 = (warp & 3) * kTile, j0 = p0 + (warp >> 2);
@@ -797,12 +823,16 @@ msa_status launch_dense_decode_q4(const msa_dense_decode_q4_args& a, void* ws, c
   p.seq_pt = a.seq_pt; p.seq_len = a.seq_len; p.max_pages = a.max_pages;
   p.bin_size = (a.B + kBins - 1) / kBins;
   const int64_t rows = static_cast<int64_t>(a.B) * a.Hkv;
-  if (rows > many) {       // rows enough for all CTAs: their ends count (the lengths are on the device)
+  // Many rows, whose ends count (their lengths are on the device).  Four warps from half as many rows as there are
+  // CTAs of eight on: 256 rows of 500 to 4,000 tokens 22 us for 29, of 30,000 tokens 173 for 171.
+  if (2 * rows > many) {
     p.row_cost = kRowCost;
+    p.whole_parts = p.bin_size == 1 && 2 * rows <= few;
     if (few > kMostParts * a.Hkv) return launch<true, kFew, true>(p, few, a.scratch_zeroed, stream);
     return launch<true, kFew, false>(p, few, a.scratch_zeroed, stream);
   }
   const int grid = static_cast<int>(std::min<int64_t>(many, rows * a.max_pages));
+  p.whole_parts = p.bin_size == 1 && 2 * rows <= grid;
   // (a sequence may be all that there is to do, and its Hkv heads are equally long)
   if (grid > kMostParts * a.Hkv) return launch<true, kMany, true>(p, grid, a.scratch_zeroed, stream);
   return launch<true, kMany, false>(p, grid, a.scratch_zeroed, stream);

@@ -433,6 +433,14 @@ def test_dense_decode_q4_many_parts(msa, L, Hq, Hkv):
         assert torch.equal(O, O2) and torch.equal(LSE, L2)
 
 
+@pytest.mark.parametrize("L,Hq,Hkv", [([437 + 35 * i for i in range(40)], 2, 1), ([1 + 26 * i for i in range(20)], 8, 8),
+                                      ([129] * 152, 1, 1), ([129 + i for i in range(153)], 1, 1), ([0, 300, 0, 1] * 19, 4, 4),
+                                      ([640] * 77, 4, 4), ([1500] * 30 + [0], 5, 5), ([20000, 1, 1, 0], 2, 1)])
+def test_dense_decode_q4_whole_parts(msa, L, Hq, Hkv):
+    """Around the sizes from which CTAs take whole parts of rows, and four warps instead of eight."""
+    test_dense_decode_q4_many_parts(msa, L, Hq, Hkv)
+
+
 @pytest.mark.parametrize("amp,spread", [(40.0, 4.0), (1e-3, 1e-2), (2.0 ** 100, 2.0 ** -3), (0.0, 1.0)])
 def test_decode_q4_score_ranges(msa, amp, spread):
     """Scores that concentrate on one token, that are all alike, queries far outside fp16's range, and zeros."""
