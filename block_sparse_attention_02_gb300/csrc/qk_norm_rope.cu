@@ -277,9 +277,12 @@ msa_status launch_qk_norm_rope(const msa_norm_rope_args& a, cudaStream_t stream)
   p.slots = a.slots; p.dev_err = a.dev_err;
   const int heads = a.D == 128 ? 4 : 8;       // per warp and step
   const int steps = (a.Hq + heads - 1) / heads + (a.V != nullptr ? 2 : 1) * ((a.Hkv + heads - 1) / heads);
-  // few tokens: their heads spread over enough warps to fill the SMs
-  const int64_t want = static_cast<int64_t>(dev.num_sms) * kCtasPerSm * kWarps;
-  p.parts = static_cast<int>(std::min<int64_t>(std::max<int64_t>((want + a.N - 1) / a.N, 1), std::max(steps, 1)));
+  // few tokens: their heads spread over the warps that run at once, in equal parts, but not over more (2,000
+  // tokens of 64 heads in two parts, some warps having a second one: 19.4 us for 18.2)
+  const int64_t warps = static_cast<int64_t>(dev.num_sms) * kCtasPerSm * kWarps;
+  const int most = static_cast<int>(std::min<int64_t>(std::max<int64_t>(warps / a.N, 1), steps));
+  const int part_steps = (steps + most - 1) / most;
+  p.parts = (steps + part_steps - 1) / part_steps;
   const int64_t items = a.N * p.parts;
   const unsigned grid =
       static_cast<unsigned>(std::min<int64_t>((items + kWarps - 1) / kWarps, static_cast<int64_t>(dev.num_sms) * kCtasPerSm));
