@@ -8,8 +8,8 @@
 // The angle.  A position of a million times a frequency near 1 needs more than
 // fp32's 24 bits.  Only the fraction of a turn matters, so each lane keeps its
 // frequencies as turns per token in 64-bit fixed point (2^64 = one turn) and
-// pos * that, modulo 2^64, is the angle: one integer product, exact but for the
-// 53 bits of the frequency itself (2^-33 turns at 2^20 tokens).
+// pos * that, modulo 2^64, is the angle: one integer product, off by less than 2^-43
+// turns at 2^20 tokens.
 //
 // Layout: D / 16 lanes hold a head, 16 values each as two 16-byte chunks that
 // contain both members of every pair (chunks i and i + rot / 16 for split pairs,
@@ -20,10 +20,10 @@
 // share the token's sines; with few tokens the heads are split over warps.
 //
 // Bound: HBM, every value read and written once: 65,536 tokens of 48 + 8 + 8 heads of
-// 128 in 327 us, 97 % of the copy rate.  Each lane copies its chunks into shared memory two
+// 128 in 331 us, 96 % of the copy rate.  Each lane copies its chunks into shared memory two
 // steps (of four or eight heads) ahead, across tokens: 370 us with plain loads,
 // 352 with a ring of two steps, 333 to 339 with four to six.  4,097 tokens of 40 heads of
-// 64, which fit L2: 12.7 us, bound by issue (floor 6.2); 8 tokens: 3.9 us, a launch's latency.
+// 64, which fit L2: 12.3 us, bound by issue (floor 6.2); 8 tokens: 3.8 us, a launch's latency.
 #include "launch_early.cuh"
 #include "msa_internal.h"
 #include "msa_ptx.cuh"
@@ -72,6 +72,21 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
+// f / (2 pi) modulo 1 in units of 2^-64, off by less than two of them: the 24 bits of f times 1 / (2 pi) to 96 bits,
+// shifted.  (In doubles, which this GPU has few units for: 500 tokens 8.1 us for 7.5.)
+__device__ __forceinline__ uint64_t turns_of(float f) {
+  const uint32_t bits = __float_as_uint(f), ex = bits >> 23 & 0xff;
+  if (ex >= 150) {         // 2^23 or more, infinite or NaN
+    const double t = static_cast<double>(f) * 0.15915494309189533577;
+    return __double2ull_rz((t - floor(t)) * 18446744073709551616.0);
+  }
+  const uint64_t m = (bits & 0x7fffffu) | (ex != 0 ? 0x800000u : 0u);       // f = m * 2^(max(ex, 1) - 150)
+  const uint64_t low = m * 0x7f09d5f4u, mid = m * 0x9391054au + (low >> 32), top = m * 0x28be60dbu + (mid >> 32);   // m / (2 pi) * 2^96
+  const uint32_t down = 150 - max(ex, 1u);                                  // of top and mid's 32 bits, from 2^-64 turns
+  uint64_t t = down < 32 ? top << (32 - down) | static_cast<uint32_t>(mid) >> down : down < 96 ? top >> (down - 32) : 0;
+  return bits >> 31 ? 0 - t : t;
+}
+
 template <int D, bool PAIRS>   // PAIRS: the rotated pairs are neighbours (2i, 2i + 1)
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const NormRopeParams p) {
   constexpr int kLanes = D / 16;              // lanes per head
@@ -80,7 +95,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const N
   __shared__ float2 s_turn[kWarps][D / 2];    // cosine and sine of every pair of a warp's token
   __shared__ __align__(16) uint8_t s_ring[kWarps][kAhead * 1024];
   wait_for_stream();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (from lane 0: the compiler then knows that a warp goes one way; 4,097 tokens 4 % faster)
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int sub = lane % kLanes, hl = lane / kLanes;
   const int half = p.rot >> 4;                // chunks of 8 values in each half of the rotated ones
   int c0, c1;                                 // this lane's chunks
@@ -145,11 +161,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const N
 #pragma unroll
   for (int e = 0; e < D / 64; ++e) {
     turns[e] = 0;
-    if (lane + 32 * e < p.rot / 2) {
-      double t = static_cast<double>(p.inv_freq[lane + 32 * e]) * 0.15915494309189533577;   // 1 / (2 pi)
-      t -= floor(t);
-      turns[e] = __double2ull_rz(t * 18446744073709551616.0);
-    }
+    if (lane + 32 * e < p.rot / 2) turns[e] = turns_of(p.inv_freq[lane + 32 * e]);
   }
   __syncthreads();
 

@@ -199,6 +199,21 @@ def test_norm_rope_options(msa):
     check_rope(Qt, Q, wq, pos, f, False)
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_norm_rope_frequencies(msa, interleaved):
+    """Frequencies of every size and sign: turns of a token from 2^-130 to 2^22, no rotation, negative ones."""
+    Q, K, V, wq, wk, pos, f = rope_case(90, 2, 1, 128, 128, 8, far=1000)
+    r = np.random.default_rng(3)
+    v = 2.0 ** r.uniform(-126, 22.9, 64) * r.choice([-1, 1], 64)
+    v[:24] = [0.0, -0.0, 2.0 ** -149, 2.0 ** -126, 1.0, -1.0, 0.5, 2.0 ** 22, 8388607.5, 2.0 ** 23, -2.0 ** 23, 2.0 ** 24 + 2, 3.14159274,
+              6.28318548, -6.28318548, 1e-3, 2.0 ** -23, 2.0 ** -24, 2.0 ** -31, 2.0 ** -32, 2.0 ** -33, 2.0 ** -64, 1e5, -1e5]
+    f = torch.tensor(v, dtype=torch.float32, device="cuda")
+    Qo, Ko = torch.empty(90, 2, 128, dtype=torch.bfloat16, device="cuda"), torch.empty(90, 1, 128, dtype=torch.bfloat16, device="cuda")
+    msa.msa_qk_norm_rope(Q, K, pos, f, Qo, Ko, q_weight=wq, interleaved=interleaved)
+    check_rope(Qo, Q, wq, pos, f, interleaved)
+    check_rope(Ko, K, None, pos, f, interleaved)
+
+
 def test_norm_rope_rows_left_out(msa):
     """pos < 0 leaves a row's outputs as they were; slot < 0 stores no key; one past the pool is named."""
     N = 40
