@@ -20,10 +20,11 @@
 // share the token's sines; with few tokens the heads are split over warps.
 //
 // Bound: HBM, every value read and written once: 65,536 tokens of 48 + 8 + 8 heads of
-// 128 in 331 us, 96 % of the copy rate.  Each lane copies its chunks into shared memory two
-// steps (of four or eight heads) ahead, across tokens: 370 us with plain loads,
-// 352 with a ring of two steps, 333 to 339 with four to six.  4,097 tokens of 40 heads of
-// 64, which fit L2: 12.3 us, bound by issue (floor 6.2); 8 tokens: 3.8 us, a launch's latency.
+// 128 in 319 us, 99 % of the copy rate.  Each lane copies its chunks into shared memory
+// three steps (of four or eight heads) ahead, across tokens (370 us with plain loads).  16
+// warps on an SM are enough, and more in flight serves HBM worse: 323 us with four steps ahead, 325 with 18 or
+// 20 warps and two, 338 with 24 and two, 351 with 24 and three.  4,097 tokens of 40 heads of 64,
+// which fit L2: 12.0 us, bound by issue (floor 6.2); 8 tokens: 3.4 us, a launch's latency.
 #include "launch_early.cuh"
 #include "msa_internal.h"
 #include "msa_ptx.cuh"
@@ -31,10 +32,10 @@
 namespace msa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCtasPerSm = 3;
-constexpr int kAhead = 3;                     // steps of 1 KiB per warp in shared memory
+constexpr int kCtasPerSm = 4;
+constexpr int kAhead = 4;                     // steps of 1 KiB per warp in shared memory, one of them worked on
 
 struct NormRopeParams {
   int64_t N, num_pages;
@@ -73,7 +74,7 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 // f / (2 pi) modulo 1 in units of 2^-64, off by less than two of them: the 24 bits of f times 1 / (2 pi) to 96 bits,
-// shifted.  (In doubles, which this GPU has few units for: 500 tokens 8.1 us for 7.5.)
+// shifted.  (In doubles, which this GPU has few units for: 500 tokens 7 % slower.)
 __device__ __forceinline__ uint64_t turns_of(float f) {
   const uint32_t bits = __float_as_uint(f), ex = bits >> 23 & 0xff;
   if (ex >= 150) {         // 2^23 or more, infinite or NaN
@@ -290,7 +291,7 @@ msa_status launch_qk_norm_rope(const msa_norm_rope_args& a, cudaStream_t stream)
   const int heads = a.D == 128 ? 4 : 8;       // per warp and step
   const int steps = (a.Hq + heads - 1) / heads + (a.V != nullptr ? 2 : 1) * ((a.Hkv + heads - 1) / heads);
   // few tokens: their heads spread over the warps that run at once, in equal parts, but not over more (2,000
-  // tokens of 64 heads in two parts, some warps having a second one: 19.4 us for 18.2)
+  // tokens of 64 heads in two parts, some warps having a second one, took 7 % longer)
   const int64_t warps = static_cast<int64_t>(dev.num_sms) * kCtasPerSm * kWarps;
   const int most = static_cast<int>(std::min<int64_t>(std::max<int64_t>(warps / a.N, 1), steps));
   const int part_steps = (steps + most - 1) / most;
