@@ -794,13 +794,15 @@ msa_status launch_sparse_decode_q4(const msa_decode_q4_args& a, void* ws, cudaSt
   const int rows = a.B * a.Hkv;
   int grid = room;
   if (rows <= room) {
-    // Few rows: each is cut into equal parts, as many as there are CTAs for, so that no CTA has pages of two rows
-    // (32 pages of 64 rows, now 14.9 us, gained a fifth over runs of 7 units, most of them across two rows).  Up
-    // to four parts are a cluster, which joins its row without the workspace (8 rows of 4 pages: 5.8 us
-    // for 6.4); a cluster's barrier grows with it, and at eight (6.8 us for 6.4) the workspace is as fast.  Clusters
-    // of three and four that nearly fill the GPU do not all fit at once (200 rows in three parts: 22.4 us for
-    // 17.7 through the workspace); those of two do (300 rows: 20.4 us for 22.3).
-    const int most = room / rows;
+    // Few rows: each is cut into equal parts, so that no CTA has pages of two rows (32 pages of 64 rows in runs of
+    // 7 units, most of them across two rows, took a quarter longer).  Up to four parts are a cluster, which joins its
+    // row without the workspace.  That costs so much less that four parts of up to eight pages, or two, are better
+    // than parts for every CTA (64 rows of 16 pages 8.9 us for 10.3 in eight parts, 200 rows 16.5 for 18.1 in three);
+    // longer rows take those, but few rows no more than half of them (8 rows of 64 pages 10.8 us for 13.4).
+    // Clusters of three and four that nearly fill the GPU do not all fit at once (200 rows in three: 22.4 us for
+    // 17.7 through the workspace); those of two do.
+    const int cluster = 16 * rows <= 3 * room ? 4 : 2 * rows <= room ? 2 : 1;
+    const int most = a.k <= 8 * cluster ? cluster : std::max((16 * rows <= room ? room / 2 : room) / rows, cluster);
     const int per = (a.k + most - 1) / most;
     const int parts = (a.k + per - 1) / per;
     p.row_units = parts * per;

@@ -386,7 +386,8 @@ def test_sparse_decode_q4(msa, B, Hq, Hkv, k):
     assert torch.equal(O, O3)
 
 
-@pytest.mark.parametrize("B,Hq,Hkv,k", [(50, 8, 4, 16), (38, 4, 4, 16), (75, 4, 4, 4), (14, 8, 8, 4), (13, 8, 8, 3), (152, 1, 1, 9)])
+@pytest.mark.parametrize("B,Hq,Hkv,k", [(50, 8, 4, 16), (38, 4, 4, 16), (75, 4, 4, 4), (14, 8, 8, 4), (13, 8, 8, 3), (152, 1, 1, 9),
+                                        (26, 4, 4, 64), (8, 8, 8, 32), (5, 16, 8, 64)])
 def test_sparse_decode_q4_in_parts(msa, B, Hq, Hkv, k):
     """Rows in two, three and four parts, as clusters and through the workspace."""
     test_sparse_decode_q4(msa, B, Hq, Hkv, k)
