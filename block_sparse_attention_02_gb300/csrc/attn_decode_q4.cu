@@ -21,12 +21,13 @@
 // of two; P = 2^(z - m + 8) with m the running maximum or up to 7 below it, at most
 // 2^15, is rounded to fp16 (2^-11 of the value down to 2^-22 of the largest).
 //
-// Work.  The (row, page) units of all rows form one list; each CTA takes an equal
-// run of it, or, where there are few pages, one part of one row.  Four warps share a page, a warp takes 32 tokens of it through two
-// stages in shared memory of its own (more bytes in flight serve HBM worse, see kStages)
-// with a softmax of its own; the warps' softmaxes are joined in shared memory at the
-// end of a row's part.  Rows cut by a run's end go through the workspace, where
-// the CTA that arrives last joins them, or, cut into few equal parts, through a cluster's shared memory.
+// Work.  Dense: the (row, page) units of all rows form one list; each CTA takes an equal
+// run of it, or, where there are few pages, one part of one row.  Sparse: a CTA has a row, or
+// one of its equal parts where there are few rows.  Four warps share a page; a warp takes 32
+// tokens of it through two stages in shared memory of its own (more bytes in flight serve
+// HBM worse, see kStages) with a softmax of its own; the warps' softmaxes are joined in
+// shared memory at the end of a row's part.  Parts of a row are joined through the workspace by
+// the CTA that arrives last, or, if they are a few equal ones, through a cluster's shared memory.
 //
 // Bound: 257 instructions a warp for 16 tokens, 160 of them conversions, scalings and
 // products, leave the SMs issuing in 60 % of their cycles at 94 % of the copy
@@ -53,7 +54,7 @@ namespace {
 constexpr int kFew = 4, kMany = 8;
 constexpr int kSmWarps = 16;                            // that the registers of an SM hold
 constexpr int kStages = 2;                              // tiles of 32 tokens per warp in shared memory (three: 3 % slower)
-constexpr int kBins = 256;                              // that the units are counted by
+constexpr int kBins = 256;                              // that the dense form's units are counted by
 constexpr int kRowCost = 3;                             // pages' time that a row's end and the next one's start take
 constexpr int kMaxParts = 4;                            // CTAs of a row up to which they form a cluster
 constexpr int kGroup = 16, kMostFlat = 32;              // parts joined at a time where a row has more than kMostFlat
@@ -68,8 +69,8 @@ constexpr float kPMost = 32768.f;                       // most of a lane's sum 
 
 struct Params {
   int B, Hq, Hkv, G, k;
-  // Units of a row: row_units for every one (sparse, few rows; k or a few more, the last ones without a page), or 0:
-  // each row's own pages and row_cost more, counted by bins of bin_size sequences (dense) or rows (sparse).
+  // Units of a row.  Sparse: row_units for every one (k or a few more, the last ones without a page).  Dense: each
+  // row's own pages and row_cost more, counted by bins of bin_size sequences.
   int row_units, bin_size, row_cost;
   bool whole_parts;                     // dense: the units may become parts of rows, one per CTA
   int parts;                            // sparse: CTAs of a row that form a cluster (0 or 1: none)
@@ -285,14 +286,14 @@ __global__ void __launch_bounds__(32 * kWarps, kSmWarps / kWarps) attn_q4_kernel
   extern __shared__ __align__(128) uint8_t s_ring[];
   float4(*s_o)[8][32] = reinterpret_cast<float4(*)[8][32]>(s_ring);   // after a row's part: [warp][i][lane]
   __shared__ __align__(8) float s_m[kWarps][kMaxG], s_l[kWarps][kMaxG];
-  __shared__ int s_pre[kBins + 1];          // units before a bin of sequences (of one head; dense) or rows
+  __shared__ int s_pre[kBins + 1];          // dense: units before a bin of sequences (of one head)
   __shared__ int s_wsum[kWarps];
   __shared__ int s_last;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int rows = p.B * p.Hkv;
   wait_for_stream();
 
-  // pages of one head of sequence x (dense) or of row x (sparse), and its units where they are counted
+  // pages of one head of sequence x (dense) or of row x (sparse), and its units (dense)
   auto pages_of = [&](int x) {
     if (!DENSE) return min(max(p.n[x], 0), p.k);
     const int L = p.seq_len[x];
@@ -302,11 +303,10 @@ __global__ void __launch_bounds__(32 * kWarps, kSmWarps / kWarps) attn_q4_kernel
   int chunk = 1, row_cost = settled ? p.row_cost : 0;   // pages of a unit, units that a row has more
   auto units_of = [&](int x) {
     const int pages = pages_of(x);
-    return pages > 0 ? (DENSE && chunk > 1 ? (pages + chunk - 1) / chunk : pages) + row_cost : 0;
+    return pages > 0 ? (chunk > 1 ? (pages + chunk - 1) / chunk : pages) + row_cost : 0;
   };
-  const int counted = DENSE ? p.B : rows, per_item = DENSE ? p.Hkv : 1;
-  const int bins = p.row_units > 0 ? 0 : (counted + p.bin_size - 1) / p.bin_size;
-  if (bins > 0) {
+  const int bins = DENSE ? (p.B + p.bin_size - 1) / p.bin_size : 0;
+  if (DENSE) {
     constexpr int kPer = (kBins + kThreads - 1) / kThreads;
     int mine[kPer], sum = 0;
 #pragma unroll
@@ -314,9 +314,9 @@ __global__ void __launch_bounds__(32 * kWarps, kSmWarps / kWarps) attn_q4_kernel
       const int b = tid * kPer + i;
       mine[i] = 0;
       if (b < bins) {
-        for (int x = b * p.bin_size; x < min(counted, (b + 1) * p.bin_size); ++x) {
+        for (int x = b * p.bin_size; x < min(p.B, (b + 1) * p.bin_size); ++x) {
           mine[i] += units_of(x);
-          if (DENSE && blockIdx.x == 0 && (p.seq_len[x] < 0 || p.seq_len[x] > p.max_pages * kBk))
+          if (blockIdx.x == 0 && (p.seq_len[x] < 0 || p.seq_len[x] > p.max_pages * kBk))
             report(p.dev_err, MSA_DEVERR_BAD_LEN);
         }
       }
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(32 * kWarps, kSmWarps / kWarps) attn_q4_kernel
       // Few pages: a unit becomes a part of a row that is all a CTA has, if that makes the longest one at most
       // kRowCost pages longer (a row's end costs that much; 40 sequences of 437 to 1,825 tokens of one head 10.5 us
       // for 14.5).  ceil(x / c) <= x / c + 1, so as many fit.
-      const int total = s_pre[bins] * per_item, ctas = gridDim.x;
+      const int total = s_pre[bins] * p.Hkv, ctas = gridDim.x;
       const int pages = (total + ctas - rows - 1) / (ctas - rows);
       if (pages <= (total + ctas - 1) / ctas + kRowCost) chunk = max(pages, 1);
       else row_cost = p.row_cost;
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(32 * kWarps, kSmWarps / kWarps) attn_q4_kernel
       __syncthreads();                      // the pages' sums are read
     }
   }
-  const int64_t units = bins > 0 ? static_cast<int64_t>(s_pre[bins]) * per_item : static_cast<int64_t>(rows) * p.row_units;
+  const int64_t units = DENSE ? static_cast<int64_t>(s_pre[bins]) * p.Hkv : static_cast<int64_t>(rows) * p.row_units;
   const uint32_t pool_pages = static_cast<uint32_t>(p.num_pages);
   const uint32_t code_stride = static_cast<uint32_t>(p.c0), scale_stride = static_cast<uint32_t>(p.s0);
   const int64_t per = (units + gridDim.x - 1) / gridDim.x;
@@ -371,15 +371,15 @@ __global__ void __launch_bounds__(32 * kWarps, kSmWarps / kWarps) attn_q4_kernel
     int b, head, p0, row_pages, tokens;
     const int32_t* list;
     int item, rem;                          // sequence (dense) or row (sparse), and the unit within it
-    if (bins > 0) {
+    if (DENSE) {
       int x = 0, y = bins;                  // the last bin whose units start at or before u
       while (y - x > 1) {
         const int mid = (x + y) >> 1;
-        if (static_cast<int64_t>(s_pre[mid]) * per_item <= u) x = mid; else y = mid;
+        if (static_cast<int64_t>(s_pre[mid]) * p.Hkv <= u) x = mid; else y = mid;
       }
       item = x * p.bin_size;
-      rem = static_cast<int>(u - static_cast<int64_t>(s_pre[x]) * per_item);
-      for (row_pages = units_of(item); rem >= row_pages * per_item; row_pages = units_of(++item)) rem -= row_pages * per_item;
+      rem = static_cast<int>(u - static_cast<int64_t>(s_pre[x]) * p.Hkv);
+      for (row_pages = units_of(item); rem >= row_pages * p.Hkv; row_pages = units_of(++item)) rem -= row_pages * p.Hkv;
     } else {
       item = static_cast<int>(u / p.row_units);
       rem = static_cast<int>(u - static_cast<int64_t>(item) * p.row_units);
@@ -714,10 +714,10 @@ __global__ void __launch_bounds__(32 * kWarps, kSmWarps / kWarps) attn_q4_kernel
     __syncthreads();
   }
 
-  if (bins > 0) {          // rows without a page have no units
+  if (DENSE) {             // rows without a page have no units
     for (int r = blockIdx.x; r < rows; r += gridDim.x) {
       const int b = r / p.Hkv, head = r - b * p.Hkv;
-      if (pages_of(DENSE ? b : r) != 0) continue;
+      if (pages_of(b) != 0) continue;
       for (int h = warp; h < p.G; h += kWarps) {
         const int64_t at = static_cast<int64_t>(b) * p.Hq + head * p.G + h;
         *reinterpret_cast<uint2*>(p.O + at * kD + lane * 4) = make_uint2(0, 0);
@@ -792,7 +792,7 @@ msa_status launch_sparse_decode_q4(const msa_decode_q4_args& a, void* ws, cudaSt
   p.k = a.k;
   p.pt = a.pt; p.n = a.n; p.last_len = a.last_len;
   const int rows = a.B * a.Hkv;
-  int grid = room;
+  int grid = rows;
   if (rows <= room) {
     // Few rows: each is cut into equal parts, so that no CTA has pages of two rows (32 pages of 64 rows in runs of
     // 7 units, most of them across two rows, took a quarter longer).  Up to four parts are a cluster, which joins its
@@ -809,10 +809,9 @@ msa_status launch_sparse_decode_q4(const msa_decode_q4_args& a, void* ws, cudaSt
     grid = rows * parts;
     p.parts = parts == 2 || (parts <= kMaxParts && 4 * grid <= 3 * room) ? parts : 1;
   } else {
-    // Many rows: equal runs over the pages that the rows have, each row's change of pages counted as kRowCost
-    // more (192 sequences, a fifth of them short, 78.7 us: 17 % slower with none, 1 to 2 % with 2 or 4).
-    p.bin_size = (rows + kBins - 1) / kBins;
-    p.row_cost = kRowCost;
+    // Many rows: a CTA each, a new one where one ends.  (Equal runs of pages over the CTAs that run at once cut rows
+    // and join them: 192 sequences of 16 pages 87 us for 80, 116 of 4 pages 27.4 for 20.7.)
+    p.row_units = a.k;
   }
   return launch<false, kFew, false>(p, grid, a.scratch_zeroed, stream);
 }
