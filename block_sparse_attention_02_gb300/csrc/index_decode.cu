@@ -286,7 +286,7 @@ index_decode_kernel(const __grid_constant__ CUtensorMap kmap, const Params p) {
     } else {
       const int L = p.seq_len[b];
       if (L < 1 || static_cast<int64_t>(L) > p.max_pages * p.Bk || (L - 1) / p.Bk >= p.nb_stride) {
-        if (blockIdx.x == 0) report(p.dev_err, MSA_DEVERR_BAD_LEN);
+        if (L != 0 && blockIdx.x == 0) report(p.dev_err, MSA_DEVERR_BAD_LEN);   // 0: an empty sequence
       } else {
         own = (L - 1) / p.Bk;
       }
@@ -344,7 +344,7 @@ index_decode_kernel(const __grid_constant__ CUtensorMap kmap, const Params p) {
     }
   }
   if (!MQ && p.sel != nullptr && blockIdx.x == 0) {
-    // rows with nothing to score: own block only (or nothing for a bad length)
+    // rows with nothing to score: own block only (or nothing for an empty sequence and a bad length)
     for (int r = tid; r < p.B * p.Hkv; r += kThreads) {
       const int b = r / p.Hkv;
       if (s_own[b] != 0) continue;

@@ -37,7 +37,8 @@ struct RowInfo {
   int own;            // own block = number of candidates
   int32_t* sel;
   int32_t* cnt;
-  bool valid;
+  bool valid;         // false: nothing is selected
+  bool bad;           // and the length is no empty sequence's either
 };
 
 __device__ __forceinline__ RowInfo row_info(const msa_topk_args& a, int64_t row) {
@@ -52,12 +53,14 @@ __device__ __forceinline__ RowInfo row_info(const msa_topk_args& a, int64_t row)
     const int64_t q0 = a.mode == MSA_MODE_CHUNK ? a.q_pos[b] : 0;
     const int64_t pos = q0 + s;
     r.valid = q0 >= 0 && (q0 + a.S - 1) / a.Bk < a.nb_stride;
+    r.bad = !r.valid;
     r.own = r.valid ? static_cast<int>(pos / a.Bk) : 0;
   } else {
     const int64_t g = row % a.Hkv, b = row / a.Hkv;
     r.c = a.C + b * a.C_stride[0] + g * a.C_stride[1];
     const int L = a.seq_len[b];
     r.valid = L >= 1 && (L - 1) / a.Bk < a.nb_stride;
+    r.bad = !r.valid && L != 0;
     r.own = r.valid ? (L - 1) / a.Bk : 0;
   }
   r.sel = a.sel + row * a.k;
@@ -84,7 +87,7 @@ topk_warp_kernel(const msa_topk_args a, int64_t rows) {
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarpsPerCta + wid;
   if (row >= rows) return;
   RowInfo r = row_info(a, row);
-  if (!r.valid && lane == 0) report(a.dev_err, MSA_DEVERR_BAD_LEN);
+  if (r.bad && lane == 0) report(a.dev_err, MSA_DEVERR_BAD_LEN);
   const int m = a.k - 1;
   const int n = r.own;
   if (!r.valid || n <= m) {
@@ -119,7 +122,7 @@ topk_cta_kernel(const msa_topk_args a, int64_t rows) {
   const int64_t row = blockIdx.x;
   if (row >= rows) return;
   RowInfo r = row_info(a, row);
-  if (!r.valid && tid == 0) report(a.dev_err, MSA_DEVERR_BAD_LEN);
+  if (r.bad && tid == 0) report(a.dev_err, MSA_DEVERR_BAD_LEN);
   const int m = a.k - 1;
   const int n = r.own;
   if (!r.valid || n <= m) {

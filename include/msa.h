@@ -125,9 +125,10 @@ const char *msa_status_string(msa_status s);
  *           nb_stride >= max over b of ceil(L_b / Bk) (entries past the own
  *           block, up to nb_stride, are written -inf).
  *   Page ids outside [0, num_pages) are not read: the block gets -inf and
- *   MSA_DEVERR_BAD_PAGE is raised.  A sequence whose length is outside
- *   [1, max_pages * Bk], or whose own block is not below nb_stride, is not
- *   scored (its row stays -inf) and raises MSA_DEVERR_BAD_LEN.
+ *   MSA_DEVERR_BAD_PAGE is raised.  A length of 0 is an empty sequence (a free
+ *   row of a batch): its row stays -inf, no error.  A sequence whose length is
+ *   outside [0, max_pages * Bk], or whose own block is not below nb_stride, is
+ *   not scored (its row stays -inf) and raises MSA_DEVERR_BAD_LEN.
  * CHUNK: queries as in PREFILL (q_idx, w and C with the same shapes and
  *   strides, S = queries per sequence); index keys in pages as in DECODE
  *   (k_idx page pool, num_pages, seq_pt, max_pages; group stride 0 allowed).
@@ -207,8 +208,8 @@ msa_status msa_index_score(const msa_index_args *args, msa_stream_t stream);
  *     block (q_pos[b] + S - 1) / Bk is not below nb_stride, gets count 0 and
  *     all -1 selections in every row, and MSA_DEVERR_BAD_LEN.
  * Scores are compared as fp32 (-0 equals +0); NaN scores rank below -inf.
- * A decode row whose length is outside [1, nb_stride * Bk] gets count 0, an
- * all -1 selection and MSA_DEVERR_BAD_LEN.
+ * A decode row of length 0 gets count 0 and an all -1 selection; one whose
+ * length is outside [0, nb_stride * Bk] gets the same and MSA_DEVERR_BAD_LEN.
  * ------------------------------------------------------------------------ */
 typedef struct msa_topk_args {
     msa_mode mode;
@@ -234,7 +235,8 @@ msa_status msa_topk_blocks(const msa_topk_args *args, msa_stream_t stream);
  *     pt[r][s]    = seq_pt[b][sel[b][g][s]]  for s < count[b][g], else -1
  *     n[r]        = count[b][g]
  *     last_len[r] = valid tokens of the row's last selected page (its own
- *                   block): seq_len[b] - Bk * ((seq_len[b] - 1) / Bk).
+ *                   block): seq_len[b] - Bk * ((seq_len[b] - 1) / Bk),
+ *                   0 for an empty sequence.
  * sel [B, Hkv, k], count [B, Hkv], seq_pt [B, max_pages], seq_len [B];
  * pt [B*Hkv, k], n [B*Hkv], last_len [B*Hkv] (all int32, dense).
  * A selected index outside [0, own block] yields page -1 and MSA_DEVERR_BAD_SEL.
