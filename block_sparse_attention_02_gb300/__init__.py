@@ -481,7 +481,9 @@ def msa_plan_step(seq_len: torch.Tensor, new_len: torch.Tensor, seq_pt: torch.Te
     seq_len, new_len [B] int32 (cached and new tokens); seq_pt [B,max_pages] int32, written where pages are given;
     free_pages [F] int32 with free_count [1] int32 (a stack of page ids).  Outputs: seq_len_out [B] (may be seq_len),
     free_count_out [1] (may be free_count), cu [B+1], and for N token rows tok_slot [N] int64, tok_pos and tok_seq [N]
-    int32 (-1 in rows past the last token and in those of requests that were not served).
+    int32 (-1 in rows past the last token and in those of requests that were not served).  Token rows are packed, in the
+    order of the requests; the attention calls take a row per request (its newest token's is cu[b + 1] - 1, if tok_seq
+    there is b).
     """
     _call("msa_plan_step", _abi.binding().plan_step(
         seq_len, new_len, seq_pt, free_pages, free_count, seq_len_out, free_count_out, cu, tok_slot, tok_pos, tok_seq,
@@ -602,8 +604,8 @@ def decode_step(inp: Dict[str, torch.Tensor], k: int, bufs: Optional[Dict[str, t
                 scratch_zeroed: bool = False) -> Dict[str, torch.Tensor]:
     """One MSA decode step: a1 index score -> a2 top-k -> a3 page table -> a5/a6 attention.
 
-    ``inp`` holds Q, q_idx, w, kidx_pool, K_pool, V_pool, seq_pt, seq_len (device tensors).
-    With ``fused`` (default) a1-a3 run in one index-score call; otherwise the
+    ``inp`` holds Q, q_idx, w, kidx_pool, K_pool, V_pool, seq_pt, seq_len (device tensors; a sequence of length 0 is
+    empty: O = 0, LSE = -inf).  With ``fused`` (default) a1-a3 run in one index-score call; otherwise the
     four entry points are called one by one.  ``scratch_zeroed`` skips the
     counter clears (valid with ``decode_buffers`` scratch that every previous
     call left zero, i.e. no device error was raised).
@@ -643,7 +645,8 @@ def decode_step_q4(inp: Dict[str, torch.Tensor], cache: Q4Cache, k: int,
                    bufs: Optional[Dict[str, torch.Tensor]] = None, softmax_scale: float = 0.0, stream=None,
                    scratch_zeroed: bool = False) -> Dict[str, torch.Tensor]:
     """``decode_step`` with K and V in a 4-bit cache: the index branch and selection are the same (``inp`` holds Q,
-    q_idx, w, kidx_pool, seq_pt, seq_len), the attention reads ``cache``."""
+    q_idx, w, kidx_pool, seq_pt, seq_len), the attention reads ``cache``.  Row b of Q, q_idx and w is sequence b's
+    query; a sequence of length 0 is empty (O = 0, LSE = -inf)."""
     B, Hq, _ = inp["Q"].shape
     Hkv = cache.K_codes.shape[1]
     if bufs is None:

@@ -554,7 +554,10 @@ msa_status msa_cache_append(const msa_append_args *args, msa_stream_t stream);
  *     free_count_out       = free_count - (pages taken)
  * Rows from cu[B] to N (the padding of a captured graph) and the rows of a
  * request that is not served get tok_seq = tok_pos = tok_slot = -1, which the
- * calls that take slots and positions leave alone.
+ * calls that take slots and positions leave alone.  The attention calls take one
+ * row per request, not per token row: request b's newest token is row cu[b + 1] - 1
+ * if tok_seq of that row is b; otherwise b brings no token in this step, and a
+ * length of 0 makes it an empty sequence there.
  *   - A request whose pages go past the stack (off_b + need > free_count) is not
  *     served: its length stays, its rows are -1, MSA_DEVERR_NO_PAGES.  Every
  *     later request that needs a page is then refused too.
