@@ -8,8 +8,8 @@
 // The angle.  A position of a million times a frequency near 1 needs more than
 // fp32's 24 bits.  Only the fraction of a turn matters, so each lane keeps its
 // frequencies as turns per token in 64-bit fixed point (2^64 = one turn) and
-// pos * that, modulo 2^64, is the angle: one integer product, off by less than 2^-43
-// turns at 2^20 tokens.
+// pos * that, modulo 2^64, is the angle: one integer product, off by at most 2^-43
+// turns at 2^20 tokens (two units of 2^-64 turns a token), for frequencies of any size.
 //
 // Layout: D / 16 lanes hold a head, 16 values each as two 16-byte chunks that
 // contain both members of every pair (chunks i and i + rot / 16 for split pairs,
@@ -73,17 +73,23 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-// f / (2 pi) modulo 1 in units of 2^-64, off by less than two of them: the 24 bits of f times 1 / (2 pi) to 96 bits,
-// shifted.  (In doubles, which this GPU has few units for: 500 tokens 7 % slower.)
+// 1 / (2 pi), 2^-1 in the top bit of the first word: enough words for the 96 bits at any power of two of a float.
+__constant__ uint32_t kTurnWords[7] = {0x28be60db, 0x9391054a, 0x7f09d5f4, 0x7d4d3770, 0x36d8a566, 0x4f10e410, 0x7f9458ea};
+// f / (2 pi) modulo 1 in units of 2^-64, off by two of them at most, for any finite f (Payne and Hanek, "Radian
+// reduction for trigonometric functions", 1983: of 1 / (2 pi) only the bits that reach the fraction are multiplied): f's
+// 24 bits times 96 of 1 / (2 pi), shifted.  (In doubles, which this GPU has few units for: 500 tokens 7 % slower.)
 __device__ __forceinline__ uint64_t turns_of(float f) {
   const uint32_t bits = __float_as_uint(f), ex = bits >> 23 & 0xff;
-  if (ex >= 150) {         // 2^23 or more, infinite or NaN
-    const double t = static_cast<double>(f) * 0.15915494309189533577;
-    return __double2ull_rz((t - floor(t)) * 18446744073709551616.0);
-  }
   const uint64_t m = (bits & 0x7fffffu) | (ex != 0 ? 0x800000u : 0u);       // f = m * 2^(max(ex, 1) - 150)
-  const uint64_t low = m * 0x7f09d5f4u, mid = m * 0x9391054au + (low >> 32), top = m * 0x28be60dbu + (mid >> 32);   // m / (2 pi) * 2^96
-  const uint32_t down = 150 - max(ex, 1u);                                  // of top and mid's 32 bits, from 2^-64 turns
+  uint32_t w0 = 0x28be60db, w1 = 0x9391054a, w2 = 0x7f09d5f4;
+  if (ex > 150) {          // 2^24 or more: the bits before the window give whole turns
+    const uint32_t up = ex - 150, i = min(up >> 5, 3u);                     // (3: infinite and NaN)
+    w0 = __funnelshift_l(kTurnWords[i + 1], kTurnWords[i], up);
+    w1 = __funnelshift_l(kTurnWords[i + 2], kTurnWords[i + 1], up);
+    w2 = __funnelshift_l(kTurnWords[i + 3], kTurnWords[i + 2], up);
+  }
+  const uint64_t low = m * w2, mid = m * w1 + (low >> 32), top = m * w0 + (mid >> 32);   // of the product's 2^-96 turns
+  const uint32_t down = ex < 150 ? 150 - max(ex, 1u) : 0;                   // of top and mid's 32 bits, from 2^-64 turns
   uint64_t t = down < 32 ? top << (32 - down) | static_cast<uint32_t>(mid) >> down : down < 96 ? top >> (down - 32) : 0;
   return bits >> 31 ? 0 - t : t;
 }
@@ -117,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const N
   const int64_t items = p.N * p.parts, stride = static_cast<int64_t>(gridDim.x) * kWarps;
   const int64_t item0 = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
 
-  // The loads run kAhead steps before the work, across tokens (they need no position): each lane
+  // The loads run kAhead - 1 steps before the work, across tokens (they need no position): each lane
   // copies its two chunks into shared memory places that it alone reads.
   const uint32_t ring = smem_u32(s_ring[warp]) + lane * 16;
   int64_t load_item = item0, load_n = 0;
@@ -159,10 +165,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const N
   }
   // turns per token, in units of 2^-64 turns, of pairs lane and lane + 32
   uint64_t turns[D / 64];
+  float half_turns[D / 64];                   // of the angle's top 32 bits' unit: 2^-31, or NaN for no finite frequency
 #pragma unroll
   for (int e = 0; e < D / 64; ++e) {
     turns[e] = 0;
-    if (lane + 32 * e < p.rot / 2) turns[e] = turns_of(p.inv_freq[lane + 32 * e]);
+    half_turns[e] = 4.656612873077393e-10f;
+    if (lane + 32 * e < p.rot / 2) {
+      const float f = p.inv_freq[lane + 32 * e];
+      turns[e] = turns_of(f);
+      if (!isfinite(f)) half_turns[e] = NAN;
+    }
   }
   __syncthreads();
 
@@ -189,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const N
       if (lane + 32 * e < p.rot / 2) {
         const int32_t a = static_cast<int32_t>((turns[e] * static_cast<uint64_t>(max(pos, 0))) >> 32);
         float2 cs;
-        sincospif(static_cast<float>(a) * 4.656612873077393e-10f, &cs.y, &cs.x);   // 2^-31: half turns
+        sincospif(static_cast<float>(a) * half_turns[e], &cs.y, &cs.x);
         s_turn[warp][lane + 32 * e] = cs;
       }
     }

@@ -626,6 +626,7 @@ msa_status msa_release_pages(const msa_release_args *args, msa_stream_t stream);
  *     pos[r] * inv_freq[i], i < rot / 2:  (a cos - b sin, b cos + a sin);
  *     pair i is (i, i + rot / 2), or (2i, 2i + 1) with interleaved = 1
  * fp32 throughout, the angle reduced in 64 bits, one rounding to bf16 at the end.
+ * inv_freq may be of any finite size; a pair whose frequency is not finite becomes NaN.
  *     Q [N, Hq, D], K and V [N, Hkv, D] bf16, strides (n, h); Q_out [N, Hq, D]
  *     q_weight, k_weight [D], bf16 or (weight_fp32 = 1) fp32; pos [N] int32;
  *     inv_freq [rot / 2] fp32; rot a multiple of 16 up to D, 0: no rotation
