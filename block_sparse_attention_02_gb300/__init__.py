@@ -458,11 +458,6 @@ def msa_cache_append(K_new: torch.Tensor, V_new: torch.Tensor, kidx_new: torch.T
 # _msa_binding (csrc/binding.cpp), which raises ValueError where one does not fit.
 # ---------------------------------------------------------------------------
 
-def _call(name: str, status: int) -> None:
-    if status:
-        _abi.check(status, name)
-
-
 def plan_buffers(B: int, N: int, device) -> Dict[str, torch.Tensor]:
     """Outputs of ``msa_plan_step`` for B requests and N token rows."""
     dev = torch.device(device)
@@ -485,9 +480,11 @@ def msa_plan_step(seq_len: torch.Tensor, new_len: torch.Tensor, seq_pt: torch.Te
     order of the requests; the attention calls take a row per request (its newest token's is cu[b + 1] - 1, if tok_seq
     there is b).
     """
-    _call("msa_plan_step", _abi.binding().plan_step(
+    status = _abi.binding().plan_step(
         seq_len, new_len, seq_pt, free_pages, free_count, seq_len_out, free_count_out, cu, tok_slot, tok_pos, tok_seq,
-        num_pages, dev_err, stream))
+        num_pages, dev_err, stream)
+    if status:
+        _abi.check(status, "msa_plan_step")
 
 
 def msa_release_pages(seq_len: torch.Tensor, done: torch.Tensor, seq_pt: torch.Tensor, free_pages: torch.Tensor,
@@ -498,8 +495,10 @@ def msa_release_pages(seq_len: torch.Tensor, done: torch.Tensor, seq_pt: torch.T
     seq_len, done [B] int32, seq_pt [B,max_pages] int32 (left as it is), free_pages [F] int32 (written above
     free_count), free_count [1]; seq_len_out [B] and free_count_out [1] may be the inputs.
     """
-    _call("msa_release_pages", _abi.binding().release_pages(
-        seq_len, done, seq_pt, free_pages, free_count, seq_len_out, free_count_out, dev_err, stream))
+    status = _abi.binding().release_pages(
+        seq_len, done, seq_pt, free_pages, free_count, seq_len_out, free_count_out, dev_err, stream)
+    if status:
+        _abi.check(status, "msa_release_pages")
 
 
 def msa_qk_norm_rope(Q: torch.Tensor, K: Optional[torch.Tensor], pos: torch.Tensor, inv_freq: Optional[torch.Tensor],
@@ -515,8 +514,10 @@ def msa_qk_norm_rope(Q: torch.Tensor, K: Optional[torch.Tensor], pos: torch.Tens
     K_out [N,Hkv,D], or with ``slots`` [N] int64 the page pool [P,Hkv,Bk,D] that K goes into, and V into V_out.
     Q_out may be Q and K_out may be K.  Rows with pos < 0 are left out.
     """
-    _call("msa_qk_norm_rope", _abi.binding().qk_norm_rope(
-        Q, K, pos, inv_freq, Q_out, K_out, V, V_out, slots, q_weight, k_weight, eps, interleaved, dev_err, stream))
+    status = _abi.binding().qk_norm_rope(
+        Q, K, pos, inv_freq, Q_out, K_out, V, V_out, slots, q_weight, k_weight, eps, interleaved, dev_err, stream)
+    if status:
+        _abi.check(status, "msa_qk_norm_rope")
 
 
 class Q4Cache(NamedTuple):
@@ -540,13 +541,17 @@ def q4_cache(num_pages: int, Hkv: int, device, k_scale: float = 1.0, v_scale: fl
 def msa_cache_append_q4(K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, cache: Q4Cache, *,
                         dev_err: Optional[torch.Tensor] = None, stream=None) -> None:
     """Stores K, V [N,Hkv,D] bf16 in 4 bits at slots [N] int64 (page * Bk + row; < 0: not stored) (see msa.h)."""
-    _call("msa_cache_append_q4", _abi.binding().cache_append_q4(K, V, slots, cache, dev_err, stream))
+    status = _abi.binding().cache_append_q4(K, V, slots, cache, dev_err, stream)
+    if status:
+        _abi.check(status, "msa_cache_append_q4")
 
 
 def msa_cache_expand_q4(cache: Q4Cache, pages: torch.Tensor, K_out: torch.Tensor, V_out: torch.Tensor, *,
                         dev_err: Optional[torch.Tensor] = None, stream=None) -> None:
     """The bf16 values of pages [n] int32 into K_out, V_out [n,Hkv,Bk,D] (see msa.h)."""
-    _call("msa_cache_expand_q4", _abi.binding().cache_expand_q4(cache, pages, K_out, V_out, dev_err, stream))
+    status = _abi.binding().cache_expand_q4(cache, pages, K_out, V_out, dev_err, stream)
+    if status:
+        _abi.check(status, "msa_cache_expand_q4")
 
 
 def msa_attn_decode_q4_workspace_size(B: int, Hkv: int) -> int:
@@ -559,8 +564,10 @@ def msa_sparse_attn_decode_q4(Q: torch.Tensor, cache: Q4Cache, pt: torch.Tensor,
                               scratch_zeroed: bool = False) -> None:
     """``msa_sparse_attn_decode`` over a 4-bit cache (see msa.h): Q [B,Hq,D] bf16, pt [B*Hkv,k], n, last_len [B*Hkv]
     int32; O [B,Hq,D] bf16, LSE [B,Hq] fp32; ws of ``msa_attn_decode_q4_workspace_size`` bytes."""
-    _call("msa_sparse_attn_decode_q4", _abi.binding().sparse_attn_decode_q4(
-        Q, cache, pt, n, last_len, O, LSE, ws, softmax_scale, dev_err, stream, scratch_zeroed))
+    status = _abi.binding().sparse_attn_decode_q4(
+        Q, cache, pt, n, last_len, O, LSE, ws, softmax_scale, dev_err, stream, scratch_zeroed)
+    if status:
+        _abi.check(status, "msa_sparse_attn_decode_q4")
 
 
 def msa_dense_attn_decode_q4(Q: torch.Tensor, cache: Q4Cache, seq_pt: torch.Tensor, seq_len: torch.Tensor,
@@ -569,8 +576,10 @@ def msa_dense_attn_decode_q4(Q: torch.Tensor, cache: Q4Cache, seq_pt: torch.Tens
                              scratch_zeroed: bool = False) -> None:
     """``msa_dense_attn_decode`` over a 4-bit cache (see msa.h): Q [B,Hq,D] bf16, seq_pt [B,max_pages], seq_len [B]
     int32 (0: an empty sequence); O [B,Hq,D] bf16, LSE [B,Hq] fp32; ws as for ``msa_sparse_attn_decode_q4``."""
-    _call("msa_dense_attn_decode_q4", _abi.binding().dense_attn_decode_q4(
-        Q, cache, seq_pt, seq_len, O, LSE, ws, softmax_scale, dev_err, stream, scratch_zeroed))
+    status = _abi.binding().dense_attn_decode_q4(
+        Q, cache, seq_pt, seq_len, O, LSE, ws, softmax_scale, dev_err, stream, scratch_zeroed)
+    if status:
+        _abi.check(status, "msa_dense_attn_decode_q4")
 
 
 # ---------------------------------------------------------------------------

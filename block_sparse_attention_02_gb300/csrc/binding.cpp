@@ -189,10 +189,18 @@ int q4_cache(PyObject* o, int dev, msa_q4_cache* c) {
   return as_int(H, "Hkv");
 }
 
-// Runs the entry point with the tensors' device current.
+// Lets other Python threads run while it lives: a launch waits where the stream's queue is full.
+struct Unlocked {
+  PyThreadState* const state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
+// Runs the entry point with the tensors' device current and the interpreter's lock released.  (The arguments, and
+// with them the tensors, are held by the caller.)
 template <class F>
 msa_status on_device(int dev, F f) {
   const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
+  const Unlocked unlocked;
   return f();
 }
 
