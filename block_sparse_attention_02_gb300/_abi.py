@@ -241,6 +241,10 @@ def binding():
         except ImportError as e:
             raise RuntimeError("_msa_binding is missing: build it with "
                                "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+        import torch
+        if _msa_binding.built_for != str(torch.__version__):
+            raise RuntimeError(f"_msa_binding was built for torch {_msa_binding.built_for}, this is {torch.__version__}: build it "
+                               "again with `python -c 'import __graft_entry__ as g; g.build()'`")
         _binding = _msa_binding
     return _binding
 

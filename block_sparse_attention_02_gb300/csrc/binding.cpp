@@ -444,4 +444,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_msa_binding", nullptr, -1, method
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__msa_binding(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__msa_binding(void) {
+  PyObject* const m = PyModule_Create(&module);
+  if (m != nullptr && PyModule_AddStringConstant(m, "built_for", MSA_BUILT_FOR) != 0) {   // the torch whose headers it has
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
