@@ -489,14 +489,15 @@ def msa_plan_step(seq_len: torch.Tensor, new_len: torch.Tensor, seq_pt: torch.Te
 
 def msa_release_pages(seq_len: torch.Tensor, done: torch.Tensor, seq_pt: torch.Tensor, free_pages: torch.Tensor,
                       free_count: torch.Tensor, seq_len_out: torch.Tensor, free_count_out: torch.Tensor, *,
-                      dev_err: Optional[torch.Tensor] = None, stream=None) -> None:
+                      num_pages: Optional[int] = None, dev_err: Optional[torch.Tensor] = None, stream=None) -> None:
     """Returns the pages of every request with done[b] != 0 to the stack (see msa.h, msa_release_pages).
 
     seq_len, done [B] int32, seq_pt [B,max_pages] int32 (left as it is), free_pages [F] int32 (written above
-    free_count), free_count [1]; seq_len_out [B] and free_count_out [1] may be the inputs.
+    free_count), free_count [1]; seq_len_out [B] and free_count_out [1] may be the inputs.  A page id that goes back and
+    is below 0, or at or past ``num_pages`` where that is given, is named in dev_err.
     """
     status = _abi.binding().release_pages(
-        seq_len, done, seq_pt, free_pages, free_count, seq_len_out, free_count_out, dev_err, stream)
+        seq_len, done, seq_pt, free_pages, free_count, seq_len_out, free_count_out, num_pages, dev_err, stream)
     if status:
         _abi.check(status, "msa_release_pages")
 

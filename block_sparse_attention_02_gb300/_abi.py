@@ -125,7 +125,7 @@ class ReleaseArgs(C.Structure):
     _fields_ = [
         ("B", C.c_int), ("Bk", C.c_int), ("seq_len", _p), ("done", _p), ("seq_pt", _p), ("max_pages", C.c_int64),
         ("free_pages", _p), ("free_cap", C.c_int64), ("free_count", _p),
-        ("seq_len_out", _p), ("free_count_out", _p), ("dev_err", _p),
+        ("seq_len_out", _p), ("free_count_out", _p), ("dev_err", _p), ("num_pages", C.c_int64),
     ]
 
 

@@ -148,7 +148,7 @@ msa_status msa::check_decode_args(const msa_decode_args* a) {
 
 extern "C" {
 
-int msa_version(void) { return 200; }
+int msa_version(void) { return 300; }
 
 const char* msa_last_error_string(void) { return g_last_error.c_str(); }
 
@@ -487,6 +487,8 @@ msa_status msa_release_pages(const msa_release_args* a, msa_stream_t stream) {
   g_last_error.clear();
   MSA_REQUIRE(a != nullptr, MSA_ERR_INVALID_ARG, "args is NULL");
   if (msa_status st = check_tables(a->B, a->Bk, a->max_pages, a->free_cap); st != MSA_OK) return st;
+  MSA_REQUIRE(a->num_pages >= 0 && a->num_pages < (int64_t(1) << 31), MSA_ERR_INVALID_ARG, "num_pages = %" PRId64,
+              a->num_pages);
   MSA_REQUIRE(a->B == 0 || (a->seq_len && a->done && a->seq_pt && a->seq_len_out), MSA_ERR_INVALID_ARG,
               "seq_len, done, seq_pt and seq_len_out must be non-NULL");
   MSA_REQUIRE(a->free_count && a->free_count_out && (a->free_cap == 0 || a->free_pages), MSA_ERR_INVALID_ARG,

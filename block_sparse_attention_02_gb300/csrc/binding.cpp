@@ -235,7 +235,7 @@ msa_status plan_step(PyObject* const* o) {
   return on_device(dev, [&] { return msa_plan_step(&a, s); });
 }
 
-// seq_len, done, seq_pt, free_pages, free_count, seq_len_out, free_count_out, dev_err, stream
+// seq_len, done, seq_pt, free_pages, free_count, seq_len_out, free_count_out, num_pages (None: not given), dev_err, stream
 msa_status release_pages(PyObject* const* o) {
   const at::Tensor& L = tensor(o[0], "seq_len");
   const int dev = device_of(L, "seq_len");
@@ -253,8 +253,12 @@ msa_status release_pages(PyObject* const* o) {
   a.free_count = dense<int32_t>(o[4], "free_count", at::kInt, dev, 1, 1);
   a.seq_len_out = dense<int32_t>(o[5], "seq_len_out", at::kInt, dev, 1, B);
   a.free_count_out = dense<int32_t>(o[6], "free_count_out", at::kInt, dev, 1, 1);
-  a.dev_err = err_word(o[7], dev);
-  msa_stream_t s = stream_of(o[8], dev);
+  if (o[7] != Py_None) {
+    a.num_pages = integer(o[7], "num_pages");
+    if (a.num_pages < 1) refuse("num_pages = %lld", static_cast<long long>(a.num_pages));
+  }
+  a.dev_err = err_word(o[8], dev);
+  msa_stream_t s = stream_of(o[9], dev);
   return on_device(dev, [&] { return msa_release_pages(&a, s); });
 }
 
@@ -431,7 +435,7 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef methods[] = {
     method<plan_step, 14>("plan_step"),
-    method<release_pages, 9>("release_pages"),
+    method<release_pages, 10>("release_pages"),
     method<qk_norm_rope, 15>("qk_norm_rope"),
     method<cache_append_q4, 6>("cache_append_q4"),
     method<cache_expand_q4, 6>("cache_expand_q4"),

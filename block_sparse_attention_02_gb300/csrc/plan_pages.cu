@@ -251,10 +251,14 @@ __global__ void __launch_bounds__(kPlanThreads) release_kernel(const msa_release
     }
     if (tid == 0) *p.free_count_out = static_cast<int>(count + back);
   }
+  bool bad = false;
   for (int64_t x = rank * blockDim.x + tid; x < back; x += ctas * blockDim.x) {
     const int b = last_at_most(s_off, B, static_cast<int>(x));
-    p.free_pages[count + x] = p.seq_pt[b * p.max_pages + (x - s_off[b])];
+    const int page = p.seq_pt[b * p.max_pages + (x - s_off[b])];
+    bad |= page < 0 || (p.num_pages != 0 && page >= p.num_pages);
+    p.free_pages[count + x] = page;
   }
+  if (bad) report(p.dev_err, MSA_DEVERR_BAD_PAGE);
 }
 
 // One CTA, a plain grid, or (an update in place with more than one CTA's rows) one cluster.

@@ -598,8 +598,11 @@ msa_status msa_plan_step(const msa_plan_args *args, msa_stream_t stream);
  * height.  seq_pt is left as it is.  A length outside [0, max_pages * Bk] of an
  * ended request is not returned and keeps its length (MSA_DEVERR_BAD_LEN);
  * pages past free_cap are dropped (MSA_DEVERR_NO_PAGES), and so is the part of a
- * free_count outside [0, free_cap].  seq_len_out may be seq_len and
- * free_count_out may be free_count.  B <= 4096. */
+ * free_count outside [0, free_cap].  Page ids go back as they stand in the table;
+ * one below 0, or with num_pages given one at or past it, raises
+ * MSA_DEVERR_BAD_PAGE: it would be handed out again, so the caller has to mend
+ * the stack.  seq_len_out may be seq_len and free_count_out may be free_count.
+ * B <= 4096. */
 typedef struct msa_release_args {
     int B, Bk;
     const int32_t *seq_len;       /* [B] */
@@ -612,6 +615,7 @@ typedef struct msa_release_args {
     int32_t *seq_len_out;         /* [B] */
     int32_t *free_count_out;      /* [1] */
     int32_t *dev_err;
+    int64_t num_pages;            /* 0: not given */
 } msa_release_args;
 
 msa_status msa_release_pages(const msa_release_args *args, msa_stream_t stream);
