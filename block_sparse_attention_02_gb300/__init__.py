@@ -14,6 +14,7 @@ and ``chunk_layer``) call the entry points in hot-path order: index score -> top
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 from typing import Dict, NamedTuple, Optional
 
@@ -56,6 +57,16 @@ def _stream(stream) -> C.c_void_p:
     if isinstance(stream, torch.cuda.Stream):
         return C.c_void_p(stream.cuda_stream)
     return C.c_void_p(int(stream))
+
+
+def _buffers_on(stream, device):
+    """Context of a pipeline's own buffers: torch gives them out, and fills them, in the order of the stream that the calls
+    run on (on the current stream, work queued there may still use the memory or fill it later)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 def _inner_contig(t: torch.Tensor, name: str):
@@ -365,7 +376,8 @@ def dense_decode_step(inp: Dict[str, torch.Tensor], bufs: Optional[Dict[str, tor
     B, Hq, _ = inp["Q"].shape
     Hkv = inp["K_pool"].shape[1]
     if bufs is None:
-        bufs = dense_decode_buffers(B, Hq, Hkv, inp["seq_pt"].shape[1], inp["Q"].device)
+        with _buffers_on(stream, inp["Q"].device):
+            bufs = dense_decode_buffers(B, Hq, Hkv, inp["seq_pt"].shape[1], inp["Q"].device)
     msa_dense_attn_decode(inp["Q"], inp["K_pool"], inp["V_pool"], inp["seq_pt"], inp["seq_len"], bufs["O"],
                           bufs["LSE"], bufs["ws"], softmax_scale=softmax_scale, dev_err=bufs["dev_err"],
                           stream=stream, scratch_zeroed=scratch_zeroed)
@@ -398,9 +410,10 @@ def dense_prefill_layer(inp: Dict[str, torch.Tensor], bufs: Optional[Dict[str, t
     B, S, Hq, _ = inp["Q"].shape
     if bufs is None:
         dev = inp["Q"].device
-        bufs = {"O": torch.empty(B, S, Hq, D, dtype=torch.bfloat16, device=dev),
-                "LSE": torch.empty(B, S, Hq, dtype=torch.float32, device=dev),
-                "dev_err": torch.zeros(1, dtype=torch.int32, device=dev)}
+        with _buffers_on(stream, dev):
+            bufs = {"O": torch.empty(B, S, Hq, D, dtype=torch.bfloat16, device=dev),
+                    "LSE": torch.empty(B, S, Hq, dtype=torch.float32, device=dev),
+                    "dev_err": torch.zeros(1, dtype=torch.int32, device=dev)}
     msa_dense_attn_prefill(inp["Q"], inp["K"], inp["V"], bufs["O"], bufs["LSE"], softmax_scale=softmax_scale,
                            dev_err=bufs["dev_err"], stream=stream)
     return bufs
@@ -623,7 +636,8 @@ def decode_step(inp: Dict[str, torch.Tensor], k: int, bufs: Optional[Dict[str, t
     B, Hq, _ = inp["Q"].shape
     Hkv = inp["K_pool"].shape[1]
     if bufs is None:
-        bufs = decode_buffers(B, Hq, Hkv, k, inp["seq_pt"].shape[1], inp["Q"].device)
+        with _buffers_on(stream, inp["Q"].device):
+            bufs = decode_buffers(B, Hq, Hkv, k, inp["seq_pt"].shape[1], inp["Q"].device)
     e = bufs["dev_err"]
     if fused:
         msa_index_score(MSA_MODE_DECODE, inp["q_idx"], inp["w"], inp["kidx_pool"], bufs["C"], seq_pt=inp["seq_pt"],
@@ -660,7 +674,8 @@ def decode_step_q4(inp: Dict[str, torch.Tensor], cache: Q4Cache, k: int,
     B, Hq, _ = inp["Q"].shape
     Hkv = cache.K_codes.shape[1]
     if bufs is None:
-        bufs = decode_q4_buffers(B, Hq, Hkv, k, inp["seq_pt"].shape[1], inp["Q"].device)
+        with _buffers_on(stream, inp["Q"].device):
+            bufs = decode_q4_buffers(B, Hq, Hkv, k, inp["seq_pt"].shape[1], inp["Q"].device)
     e = bufs["dev_err"]
     msa_index_score(MSA_MODE_DECODE, inp["q_idx"], inp["w"], inp["kidx_pool"], bufs["C"], seq_pt=inp["seq_pt"],
                     seq_len=inp["seq_len"], dev_err=e, stream=stream, k=k, sel=bufs["sel"], count=bufs["count"],
@@ -699,7 +714,8 @@ def prefill_layer(inp: Dict[str, torch.Tensor], k: int, bufs: Optional[Dict[str,
         if ws_bytes is None:
             sel_probe = torch.empty(1, 1, 1, k, dtype=torch.int32)
             ws_bytes = msa_sparse_attn_prefill_workspace_size(inp["Q"], inp["K"], sel_probe, min(S, 8192) * B)
-        bufs = prefill_buffers(B, S, Hq, Hkv, k, inp["Q"].device, ws_bytes)
+        with _buffers_on(stream, inp["Q"].device):
+            bufs = prefill_buffers(B, S, Hq, Hkv, k, inp["Q"].device, ws_bytes)
     e = bufs["dev_err"]
     msa_index_score(MSA_MODE_PREFILL, inp["q_idx"], inp["w"], inp["k_idx"], bufs["C"], dev_err=e, stream=stream)
     msa_topk_blocks(MSA_MODE_PREFILL, bufs["C"], k, bufs["sel"], bufs["count"], dev_err=e, stream=stream)
@@ -736,7 +752,8 @@ def chunk_layer(inp: Dict[str, torch.Tensor], k: int, bufs: Optional[Dict[str, t
             sel_probe = torch.empty(1, 1, 1, k, dtype=torch.int32)
             ws_bytes = msa_sparse_attn_prefill_workspace_size(inp["Q"], inp["K_pool"], sel_probe,
                                                               min(S, 8192) * B, max_pages=max_pages)
-        bufs = chunk_buffers(B, S, Hq, Hkv, k, max_pages, inp["Q"].device, ws_bytes)
+        with _buffers_on(stream, inp["Q"].device):
+            bufs = chunk_buffers(B, S, Hq, Hkv, k, max_pages, inp["Q"].device, ws_bytes)
     e = bufs["dev_err"]
     msa_index_score(MSA_MODE_CHUNK, inp["q_idx"], inp["w"], inp["kidx_pool"], bufs["C"], seq_pt=inp["seq_pt"],
                     q_pos=inp["q_pos"], dev_err=e, stream=stream)
