@@ -64,7 +64,7 @@ constexpr int kPart = kMaxG * kD + 2 * kMaxG;           // floats of a partial: 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPShift = 8.f;                          // P is held as 2^(z - m + 8)
-constexpr float kNoMax = -1e30f;                        // m before a first score: finite, so that no difference is NaN
+constexpr float kNoMax = -FLT_MAX;                      // m before a first score: finite, so that no difference is NaN
 constexpr float kPMost = 32768.f;                       // most of a lane's sum of P (fp16 ends at 65504)
 
 struct Params {
@@ -210,12 +210,14 @@ __device__ __forceinline__ void attend_tile(const uint32_t (&q)[16], const float
   }
   // P as 2^(z - m + 8): infinite against kNoMax, and 0 where z is -inf.  A sum above 2^15
   // means that some score passed m by more than 5: m follows and P is formed again.
+  // z is rounded before m goes off it, as m was: fused, scores of 2^24 and more left their product's rounding error, 2^x of
+  // which is anything.  8 - m is rounded down, so that P ends at 2^8 where that sum is not exact (m of 2^27 and more).
   float e[2][4], sum[2];
   auto form = [&] {
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) e[u][i] = ex2(fmaf(s[u][i], coef[i & 1], kPShift - st->m[i & 1]));
+      for (int i = 0; i < 4; ++i) e[u][i] = ex2(__fadd_rn(__fmul_rn(s[u][i], coef[i & 1]), __fsub_rd(kPShift, st->m[i & 1])));
 #pragma unroll
     for (int c = 0; c < 2; ++c) sum[c] = (e[0][c] + e[0][c + 2]) + (e[1][c] + e[1][c + 2]);
   };
