@@ -670,7 +670,11 @@ def decode_step_q4(inp: Dict[str, torch.Tensor], cache: Q4Cache, k: int,
                    scratch_zeroed: bool = False) -> Dict[str, torch.Tensor]:
     """``decode_step`` with K and V in a 4-bit cache: the index branch and selection are the same (``inp`` holds Q,
     q_idx, w, kidx_pool, seq_pt, seq_len), the attention reads ``cache``.  Row b of Q, q_idx and w is sequence b's
-    query; a sequence of length 0 is empty (O = 0, LSE = -inf)."""
+    query; a sequence of length 0 is empty (O = 0, LSE = -inf).  The step runs on the tensors' device."""
+    dev = inp["Q"].device
+    if dev.type == "cuda" and dev.index != torch.cuda.current_device():   # the index call would go to the current one
+        with torch.cuda.device(dev):
+            return decode_step_q4(inp, cache, k, bufs, softmax_scale, stream, scratch_zeroed)
     B, Hq, _ = inp["Q"].shape
     Hkv = cache.K_codes.shape[1]
     if bufs is None:
