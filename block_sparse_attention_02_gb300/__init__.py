@@ -747,15 +747,19 @@ def chunk_layer(inp: Dict[str, torch.Tensor], k: int, bufs: Optional[Dict[str, t
     pools K_pool, V_pool [P,Hkv,Bk,D] and kidx_pool [P,Hkv,Bk,dI], seq_pt
     [B,max_pages] and q_pos [B] int32 (the chunk's own tokens already in the
     pages).  Score rows span max_pages blocks unless ``bufs`` says otherwise.
+    With ``kv_seq_pt`` [B,max_pages] in ``inp`` K_pool and V_pool have a page table of
+    their own: the expanded pages of a 4-bit cache (``msa_cache_expand_q4``), beside
+    index keys in the cache's pages.
     """
     B, S, Hq, _ = inp["Q"].shape
     Hkv = inp["K_pool"].shape[1]
     max_pages = inp["seq_pt"].shape[1]
+    kv_pt = inp.get("kv_seq_pt", inp["seq_pt"])
     if bufs is None:
         if ws_bytes is None:
             sel_probe = torch.empty(1, 1, 1, k, dtype=torch.int32)
             ws_bytes = msa_sparse_attn_prefill_workspace_size(inp["Q"], inp["K_pool"], sel_probe,
-                                                              min(S, 8192) * B, max_pages=max_pages)
+                                                              min(S, 8192) * B, max_pages=kv_pt.shape[1])
         with _buffers_on(stream, inp["Q"].device):
             bufs = chunk_buffers(B, S, Hq, Hkv, k, max_pages, inp["Q"].device, ws_bytes)
     e = bufs["dev_err"]
@@ -765,5 +769,5 @@ def chunk_layer(inp: Dict[str, torch.Tensor], k: int, bufs: Optional[Dict[str, t
                     stream=stream)
     msa_sparse_attn_prefill(inp["Q"], inp["K_pool"], inp["V_pool"], bufs["sel"], bufs["count"], bufs["O"],
                             bufs["LSE"], bufs["ws"], softmax_scale=softmax_scale, dev_err=e, stream=stream,
-                            seq_pt=inp["seq_pt"], q_pos=inp["q_pos"])
+                            seq_pt=kv_pt, q_pos=inp["q_pos"])
     return bufs

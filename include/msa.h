@@ -717,7 +717,9 @@ msa_status msa_cache_append_q4(const msa_append_q4_args *args, msa_stream_t stre
 
 /* The bf16 values of n pages: K_out, V_out [n, Hkv, Bk, D] (dense) from pages
  * pages[i], for the calls that read bf16 pools (chunk prefill over a 4-bit
- * prefix).  A page id outside [0, num_pages) leaves its block of the outputs
+ * prefix: the outputs are pools of n pages with a table of their own, in which
+ * page pages[i] is page i; msa_sparse_attn_prefill takes that table, and the index
+ * score the cache's).  A page id outside [0, num_pages) leaves its block of the outputs
  * untouched and raises MSA_DEVERR_BAD_PAGE.  Values past bf16's range become infinite. */
 typedef struct msa_expand_q4_args {
     int64_t n;
