@@ -1,12 +1,12 @@
 """MiniMax Sparse Attention (MSA) hot path on one GB300 -- Python binding.
 
-Thin ctypes marshalling over ``libmsa.so`` (include/msa.h).  Every function
+Marshalling over ``libmsa.so`` (include/msa.h), in ctypes or C++.  Every function
 takes torch CUDA tensors, passes their pointers and element strides to the C
 entry point of the same name, and raises ``MSAError`` on a non-OK status.  All
 computation runs in the library's sm_103a kernels; there is no fallback path.
 PyTorch provides device memory and streams only.  The calls of the serving step around the
-cache (page tables, norm with rotation, the 4-bit cache and its attention) are marshalled in C++
-(``_msa_binding``): their kernels take a few microseconds.
+cache (page tables, norm with rotation, the 4-bit cache and its attention) go through a module in
+C++ (``_msa_binding``): their kernels take a few microseconds, and so would Python on their arguments.
 
 The pipelines at the bottom (``decode_step``, ``decode_step_q4``, ``prefill_layer``
 and ``chunk_layer``) call the entry points in hot-path order: index score -> top-k

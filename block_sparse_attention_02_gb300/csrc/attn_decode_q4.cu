@@ -29,7 +29,7 @@
 // shared memory at the end of a row's part.  Parts of a row are joined through the workspace by
 // the CTA that arrives last, or, if they are a few equal ones, through a cluster's shared memory.
 //
-// Bound: 257 instructions a warp for 16 tokens, 160 of them conversions, scalings and
+// Bound: 261 instructions a warp for 16 tokens, 164 of them conversions, scalings and
 // products, leave the SMs issuing in 60 % of their cycles at 94 % of the copy
 // rate (1,048,576 tokens 189 us, floor 178); 8 x 60,001 tokens 94 us (floor 82)
 // pay 6 us of starting, joining and ending besides.

@@ -14,9 +14,9 @@
 // wait for and the grid is as large as the rows ask for.
 //
 // Bound: latency (the lengths, the sums, one page id per row, the stores); the
-// 16 bytes written per token row are far below it.  8 requests 3.0 us, one kernel after
+// 16 bytes written per token row are far below it.  8 requests 2.9 us, one kernel after
 // another; with the release of ended requests, two launches, 64 requests (0.5 MB of rows and
-// table entries) 5.9 us, 1,024 requests (1.1 MB) 7.7 us.
+// table entries) 6.2 us, 1,024 requests (1.1 MB) 7.9 us.
 #include <cooperative_groups.h>
 
 #include <climits>

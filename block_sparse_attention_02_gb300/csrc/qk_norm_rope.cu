@@ -20,11 +20,12 @@
 // share the token's sines; with few tokens the heads are split over warps.
 //
 // Bound: HBM, every value read and written once: 65,536 tokens of 48 + 8 + 8 heads of
-// 128 in 319 us, 99 % of the copy rate.  Each lane copies its chunks into shared memory
+// 128 in 318 us, the copy rate.  Each lane copies its chunks into shared memory
 // three steps (of four or eight heads) ahead, across tokens (370 us with plain loads).  16
 // warps on an SM are enough, and more in flight serves HBM worse: 323 us with four steps ahead, 325 with 18 or
 // 20 warps and two, 338 with 24 and two, 351 with 24 and three.  4,097 tokens of 40 heads of 64,
-// which fit L2: 12.0 us, bound by issue (floor 6.2); 8 tokens: 3.4 us, a launch's latency.
+// which fit L2: 11.5 us (floor 6.2), bound by latency (issue 45 %): two rounds of tokens on 2,432 warps, each a
+// position, its sines and five steps; 8 tokens: 3.3 us, a launch's latency.
 #include "launch_early.cuh"
 #include "msa_internal.h"
 #include "msa_ptx.cuh"
