@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const N
   }
   // turns per token, in units of 2^-64 turns, of pairs lane and lane + 32
   uint64_t turns[D / 64];
-  float half_turns[D / 64];                   // of the angle's top 32 bits' unit: 2^-31, or NaN for no finite frequency
+  float half_turns[D / 64];                   // in a unit of an angle's top 32 bits: 2^-31, or NaN where the frequency is not finite
 #pragma unroll
   for (int e = 0; e < D / 64; ++e) {
     turns[e] = 0;

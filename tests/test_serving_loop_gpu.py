@@ -75,7 +75,7 @@ class Loop:
         v, B, N = self.v, self.v["B"], self.v["N"]
         for x in ("Q", "q_idx", "k_idx", "w", "K", "V"):
             v[x].copy_(torch.from_numpy(self.rng.standard_normal(v[x].shape)).to(v[x].dtype))
-        v["new_len"].copy_(i32(new)), v["done"].copy_(i32(done))
+        v["new_len"].copy_(i32(new)), v["done"].copy_(i32(done)), v["err"].zero_()
         before = {x: v[x].clone() for x in ("Q", "K", "k_idx")}
         host = lambda x: v[x].cpu().numpy().astype(np.int64)  # noqa: E731
         back = ref.release(host("seq_len"), done, host("seq_pt"), host("free_pages"), int(v["free_count"]))
@@ -102,7 +102,7 @@ class Loop:
                 self.fed[b].append((K[r], V[r]))
                 newest[b] = Q[r]
         assert [len(x) for x in self.fed] == host("seq_len").tolist()
-        assert int(v["bufs"]["dev_err"]) == 0
+        assert int(v["err"]) == want["err"] | back["err"] and int(v["bufs"]["dev_err"]) == 0
         for O, LSE in ((v["bufs"]["O"], v["bufs"]["LSE"]), (v["O"], v["LSE"])):
             for b in range(B):
                 if b not in newest:
