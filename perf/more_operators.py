@@ -272,7 +272,7 @@ def prepare(case, seed):
         s["O"] = torch.empty(B, Hq, D, dtype=torch.bfloat16, device="cuda")
         s["LSE"] = torch.empty(B, Hq, dtype=torch.float32, device="cuda")
         # scratch, as a program keeps it: zero-filled, and large enough for any split of the work
-        s["ws"] = torch.zeros(256 << 20, dtype=torch.uint8, device="cuda")
+        s["ws"] = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
     elif op == "window":
         B, S, Hq = case["B"], case["S"], case["Hq"]
         s |= {"Q": _bf16(g, B, S, Hq, D, scale=1.5), "scale": 1 / math.sqrt(D), "window": case["window"], "sinks": case["sinks"]}
@@ -539,8 +539,8 @@ def run(state):
             return {"seq_pt": s["pt_out"], "shares": s["shares_out"], "free": s["free_out"], "free_count": s["count_out"],
                     "move_src": s["move_src"], "move_dst": s["move_dst"], "pools": s["pools"]}
         if "K_pool" in s:
-            msa.msa_dense_attn_decode(s["Q"], s["K_pool"], s["V_pool"], s["seq_pt"], s["seq_len"], s["O"], s["LSE"], s["ws"],
-                                      window=s["window"], sinks=s["sinks"], dev_err=e, scratch_zeroed=True)
+            msa.msa_window_attn_decode(s["Q"], s["K_pool"], s["V_pool"], s["seq_pt"], s["seq_len"], s["O"], s["LSE"], s["ws"],
+                                       window=s["window"], sinks=s["sinks"], dev_err=e, scratch_zeroed=True)
             return [s["O"], s["LSE"]]
         cache = msa.Q8Cache(s["K_codes"], s["K_scales"], s["V_codes"], s["V_scales"])
         if s["op"] == "store":
