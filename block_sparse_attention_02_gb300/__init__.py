@@ -5,10 +5,10 @@ takes torch CUDA tensors, passes their pointers and element strides to the C
 entry point of the same name, and raises ``MSAError`` on a non-OK status.  All
 computation runs in the library's sm_103a kernels; there is no fallback path.
 PyTorch provides device memory and streams only.  The calls of the serving step around the
-cache (page tables, norm with rotation, the 4-bit cache and its attention) go through a module in
+cache (page tables, norm with rotation, the 4-bit and 8-bit caches and their attention) go through a module in
 C++ (``_msa_binding``): their kernels take a few microseconds, and so would Python on their arguments.
 
-The pipelines at the bottom (``decode_step``, ``decode_step_q4``, ``prefill_layer``
+The pipelines at the bottom (``decode_step``, ``decode_step_q4``, ``decode_step_q8``, ``prefill_layer``
 and ``chunk_layer``) call the entry points in hot-path order: index score -> top-k
 -> (decode: page table) -> sparse attention (with its log-sum-exp merge).
 """
@@ -33,6 +33,9 @@ __all__ = [
     "msa_plan_step", "msa_release_pages", "plan_buffers", "msa_qk_norm_rope", "Q4Cache", "q4_cache",
     "msa_cache_append_q4", "msa_cache_expand_q4", "msa_attn_decode_q4_workspace_size", "msa_sparse_attn_decode_q4",
     "msa_dense_attn_decode_q4", "decode_q4_buffers", "decode_step_q4",
+    "Q8Cache", "q8_cache", "msa_cache_append_q8", "msa_cache_expand_q8", "msa_attn_decode_q8_workspace_size",
+    "msa_sparse_attn_decode_q8", "msa_dense_attn_decode_q8", "decode_q8_buffers", "decode_step_q8",
+    "msa_window_attn_decode", "msa_window_attn_decode_workspace_size",
     "lib", "MSAError",
     "MSA_MODE_PREFILL", "MSA_MODE_DECODE", "MSA_MODE_CHUNK", "MSA_DEVERR_TIMEOUT", "MSA_DEVERR_BAD_PAGE",
     "MSA_DEVERR_BAD_SEL", "MSA_DEVERR_BAD_LEN", "MSA_DEVERR_NO_PAGES", "Bk", "D", "dI",
@@ -596,6 +599,89 @@ def msa_dense_attn_decode_q4(Q: torch.Tensor, cache: Q4Cache, seq_pt: torch.Tens
         _abi.check(status, "msa_dense_attn_decode_q4")
 
 
+class Q8Cache(NamedTuple):
+    """A paged K/V cache in 8 bits (see msa.h): E4M3 codes [P,Hkv,Bk,D] and a scale byte for each page and head [P,Hkv]
+    (2^(byte - 127)), uint8."""
+    K_codes: torch.Tensor
+    K_scales: torch.Tensor
+    V_codes: torch.Tensor
+    V_scales: torch.Tensor
+
+
+def q8_cache(num_pages: int, Hkv: int, device) -> Q8Cache:
+    """An 8-bit cache of zeros."""
+    def pool(*shape):
+        return torch.zeros(num_pages, Hkv, *shape, dtype=torch.uint8, device=torch.device(device))
+    return Q8Cache(pool(Bk, D), pool(), pool(Bk, D), pool())
+
+
+def msa_cache_append_q8(K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, cache: Q8Cache, *,
+                        dev_err: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Stores K, V [N,Hkv,D] bf16 in 8 bits at slots [N] int64 (page * Bk + row; < 0: not stored) (see msa.h).  The tokens
+    of a page are consecutive rows in consecutive slots, as ``msa_plan_step`` lays them out; a page fills from row 0 on."""
+    status = _abi.binding().cache_append_q8(K, V, slots, cache, dev_err, stream)
+    if status:
+        _abi.check(status, "msa_cache_append_q8")
+
+
+def msa_cache_expand_q8(cache: Q8Cache, pages: torch.Tensor, K_out: torch.Tensor, V_out: torch.Tensor, *,
+                        dev_err: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The bf16 values of pages [n] int32 into K_out, V_out [n,Hkv,Bk,D] (see msa.h)."""
+    status = _abi.binding().cache_expand_q8(cache, pages, K_out, V_out, dev_err, stream)
+    if status:
+        _abi.check(status, "msa_cache_expand_q8")
+
+
+def msa_attn_decode_q8_workspace_size(B: int, Hkv: int) -> int:
+    return int(lib().msa_attn_decode_q8_workspace_size(B, Hkv))
+
+
+def msa_sparse_attn_decode_q8(Q: torch.Tensor, cache: Q8Cache, pt: torch.Tensor, n: torch.Tensor,
+                              last_len: torch.Tensor, O: torch.Tensor, LSE: Optional[torch.Tensor], ws: torch.Tensor,
+                              *, softmax_scale: float = 0.0, dev_err: Optional[torch.Tensor] = None, stream=None,
+                              scratch_zeroed: bool = False) -> None:
+    """``msa_sparse_attn_decode`` over an 8-bit cache (see msa.h); arguments as in ``msa_sparse_attn_decode_q4``, ws of
+    ``msa_attn_decode_q8_workspace_size`` bytes."""
+    status = _abi.binding().sparse_attn_decode_q8(
+        Q, cache, pt, n, last_len, O, LSE, ws, softmax_scale, dev_err, stream, scratch_zeroed)
+    if status:
+        _abi.check(status, "msa_sparse_attn_decode_q8")
+
+
+def msa_dense_attn_decode_q8(Q: torch.Tensor, cache: Q8Cache, seq_pt: torch.Tensor, seq_len: torch.Tensor,
+                             O: torch.Tensor, LSE: Optional[torch.Tensor], ws: torch.Tensor, *, window: int = 0,
+                             sinks: int = 0, softmax_scale: float = 0.0, dev_err: Optional[torch.Tensor] = None,
+                             stream=None, scratch_zeroed: bool = False) -> None:
+    """``msa_dense_attn_decode`` over an 8-bit cache (see msa.h): Q [B,Hq,D] bf16, seq_pt [B,max_pages], seq_len [B]
+    int32 (0: an empty sequence); O [B,Hq,D] bf16, LSE [B,Hq] fp32; ws as for ``msa_sparse_attn_decode_q8``.  With
+    ``window`` > 0 a query sees the last ``window`` tokens and the first ``sinks``."""
+    status = _abi.binding().dense_attn_decode_q8(
+        Q, cache, seq_pt, seq_len, O, LSE, ws, softmax_scale, dev_err, stream, scratch_zeroed, window, sinks)
+    if status:
+        _abi.check(status, "msa_dense_attn_decode_q8")
+
+
+# ---------------------------------------------------------------------------
+# attention through a sliding window with sinks
+# ---------------------------------------------------------------------------
+
+def msa_window_attn_decode_workspace_size(B: int, Hkv: int) -> int:
+    return int(lib().msa_window_attn_decode_workspace_size(B, Hkv))
+
+
+def msa_window_attn_decode(Q: torch.Tensor, K_pool: torch.Tensor, V_pool: torch.Tensor, seq_pt: torch.Tensor,
+                           seq_len: torch.Tensor, O: torch.Tensor, LSE: Optional[torch.Tensor], ws: torch.Tensor, *,
+                           window: int, sinks: int = 0, softmax_scale: float = 0.0,
+                           dev_err: Optional[torch.Tensor] = None, stream=None, scratch_zeroed: bool = False) -> None:
+    """Decode attention over the last ``window`` tokens of each sequence and its first ``sinks`` (see msa.h): Q [B,Hq,D],
+    K_pool, V_pool [P,Hkv,Bk,D] bf16, seq_pt [B,max_pages], seq_len [B] int32 (0: an empty sequence); O [B,Hq,D] bf16,
+    LSE [B,Hq] fp32; ws of ``msa_window_attn_decode_workspace_size`` bytes."""
+    status = _abi.binding().window_attn_decode(
+        Q, K_pool, V_pool, seq_pt, seq_len, O, LSE, ws, softmax_scale, dev_err, stream, scratch_zeroed, window, sinks)
+    if status:
+        _abi.check(status, "msa_window_attn_decode")
+
+
 # ---------------------------------------------------------------------------
 # pipelines (hot-path order; marshalling and buffer allocation only)
 # ---------------------------------------------------------------------------
@@ -665,30 +751,56 @@ def decode_q4_buffers(B: int, Hq: int, Hkv: int, k: int, nb_stride: int, device)
     return bufs
 
 
+def _decode_step_paged(inp, Hkv, k, bufs, softmax_scale, stream, scratch_zeroed, buffers, attend):
+    """Index score, selection and page table, then ``attend`` over the selected pages of a cache."""
+    dev = inp["Q"].device
+    if dev.type == "cuda" and dev.index != torch.cuda.current_device():   # the index call would go to the current one
+        with torch.cuda.device(dev):
+            return _decode_step_paged(inp, Hkv, k, bufs, softmax_scale, stream, scratch_zeroed, buffers, attend)
+    B, Hq, _ = inp["Q"].shape
+    if bufs is None:
+        with _buffers_on(stream, dev):
+            bufs = buffers(B, Hq, Hkv, k, inp["seq_pt"].shape[1], dev)
+    e = bufs["dev_err"]
+    msa_index_score(MSA_MODE_DECODE, inp["q_idx"], inp["w"], inp["kidx_pool"], bufs["C"], seq_pt=inp["seq_pt"],
+                    seq_len=inp["seq_len"], dev_err=e, stream=stream, k=k, sel=bufs["sel"], count=bufs["count"],
+                    pt=bufs["pt"], n=bufs["n"], last_len=bufs["last_len"], row_scratch=bufs["row_scratch"],
+                    scratch_zeroed=scratch_zeroed)
+    attend(inp["Q"], bufs["pt"], bufs["n"], bufs["last_len"], bufs["O"], bufs["LSE"], bufs["ws"],
+           softmax_scale=softmax_scale, dev_err=e, stream=stream, scratch_zeroed=scratch_zeroed)
+    return bufs
+
+
 def decode_step_q4(inp: Dict[str, torch.Tensor], cache: Q4Cache, k: int,
                    bufs: Optional[Dict[str, torch.Tensor]] = None, softmax_scale: float = 0.0, stream=None,
                    scratch_zeroed: bool = False) -> Dict[str, torch.Tensor]:
     """``decode_step`` with K and V in a 4-bit cache: the index branch and selection are the same (``inp`` holds Q,
     q_idx, w, kidx_pool, seq_pt, seq_len), the attention reads ``cache``.  Row b of Q, q_idx and w is sequence b's
     query; a sequence of length 0 is empty (O = 0, LSE = -inf).  The step runs on the tensors' device."""
-    dev = inp["Q"].device
-    if dev.type == "cuda" and dev.index != torch.cuda.current_device():   # the index call would go to the current one
-        with torch.cuda.device(dev):
-            return decode_step_q4(inp, cache, k, bufs, softmax_scale, stream, scratch_zeroed)
-    B, Hq, _ = inp["Q"].shape
-    Hkv = cache.K_codes.shape[1]
-    if bufs is None:
-        with _buffers_on(stream, inp["Q"].device):
-            bufs = decode_q4_buffers(B, Hq, Hkv, k, inp["seq_pt"].shape[1], inp["Q"].device)
-    e = bufs["dev_err"]
-    msa_index_score(MSA_MODE_DECODE, inp["q_idx"], inp["w"], inp["kidx_pool"], bufs["C"], seq_pt=inp["seq_pt"],
-                    seq_len=inp["seq_len"], dev_err=e, stream=stream, k=k, sel=bufs["sel"], count=bufs["count"],
-                    pt=bufs["pt"], n=bufs["n"], last_len=bufs["last_len"], row_scratch=bufs["row_scratch"],
-                    scratch_zeroed=scratch_zeroed)
-    msa_sparse_attn_decode_q4(inp["Q"], cache, bufs["pt"], bufs["n"], bufs["last_len"], bufs["O"], bufs["LSE"],
-                              bufs["ws"], softmax_scale=softmax_scale, dev_err=e, stream=stream,
-                              scratch_zeroed=scratch_zeroed)
+    def attend(Q, *rest, **kw):
+        msa_sparse_attn_decode_q4(Q, cache, *rest, **kw)
+    return _decode_step_paged(inp, cache.K_codes.shape[1], k, bufs, softmax_scale, stream, scratch_zeroed,
+                              decode_q4_buffers, attend)
+
+
+def decode_q8_buffers(B: int, Hq: int, Hkv: int, k: int, nb_stride: int, device) -> Dict[str, torch.Tensor]:
+    """``decode_buffers`` with the workspace of the 8-bit attention."""
+    dev = torch.device(device)
+    bufs = {n: t for n, t in decode_buffers(B, Hq, Hkv, k, nb_stride, dev).items() if n != "ws"}
+    bufs["ws"] = torch.zeros(msa_attn_decode_q8_workspace_size(B, Hkv), dtype=torch.uint8, device=dev)
     return bufs
+
+
+def decode_step_q8(inp: Dict[str, torch.Tensor], cache: Q8Cache, k: int,
+                   bufs: Optional[Dict[str, torch.Tensor]] = None, softmax_scale: float = 0.0, stream=None,
+                   scratch_zeroed: bool = False) -> Dict[str, torch.Tensor]:
+    """``decode_step`` with K and V in an 8-bit cache: the index branch and selection are the same (``inp`` holds Q,
+    q_idx, w, kidx_pool, seq_pt, seq_len), the attention reads ``cache``.  Row b of Q, q_idx and w is sequence b's
+    query; a sequence of length 0 is empty (O = 0, LSE = -inf).  The step runs on the tensors' device."""
+    def attend(Q, *rest, **kw):
+        msa_sparse_attn_decode_q8(Q, cache, *rest, **kw)
+    return _decode_step_paged(inp, cache.K_codes.shape[1], k, bufs, softmax_scale, stream, scratch_zeroed,
+                              decode_q8_buffers, attend)
 
 
 def prefill_buffers(B: int, S: int, Hq: int, Hkv: int, k: int, device, ws_bytes: int) -> Dict[str, torch.Tensor]:

@@ -180,6 +180,39 @@ class DenseDecodeQ4Args(C.Structure):
     ]
 
 
+class Q8CacheArgs(C.Structure):
+    _fields_ = [
+        ("K_codes", _p), ("K_scales", _p), ("V_codes", _p), ("V_scales", _p),
+        ("code_stride", _i64x2), ("scale_stride", _i64x2), ("num_pages", C.c_int64),
+    ]
+
+
+class AppendQ8Args(C.Structure):
+    _fields_ = [f if f[0] != "cache" else ("cache", Q8CacheArgs) for f in AppendQ4Args._fields_]
+
+
+class ExpandQ8Args(C.Structure):
+    _fields_ = [f if f[0] != "cache" else ("cache", Q8CacheArgs) for f in ExpandQ4Args._fields_]
+
+
+class DecodeQ8Args(C.Structure):
+    _fields_ = [f if f[0] != "cache" else ("cache", Q8CacheArgs) for f in DecodeQ4Args._fields_]
+
+
+class DenseDecodeQ8Args(C.Structure):
+    _fields_ = [f if f[0] != "cache" else ("cache", Q8CacheArgs) for f in DenseDecodeQ4Args._fields_] + [
+        ("window", C.c_int), ("sinks", C.c_int)]
+
+
+class WindowDecodeArgs(C.Structure):
+    _fields_ = [
+        ("B", C.c_int), ("Hq", C.c_int), ("Hkv", C.c_int), ("D", C.c_int), ("Bk", C.c_int),
+        ("softmax_scale", C.c_float), ("Q", _p), ("Q_stride", _i64x2), ("K_pool", _p), ("V_pool", _p),
+        ("kv_stride", _i64x3), ("num_pages", C.c_int64), ("seq_pt", _p), ("max_pages", C.c_int64), ("seq_len", _p),
+        ("window", C.c_int), ("sinks", C.c_int), ("O", _p), ("LSE", _p), ("dev_err", _p), ("scratch_zeroed", C.c_int),
+    ]
+
+
 # exported function name -> (restype, argtypes)
 SIGNATURES = {
     "msa_version": (C.c_int, []),
@@ -207,6 +240,13 @@ SIGNATURES = {
     "msa_attn_decode_q4_workspace_size": (C.c_size_t, [C.c_int, C.c_int]),
     "msa_sparse_attn_decode_q4": (C.c_int, [C.POINTER(DecodeQ4Args), _p, C.c_size_t, _p]),
     "msa_dense_attn_decode_q4": (C.c_int, [C.POINTER(DenseDecodeQ4Args), _p, C.c_size_t, _p]),
+    "msa_cache_append_q8": (C.c_int, [C.POINTER(AppendQ8Args), _p]),
+    "msa_cache_expand_q8": (C.c_int, [C.POINTER(ExpandQ8Args), _p]),
+    "msa_attn_decode_q8_workspace_size": (C.c_size_t, [C.c_int, C.c_int]),
+    "msa_sparse_attn_decode_q8": (C.c_int, [C.POINTER(DecodeQ8Args), _p, C.c_size_t, _p]),
+    "msa_dense_attn_decode_q8": (C.c_int, [C.POINTER(DenseDecodeQ8Args), _p, C.c_size_t, _p]),
+    "msa_window_attn_decode_workspace_size": (C.c_size_t, [C.c_int, C.c_int]),
+    "msa_window_attn_decode": (C.c_int, [C.POINTER(WindowDecodeArgs), _p, C.c_size_t, _p]),
 }
 
 _lock = threading.Lock()

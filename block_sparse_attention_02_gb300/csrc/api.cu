@@ -642,4 +642,118 @@ msa_status msa_dense_attn_decode_q4(const msa_dense_decode_q4_args* a, void* ws,
   return launch_dense_decode_q4(*a, ws, reinterpret_cast<cudaStream_t>(stream));
 }
 
+// ---------------------------------------------------------------------------
+static msa_status check_q8(const msa_q8_cache& c, int Hkv, int D, int Bk) {
+  MSA_REQUIRE(Hkv >= 1, MSA_ERR_INVALID_ARG, "Hkv = %d", Hkv);
+  if (msa_status st = check_common_shape(Bk, D, kD, "D"); st != MSA_OK) return st;
+  MSA_REQUIRE(c.K_codes && c.K_scales && c.V_codes && c.V_scales, MSA_ERR_INVALID_ARG,
+              "the cache's codes and scales must be non-NULL");
+  MSA_REQUIRE(aligned16(c.K_codes) && aligned16(c.V_codes), MSA_ERR_INVALID_ARG, "the cache's codes must be 16-byte aligned");
+  for (int i = 0; i < 2; ++i)
+    MSA_REQUIRE(vec_stride_ok(c.code_stride[i], 1) && c.scale_stride[i] >= 1, MSA_ERR_INVALID_ARG,
+                "the cache's strides must be positive, the codes' multiples of 16 bytes");
+  MSA_REQUIRE(c.num_pages >= 1 && c.num_pages < (int64_t(1) << 31), MSA_ERR_INVALID_ARG, "num_pages = %" PRId64,
+              c.num_pages);
+  return MSA_OK;
+}
+
+msa_status msa_cache_append_q8(const msa_append_q8_args* a, msa_stream_t stream) {
+  g_last_error.clear();
+  MSA_REQUIRE(a != nullptr, MSA_ERR_INVALID_ARG, "args is NULL");
+  MSA_REQUIRE(a->N >= 0 && a->N < (int64_t(1) << 31), MSA_ERR_INVALID_ARG, "N = %" PRId64, a->N);
+  if (msa_status st = check_q8(a->cache, a->Hkv, a->D, a->Bk); st != MSA_OK) return st;
+  if (a->N == 0) return MSA_OK;
+  MSA_REQUIRE(a->K && a->V && a->slots, MSA_ERR_INVALID_ARG, "K, V and slots must be non-NULL");
+  MSA_REQUIRE(aligned16(a->K) && aligned16(a->V), MSA_ERR_INVALID_ARG, "K and V must be 16-byte aligned");
+  for (int i = 0; i < 2; ++i)
+    MSA_REQUIRE(vec_stride_ok(a->K_stride[i], 2) && vec_stride_ok(a->V_stride[i], 2), MSA_ERR_INVALID_ARG,
+                "K and V strides must be positive multiples of 8 elements");
+  return launch_append_q8(*a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+msa_status msa_cache_expand_q8(const msa_expand_q8_args* a, msa_stream_t stream) {
+  g_last_error.clear();
+  MSA_REQUIRE(a != nullptr, MSA_ERR_INVALID_ARG, "args is NULL");
+  MSA_REQUIRE(a->n >= 0 && a->n < (int64_t(1) << 31), MSA_ERR_INVALID_ARG, "n = %" PRId64, a->n);
+  if (msa_status st = check_q8(a->cache, a->Hkv, a->D, a->Bk); st != MSA_OK) return st;
+  if (a->n == 0) return MSA_OK;
+  MSA_REQUIRE(a->pages && a->K_out && a->V_out, MSA_ERR_INVALID_ARG, "pages, K_out and V_out must be non-NULL");
+  MSA_REQUIRE(aligned16(a->K_out) && aligned16(a->V_out), MSA_ERR_INVALID_ARG, "K_out and V_out must be 16-byte aligned");
+  return launch_expand_q8(*a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// What the calls of attn_decode_rows.cu share: the query, the tables of a dense list, the workspace.
+static msa_status check_rows(int B, int max_B, int Hq, int Hkv, const void* Q, const int64_t* Q_stride, const void* O) {
+  MSA_REQUIRE(B >= 0 && B <= max_B && Hq >= 1 && Hkv >= 1, MSA_ERR_INVALID_ARG, "B = %d (at most %d), Hq = %d, Hkv = %d",
+              B, max_B, Hq, Hkv);
+  MSA_REQUIRE(Hq % Hkv == 0 && Hq / Hkv <= kMaxG, MSA_ERR_UNSUPPORTED, "GQA ratio Hq/Hkv = %d/%d not in 1..%d", Hq, Hkv,
+              kMaxG);
+  MSA_REQUIRE(static_cast<int64_t>(B) * Hq < (int64_t(1) << 24), MSA_ERR_UNSUPPORTED, "B * Hq = %d * %d too large", B, Hq);
+  MSA_REQUIRE(B == 0 || (Q && O), MSA_ERR_INVALID_ARG, "Q and O must be non-NULL");
+  MSA_REQUIRE(aligned16(Q) && aligned16(O), MSA_ERR_INVALID_ARG, "Q and O must be 16-byte aligned");
+  for (int i = 0; i < 2; ++i)
+    MSA_REQUIRE(vec_stride_ok(Q_stride[i], 2), MSA_ERR_INVALID_ARG,
+                "Q_stride[%d] = %" PRId64 " must be a positive multiple of 8 elements", i, Q_stride[i]);
+  return MSA_OK;
+}
+static msa_status check_lists(int B, int Hkv, const int32_t* seq_pt, const int32_t* seq_len, int64_t max_pages) {
+  MSA_REQUIRE(seq_pt && seq_len, MSA_ERR_INVALID_ARG, "seq_pt and seq_len must be non-NULL");
+  MSA_REQUIRE(max_pages >= 1 && max_pages < (int64_t(1) << 31) / kBk &&
+                  static_cast<int64_t>(B) * Hkv * max_pages < (int64_t(1) << 30),
+              MSA_ERR_INVALID_ARG, "max_pages = %" PRId64 ": B * Hkv * max_pages must be below 2^30", max_pages);
+  return MSA_OK;
+}
+static msa_status check_rows_ws(int B, int Hkv, const void* ws, size_t ws_bytes) {
+  const size_t need = attn_rows_workspace_size(B, Hkv);
+  MSA_REQUIRE(ws != nullptr && ws_bytes >= need, MSA_ERR_WORKSPACE, "workspace %zu bytes, need %zu", ws_bytes, need);
+  MSA_REQUIRE(aligned16(ws), MSA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  return MSA_OK;
+}
+
+size_t msa_attn_decode_q8_workspace_size(int B, int Hkv) { return B < 0 || Hkv < 1 ? 0 : attn_rows_workspace_size(B, Hkv); }
+size_t msa_window_attn_decode_workspace_size(int B, int Hkv) { return msa_attn_decode_q8_workspace_size(B, Hkv); }
+
+msa_status msa_sparse_attn_decode_q8(const msa_decode_q8_args* a, void* ws, size_t ws_bytes, msa_stream_t stream) {
+  g_last_error.clear();
+  MSA_REQUIRE(a != nullptr, MSA_ERR_INVALID_ARG, "args is NULL");
+  if (msa_status st = check_rows(a->B, kMaxDecodeBatch, a->Hq, a->Hkv, a->Q, a->Q_stride, a->O); st != MSA_OK) return st;
+  if (msa_status st = check_q8(a->cache, a->Hkv, a->D, a->Bk); st != MSA_OK) return st;
+  MSA_REQUIRE(a->k >= 1 && a->k <= kMaxK, MSA_ERR_UNSUPPORTED, "k = %d, supported 1..%d", a->k, kMaxK);
+  if (a->B == 0) return MSA_OK;
+  MSA_REQUIRE(a->pt && a->n && a->last_len, MSA_ERR_INVALID_ARG, "pt, n and last_len must be non-NULL");
+  if (msa_status st = check_rows_ws(a->B, a->Hkv, ws, ws_bytes); st != MSA_OK) return st;
+  return launch_sparse_decode_q8(*a, ws, reinterpret_cast<cudaStream_t>(stream));
+}
+
+msa_status msa_dense_attn_decode_q8(const msa_dense_decode_q8_args* a, void* ws, size_t ws_bytes, msa_stream_t stream) {
+  g_last_error.clear();
+  MSA_REQUIRE(a != nullptr, MSA_ERR_INVALID_ARG, "args is NULL");
+  if (msa_status st = check_rows(a->B, kDenseMaxBatch, a->Hq, a->Hkv, a->Q, a->Q_stride, a->O); st != MSA_OK) return st;
+  if (msa_status st = check_q8(a->cache, a->Hkv, a->D, a->Bk); st != MSA_OK) return st;
+  MSA_REQUIRE(a->window >= 0 && a->sinks >= 0 && (a->window > 0 || a->sinks == 0), MSA_ERR_INVALID_ARG,
+              "window = %d, sinks = %d", a->window, a->sinks);
+  if (a->B == 0) return MSA_OK;
+  if (msa_status st = check_lists(a->B, a->Hkv, a->seq_pt, a->seq_len, a->max_pages); st != MSA_OK) return st;
+  if (msa_status st = check_rows_ws(a->B, a->Hkv, ws, ws_bytes); st != MSA_OK) return st;
+  return launch_dense_decode_q8(*a, ws, reinterpret_cast<cudaStream_t>(stream));
+}
+
+msa_status msa_window_attn_decode(const msa_window_decode_args* a, void* ws, size_t ws_bytes, msa_stream_t stream) {
+  g_last_error.clear();
+  MSA_REQUIRE(a != nullptr, MSA_ERR_INVALID_ARG, "args is NULL");
+  if (msa_status st = check_rows(a->B, kDenseMaxBatch, a->Hq, a->Hkv, a->Q, a->Q_stride, a->O); st != MSA_OK) return st;
+  if (msa_status st = check_common_shape(a->Bk, a->D, kD, "D"); st != MSA_OK) return st;
+  MSA_REQUIRE(a->window >= 1 && a->sinks >= 0, MSA_ERR_INVALID_ARG, "window = %d, sinks = %d", a->window, a->sinks);
+  if (a->B == 0) return MSA_OK;
+  MSA_REQUIRE(a->K_pool && a->V_pool, MSA_ERR_INVALID_ARG, "K_pool and V_pool must be non-NULL");
+  MSA_REQUIRE(aligned16(a->K_pool) && aligned16(a->V_pool), MSA_ERR_INVALID_ARG, "the pools must be 16-byte aligned");
+  for (int i = 0; i < 3; ++i)
+    MSA_REQUIRE(vec_stride_ok(a->kv_stride[i], 2), MSA_ERR_INVALID_ARG,
+                "kv_stride[%d] = %" PRId64 " must be a positive multiple of 8 elements", i, a->kv_stride[i]);
+  MSA_REQUIRE(a->num_pages >= 1 && a->num_pages < (int64_t(1) << 31), MSA_ERR_INVALID_ARG, "num_pages = %" PRId64, a->num_pages);
+  if (msa_status st = check_lists(a->B, a->Hkv, a->seq_pt, a->seq_len, a->max_pages); st != MSA_OK) return st;
+  if (msa_status st = check_rows_ws(a->B, a->Hkv, ws, ws_bytes); st != MSA_OK) return st;
+  return launch_window_decode(*a, ws, reinterpret_cast<cudaStream_t>(stream));
+}
+
 }  // extern "C"

@@ -189,6 +189,39 @@ int q4_cache(PyObject* o, int dev, msa_q4_cache* c) {
   return as_int(H, "Hkv");
 }
 
+// Q8Cache: (K_codes, K_scales, V_codes, V_scales).  Fills the struct; returns the heads.
+int q8_cache(PyObject* o, int dev, msa_q8_cache* c) {
+  if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 4) refuse("cache: need a Q8Cache");
+  static const char* const names[4] = {"K_codes", "K_scales", "V_codes", "V_scales"};
+  const at::Tensor* t[4];
+  void* p[4];
+  for (int i = 0; i < 4; ++i) {
+    t[i] = &tensor(PyTuple_GET_ITEM(o, i), names[i]);
+    check(*t[i], names[i], at::kByte, dev, i & 1 ? 2 : 4);
+    p[i] = t[i]->data_ptr();
+  }
+  const int64_t P = t[0]->size(0), H = t[0]->size(1);
+  for (int i = 0; i < 4; ++i) {
+    if (i & 1) {
+      need_shape(*t[i], names[i], {P, H});
+    } else {
+      need_shape(*t[i], names[i], {P, H, kBk, kD});
+      if (t[i]->stride(3) != 1 || t[i]->stride(2) != kD) refuse("%s: a block's rows must be contiguous", names[i]);
+    }
+  }
+  if (t[0]->strides() != t[2]->strides() || t[1]->strides() != t[3]->strides()) refuse("cache: K and V must share strides");
+  c->K_codes = p[0]; c->K_scales = p[1]; c->V_codes = p[2]; c->V_scales = p[3];
+  for (int i = 0; i < 2; ++i) {
+    c->code_stride[i] = t[0]->stride(i);
+    c->scale_stride[i] = t[1]->stride(i);
+  }
+  c->num_pages = P;
+  return as_int(H, "Hkv");
+}
+
+int cache_of(PyObject* o, int dev, msa_q4_cache* c) { return q4_cache(o, dev, c); }
+int cache_of(PyObject* o, int dev, msa_q8_cache* c) { return q8_cache(o, dev, c); }
+
 // Lets other Python threads run while it lives: a launch waits where the stream's queue is full.
 struct Unlocked {
   PyThreadState* const state = PyEval_SaveThread();
@@ -324,29 +357,31 @@ msa_status qk_norm_rope(PyObject* const* o) {
 }
 
 // K, V, slots, cache, dev_err, stream
-msa_status cache_append_q4(PyObject* const* o) {
+template <class Args, msa_status (*F)(const Args*, msa_stream_t)>
+msa_status cache_append(PyObject* const* o) {
   const at::Tensor &K = tensor(o[0], "K"), &V = tensor(o[1], "V");
   const int dev = device_of(K, "K");
-  msa_append_q4_args a = {};
+  Args a = {};
   a.K = rows<3>(K, "K", dev, a.K_stride);
   a.V = rows<3>(V, "V", dev, a.V_stride);
   need_shape(V, "V", K.sizes());
   a.N = K.size(0); a.Hkv = as_int(K.size(1), "Hkv"); a.D = as_int(K.size(2), "D"); a.Bk = kBk;
   a.slots = dense<int64_t>(o[2], "slots", at::kLong, dev, 1, a.N);
-  if (q4_cache(o[3], dev, &a.cache) != a.Hkv) refuse("the cache and K must have the same heads");
+  if (cache_of(o[3], dev, &a.cache) != a.Hkv) refuse("the cache and K must have the same heads");
   a.dev_err = err_word(o[4], dev);
   msa_stream_t s = stream_of(o[5], dev);
-  return on_device(dev, [&] { return msa_cache_append_q4(&a, s); });
+  return on_device(dev, [&] { return F(&a, s); });
 }
 
 // cache, pages, K_out, V_out, dev_err, stream
-msa_status cache_expand_q4(PyObject* const* o) {
+template <class Args, msa_status (*F)(const Args*, msa_stream_t)>
+msa_status cache_expand(PyObject* const* o) {
   const at::Tensor& pages = tensor(o[1], "pages");
   const int dev = device_of(pages, "pages");
-  msa_expand_q4_args a = {};
+  Args a = {};
   a.pages = dense<int32_t>(o[1], "pages", at::kInt, dev, 1);
   a.n = pages.size(0);
-  a.Hkv = q4_cache(o[0], dev, &a.cache);
+  a.Hkv = cache_of(o[0], dev, &a.cache);
   a.D = kD; a.Bk = kBk;
   a.K_out = dense<void>(o[2], "K_out", at::kBFloat16, dev, 4);
   a.V_out = dense<void>(o[3], "V_out", at::kBFloat16, dev, 4);
@@ -354,17 +389,16 @@ msa_status cache_expand_q4(PyObject* const* o) {
   need_shape(THPVariable_Unpack(o[3]), "V_out", {a.n, a.Hkv, kBk, kD});
   a.dev_err = err_word(o[4], dev);
   msa_stream_t s = stream_of(o[5], dev);
-  return on_device(dev, [&] { return msa_cache_expand_q4(&a, s); });
+  return on_device(dev, [&] { return F(&a, s); });
 }
 
-// The fields that the two attention calls share; returns the device.
+// The fields that the attention calls share, but for the cache; returns the device.
 template <class Args>
-int attention(PyObject* q, PyObject* cache, PyObject* out, PyObject* lse, PyObject* ws, Args* a, void** work, size_t* bytes) {
+int query(PyObject* q, PyObject* out, PyObject* lse, PyObject* ws, Args* a, void** work, size_t* bytes) {
   const at::Tensor& Q = tensor(q, "Q");
   const int dev = device_of(Q, "Q");
   a->Q = rows<3>(Q, "Q", dev, a->Q_stride);
   a->B = as_int(Q.size(0), "B"); a->Hq = as_int(Q.size(1), "Hq"); a->D = as_int(Q.size(2), "D"); a->Bk = kBk;
-  a->Hkv = q4_cache(cache, dev, &a->cache);
   a->O = dense<void>(out, "O", at::kBFloat16, dev, 3);
   need_shape(THPVariable_Unpack(out), "O", Q.sizes());
   if (lse != Py_None) {
@@ -379,11 +413,13 @@ int attention(PyObject* q, PyObject* cache, PyObject* out, PyObject* lse, PyObje
 }
 
 // Q, cache, pt, n, last_len, O, LSE, ws, softmax_scale, dev_err, stream, scratch_zeroed
-msa_status sparse_attn_decode_q4(PyObject* const* o) {
-  msa_decode_q4_args a = {};
+template <class Args, msa_status (*F)(const Args*, void*, size_t, msa_stream_t)>
+msa_status sparse_attn_decode(PyObject* const* o) {
+  Args a = {};
   void* work;
   size_t bytes;
-  const int dev = attention(o[0], o[1], o[5], o[6], o[7], &a, &work, &bytes);
+  const int dev = query(o[0], o[5], o[6], o[7], &a, &work, &bytes);
+  a.Hkv = cache_of(o[1], dev, &a.cache);
   const int64_t r = static_cast<int64_t>(a.B) * a.Hkv;
   a.pt = dense<int32_t>(o[2], "pt", at::kInt, dev, 2, r);
   a.k = as_int(THPVariable_Unpack(o[2]).size(1), "k");
@@ -393,7 +429,24 @@ msa_status sparse_attn_decode_q4(PyObject* const* o) {
   a.dev_err = err_word(o[9], dev);
   msa_stream_t s = stream_of(o[10], dev);
   a.scratch_zeroed = truth(o[11], "scratch_zeroed");
-  return on_device(dev, [&] { return msa_sparse_attn_decode_q4(&a, work, bytes, s); });
+  return on_device(dev, [&] { return F(&a, work, bytes, s); });
+}
+
+// seq_pt, seq_len
+template <class Args>
+void tables(PyObject* const* o, int dev, Args* a) {
+  a->seq_pt = dense<int32_t>(o[0], "seq_pt", at::kInt, dev, 2, a->B);
+  a->max_pages = THPVariable_Unpack(o[0]).size(1);
+  a->seq_len = dense<int32_t>(o[1], "seq_len", at::kInt, dev, 1, a->B);
+}
+// softmax_scale, dev_err, stream, scratch_zeroed; returns the stream
+template <class Args>
+msa_stream_t last_arguments(PyObject* const* o, int dev, Args* a) {
+  a->softmax_scale = real(o[0], "softmax_scale");
+  a->dev_err = err_word(o[1], dev);
+  msa_stream_t s = stream_of(o[2], dev);
+  a->scratch_zeroed = truth(o[3], "scratch_zeroed");
+  return s;
 }
 
 // Q, cache, seq_pt, seq_len, O, LSE, ws, softmax_scale, dev_err, stream, scratch_zeroed
@@ -401,15 +454,46 @@ msa_status dense_attn_decode_q4(PyObject* const* o) {
   msa_dense_decode_q4_args a = {};
   void* work;
   size_t bytes;
-  const int dev = attention(o[0], o[1], o[4], o[5], o[6], &a, &work, &bytes);
-  a.seq_pt = dense<int32_t>(o[2], "seq_pt", at::kInt, dev, 2, a.B);
-  a.max_pages = THPVariable_Unpack(o[2]).size(1);
-  a.seq_len = dense<int32_t>(o[3], "seq_len", at::kInt, dev, 1, a.B);
-  a.softmax_scale = real(o[7], "softmax_scale");
-  a.dev_err = err_word(o[8], dev);
-  msa_stream_t s = stream_of(o[9], dev);
-  a.scratch_zeroed = truth(o[10], "scratch_zeroed");
+  const int dev = query(o[0], o[4], o[5], o[6], &a, &work, &bytes);
+  a.Hkv = q4_cache(o[1], dev, &a.cache);
+  tables(o + 2, dev, &a);
+  msa_stream_t s = last_arguments(o + 7, dev, &a);
   return on_device(dev, [&] { return msa_dense_attn_decode_q4(&a, work, bytes, s); });
+}
+
+// Q, cache, seq_pt, seq_len, O, LSE, ws, softmax_scale, dev_err, stream, scratch_zeroed, window, sinks
+msa_status dense_attn_decode_q8(PyObject* const* o) {
+  msa_dense_decode_q8_args a = {};
+  void* work;
+  size_t bytes;
+  const int dev = query(o[0], o[4], o[5], o[6], &a, &work, &bytes);
+  a.Hkv = q8_cache(o[1], dev, &a.cache);
+  tables(o + 2, dev, &a);
+  msa_stream_t s = last_arguments(o + 7, dev, &a);
+  a.window = as_int(integer(o[11], "window"), "window");
+  a.sinks = as_int(integer(o[12], "sinks"), "sinks");
+  return on_device(dev, [&] { return msa_dense_attn_decode_q8(&a, work, bytes, s); });
+}
+
+// Q, K_pool, V_pool, seq_pt, seq_len, O, LSE, ws, softmax_scale, dev_err, stream, scratch_zeroed, window, sinks
+msa_status window_attn_decode(PyObject* const* o) {
+  msa_window_decode_args a = {};
+  void* work;
+  size_t bytes;
+  const int dev = query(o[0], o[5], o[6], o[7], &a, &work, &bytes);
+  const at::Tensor &K = tensor(o[1], "K_pool"), &V = tensor(o[2], "V_pool");
+  a.K_pool = rows<4>(K, "K_pool", dev, a.kv_stride);
+  a.Hkv = as_int(K.size(1), "Hkv");
+  a.num_pages = K.size(0);
+  need_shape(K, "K_pool", {K.size(0), K.size(1), kBk, a.D});
+  need_shape(V, "V_pool", K.sizes());
+  a.V_pool = rows<4>(V, "V_pool", dev, a.kv_stride);
+  if (K.strides() != V.strides()) refuse("K_pool and V_pool must share strides");
+  tables(o + 3, dev, &a);
+  msa_stream_t s = last_arguments(o + 8, dev, &a);
+  a.window = as_int(integer(o[12], "window"), "window");
+  a.sinks = as_int(integer(o[13], "sinks"), "sinks");
+  return on_device(dev, [&] { return msa_window_attn_decode(&a, work, bytes, s); });
 }
 
 template <msa_status (*F)(PyObject* const*), int ARGS>
@@ -437,10 +521,15 @@ PyMethodDef methods[] = {
     method<plan_step, 14>("plan_step"),
     method<release_pages, 10>("release_pages"),
     method<qk_norm_rope, 15>("qk_norm_rope"),
-    method<cache_append_q4, 6>("cache_append_q4"),
-    method<cache_expand_q4, 6>("cache_expand_q4"),
-    method<sparse_attn_decode_q4, 12>("sparse_attn_decode_q4"),
+    method<cache_append<msa_append_q4_args, msa_cache_append_q4>, 6>("cache_append_q4"),
+    method<cache_expand<msa_expand_q4_args, msa_cache_expand_q4>, 6>("cache_expand_q4"),
+    method<sparse_attn_decode<msa_decode_q4_args, msa_sparse_attn_decode_q4>, 12>("sparse_attn_decode_q4"),
     method<dense_attn_decode_q4, 11>("dense_attn_decode_q4"),
+    method<cache_append<msa_append_q8_args, msa_cache_append_q8>, 6>("cache_append_q8"),
+    method<cache_expand<msa_expand_q8_args, msa_cache_expand_q8>, 6>("cache_expand_q8"),
+    method<sparse_attn_decode<msa_decode_q8_args, msa_sparse_attn_decode_q8>, 12>("sparse_attn_decode_q8"),
+    method<dense_attn_decode_q8, 13>("dense_attn_decode_q8"),
+    method<window_attn_decode, 14>("window_attn_decode"),
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -63,6 +63,12 @@ msa_status launch_expand_q4(const msa_expand_q4_args& a, cudaStream_t stream);
 msa_status launch_sparse_decode_q4(const msa_decode_q4_args& a, void* ws, cudaStream_t stream);
 msa_status launch_dense_decode_q4(const msa_dense_decode_q4_args& a, void* ws, cudaStream_t stream);
 size_t attn_decode_q4_workspace_size(int B, int Hkv);
+msa_status launch_append_q8(const msa_append_q8_args& a, cudaStream_t stream);
+msa_status launch_expand_q8(const msa_expand_q8_args& a, cudaStream_t stream);
+msa_status launch_sparse_decode_q8(const msa_decode_q8_args& a, void* ws, cudaStream_t stream);
+msa_status launch_dense_decode_q8(const msa_dense_decode_q8_args& a, void* ws, cudaStream_t stream);
+msa_status launch_window_decode(const msa_window_decode_args& a, void* ws, cudaStream_t stream);
+size_t attn_rows_workspace_size(int B, int Hkv);   // of the three calls before
 // Host-side argument checks of msa_sparse_attn_decode (no CUDA call).
 msa_status check_decode_args(const msa_decode_args* a);
 size_t attn_prefill_workspace_size(const msa_prefill_args& a, int64_t chunk_queries);

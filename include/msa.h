@@ -787,6 +787,145 @@ typedef struct msa_dense_decode_q4_args {
 msa_status msa_dense_attn_decode_q4(const msa_dense_decode_q4_args *args, void *ws, size_t ws_bytes,
                                     msa_stream_t stream);
 
+/* --------------------------------------------------------------------------
+ * Paged cache held in 8 bits
+ *
+ * K and V as 8-bit floats (E4M3: 1 sign, 4 exponent, 3 mantissa bits, up to 448) with one power of two for each block
+ * of the Bk tokens of a page and head: 256 bytes per token and head for both where bf16 takes 512 and 4 bits 144, at a
+ * sixteenth of a value's error at most where 4 bits leave a sixth.
+ *     scale = the smallest 2^e, e in [-40, 40], with amax <= 448 * 2^e     amax over the block's finite values
+ *     code  = e4m3(x / scale), round to nearest even                       the value is code * scale
+ * A value past the range (an infinity too) becomes the largest code, a NaN stays one.
+ * Pools: codes [num_pages, Hkv, Bk, D] bytes, a block's Bk * D contiguous; scales [num_pages, Hkv] bytes, 2^(byte - 127),
+ * where a byte outside [87, 167] counts as its nearer end (a block of zeros has byte 0 or 87).  K's and V's share strides
+ * (page, g); code strides are multiples of 16 bytes.  D = 128.
+ * ------------------------------------------------------------------------ */
+typedef struct msa_q8_cache {
+    void *K_codes, *K_scales, *V_codes, *V_scales;
+    int64_t code_stride[2];       /* bytes: (page, g) */
+    int64_t scale_stride[2];      /* bytes: (page, g) */
+    int64_t num_pages;
+} msa_q8_cache;
+
+/* Token r's K and V [N, Hkv, D] bf16 (strides (n, h)) into slot slots[r] (page * Bk +
+ * row, as msa_plan_step writes).  slots[r] < 0: nothing is stored; at or past
+ * num_pages * Bk: nothing, and MSA_DEVERR_BAD_PAGE.
+ * The tokens that a call brings to a page are consecutive rows of K and V in consecutive slots (msa_plan_step's are); a page
+ * whose tokens come otherwise, or twice, is left with codes and a scale that fit no sum of them.  Pages fill from row 0 on:
+ * tokens from row 0 on start the block anew (scale of these tokens alone, whatever the page held before), tokens from
+ * a later row on keep the rows before them.  Where these need a larger scale, the rows before are rounded
+ * again (which changes only values that become subnormal codes).  Rows behind the last token keep their codes. */
+typedef struct msa_append_q8_args {
+    int64_t N;
+    int Hkv, D, Bk;
+    const void *K;
+    int64_t K_stride[2];
+    const void *V;
+    int64_t V_stride[2];
+    const int64_t *slots;
+    msa_q8_cache cache;
+    int32_t *dev_err;
+} msa_append_q8_args;
+
+msa_status msa_cache_append_q8(const msa_append_q8_args *args, msa_stream_t stream);
+
+/* The bf16 values of n pages (exact): K_out, V_out [n, Hkv, Bk, D] (dense) from pages pages[i], as msa_cache_expand_q4.
+ * A page id outside [0, num_pages) leaves its block of the outputs untouched and raises MSA_DEVERR_BAD_PAGE. */
+typedef struct msa_expand_q8_args {
+    int64_t n;
+    int Hkv, D, Bk;
+    const int32_t *pages;
+    msa_q8_cache cache;
+    void *K_out;
+    void *V_out;
+    int32_t *dev_err;
+} msa_expand_q8_args;
+
+msa_status msa_cache_expand_q8(const msa_expand_q8_args *args, msa_stream_t stream);
+
+/* msa_sparse_attn_decode over an 8-bit cache: rows, page table, outputs, empty rows, page ids and workspace rules as in
+ * msa_sparse_attn_decode_q4.  Cached values are exact in the products' fp16 operands, the block scales multiply scores and
+ * probabilities in fp32; Q is scaled by a power of two per head into fp16's range, P is rounded to fp16.
+ * Slots past a row's last token may hold anything.  Workspace: msa_attn_decode_q8_workspace_size(B, Hkv) bytes. */
+typedef struct msa_decode_q8_args {
+    int B, Hq, Hkv, D, Bk, k;
+    float softmax_scale;
+    const void *Q;
+    int64_t Q_stride[2];
+    msa_q8_cache cache;
+    const int32_t *pt;
+    const int32_t *n;
+    const int32_t *last_len;
+    void *O;
+    float *LSE;
+    int32_t *dev_err;
+    int scratch_zeroed;
+} msa_decode_q8_args;
+
+size_t msa_attn_decode_q8_workspace_size(int B, int Hkv);
+msa_status msa_sparse_attn_decode_q8(const msa_decode_q8_args *args, void *ws, size_t ws_bytes, msa_stream_t stream);
+
+/* msa_dense_attn_decode over an 8-bit cache: every cached token of each sequence, or with window > 0 a sliding window with
+ * sinks (msa_window_attn_decode below; sinks = 0 with window = 0).  A length of 0 is an empty sequence (O = 0, LSE = -inf, no error); one outside
+ * [0, max_pages * Bk] gives the same and raises MSA_DEVERR_BAD_LEN.  Workspace as in msa_sparse_attn_decode_q8;
+ * B <= 1024 and B * Hkv * max_pages < 2^30. */
+typedef struct msa_dense_decode_q8_args {
+    int B, Hq, Hkv, D, Bk;
+    float softmax_scale;
+    const void *Q;
+    int64_t Q_stride[2];
+    msa_q8_cache cache;
+    const int32_t *seq_pt;
+    int64_t max_pages;
+    const int32_t *seq_len;
+    void *O;
+    float *LSE;
+    int32_t *dev_err;
+    int scratch_zeroed;
+    int window;                   /* 0: every token */
+    int sinks;
+} msa_dense_decode_q8_args;
+
+msa_status msa_dense_attn_decode_q8(const msa_dense_decode_q8_args *args, void *ws, size_t ws_bytes,
+                                    msa_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * Attention through a sliding window with sinks
+ *
+ * The query at position i of its sequence sees the tokens t <= i with t > i - window, and the first ones, t < sinks (which
+ * stay visible however far the window has moved):
+ *     O = sum_t softmax_t(scale * Q . K[t]) V[t],  LSE = ln sum_t exp(scale * Q . K[t]),  t over the tokens seen.
+ * window >= 1, sinks >= 0; a window of the whole length is causal attention.
+ *
+ * msa_window_attn_decode: one query per sequence, at position seq_len[b] - 1, over bf16 pages; tensors as in
+ * msa_dense_attn_decode.  Only pages that hold a seen token are read, their ids too; slots that are not seen may
+ * hold anything.  P is rounded to bf16.  A length of 0 is an empty sequence (O = 0, LSE = -inf, no error); one outside
+ * [0, max_pages * Bk] gives the same and raises MSA_DEVERR_BAD_LEN.  A page id outside [0, num_pages) is not read
+ * (MSA_DEVERR_BAD_PAGE) and its tokens are left out.  Workspace: msa_window_attn_decode_workspace_size(B, Hkv) bytes, with the
+ * rules of msa_sparse_attn_decode_q8's: one that is zero-filled and large enough serves these three calls in
+ * turn.  B <= 1024, B * Hq < 2^24 and B * Hkv * max_pages < 2^30. */
+typedef struct msa_window_decode_args {
+    int B, Hq, Hkv, D, Bk;
+    float softmax_scale;
+    const void *Q;
+    int64_t Q_stride[2];
+    const void *K_pool;
+    const void *V_pool;
+    int64_t kv_stride[3];
+    int64_t num_pages;
+    const int32_t *seq_pt;
+    int64_t max_pages;
+    const int32_t *seq_len;
+    int window, sinks;
+    void *O;
+    float *LSE;
+    int32_t *dev_err;
+    int scratch_zeroed;
+} msa_window_decode_args;
+
+size_t msa_window_attn_decode_workspace_size(int B, int Hkv);
+msa_status msa_window_attn_decode(const msa_window_decode_args *args, void *ws, size_t ws_bytes, msa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
