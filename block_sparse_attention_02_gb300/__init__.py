@@ -21,8 +21,8 @@ from typing import Dict, NamedTuple, Optional
 import torch
 
 from . import _abi
-from ._abi import (MSA_DEVERR_BAD_LEN, MSA_DEVERR_BAD_PAGE, MSA_DEVERR_BAD_SEL, MSA_DEVERR_NO_PAGES,
-                   MSA_DEVERR_TIMEOUT, MSA_MODE_CHUNK, MSA_MODE_DECODE, MSA_MODE_PREFILL, MSAError)
+from ._abi import (MSA_DEVERR_BAD_LEN, MSA_DEVERR_BAD_PAGE, MSA_DEVERR_BAD_ROW, MSA_DEVERR_BAD_SEL,
+                   MSA_DEVERR_NO_PAGES, MSA_DEVERR_TIMEOUT, MSA_MODE_CHUNK, MSA_MODE_DECODE, MSA_MODE_PREFILL, MSAError)
 
 __all__ = [
     "msa_index_score", "msa_topk_blocks", "msa_build_page_table", "msa_sparse_attn_prefill",
@@ -36,9 +36,10 @@ __all__ = [
     "Q8Cache", "q8_cache", "msa_cache_append_q8", "msa_cache_expand_q8", "msa_attn_decode_q8_workspace_size",
     "msa_sparse_attn_decode_q8", "msa_dense_attn_decode_q8", "decode_q8_buffers", "decode_step_q8",
     "msa_window_attn_decode", "msa_window_attn_decode_workspace_size",
+    "msa_fork_requests", "msa_release_shared_pages", "msa_compact_pages", "msa_copy_pages",
     "lib", "MSAError",
     "MSA_MODE_PREFILL", "MSA_MODE_DECODE", "MSA_MODE_CHUNK", "MSA_DEVERR_TIMEOUT", "MSA_DEVERR_BAD_PAGE",
-    "MSA_DEVERR_BAD_SEL", "MSA_DEVERR_BAD_LEN", "MSA_DEVERR_NO_PAGES", "Bk", "D", "dI",
+    "MSA_DEVERR_BAD_SEL", "MSA_DEVERR_BAD_LEN", "MSA_DEVERR_NO_PAGES", "MSA_DEVERR_BAD_ROW", "Bk", "D", "dI",
 ]
 
 Bk = 128
@@ -659,6 +660,67 @@ def msa_dense_attn_decode_q8(Q: torch.Tensor, cache: Q8Cache, seq_pt: torch.Tens
         Q, cache, seq_pt, seq_len, O, LSE, ws, softmax_scale, dev_err, stream, scratch_zeroed, window, sinks)
     if status:
         _abi.check(status, "msa_dense_attn_decode_q8")
+
+
+# ---------------------------------------------------------------------------
+# pages that several requests hold: forks, their release, compaction, copies
+# ---------------------------------------------------------------------------
+
+def msa_fork_requests(src: torch.Tensor, dst: torch.Tensor, seq_len: torch.Tensor, seq_pt: torch.Tensor,
+                      free_pages: torch.Tensor, free_count: torch.Tensor, page_shares: torch.Tensor,
+                      seq_len_out: torch.Tensor, seq_pt_out: torch.Tensor, free_count_out: torch.Tensor,
+                      page_shares_out: torch.Tensor, copy_src: torch.Tensor, copy_dst: torch.Tensor, *,
+                      dev_err: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Request dst[i] goes on from the cached tokens of request src[i] (see msa.h): full pages are shared, of a page that
+    is partly filled the copy is named in copy_src, copy_dst for ``msa_copy_pages``.
+
+    src, dst, copy_src, copy_dst [F] int32 (src < 0: left out); seq_len [B], seq_pt [B,max_pages], free_pages [F] and
+    free_count [1] as in ``msa_plan_step``; page_shares [num_pages] int32, a page's holders beyond the first (0 at the
+    start).  The outputs may be the inputs.
+    """
+    status = _abi.binding().fork_requests(
+        src, dst, seq_len, seq_pt, free_pages, free_count, page_shares, seq_len_out, seq_pt_out, free_count_out,
+        page_shares_out, copy_src, copy_dst, dev_err, stream)
+    if status:
+        _abi.check(status, "msa_fork_requests")
+
+
+def msa_release_shared_pages(seq_len: torch.Tensor, done: torch.Tensor, seq_pt: torch.Tensor, free_pages: torch.Tensor,
+                             free_count: torch.Tensor, page_shares: torch.Tensor, seq_len_out: torch.Tensor,
+                             free_count_out: torch.Tensor, page_shares_out: torch.Tensor, *,
+                             dev_err: Optional[torch.Tensor] = None, stream=None) -> None:
+    """``msa_release_pages`` where requests share pages (see msa.h): a page goes back on the stack with its last holder,
+    in the order of page numbers.  seq_len_out, free_count_out and page_shares_out may be the inputs."""
+    status = _abi.binding().release_shared_pages(
+        seq_len, done, seq_pt, free_pages, free_count, page_shares, seq_len_out, free_count_out, page_shares_out,
+        dev_err, stream)
+    if status:
+        _abi.check(status, "msa_release_shared_pages")
+
+
+def msa_compact_pages(seq_len: torch.Tensor, seq_pt: torch.Tensor, page_shares: torch.Tensor, seq_pt_out: torch.Tensor,
+                      page_shares_out: torch.Tensor, free_pages: torch.Tensor, free_count: torch.Tensor,
+                      move_src: torch.Tensor, move_dst: torch.Tensor, *, dev_err: Optional[torch.Tensor] = None,
+                      stream=None) -> None:
+    """The moves (for ``msa_copy_pages``) after which the pages in use are the pool's first ones, the requests' tables
+    with the new numbers, and the stack of free pages anew (see msa.h).
+
+    seq_len [B], seq_pt [B,max_pages], page_shares, move_src and move_dst [num_pages] int32; free_pages of at least
+    num_pages values and free_count [1] are outputs.  seq_pt_out and page_shares_out may be the inputs.
+    """
+    status = _abi.binding().compact_pages(
+        seq_len, seq_pt, page_shares, seq_pt_out, page_shares_out, free_pages, free_count, move_src, move_dst, dev_err, stream)
+    if status:
+        _abi.check(status, "msa_compact_pages")
+
+
+def msa_copy_pages(pools, src: torch.Tensor, dst: torch.Tensor, *, dev_err: Optional[torch.Tensor] = None,
+                   stream=None) -> None:
+    """Page src[i] to page dst[i] in every pool (see msa.h): pools a list of up to 16 tensors [P, ..] of any type, each
+    page contiguous; src, dst [n] int32, negative ones left out.  No target may be a source or another's target."""
+    status = _abi.binding().copy_pages(pools, src, dst, dev_err, stream)
+    if status:
+        _abi.check(status, "msa_copy_pages")
 
 
 # ---------------------------------------------------------------------------

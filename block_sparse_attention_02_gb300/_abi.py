@@ -25,6 +25,8 @@ MSA_DEVERR_BAD_PAGE = 0x2
 MSA_DEVERR_BAD_SEL = 0x4
 MSA_DEVERR_BAD_LEN = 0x8
 MSA_DEVERR_NO_PAGES = 0x10
+MSA_DEVERR_BAD_ROW = 0x20
+MSA_MAX_POOLS = 16
 
 MSA_MODE_PREFILL = 0
 MSA_MODE_DECODE = 1
@@ -213,6 +215,39 @@ class WindowDecodeArgs(C.Structure):
     ]
 
 
+class ForkArgs(C.Structure):
+    _fields_ = [
+        ("B", C.c_int), ("F", C.c_int), ("Bk", C.c_int), ("src", _p), ("dst", _p), ("seq_len", _p), ("seq_pt", _p),
+        ("max_pages", C.c_int64), ("free_pages", _p), ("free_cap", C.c_int64), ("free_count", _p), ("page_shares", _p),
+        ("num_pages", C.c_int64), ("seq_len_out", _p), ("seq_pt_out", _p), ("free_count_out", _p),
+        ("page_shares_out", _p), ("copy_src", _p), ("copy_dst", _p), ("dev_err", _p),
+    ]
+
+
+class ReleaseSharedArgs(C.Structure):
+    _fields_ = [
+        ("B", C.c_int), ("Bk", C.c_int), ("seq_len", _p), ("done", _p), ("seq_pt", _p), ("max_pages", C.c_int64),
+        ("free_pages", _p), ("free_cap", C.c_int64), ("free_count", _p), ("page_shares", _p), ("num_pages", C.c_int64),
+        ("seq_len_out", _p), ("free_count_out", _p), ("page_shares_out", _p), ("dev_err", _p),
+    ]
+
+
+class CompactArgs(C.Structure):
+    _fields_ = [
+        ("B", C.c_int), ("Bk", C.c_int), ("seq_len", _p), ("seq_pt", _p), ("max_pages", C.c_int64), ("page_shares", _p),
+        ("num_pages", C.c_int64), ("seq_pt_out", _p), ("page_shares_out", _p), ("free_pages", _p),
+        ("free_cap", C.c_int64), ("free_count", _p), ("move_src", _p), ("move_dst", _p), ("dev_err", _p),
+    ]
+
+
+class CopyPagesArgs(C.Structure):
+    _fields_ = [
+        ("n", C.c_int64), ("num_pages", C.c_int64), ("src", _p), ("dst", _p), ("pools", C.c_int),
+        ("pool", _p * MSA_MAX_POOLS), ("page_stride", C.c_int64 * MSA_MAX_POOLS),
+        ("page_bytes", C.c_int64 * MSA_MAX_POOLS), ("dev_err", _p),
+    ]
+
+
 # exported function name -> (restype, argtypes)
 SIGNATURES = {
     "msa_version": (C.c_int, []),
@@ -247,6 +282,10 @@ SIGNATURES = {
     "msa_dense_attn_decode_q8": (C.c_int, [C.POINTER(DenseDecodeQ8Args), _p, C.c_size_t, _p]),
     "msa_window_attn_decode_workspace_size": (C.c_size_t, [C.c_int, C.c_int]),
     "msa_window_attn_decode": (C.c_int, [C.POINTER(WindowDecodeArgs), _p, C.c_size_t, _p]),
+    "msa_fork_requests": (C.c_int, [C.POINTER(ForkArgs), _p]),
+    "msa_release_shared_pages": (C.c_int, [C.POINTER(ReleaseSharedArgs), _p]),
+    "msa_compact_pages": (C.c_int, [C.POINTER(CompactArgs), _p]),
+    "msa_copy_pages": (C.c_int, [C.POINTER(CopyPagesArgs), _p]),
 }
 
 _lock = threading.Lock()

@@ -756,4 +756,75 @@ msa_status msa_window_attn_decode(const msa_window_decode_args* a, void* ws, siz
   return launch_window_decode(*a, ws, reinterpret_cast<cudaStream_t>(stream));
 }
 
+// ---------------------------------------------------------------------------
+static msa_status check_pool(int64_t num_pages) {
+  MSA_REQUIRE(num_pages >= 1 && num_pages <= (int64_t(1) << 24), MSA_ERR_INVALID_ARG, "num_pages = %" PRId64 ", supported 1..2^24",
+              num_pages);
+  return MSA_OK;
+}
+
+msa_status msa_fork_requests(const msa_fork_args* a, msa_stream_t stream) {
+  g_last_error.clear();
+  MSA_REQUIRE(a != nullptr, MSA_ERR_INVALID_ARG, "args is NULL");
+  if (msa_status st = check_tables(a->B, a->Bk, a->max_pages, a->free_cap); st != MSA_OK) return st;
+  if (msa_status st = check_pool(a->num_pages); st != MSA_OK) return st;
+  MSA_REQUIRE(a->F >= 0 && a->F <= kMaxDecodeBatch, MSA_ERR_UNSUPPORTED, "F = %d, supported 0..%d", a->F, kMaxDecodeBatch);
+  MSA_REQUIRE(static_cast<int64_t>(a->F) * a->max_pages < (int64_t(1) << 31), MSA_ERR_UNSUPPORTED,
+              "F * max_pages = %d * %" PRId64 " too large", a->F, a->max_pages);
+  MSA_REQUIRE(a->F == 0 || (a->src && a->dst && a->copy_src && a->copy_dst), MSA_ERR_INVALID_ARG,
+              "src, dst, copy_src and copy_dst must be non-NULL");
+  MSA_REQUIRE(a->B == 0 || (a->seq_len && a->seq_pt && a->seq_len_out && a->seq_pt_out), MSA_ERR_INVALID_ARG,
+              "seq_len, seq_pt and their outputs must be non-NULL");
+  MSA_REQUIRE(a->free_count && a->free_count_out && a->page_shares && a->page_shares_out && (a->free_cap == 0 || a->free_pages),
+              MSA_ERR_INVALID_ARG, "free_pages, free_count, page_shares and their outputs must be non-NULL");
+  return launch_fork(*a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+msa_status msa_release_shared_pages(const msa_release_shared_args* a, msa_stream_t stream) {
+  g_last_error.clear();
+  MSA_REQUIRE(a != nullptr, MSA_ERR_INVALID_ARG, "args is NULL");
+  if (msa_status st = check_tables(a->B, a->Bk, a->max_pages, a->free_cap); st != MSA_OK) return st;
+  if (msa_status st = check_pool(a->num_pages); st != MSA_OK) return st;
+  MSA_REQUIRE(static_cast<int64_t>(a->B) * a->max_pages < (int64_t(1) << 31), MSA_ERR_UNSUPPORTED,
+              "B * max_pages = %d * %" PRId64 " too large", a->B, a->max_pages);
+  MSA_REQUIRE(a->B == 0 || (a->seq_len && a->done && a->seq_pt && a->seq_len_out), MSA_ERR_INVALID_ARG,
+              "seq_len, done, seq_pt and seq_len_out must be non-NULL");
+  MSA_REQUIRE(a->free_count && a->free_count_out && a->page_shares && a->page_shares_out && (a->free_cap == 0 || a->free_pages),
+              MSA_ERR_INVALID_ARG, "free_pages, free_count, page_shares and their outputs must be non-NULL");
+  return launch_release_shared(*a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+msa_status msa_compact_pages(const msa_compact_args* a, msa_stream_t stream) {
+  g_last_error.clear();
+  MSA_REQUIRE(a != nullptr, MSA_ERR_INVALID_ARG, "args is NULL");
+  if (msa_status st = check_tables(a->B, a->Bk, a->max_pages, a->free_cap); st != MSA_OK) return st;
+  if (msa_status st = check_pool(a->num_pages); st != MSA_OK) return st;
+  MSA_REQUIRE(a->free_cap >= a->num_pages, MSA_ERR_INVALID_ARG, "free_cap = %" PRId64 " is below num_pages = %" PRId64, a->free_cap,
+              a->num_pages);
+  MSA_REQUIRE(static_cast<int64_t>(a->B) * a->max_pages < (int64_t(1) << 31), MSA_ERR_UNSUPPORTED,
+              "B * max_pages = %d * %" PRId64 " too large", a->B, a->max_pages);
+  MSA_REQUIRE(a->B == 0 || (a->seq_len && a->seq_pt && a->seq_pt_out), MSA_ERR_INVALID_ARG,
+              "seq_len, seq_pt and seq_pt_out must be non-NULL");
+  MSA_REQUIRE(a->page_shares && a->page_shares_out && a->free_pages && a->free_count && a->move_src && a->move_dst, MSA_ERR_INVALID_ARG,
+              "page_shares, free_pages, free_count, move_src and move_dst must be non-NULL");
+  return launch_compact(*a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+msa_status msa_copy_pages(const msa_copy_pages_args* a, msa_stream_t stream) {
+  g_last_error.clear();
+  MSA_REQUIRE(a != nullptr, MSA_ERR_INVALID_ARG, "args is NULL");
+  MSA_REQUIRE(a->n >= 0 && a->n < (int64_t(1) << 31), MSA_ERR_INVALID_ARG, "n = %" PRId64, a->n);
+  MSA_REQUIRE(a->num_pages >= 1 && a->num_pages < (int64_t(1) << 31), MSA_ERR_INVALID_ARG, "num_pages = %" PRId64, a->num_pages);
+  MSA_REQUIRE(a->pools >= 0 && a->pools <= MSA_MAX_POOLS, MSA_ERR_UNSUPPORTED, "pools = %d, supported 0..%d", a->pools, MSA_MAX_POOLS);
+  for (int i = 0; i < a->pools; ++i) {
+    MSA_REQUIRE(a->pool[i] != nullptr, MSA_ERR_INVALID_ARG, "pool %d must be non-NULL", i);
+    MSA_REQUIRE(a->page_bytes[i] >= 1 && a->page_bytes[i] <= (int64_t(1) << 32) && a->page_stride[i] >= a->page_bytes[i] &&
+                    a->page_stride[i] < (int64_t(1) << 40),
+                MSA_ERR_INVALID_ARG, "pool %d: pages of %" PRId64 " bytes, %" PRId64 " apart", i, a->page_bytes[i], a->page_stride[i]);
+  }
+  if (a->n == 0 || a->pools == 0) return MSA_OK;
+  MSA_REQUIRE(a->src && a->dst, MSA_ERR_INVALID_ARG, "src and dst must be non-NULL");
+  return launch_copy_pages(*a, reinterpret_cast<cudaStream_t>(stream));
+}
+
 }  // extern "C"

@@ -496,6 +496,123 @@ msa_status window_attn_decode(PyObject* const* o) {
   return on_device(dev, [&] { return msa_window_attn_decode(&a, work, bytes, s); });
 }
 
+// The stack of free pages and the pages' counts, with their outputs: free_pages, free_count, page_shares; free_count_out,
+// page_shares_out.
+template <class Args>
+void stack(PyObject* const* o, PyObject* count_out, PyObject* shares_out, int dev, Args* a) {
+  a->free_pages = dense<int32_t>(o[0], "free_pages", at::kInt, dev, 1);
+  a->free_cap = THPVariable_Unpack(o[0]).size(0);
+  a->free_count = dense<int32_t>(o[1], "free_count", at::kInt, dev, 1, 1);
+  a->page_shares = dense<int32_t>(o[2], "page_shares", at::kInt, dev, 1);
+  a->num_pages = THPVariable_Unpack(o[2]).size(0);
+  a->free_count_out = dense<int32_t>(count_out, "free_count_out", at::kInt, dev, 1, 1);
+  a->page_shares_out = dense<int32_t>(shares_out, "page_shares_out", at::kInt, dev, 1, a->num_pages);
+}
+
+// src, dst, seq_len, seq_pt, free_pages, free_count, page_shares, seq_len_out, seq_pt_out, free_count_out, page_shares_out,
+// copy_src, copy_dst, dev_err, stream
+msa_status fork_requests(PyObject* const* o) {
+  const at::Tensor &src = tensor(o[0], "src"), &L = tensor(o[2], "seq_len");
+  const int dev = device_of(L, "seq_len");
+  if (src.dim() != 1 || L.dim() != 1) refuse("src must be [F] and seq_len [B]");
+  const int64_t F = src.size(0), B = L.size(0);
+  msa_fork_args a = {};
+  a.B = as_int(B, "B"); a.F = as_int(F, "F"); a.Bk = kBk;
+  a.src = dense<int32_t>(o[0], "src", at::kInt, dev, 1);
+  a.dst = dense<int32_t>(o[1], "dst", at::kInt, dev, 1, F);
+  a.seq_len = dense<int32_t>(o[2], "seq_len", at::kInt, dev, 1);
+  a.seq_pt = dense<int32_t>(o[3], "seq_pt", at::kInt, dev, 2, B);
+  a.max_pages = THPVariable_Unpack(o[3]).size(1);
+  stack(o + 4, o[9], o[10], dev, &a);
+  a.seq_len_out = dense<int32_t>(o[7], "seq_len_out", at::kInt, dev, 1, B);
+  a.seq_pt_out = dense<int32_t>(o[8], "seq_pt_out", at::kInt, dev, 2);
+  need_shape(THPVariable_Unpack(o[8]), "seq_pt_out", {B, a.max_pages});
+  a.copy_src = dense<int32_t>(o[11], "copy_src", at::kInt, dev, 1, F);
+  a.copy_dst = dense<int32_t>(o[12], "copy_dst", at::kInt, dev, 1, F);
+  a.dev_err = err_word(o[13], dev);
+  msa_stream_t s = stream_of(o[14], dev);
+  return on_device(dev, [&] { return msa_fork_requests(&a, s); });
+}
+
+// seq_len, done, seq_pt, free_pages, free_count, page_shares, seq_len_out, free_count_out, page_shares_out, dev_err, stream
+msa_status release_shared_pages(PyObject* const* o) {
+  const at::Tensor& L = tensor(o[0], "seq_len");
+  const int dev = device_of(L, "seq_len");
+  if (L.dim() != 1) refuse("seq_len must be [B]");
+  const int64_t B = L.size(0);
+  msa_release_shared_args a = {};
+  a.B = as_int(B, "B"); a.Bk = kBk;
+  a.seq_len = dense<int32_t>(o[0], "seq_len", at::kInt, dev, 1);
+  a.done = dense<int32_t>(o[1], "done", at::kInt, dev, 1, B);
+  a.seq_pt = dense<int32_t>(o[2], "seq_pt", at::kInt, dev, 2, B);
+  a.max_pages = THPVariable_Unpack(o[2]).size(1);
+  stack(o + 3, o[7], o[8], dev, &a);
+  a.seq_len_out = dense<int32_t>(o[6], "seq_len_out", at::kInt, dev, 1, B);
+  a.dev_err = err_word(o[9], dev);
+  msa_stream_t s = stream_of(o[10], dev);
+  return on_device(dev, [&] { return msa_release_shared_pages(&a, s); });
+}
+
+// seq_len, seq_pt, page_shares, seq_pt_out, page_shares_out, free_pages, free_count, move_src, move_dst, dev_err, stream
+msa_status compact_pages(PyObject* const* o) {
+  const at::Tensor& L = tensor(o[0], "seq_len");
+  const int dev = device_of(L, "seq_len");
+  if (L.dim() != 1) refuse("seq_len must be [B]");
+  const int64_t B = L.size(0);
+  msa_compact_args a = {};
+  a.B = as_int(B, "B"); a.Bk = kBk;
+  a.seq_len = dense<int32_t>(o[0], "seq_len", at::kInt, dev, 1);
+  a.seq_pt = dense<int32_t>(o[1], "seq_pt", at::kInt, dev, 2, B);
+  a.max_pages = THPVariable_Unpack(o[1]).size(1);
+  a.page_shares = dense<int32_t>(o[2], "page_shares", at::kInt, dev, 1);
+  a.num_pages = THPVariable_Unpack(o[2]).size(0);
+  a.seq_pt_out = dense<int32_t>(o[3], "seq_pt_out", at::kInt, dev, 2);
+  need_shape(THPVariable_Unpack(o[3]), "seq_pt_out", {B, a.max_pages});
+  a.page_shares_out = dense<int32_t>(o[4], "page_shares_out", at::kInt, dev, 1, a.num_pages);
+  a.free_pages = dense<int32_t>(o[5], "free_pages", at::kInt, dev, 1);
+  a.free_cap = THPVariable_Unpack(o[5]).size(0);
+  a.free_count = dense<int32_t>(o[6], "free_count", at::kInt, dev, 1, 1);
+  a.move_src = dense<int32_t>(o[7], "move_src", at::kInt, dev, 1, a.num_pages);
+  a.move_dst = dense<int32_t>(o[8], "move_dst", at::kInt, dev, 1, a.num_pages);
+  a.dev_err = err_word(o[9], dev);
+  msa_stream_t s = stream_of(o[10], dev);
+  return on_device(dev, [&] { return msa_compact_pages(&a, s); });
+}
+
+// pools (a list or tuple of tensors [P, ..]), src, dst, dev_err, stream
+msa_status copy_pages(PyObject* const* o) {
+  if (!PyList_Check(o[0]) && !PyTuple_Check(o[0])) refuse("pools: need a list or tuple of tensors");
+  const Py_ssize_t pools = PySequence_Fast_GET_SIZE(o[0]);
+  if (pools > MSA_MAX_POOLS) refuse("pools: %zd, at most %d a call", pools, MSA_MAX_POOLS);
+  const at::Tensor& src = tensor(o[1], "src");
+  const int dev = device_of(src, "src");
+  msa_copy_pages_args a = {};
+  a.src = dense<int32_t>(o[1], "src", at::kInt, dev, 1);
+  a.n = src.size(0);
+  a.dst = dense<int32_t>(o[2], "dst", at::kInt, dev, 1, a.n);
+  a.pools = static_cast<int>(pools);
+  a.num_pages = 1;
+  for (Py_ssize_t i = 0; i < pools; ++i) {
+    const at::Tensor& t = tensor(PySequence_Fast_GET_ITEM(o[0], i), "pools");
+    if (!t.is_cuda() || t.get_device() != dev || t.dim() < 1 || t.numel() == 0)
+      refuse("pools[%zd]: need a tensor [P, ..] on cuda:%d, got %s on %s", i, dev, shape_of(t).c_str(), t.device().str().c_str());
+    if (i > 0 && t.size(0) != a.num_pages)
+      refuse("pools[%zd]: %lld pages, the first pool has %lld", i, static_cast<long long>(t.size(0)), static_cast<long long>(a.num_pages));
+    int64_t inner = 1;
+    for (int64_t d = t.dim() - 1; d > 0; --d) {
+      if (t.size(d) != 1 && t.stride(d) != inner) refuse("pools[%zd]: a page must be contiguous", i);
+      inner *= t.size(d);
+    }
+    a.num_pages = t.size(0);
+    a.pool[i] = t.data_ptr();
+    a.page_bytes[i] = inner * static_cast<int64_t>(t.element_size());
+    a.page_stride[i] = a.num_pages == 1 ? a.page_bytes[i] : t.stride(0) * static_cast<int64_t>(t.element_size());
+  }
+  a.dev_err = err_word(o[3], dev);
+  msa_stream_t s = stream_of(o[4], dev);
+  return on_device(dev, [&] { return msa_copy_pages(&a, s); });
+}
+
 template <msa_status (*F)(PyObject* const*), int ARGS>
 PyObject* call(PyObject*, PyObject* const* o, Py_ssize_t n) {
   if (n != ARGS) {
@@ -530,6 +647,10 @@ PyMethodDef methods[] = {
     method<sparse_attn_decode<msa_decode_q8_args, msa_sparse_attn_decode_q8>, 12>("sparse_attn_decode_q8"),
     method<dense_attn_decode_q8, 13>("dense_attn_decode_q8"),
     method<window_attn_decode, 14>("window_attn_decode"),
+    method<fork_requests, 15>("fork_requests"),
+    method<release_shared_pages, 11>("release_shared_pages"),
+    method<compact_pages, 11>("compact_pages"),
+    method<copy_pages, 5>("copy_pages"),
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -69,6 +69,10 @@ msa_status launch_sparse_decode_q8(const msa_decode_q8_args& a, void* ws, cudaSt
 msa_status launch_dense_decode_q8(const msa_dense_decode_q8_args& a, void* ws, cudaStream_t stream);
 msa_status launch_window_decode(const msa_window_decode_args& a, void* ws, cudaStream_t stream);
 size_t attn_rows_workspace_size(int B, int Hkv);   // of the three calls before
+msa_status launch_fork(const msa_fork_args& a, cudaStream_t stream);
+msa_status launch_release_shared(const msa_release_shared_args& a, cudaStream_t stream);
+msa_status launch_compact(const msa_compact_args& a, cudaStream_t stream);
+msa_status launch_copy_pages(const msa_copy_pages_args& a, cudaStream_t stream);
 // Host-side argument checks of msa_sparse_attn_decode (no CUDA call).
 msa_status check_decode_args(const msa_decode_args* a);
 size_t attn_prefill_workspace_size(const msa_prefill_args& a, int64_t chunk_queries);

@@ -1,0 +1,526 @@
+// share_pages.cu -- pages that several requests hold, requests that start from another's cache, pages gathered at the
+// pool's front, and the copies that these need.
+//
+// A request that continues another one's text (parallel samples, beams) needs its cached tokens.  Its full pages are
+// never written again, so both may hold them; only the page that is partly filled is copied.  page_shares counts a page's
+// holders beyond the first, so that pages given out by msa_plan_step (0) need nothing, and a page goes back on the stack
+// when the count would fall below 0.
+//
+// Each of the three index kernels is one thread-block cluster: its CTAs form the sums over the requests for themselves,
+// go through the table entries and the pages side by side, and meet at the cluster's barrier where one step needs all of
+// the step before (counts before the search for freed pages, marks before ranks, ranks before the table).  So a call is one
+// launch without scratch, lengths and counts may be updated in place, and whatever is counted by atomics is a sum, the
+// same in any order; freed pages and moves are ordered by page number.
+//
+// Bound: latency (the barriers, dependent loads of lengths, tables and counts).  The copies are bound by HBM.
+#include <cooperative_groups.h>
+
+#include <climits>
+
+#include "launch_early.cuh"
+#include "msa_internal.h"
+#include "msa_ptx.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace msa {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kCluster = 8;                                // CTAs (the portable maximum)
+constexpr int kPer = kMaxDecodeBatch / kThreads;           // requests (or forks) of a thread in the sums, at most
+constexpr int kCopyThreads = 256;
+constexpr int kCopyUnroll = 4;
+constexpr int kCopyChunk = kCopyThreads * kCopyUnroll * 16;   // bytes of a page that a CTA copies at a time
+
+// Exclusive prefix sum over the CTA's threads; the total in *total.
+__device__ __forceinline__ int block_exclusive(int v, int* total) {
+  __shared__ int s_warp[kThreads / 32 + 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  __syncthreads();                          // an earlier call's sums are read
+  if (lane == 31) s_warp[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    const int own = lane < kThreads / 32 ? s_warp[lane] : 0;
+    int w = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += x;
+    }
+    if (lane < kThreads / 32) s_warp[lane] = w - own;
+    if (lane == 31) s_warp[kThreads / 32] = w;
+  }
+  __syncthreads();
+  *total = s_warp[kThreads / 32];
+  return s_warp[warp] + inc - v;
+}
+
+// Last index i in [0, n) with first[i] <= x (first ascending, first[0] <= x).
+__device__ __forceinline__ int last_at_most(const int* first, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// A value of every CTA of the cluster: the sum over the CTAs before this one, and over all.
+struct ClusterSum {
+  int before, all;
+};
+__device__ __forceinline__ ClusterSum cluster_sum(cg::cluster_group cluster, int mine) {
+  __shared__ int s_value;
+  cluster.sync();                           // an earlier value is read
+  if (threadIdx.x == 0) s_value = mine;
+  cluster.sync();
+  ClusterSum r{0, 0};
+  for (unsigned c = 0; c < cluster.num_blocks(); ++c) {
+    const int v = *cluster.map_shared_rank(&s_value, c);
+    if (c < cluster.block_rank()) r.before += v;
+    r.all += v;
+  }
+  return r;
+}
+// (every kernel ends with a cluster barrier after its last look into another CTA's memory)
+
+__device__ __forceinline__ void copy_counts(const int32_t* from, int32_t* to, int64_t n, int64_t first, int64_t stride) {
+  if (from == to) return;
+  for (int64_t i = first; i < n; i += stride) to[i] = from[i];
+}
+
+// The table entries of the requests: entry x is of request b = last_at_most(first, B, x), page x - first[b].  f(b, j) for
+// this thread's share, four searches and loads side by side.
+template <class F>
+__device__ __forceinline__ void for_entries(const int* first, int B, int total, int at, int stride, F f) {
+  for (int x = at; x < total; x += stride) {
+    const int b = last_at_most(first, B, x);
+    f(b, x - first[b]);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) fork_kernel(const msa_fork_args p) {
+  wait_for_stream();
+  extern __shared__ int s_mem[];
+  int* s_first = s_mem;                     // [F + 1] shared table entries of the forks before
+  int* s_src = s_first + p.F + 1;           // [F] -1: not served
+  int* s_dst = s_src + p.F;                 // [F]
+  int* s_owner = s_dst + p.F;               // [B] the first fork that names a request
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, F = p.F, rank = static_cast<int>(cluster.block_rank()), ctas = static_cast<int>(cluster.num_blocks());
+  const int at = rank * kThreads + tid, stride = ctas * kThreads;
+  const int64_t cap = p.max_pages * kBk;
+  const int raw = *p.free_count;
+  const int count = static_cast<int>(min(max(static_cast<int64_t>(raw), int64_t(0)), p.free_cap));
+  int32_t err = raw == count ? 0 : MSA_DEVERR_NO_PAGES;
+  for (int b = tid; b < p.B; b += kThreads) s_owner[b] = INT_MAX;
+  __syncthreads();
+  const int per = (F + kThreads - 1) / kThreads;
+  int src[kPer], dst[kPer], L[kPer];
+  int need = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int x = tid * per + i;
+    src[i] = dst[i] = -1;
+    if (i < per && x < F) {
+      src[i] = p.src[x];
+      dst[i] = p.dst[x];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    L[i] = 0;
+    if (src[i] < 0) continue;
+    if (src[i] >= p.B || dst[i] < 0 || dst[i] >= p.B || p.seq_len[dst[i]] != 0) {
+      err |= MSA_DEVERR_BAD_ROW;
+      src[i] = -1;
+      continue;
+    }
+    L[i] = p.seq_len[src[i]];
+    if (L[i] < 0 || L[i] > cap) {
+      err |= MSA_DEVERR_BAD_LEN;
+      src[i] = -1;
+      continue;
+    }
+    atomicMin(&s_owner[dst[i]], tid * per + i);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (src[i] < 0) continue;
+    if (s_owner[dst[i]] != tid * per + i) {
+      err |= MSA_DEVERR_BAD_ROW;
+      src[i] = -1;
+      continue;
+    }
+    need += L[i] % kBk != 0;
+  }
+  int pages_needed;
+  int off = block_exclusive(need, &pages_needed);
+  int share = 0;
+  int page_at[kPer];                        // place on the stack of a fork's own page, -1: needs none
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    page_at[i] = -1;
+    if (src[i] < 0) continue;
+    if (L[i] % kBk != 0) {
+      if (off >= count) {
+        err |= MSA_DEVERR_NO_PAGES;
+        src[i] = -1;
+      } else {
+        page_at[i] = count - 1 - off;
+      }
+      ++off;
+    }
+    if (src[i] >= 0) share += L[i] / kBk;
+  }
+  int total;
+  int first = block_exclusive(share, &total);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int x = tid * per + i;
+    if (i < per && x < F) {
+      s_first[x] = first;
+      s_src[x] = src[i];
+      s_dst[x] = dst[i];
+      if (src[i] >= 0) first += L[i] / kBk;
+    }
+  }
+  if (tid == 0) s_first[F] = total;
+  copy_counts(p.page_shares, p.page_shares_out, p.num_pages, at, stride);
+  if (rank == 0 && err != 0) report(p.dev_err, err);
+  // the last CTA, which has the fewest table entries, writes lengths, copies and the stack's height; lengths of all first
+  int len[kPer];
+  const int per_b = (p.B + kThreads - 1) / kThreads;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int b = tid + i * kThreads;
+    len[i] = i < per_b && b < p.B ? p.seq_len[b] : 0;
+  }
+  cluster.sync();                           // lengths, counts and the stack's height are read, counts copied
+  if (rank == ctas - 1) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int b = tid + i * kThreads;
+      if (i < per_b && b < p.B && (s_owner[b] == INT_MAX || s_src[s_owner[b]] < 0)) p.seq_len_out[b] = len[i];
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int x = tid * per + i;
+      if (i >= per || x >= F) continue;
+      int from = -1, to = -1;
+      if (src[i] >= 0) {
+        p.seq_len_out[dst[i]] = L[i];
+        if (page_at[i] >= 0) {
+          from = p.seq_pt[src[i] * p.max_pages + L[i] / kBk];
+          to = p.free_pages[page_at[i]];
+          p.seq_pt_out[dst[i] * p.max_pages + L[i] / kBk] = to;
+        }
+      }
+      p.copy_src[x] = from;
+      p.copy_dst[x] = to;
+    }
+    if (tid == 0) *p.free_count_out = count - min(pages_needed, count);
+  }
+  bool bad = false;
+  for_entries(s_first, F, total, at, stride, [&](int x, int j) {
+    const int page = p.seq_pt[s_src[x] * p.max_pages + j];
+    p.seq_pt_out[s_dst[x] * p.max_pages + j] = page;
+    if (page >= 0 && page < p.num_pages) atomicAdd(p.page_shares_out + page, 1);
+    else bad = true;
+  });
+  if (bad) report(p.dev_err, MSA_DEVERR_BAD_PAGE);
+}
+
+// The pages of one thread, when a cluster's threads share the pool's: [lo, hi), in order.
+__device__ __forceinline__ void own_pages(int64_t num_pages, int rank, int ctas, int* lo, int* hi) {
+  const int64_t threads = static_cast<int64_t>(ctas) * kThreads;
+  const int64_t per = ((num_pages + threads - 1) / threads + 3) / 4 * 4;
+  const int64_t at = (static_cast<int64_t>(rank) * kThreads + threadIdx.x) * per;
+  *lo = static_cast<int>(min(at, num_pages));
+  *hi = static_cast<int>(min(at + per, num_pages));
+}
+
+__global__ void __launch_bounds__(kThreads) release_shared_kernel(const msa_release_shared_args p) {
+  wait_for_stream();
+  extern __shared__ int s_first[];          // [B + 1] table entries of the ended requests before
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, B = p.B, rank = static_cast<int>(cluster.block_rank()), ctas = static_cast<int>(cluster.num_blocks());
+  const int at = rank * kThreads + tid, stride = ctas * kThreads;
+  const int64_t cap = p.max_pages * kBk;
+  const int raw = *p.free_count;
+  const int64_t count = min(max(static_cast<int64_t>(raw), int64_t(0)), p.free_cap);
+  int32_t err = raw == count ? 0 : MSA_DEVERR_NO_PAGES;
+  const int per = (B + kThreads - 1) / kThreads;
+  int len[kPer], gone[kPer], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int b = tid * per + i;
+    len[i] = gone[i] = 0;
+    if (i < per && b < B) {
+      len[i] = p.seq_len[b];
+      if (p.done[b] != 0) {
+        if (len[i] < 0 || len[i] > cap) {
+          err |= MSA_DEVERR_BAD_LEN;
+        } else {
+          gone[i] = (len[i] + kBk - 1) / kBk;
+          len[i] = 0;
+        }
+      }
+      sum += gone[i];
+    }
+  }
+  int total;
+  int first = block_exclusive(sum, &total);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int b = tid * per + i;
+    if (i < per && b < B) s_first[b] = first;
+    first += gone[i];
+  }
+  if (tid == 0) s_first[B] = total;
+  copy_counts(p.page_shares, p.page_shares_out, p.num_pages, at, stride);
+  cluster.sync();                           // counts copied, lengths and the stack's height read
+  if (rank == ctas - 1) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int b = tid * per + i;
+      if (i < per && b < B) p.seq_len_out[b] = len[i];
+    }
+  }
+  bool bad = false;
+  for_entries(s_first, B, total, at, stride, [&](int b, int j) {
+    const int page = p.seq_pt[b * p.max_pages + j];
+    if (page >= 0 && page < p.num_pages) atomicSub(p.page_shares_out + page, 1);
+    else bad = true;
+  });
+  cluster.sync();                           // every holder that ended is taken off
+  int lo, hi, back = 0;
+  own_pages(p.num_pages, rank, ctas, &lo, &hi);
+  for (int x = lo; x < hi; ++x) back += __ldcg(p.page_shares_out + x) < 0 ? 1 : 0;
+  int in_cta;
+  const int before = block_exclusive(back, &in_cta);
+  const ClusterSum sums = cluster_sum(cluster, in_cta);
+  int64_t to = count + sums.before + before;
+  for (int x = lo; x < hi; ++x) {
+    const int left = __ldcg(p.page_shares_out + x);
+    if (left >= 0) continue;
+    if (left < -1) bad = true;              // given up more often than it was held
+    p.page_shares_out[x] = 0;
+    if (to < p.free_cap) p.free_pages[to] = x;
+    ++to;
+  }
+  if (count + sums.all > p.free_cap) err |= MSA_DEVERR_NO_PAGES;
+  if (rank == 0 && tid == 0) *p.free_count_out = static_cast<int>(min(count + sums.all, p.free_cap));
+  if (bad) err |= MSA_DEVERR_BAD_PAGE;
+  if ((bad || rank == 0) && err != 0) report(p.dev_err, err);
+  cluster.sync();
+}
+
+__global__ void __launch_bounds__(kThreads) compact_kernel(const msa_compact_args p) {
+  wait_for_stream();
+  extern __shared__ int s_first[];          // [B + 1] table entries of the requests before
+  __shared__ int s_low;                     // of CTA 0: pages in use among the first n
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, B = p.B, rank = static_cast<int>(cluster.block_rank()), ctas = static_cast<int>(cluster.num_blocks());
+  const int at = rank * kThreads + tid, stride = ctas * kThreads;
+  const int64_t cap = p.max_pages * kBk, P = p.num_pages;
+  int32_t err = 0;
+  int32_t* const place = p.free_pages;      // until the end: whether a page is in use, then where it goes
+  const int per = (B + kThreads - 1) / kThreads;
+  int pages[kPer], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int b = tid * per + i;
+    pages[i] = 0;
+    if (i < per && b < B) {
+      const int L = p.seq_len[b];
+      if (L < 0 || L > cap) err |= MSA_DEVERR_BAD_LEN;
+      else pages[i] = (L + kBk - 1) / kBk;
+    }
+    sum += pages[i];
+  }
+  int total;
+  int first = block_exclusive(sum, &total);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int b = tid * per + i;
+    if (i < per && b < B) s_first[b] = first;
+    first += pages[i];
+  }
+  if (tid == 0) s_first[B] = total;
+  for (int64_t x = at; x < P; x += stride) {
+    place[x] = 0;
+    p.move_src[x] = -1;
+    p.move_dst[x] = -1;
+  }
+  cluster.sync();
+  for_entries(s_first, B, total, at, stride, [&](int b, int j) {
+    const int page = p.seq_pt[b * p.max_pages + j];
+    if (page >= 0 && page < P) place[page] = 1;
+    else err |= MSA_DEVERR_BAD_PAGE;
+  });
+  cluster.sync();                           // every page in use is marked
+  int lo, hi, used = 0;
+  own_pages(P, rank, ctas, &lo, &hi);
+  for (int x = lo; x < hi; ++x) used += __ldcg(place + x);
+  int in_cta;
+  int before = block_exclusive(used, &in_cta);
+  const ClusterSum sums = cluster_sum(cluster, in_cta);
+  const int n = sums.all;                   // pages in use: they end up as 0 .. n - 1
+  before += sums.before;
+  if (lo < hi && lo <= n && n < hi) {       // (n = P: nothing lies behind)
+    int low = before;
+    for (int x = lo; x < n; ++x) low += __ldcg(place + x);
+    *cluster.map_shared_rank(&s_low, 0) = low;
+  }
+  cluster.sync();
+  const int low = n < P ? *cluster.map_shared_rank(&s_low, 0) : n;
+  // the k-th page in use behind the first n goes to the k-th free one among them
+  int rank_of = before;
+  for (int x = lo; x < hi; ++x) {
+    const int live = __ldcg(place + x);
+    if (live != 0 && x >= n) p.move_src[rank_of - low] = x;
+    if (live == 0 && x < n) p.move_dst[x - rank_of] = x;
+    rank_of += live;
+  }
+  cluster.sync();                           // the moves are known
+  rank_of = before;
+  for (int x = lo; x < hi; ++x) {
+    const int live = __ldcg(place + x);
+    const int shares = live != 0 ? p.page_shares[x] : 0;
+    if (x >= n) p.page_shares_out[x] = 0;
+    if (live != 0) {
+      const int to = x < n ? x : __ldcg(p.move_dst + (rank_of - low));
+      place[x] = to;
+      p.page_shares_out[to] = shares;
+    }
+    rank_of += live;
+  }
+  cluster.sync();                           // where each page goes is known
+  for_entries(s_first, B, total, at, stride, [&](int b, int j) {
+    const int64_t i = b * p.max_pages + j;
+    const int page = p.seq_pt[i];
+    p.seq_pt_out[i] = page >= 0 && page < P ? __ldcg(place + page) : page;
+  });
+  cluster.sync();                           // the places are read: the stack takes their room
+  for (int64_t x = at; x < p.free_cap; x += stride) p.free_pages[x] = x < P - n ? static_cast<int32_t>(P - 1 - x) : -1;
+  if (rank == 0 && tid == 0) *p.free_count = static_cast<int32_t>(P - n);
+  if (err != 0) report(p.dev_err, err);
+}
+
+// One cluster of as many CTAs as the entries and pages ask for, two at least.
+template <class Args>
+msa_status launch_cluster(void (*kernel)(const Args), const Args& a, int64_t items, size_t smem, cudaStream_t stream, const char* what) {
+  const int ctas = static_cast<int>(std::min<int64_t>(std::max<int64_t>((items + kThreads - 1) / kThreads, 2), kCluster));
+  if (smem > (40u << 10)) {                 // with the sums' own shared memory past the 48 KiB default
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return cuda_fail(e, what);
+  }
+  const cudaError_t e = launch_early(kernel, ctas, kThreads, smem, stream, ctas, a);
+  if (e != cudaSuccess) return cuda_fail(e, what);
+  return MSA_OK;
+}
+
+struct CopyParams {
+  int64_t n, num_pages;
+  const int32_t *src, *dst;
+  int pools;
+  int first[MSA_MAX_POOLS + 1];             // chunks of the pools before
+  uint8_t* base[MSA_MAX_POOLS];
+  int64_t stride[MSA_MAX_POOLS], bytes[MSA_MAX_POOLS];
+  int32_t* dev_err;
+};
+
+template <class T>
+__device__ __forceinline__ void copy_units(const uint8_t* from, uint8_t* to, int64_t units) {
+  const T* a = reinterpret_cast<const T*>(from) + threadIdx.x;
+  T* b = reinterpret_cast<T*>(to) + threadIdx.x;
+  for (int64_t u = threadIdx.x; u < units; u += kCopyThreads * kCopyUnroll, a += kCopyThreads * kCopyUnroll, b += kCopyThreads * kCopyUnroll) {
+    T v[kCopyUnroll];
+#pragma unroll
+    for (int i = 0; i < kCopyUnroll; ++i)
+      if (u + i * kCopyThreads < units) v[i] = a[i * kCopyThreads];
+#pragma unroll
+    for (int i = 0; i < kCopyUnroll; ++i)
+      if (u + i * kCopyThreads < units) b[i * kCopyThreads] = v[i];
+  }
+}
+
+// A CTA copies one chunk of a page (its place in x: pool and bytes are settled once) for its share of the pairs (y),
+// of which it looks at 32 at a time, so that rows without a pair cost little.
+__global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_constant__ CopyParams p) {
+  wait_for_stream();
+  int pool = 0;
+  while (pool + 1 < p.pools && static_cast<int>(blockIdx.x) >= p.first[pool + 1]) ++pool;
+  const int64_t at = static_cast<int64_t>(blockIdx.x - p.first[pool]) * kCopyChunk, bytes = min(p.bytes[pool] - at, static_cast<int64_t>(kCopyChunk));
+  uint8_t* base = p.base[pool] + at;
+  const int64_t stride = p.stride[pool];
+  const bool wide = ((reinterpret_cast<uintptr_t>(base) | stride | bytes) & 15) == 0;
+  const int lane = threadIdx.x & 31;
+  for (int64_t i0 = blockIdx.y; i0 < p.n; i0 += 32 * gridDim.y) {
+    const int64_t i = i0 + lane * gridDim.y;
+    int from = -1, to = -1;
+    if (i < p.n) {
+      from = p.src[i];
+      to = p.dst[i];
+    }
+    const bool some = from >= 0 && to >= 0, good = some && from < p.num_pages && to < p.num_pages;
+    if (some && !good && blockIdx.x == 0 && threadIdx.x < 32) report(p.dev_err, MSA_DEVERR_BAD_PAGE);
+    for (uint32_t todo = __ballot_sync(0xffffffffu, good); todo != 0; todo &= todo - 1) {
+      const int k = __ffs(todo) - 1;
+      const int a = __shfl_sync(0xffffffffu, from, k), b = __shfl_sync(0xffffffffu, to, k);
+      if (wide) copy_units<uint4>(base + a * stride, base + b * stride, bytes / 16);
+      else copy_units<uint8_t>(base + a * stride, base + b * stride, bytes);
+    }
+  }
+}
+
+}  // namespace
+
+msa_status launch_fork(const msa_fork_args& a, cudaStream_t stream) {
+  const size_t smem = (3 * static_cast<size_t>(a.F) + a.B + 1) * sizeof(int);
+  return launch_cluster(fork_kernel, a, static_cast<int64_t>(a.F) * std::min<int64_t>(a.max_pages, 64), smem, stream, "fork_kernel launch");
+}
+
+msa_status launch_release_shared(const msa_release_shared_args& a, cudaStream_t stream) {
+  const size_t smem = (static_cast<size_t>(a.B) + 1) * sizeof(int);
+  return launch_cluster(release_shared_kernel, a, std::max<int64_t>(static_cast<int64_t>(a.B) * a.max_pages / 8, a.num_pages / 4), smem, stream,
+                        "release_shared_kernel launch");
+}
+
+msa_status launch_compact(const msa_compact_args& a, cudaStream_t stream) {
+  const size_t smem = (static_cast<size_t>(a.B) + 1) * sizeof(int);
+  return launch_cluster(compact_kernel, a, a.num_pages, smem, stream, "compact_kernel launch");
+}
+
+msa_status launch_copy_pages(const msa_copy_pages_args& a, cudaStream_t stream) {
+  DeviceInfo dev;
+  if (msa_status st = current_device(&dev); st != MSA_OK) return st;
+  CopyParams p = {};
+  p.n = a.n; p.num_pages = a.num_pages;
+  p.src = a.src; p.dst = a.dst;
+  p.pools = a.pools;
+  for (int i = 0; i < a.pools; ++i) {
+    p.base[i] = static_cast<uint8_t*>(a.pool[i]);
+    p.stride[i] = a.page_stride[i];
+    p.bytes[i] = a.page_bytes[i];
+    p.first[i + 1] = p.first[i] + static_cast<int>((a.page_bytes[i] + kCopyChunk - 1) / kCopyChunk);
+  }
+  p.dev_err = a.dev_err;
+  const int chunks = p.first[a.pools];
+  const int64_t share = std::max<int64_t>(1, 8 * dev.num_sms / chunks);
+  const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>(std::min<int64_t>(std::min(a.n, share), 65535)));
+  const cudaError_t e = launch_early(copy_pages_kernel, grid, kCopyThreads, 0, stream, 1, p);
+  if (e != cudaSuccess) return cuda_fail(e, "copy_pages_kernel launch");
+  return MSA_OK;
+}
+
+}  // namespace msa

@@ -69,6 +69,7 @@ typedef enum msa_status {
 #define MSA_DEVERR_BAD_SEL 0x4   /* a selected block outside the causal range */
 #define MSA_DEVERR_BAD_LEN 0x8   /* seq_len[b] (or a chunk's q_pos[b]) outside the pages or past nb_stride */
 #define MSA_DEVERR_NO_PAGES 0x10 /* the stack of free pages ran out, or holds no room for returned pages */
+#define MSA_DEVERR_BAD_ROW 0x20  /* a request outside the table, or a row that is not free */
 
 /* PREFILL: a causal prefill over contiguous K/V/k_idx tensors.
  * DECODE:  one query per sequence over a paged cache.
@@ -925,6 +926,129 @@ typedef struct msa_window_decode_args {
 
 size_t msa_window_attn_decode_workspace_size(int B, int Hkv);
 msa_status msa_window_attn_decode(const msa_window_decode_args *args, void *ws, size_t ws_bytes, msa_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * Pages that several requests hold
+ *
+ * A request may go on from another one's cached tokens (parallel samples, beams, a common prompt): both hold its full
+ * pages, which no append writes again.  page_shares [num_pages] counts each page's holders beyond the first: 0 for free pages
+ * and for those that msa_plan_step gave out, so that call knows nothing of it; the calls here keep it.  Where pages are
+ * shared, ended requests go through msa_release_shared_pages instead of msa_release_pages.
+ *
+ * msa_fork_requests: for every i < F with src[i] >= 0, request dst[i], which must be empty (seq_len 0), becomes a copy of
+ * request src[i] of L = seq_len[src[i]] tokens:
+ *     seq_pt_out[dst][j] = seq_pt[src][j], page_shares_out of that page + 1,   j < L / Bk
+ *     if L % Bk != 0:  seq_pt_out[dst][L / Bk] = a page from the stack (entry free_count - 1 - its number among the forks
+ *                      that need one), copy_src[i] = seq_pt[src][L / Bk], copy_dst[i] = that page
+ *     seq_len_out[dst] = L
+ * copy_src = copy_dst = -1 where nothing is to be copied: msa_copy_pages takes both as they are, once for the pools of
+ * every layer, before the next append.  Other requests keep their length; other entries of seq_pt_out are not written.
+ *   - src[i] < 0: the row is left out (the padding of a captured graph).  src or dst outside the table, a dst that is not
+ *     empty or that an earlier i names: left out, MSA_DEVERR_BAD_ROW.  A length outside [0, max_pages * Bk]: left out,
+ *     MSA_DEVERR_BAD_LEN.  A source may be named any number of times.
+ *   - A fork that needs a page when none is left is left out, and so is every later one that needs one: MSA_DEVERR_NO_PAGES.
+ *   - A shared page id outside [0, num_pages) is handed on uncounted: MSA_DEVERR_BAD_PAGE.
+ * seq_len_out, seq_pt_out, free_count_out and page_shares_out may be the inputs.  B <= 4096, F <= 4096, num_pages <= 2^24. */
+typedef struct msa_fork_args {
+    int B, F, Bk;
+    const int32_t *src;           /* [F] */
+    const int32_t *dst;           /* [F] */
+    const int32_t *seq_len;       /* [B] */
+    const int32_t *seq_pt;        /* [B, max_pages] */
+    int64_t max_pages;
+    const int32_t *free_pages;    /* [free_cap] */
+    int64_t free_cap;
+    const int32_t *free_count;    /* [1] */
+    const int32_t *page_shares;   /* [num_pages] */
+    int64_t num_pages;
+    int32_t *seq_len_out;         /* [B] */
+    int32_t *seq_pt_out;          /* [B, max_pages] */
+    int32_t *free_count_out;      /* [1] */
+    int32_t *page_shares_out;     /* [num_pages] */
+    int32_t *copy_src;            /* [F] */
+    int32_t *copy_dst;            /* [F] */
+    int32_t *dev_err;
+} msa_fork_args;
+
+msa_status msa_fork_requests(const msa_fork_args *args, msa_stream_t stream);
+
+/* msa_release_shared_pages: every request with done[b] != 0 gives up its pages (seq_len_out[b] = 0; the others keep their
+ * length): each takes 1 off page_shares_out of its ceil(seq_len / Bk) pages, and the pages whose last holder ended go on
+ * the stack, free_pages[free_count + ..], in the order of their numbers; their count is 0 again.  seq_pt is left as it is.
+ *   - A length outside [0, max_pages * Bk] of an ended request: it keeps its length and pages, MSA_DEVERR_BAD_LEN.
+ *   - A page id outside [0, num_pages) is dropped, one that more requests gave up than held it goes back once:
+ *     MSA_DEVERR_BAD_PAGE.  Pages past free_cap are dropped: MSA_DEVERR_NO_PAGES, and so for the part of a
+ *     free_count outside [0, free_cap].
+ * seq_len_out, free_count_out and page_shares_out may be the inputs.  B <= 4096, num_pages <= 2^24. */
+typedef struct msa_release_shared_args {
+    int B, Bk;
+    const int32_t *seq_len;       /* [B] */
+    const int32_t *done;          /* [B] */
+    const int32_t *seq_pt;        /* [B, max_pages] */
+    int64_t max_pages;
+    int32_t *free_pages;          /* [free_cap] */
+    int64_t free_cap;
+    const int32_t *free_count;    /* [1] */
+    const int32_t *page_shares;   /* [num_pages] */
+    int64_t num_pages;
+    int32_t *seq_len_out;         /* [B] */
+    int32_t *free_count_out;      /* [1] */
+    int32_t *page_shares_out;     /* [num_pages] */
+    int32_t *dev_err;
+} msa_release_shared_args;
+
+msa_status msa_release_shared_pages(const msa_release_shared_args *args, msa_stream_t stream);
+
+/* msa_compact_pages: where the pages in use have to go so that they are the first n of the pool (n: pages that the B requests
+ * hold, each counted once), so that a smaller pool will do or runs of free pages come together.  The pages in use behind
+ * the first n, by their numbers, go to the free ones among them, by theirs:
+ *     move_src[k], move_dst[k]   the k-th move (-1 from the last one on, to num_pages)
+ *     seq_pt_out                 the requests' entries, renumbered (entries past a request's pages are not written)
+ *     page_shares_out            the counts, moved with their pages, 0 for free ones
+ *     free_pages, free_count     the stack anew: entry i is page num_pages - 1 - i for i < num_pages - n (the lowest one on
+ *                                top), -1 behind; free_count = num_pages - n
+ * No page is both a source and a target: msa_copy_pages takes move_src and move_dst as they are.  Whoever holds page numbers
+ * elsewhere has to follow the moves; pages that no request holds are free afterwards.
+ *   - A length outside [0, max_pages * Bk] counts as 0: MSA_DEVERR_BAD_LEN.  A page id outside [0, num_pages) stays as it is:
+ *     MSA_DEVERR_BAD_PAGE.
+ * seq_pt_out and page_shares_out may be the inputs.  free_cap >= num_pages; B <= 4096, num_pages <= 2^24,
+ * B * max_pages < 2^31. */
+typedef struct msa_compact_args {
+    int B, Bk;
+    const int32_t *seq_len;       /* [B] */
+    const int32_t *seq_pt;        /* [B, max_pages] */
+    int64_t max_pages;
+    const int32_t *page_shares;   /* [num_pages] */
+    int64_t num_pages;
+    int32_t *seq_pt_out;          /* [B, max_pages] */
+    int32_t *page_shares_out;     /* [num_pages] */
+    int32_t *free_pages;          /* [free_cap] */
+    int64_t free_cap;
+    int32_t *free_count;          /* [1] */
+    int32_t *move_src;            /* [num_pages] */
+    int32_t *move_dst;            /* [num_pages] */
+    int32_t *dev_err;
+} msa_compact_args;
+
+msa_status msa_compact_pages(const msa_compact_args *args, msa_stream_t stream);
+
+/* msa_copy_pages: page src[i] of each pool to page dst[i], for every i < n with src[i] >= 0 and dst[i] >= 0.  A pool is
+ * any device memory with page_bytes[k] bytes a page, page_stride[k] bytes apart: keys, values, index keys, codes and scales
+ * of a cache, of one layer or of several (up to MSA_MAX_POOLS a call).  A page id at or past num_pages: the pair is left
+ * out, MSA_DEVERR_BAD_PAGE.  A page that is a target must not be a source or a target of another pair. */
+#define MSA_MAX_POOLS 16
+typedef struct msa_copy_pages_args {
+    int64_t n, num_pages;
+    const int32_t *src;           /* [n] */
+    const int32_t *dst;           /* [n] */
+    int pools;
+    void *pool[MSA_MAX_POOLS];
+    int64_t page_stride[MSA_MAX_POOLS];
+    int64_t page_bytes[MSA_MAX_POOLS];
+    int32_t *dev_err;
+} msa_copy_pages_args;
+
+msa_status msa_copy_pages(const msa_copy_pages_args *args, msa_stream_t stream);
 
 #ifdef __cplusplus
 }
