@@ -35,7 +35,7 @@ __all__ = [
     "msa_dense_attn_decode_q4", "decode_q4_buffers", "decode_step_q4",
     "Q8Cache", "q8_cache", "msa_cache_append_q8", "msa_cache_expand_q8", "msa_attn_decode_q8_workspace_size",
     "msa_sparse_attn_decode_q8", "msa_dense_attn_decode_q8", "decode_q8_buffers", "decode_step_q8",
-    "msa_window_attn_decode", "msa_window_attn_decode_workspace_size",
+    "msa_window_attn_decode", "msa_window_attn_decode_workspace_size", "msa_window_attn_prefill",
     "msa_fork_requests", "msa_release_shared_pages", "msa_compact_pages", "msa_copy_pages",
     "lib", "MSAError",
     "MSA_MODE_PREFILL", "MSA_MODE_DECODE", "MSA_MODE_CHUNK", "MSA_DEVERR_TIMEOUT", "MSA_DEVERR_BAD_PAGE",
@@ -742,6 +742,23 @@ def msa_window_attn_decode(Q: torch.Tensor, K_pool: torch.Tensor, V_pool: torch.
         Q, K_pool, V_pool, seq_pt, seq_len, O, LSE, ws, softmax_scale, dev_err, stream, scratch_zeroed, window, sinks)
     if status:
         _abi.check(status, "msa_window_attn_decode")
+
+
+def msa_window_attn_prefill(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, O: torch.Tensor,
+                            LSE: Optional[torch.Tensor], *, window: int, sinks: int = 0,
+                            seq_pt: Optional[torch.Tensor] = None, q_pos: Optional[torch.Tensor] = None,
+                            softmax_scale: float = 0.0, dev_err: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Attention of many queries through a sliding window with sinks (see msa.h): query i sees the tokens t <= i with
+    t > i - window or t < sinks.
+
+    Q [B,S,Hq,D]; K, V [B,S,Hkv,D], or with ``seq_pt`` [B,max_pages] and ``q_pos`` [B] int32 the page pools [P,Hkv,Bk,D],
+    query s of sequence b then at position q_pos[b] + s (its token in the pages already); all bf16.  O [B,S,Hq,D] bf16 and
+    LSE [B,S,Hq] fp32 (dense).
+    """
+    status = _abi.binding().window_attn_prefill(
+        Q, K, V, O, LSE, softmax_scale, dev_err, stream, window, sinks, seq_pt, q_pos)
+    if status:
+        _abi.check(status, "msa_window_attn_prefill")
 
 
 # ---------------------------------------------------------------------------

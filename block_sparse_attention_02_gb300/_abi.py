@@ -215,6 +215,16 @@ class WindowDecodeArgs(C.Structure):
     ]
 
 
+class WindowPrefillArgs(C.Structure):
+    _fields_ = [
+        ("mode", C.c_int), ("B", C.c_int), ("S", C.c_int), ("Hq", C.c_int), ("Hkv", C.c_int), ("D", C.c_int),
+        ("Bk", C.c_int), ("softmax_scale", C.c_float), ("window", C.c_int), ("sinks", C.c_int),
+        ("Q", _p), ("Q_stride", _i64x3), ("K", _p), ("K_stride", _i64x3), ("V", _p), ("V_stride", _i64x3),
+        ("num_pages", C.c_int64), ("seq_pt", _p), ("max_pages", C.c_int64), ("q_pos", _p),
+        ("O", _p), ("LSE", _p), ("dev_err", _p),
+    ]
+
+
 class ForkArgs(C.Structure):
     _fields_ = [
         ("B", C.c_int), ("F", C.c_int), ("Bk", C.c_int), ("src", _p), ("dst", _p), ("seq_len", _p), ("seq_pt", _p),
@@ -282,6 +292,7 @@ SIGNATURES = {
     "msa_dense_attn_decode_q8": (C.c_int, [C.POINTER(DenseDecodeQ8Args), _p, C.c_size_t, _p]),
     "msa_window_attn_decode_workspace_size": (C.c_size_t, [C.c_int, C.c_int]),
     "msa_window_attn_decode": (C.c_int, [C.POINTER(WindowDecodeArgs), _p, C.c_size_t, _p]),
+    "msa_window_attn_prefill": (C.c_int, [C.POINTER(WindowPrefillArgs), _p]),
     "msa_fork_requests": (C.c_int, [C.POINTER(ForkArgs), _p]),
     "msa_release_shared_pages": (C.c_int, [C.POINTER(ReleaseSharedArgs), _p]),
     "msa_compact_pages": (C.c_int, [C.POINTER(CompactArgs), _p]),

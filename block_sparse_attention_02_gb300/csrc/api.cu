@@ -756,6 +756,35 @@ msa_status msa_window_attn_decode(const msa_window_decode_args* a, void* ws, siz
   return launch_window_decode(*a, ws, reinterpret_cast<cudaStream_t>(stream));
 }
 
+msa_status msa_window_attn_prefill(const msa_window_prefill_args* a, msa_stream_t stream) {
+  g_last_error.clear();
+  MSA_REQUIRE(a != nullptr, MSA_ERR_INVALID_ARG, "args is NULL");
+  MSA_REQUIRE(a->mode == MSA_MODE_PREFILL || a->mode == MSA_MODE_CHUNK, MSA_ERR_INVALID_ARG, "mode = %d", a->mode);
+  MSA_REQUIRE(a->B >= 0 && a->S >= 0 && a->Hkv >= 1 && a->Hq >= 1, MSA_ERR_INVALID_ARG,
+              "B = %d, S = %d, Hq = %d, Hkv = %d", a->B, a->S, a->Hq, a->Hkv);
+  MSA_REQUIRE(a->Hq % a->Hkv == 0 && a->Hq / a->Hkv <= kMaxG, MSA_ERR_UNSUPPORTED,
+              "GQA ratio Hq/Hkv = %d/%d not in 1..%d", a->Hq, a->Hkv, kMaxG);
+  MSA_REQUIRE(a->D == kD, MSA_ERR_UNSUPPORTED, "D = %d, only %d is supported", a->D, kD);
+  MSA_REQUIRE(a->window >= 1 && a->sinks >= 0, MSA_ERR_INVALID_ARG, "window = %d, sinks = %d", a->window, a->sinks);
+  MSA_REQUIRE(a->S <= (1 << 30) && static_cast<int64_t>(a->B) * a->S < (int64_t(1) << 31) &&
+                  (static_cast<int64_t>(a->S) / 32 + 1) * a->B * a->Hkv < (int64_t(1) << 30),
+              MSA_ERR_UNSUPPORTED, "B * S = %d * %d too large", a->B, a->S);
+  if (static_cast<int64_t>(a->B) * a->S == 0) return MSA_OK;
+  MSA_REQUIRE(a->Q && a->K && a->V && a->O, MSA_ERR_INVALID_ARG, "Q, K, V and O must be non-NULL");
+  MSA_REQUIRE(aligned16(a->Q) && aligned16(a->K) && aligned16(a->V) && aligned16(a->O), MSA_ERR_INVALID_ARG,
+              "Q, K, V and O must be 16-byte aligned");
+  for (int i = 0; i < 3; ++i)
+    MSA_REQUIRE(vec_stride_ok(a->Q_stride[i], 2) && vec_stride_ok(a->K_stride[i], 2) && vec_stride_ok(a->V_stride[i], 2),
+                MSA_ERR_INVALID_ARG, "Q/K/V strides must be positive multiples of 8 elements");
+  if (a->mode == MSA_MODE_CHUNK) {
+    MSA_REQUIRE(a->Bk == kBk, MSA_ERR_UNSUPPORTED, "Bk = %d, only %d is supported", a->Bk, kBk);
+    MSA_REQUIRE(a->num_pages >= 1 && a->num_pages < (int64_t(1) << 31) - 1, MSA_ERR_INVALID_ARG, "num_pages = %" PRId64, a->num_pages);
+    MSA_REQUIRE(a->seq_pt && a->q_pos, MSA_ERR_INVALID_ARG, "seq_pt and q_pos must be non-NULL");
+    MSA_REQUIRE(a->max_pages >= 1 && a->max_pages <= (int64_t(1) << 30) / kBk, MSA_ERR_INVALID_ARG, "max_pages = %" PRId64, a->max_pages);
+  }
+  return launch_window_prefill(*a, reinterpret_cast<cudaStream_t>(stream));
+}
+
 // ---------------------------------------------------------------------------
 static msa_status check_pool(int64_t num_pages) {
   MSA_REQUIRE(num_pages >= 1 && num_pages <= (int64_t(1) << 24), MSA_ERR_INVALID_ARG, "num_pages = %" PRId64 ", supported 1..2^24",

@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(32 * kWarps, F::kSmWarps / kWarps) attn_rows_k
 
   // what a sequence of L tokens (dense) shows its query: the first page of the window, and the sinks' pages before it
   auto first_of = [&](int L) { return MODE == kWindow ? max(L - p.window, 0) : 0; };
-  auto sink_pages = [&](int first) { return MODE == kWindow ? min((min(p.sinks, first) + kBk - 1) / kBk, first / kBk) : 0; };
+  auto sink_pages = [&](int first) { return MODE == kWindow ? min(static_cast<int>((min(p.sinks, first) + kBk - 1u) / kBk), first / kBk) : 0; };
   // pages of one head of sequence x (dense) or of row x (sparse), and its units (dense)
   auto pages_of = [&](int x) {
     if (!DENSE) return min(max(p.n[x], 0), p.k);

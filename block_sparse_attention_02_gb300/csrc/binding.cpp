@@ -496,6 +496,45 @@ msa_status window_attn_decode(PyObject* const* o) {
   return on_device(dev, [&] { return msa_window_attn_decode(&a, work, bytes, s); });
 }
 
+// Q, K, V, O, LSE, softmax_scale, dev_err, stream, window, sinks, seq_pt, q_pos (both None: contiguous K and V)
+msa_status window_attn_prefill(PyObject* const* o) {
+  const at::Tensor &Q = tensor(o[0], "Q"), &K = tensor(o[1], "K"), &V = tensor(o[2], "V"), &O = tensor(o[3], "O");
+  const int dev = device_of(Q, "Q");
+  msa_window_prefill_args a = {};
+  a.Q = rows<4>(Q, "Q", dev, a.Q_stride);
+  a.K = rows<4>(K, "K", dev, a.K_stride);
+  a.V = rows<4>(V, "V", dev, a.V_stride);
+  a.B = as_int(Q.size(0), "B"); a.S = as_int(Q.size(1), "S"); a.Hq = as_int(Q.size(2), "Hq"); a.D = as_int(Q.size(3), "D");
+  a.Bk = kBk;
+  const bool paged = o[10] != Py_None;
+  if (paged != (o[11] != Py_None)) refuse("seq_pt and q_pos go together");
+  a.mode = paged ? MSA_MODE_CHUNK : MSA_MODE_PREFILL;
+  need_shape(V, "V", K.sizes());
+  if (paged) {
+    a.num_pages = K.size(0);
+    a.Hkv = as_int(K.size(1), "Hkv");
+    need_shape(K, "K", {K.size(0), K.size(1), kBk, Q.size(3)});
+    a.seq_pt = dense<int32_t>(o[10], "seq_pt", at::kInt, dev, 2, a.B);
+    a.max_pages = THPVariable_Unpack(o[10]).size(1);
+    a.q_pos = dense<int32_t>(o[11], "q_pos", at::kInt, dev, 1, a.B);
+  } else {
+    a.Hkv = as_int(K.size(2), "Hkv");
+    need_shape(K, "K", {Q.size(0), Q.size(1), K.size(2), Q.size(3)});
+  }
+  a.O = dense<void>(o[3], "O", at::kBFloat16, dev, 4);
+  need_shape(O, "O", Q.sizes());
+  if (o[4] != Py_None) {
+    a.LSE = dense<float>(o[4], "LSE", at::kFloat, dev, 3);
+    need_shape(THPVariable_Unpack(o[4]), "LSE", {Q.size(0), Q.size(1), Q.size(2)});
+  }
+  a.softmax_scale = real(o[5], "softmax_scale");
+  a.dev_err = err_word(o[6], dev);
+  msa_stream_t s = stream_of(o[7], dev);
+  a.window = as_int(integer(o[8], "window"), "window");
+  a.sinks = as_int(integer(o[9], "sinks"), "sinks");
+  return on_device(dev, [&] { return msa_window_attn_prefill(&a, s); });
+}
+
 // The stack of free pages and the pages' counts, with their outputs: free_pages, free_count, page_shares; free_count_out,
 // page_shares_out.
 template <class Args>
@@ -647,6 +686,7 @@ PyMethodDef methods[] = {
     method<sparse_attn_decode<msa_decode_q8_args, msa_sparse_attn_decode_q8>, 12>("sparse_attn_decode_q8"),
     method<dense_attn_decode_q8, 13>("dense_attn_decode_q8"),
     method<window_attn_decode, 14>("window_attn_decode"),
+    method<window_attn_prefill, 12>("window_attn_prefill"),
     method<fork_requests, 15>("fork_requests"),
     method<release_shared_pages, 11>("release_shared_pages"),
     method<compact_pages, 11>("compact_pages"),

@@ -68,6 +68,7 @@ msa_status launch_expand_q8(const msa_expand_q8_args& a, cudaStream_t stream);
 msa_status launch_sparse_decode_q8(const msa_decode_q8_args& a, void* ws, cudaStream_t stream);
 msa_status launch_dense_decode_q8(const msa_dense_decode_q8_args& a, void* ws, cudaStream_t stream);
 msa_status launch_window_decode(const msa_window_decode_args& a, void* ws, cudaStream_t stream);
+msa_status launch_window_prefill(const msa_window_prefill_args& a, cudaStream_t stream);
 size_t attn_rows_workspace_size(int B, int Hkv);   // of the three calls before
 msa_status launch_fork(const msa_fork_args& a, cudaStream_t stream);
 msa_status launch_release_shared(const msa_release_shared_args& a, cudaStream_t stream);

@@ -927,6 +927,37 @@ typedef struct msa_window_decode_args {
 size_t msa_window_attn_decode_workspace_size(int B, int Hkv);
 msa_status msa_window_attn_decode(const msa_window_decode_args *args, void *ws, size_t ws_bytes, msa_stream_t stream);
 
+/* msa_window_attn_prefill: many queries per sequence.
+ *   mode MSA_MODE_PREFILL: query s of sequence b at position s of its own keys.  Q [B, S, Hq, D], K, V [B, S, Hkv, D] bf16,
+ *     strides (b, s, h).
+ *   mode MSA_MODE_CHUNK: query s at position q_pos[b] + s over a paged cache that holds the chunk's own tokens already (chunked
+ *     prefill, draft tokens).  K, V are pools [num_pages, Hkv, Bk, D], strides (page, g, t); seq_pt [B, max_pages],
+ *     q_pos [B].  A sequence with q_pos < 0 or q_pos + S > max_pages * Bk gets O = 0 and LSE = -inf and raises
+ *     MSA_DEVERR_BAD_LEN.  A page id outside [0, num_pages) is not read and its tokens are left out (MSA_DEVERR_BAD_PAGE).
+ *     Pages without a seen token are not read; slots of the others that no query sees must hold finite values.
+ * O [B, S, Hq, D] bf16 (dense), LSE [B, S, Hq] fp32 (dense, may be NULL).  P is rounded to bf16.  No workspace.
+ * softmax_scale <= 0 selects 1 / sqrt(D).  S <= 2^30 and max_pages * Bk <= 2^30, B * S < 2^31. */
+typedef struct msa_window_prefill_args {
+    int mode, B, S, Hq, Hkv, D, Bk;
+    float softmax_scale;
+    int window, sinks;
+    const void *Q;
+    int64_t Q_stride[3];
+    const void *K;
+    int64_t K_stride[3];
+    const void *V;
+    int64_t V_stride[3];
+    int64_t num_pages;            /* CHUNK */
+    const int32_t *seq_pt;        /* CHUNK */
+    int64_t max_pages;            /* CHUNK */
+    const int32_t *q_pos;         /* CHUNK */
+    void *O;
+    float *LSE;
+    int32_t *dev_err;
+} msa_window_prefill_args;
+
+msa_status msa_window_attn_prefill(const msa_window_prefill_args *args, msa_stream_t stream);
+
 /* --------------------------------------------------------------------------
  * Pages that several requests hold
  *
