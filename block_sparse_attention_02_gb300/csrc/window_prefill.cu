@@ -108,11 +108,6 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -399,9 +394,14 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
             uint32_t pw[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const uint64_t z = pair(__uint_as_float(v[cc][e]), __uint_as_float(v[cc][e + 1]));
+              const float y = __uint_as_float(v[cc][e]), z = __uint_as_float(v[cc][e + 1]);
               float a, b;
-              unpair(decltype(fused)::value ? fma2(z, sc2, off2) : add2(mul2(z, sc2), off2), &a, &b);
+              if (decltype(fused)::value) {
+                unpair(fma2(pair(y, z), sc2, off2), &a, &b);
+              } else {
+                a = __fadd_rn(__fmul_rn(y, sc), off);
+                b = __fadd_rn(__fmul_rn(z, sc), off);
+              }
               a = fast_exp2(a);
               b = fast_exp2(b);
               sum2[(e >> 1) & 1] = add2(sum2[(e >> 1) & 1], pair(a, b));
