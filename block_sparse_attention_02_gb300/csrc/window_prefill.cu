@@ -15,13 +15,11 @@
 // The running max m is updated lazily: O and the running sum are rescaled only when a block's max exceeds m by more than
 // 2^8, so P <= 256 and the result is exact whichever m is used.  Blocks that some row does not see whole are masked.
 //
-// Roles: warp 0 TMA of K and V (a ring of 32 KiB units, K and V apart), warp 1 tcgen05 issuer, warps 2-5 and 6-9 the two
+// Roles: warp 0 TMA of K and V (a ring of 32 KiB units, K and V apart), warp 1 tcgen05 issuer, warps 4-7 and 8-11 the two
 // slots' softmax and epilogue; a slot's softmax also sends for its next Q tile, once its last S is done.  Each slot goes
 // through its items on its own: S(j + 1) is issued right behind O(j), which reads P from the same columns (one thread's
 // MMAs run in order), and the other slot's products run meanwhile.
 #include <algorithm>
-#include <climits>
-#include <type_traits>
 
 #include "msa_internal.h"
 #include "msa_ptx.cuh"
@@ -29,12 +27,15 @@
 namespace msa {
 namespace {
 
-constexpr int kHalf = 128 * 64 * 2;          // 16 KiB: 128 rows x 64 bf16
-constexpr int kUnit = 2 * kHalf;             // 32 KiB: a tile of Q, K or V
-constexpr int kUnits = 5;                    // of K and V in shared memory
-constexpr int kNotes = 8;                    // blocks whose page's state is kept (more than are in flight)
-constexpr int kThreads = 320;                // w0 TMA, w1 MMA, w2-5 slot 0, w6-9 slot 1
-constexpr int kTmemCols = 512;               // per slot: S / P (128 columns) and O (128 columns)
+constexpr int kKeys = 64;                    // of a block
+constexpr int kQHalf = 128 * 64 * 2;         // 16 KiB: 128 rows x 64 bf16
+constexpr int kQTile = 2 * kQHalf;
+constexpr int kHalf = kKeys * 64 * 2;        // 8 KiB: a block's rows x 64 bf16
+constexpr int kUnit = 2 * kHalf;             // 16 KiB: K or V of a block
+constexpr int kUnits = 10;                   // of K and V in shared memory
+constexpr int kNotes = 16;                   // blocks whose page's state is kept (more than are in flight)
+constexpr int kThreads = 384;                // w0 TMA of K and V, w1-2 the slots' issuers, w4-7 slot 0, w8-11 slot 1
+constexpr int kTmemCols = 512;               // per slot: two of S / P (64 columns each) and O (128 columns)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;             // log2 of the largest P before the running max moves
@@ -76,9 +77,9 @@ __device__ __forceinline__ Item item_of(const Params& p, int it) {
     return x;
   }
   const int last = start + min(x.q0 + 2 * p.nq, p.S) - 1;
-  x.first = max(x.pos - p.window + 1, 0) / kBk;
-  x.sink_blocks = min((min(p.sinks, last + 1) + kBk - 1) / kBk, x.first);
-  x.blocks = x.sink_blocks + last / kBk - x.first + 1;
+  x.first = max(x.pos - p.window + 1, 0) / kKeys;
+  x.sink_blocks = min((min(p.sinks, last + 1) + kKeys - 1) / kKeys, x.first);
+  x.blocks = x.sink_blocks + last / kKeys - x.first + 1;
   return x;
 }
 
@@ -91,11 +92,52 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   __nv_bfloat162 h2 = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h2);
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-                 "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-               : "r"(taddr));
+// Products and commits by an elected lane of a converged warp (the same lane every time), under a predicate: control flow stays
+// that of the whole warp, so that descriptors are kept in uniform registers.
+__device__ __forceinline__ void umma_elect(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void commit_elect(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
+}
+// A bounded wait as mbar_wait, which reads the clock only after some tries: a read takes about as long as a block's products,
+// and most waits here are shorter.
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* dev_err) {
+  uint64_t since = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 31u) != 0) continue;
+    if (*abort_flag) return false;
+    const uint64_t now = global_timer_ns();
+    if (i == 32) since = now;
+    if (now - since > MSA_WAIT_LIMIT_NS) {
+      *abort_flag = 1;
+      report(dev_err, MSA_DEVERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* dev_err) {
+  return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag, dev_err);
 }
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
   uint64_t r;
@@ -120,25 +162,33 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* s_q = smem;                       // [2] Q tiles
-  uint8_t* s_kv = smem + 2 * kUnit;          // [kUnits] of K and V: unit 2 n is K of the CTA's n-th block, 2 n + 1 its V
+  uint8_t* s_kv = smem + 2 * kQTile;         // [kUnits] of K and V: unit 2 n is K of the CTA's n-th block, 2 n + 1 its V
 
-  __shared__ __align__(8) uint64_t bar_qfull[2], bar_full[kUnits], bar_empty[kUnits];
-  __shared__ __align__(8) uint64_t bar_sfull[2], bar_pready[2], bar_ofull[2], bar_drain;
+  __shared__ __align__(8) uint64_t bar_qfull[2], bar_qempty[2], bar_full[kUnits], bar_empty[kUnits];
+  // per slot; of S and P one for each of the two buffers: an S or P may be complete before the one before it is looked at
+  __shared__ __align__(8) uint64_t bar_sfull[2][2], bar_pready[2][2], bar_ofull[2], bar_odone[2], bar_drain[2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ volatile int s_gone[kNotes];    // of block n % kNotes: no such page
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    for (int i = 0; i < kUnits; ++i) { mbar_init(&bar_full[i], 1); mbar_init(&bar_empty[i], 1); }
+    for (int i = 0; i < kUnits; ++i) { mbar_init(&bar_full[i], 1); mbar_init(&bar_empty[i], 2); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar_qfull[i], 1);
-      mbar_init(&bar_sfull[i], 1); mbar_init(&bar_pready[i], 4); mbar_init(&bar_ofull[i], 1);
+      mbar_init(&bar_qempty[i], 1);
+      for (int k = 0; k < 2; ++k) { mbar_init(&bar_sfull[i][k], 1); mbar_init(&bar_pready[i][k], 4); }
+      mbar_init(&bar_ofull[i], 1);
+      mbar_init(&bar_odone[i], 1);
+      mbar_init(&bar_drain[i], 1);
     }
-    mbar_init(&bar_drain, 1);
     s_abort = 0;
     fence_mbar_init();
   }
+  // rows past a tile's queries, which no load writes: zeros, so that their scores are numbers
+  for (int i = tid; i < 4 * (128 - p.nq * p.G) * 8; i += kThreads)
+    reinterpret_cast<uint4*>(s_q + (i & 3) * kQHalf + p.nq * p.G * 128)[i >> 2] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
   if (warp == 1) tmem_alloc(&s_tmem, kTmemCols);
   __syncthreads();
   tc_fence_after();
@@ -147,31 +197,30 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
 
   if (warp == 0) {
     // ===================== TMA producer of K and V (warp-uniform loop, lane 0 issues) =====================
-    int n = 0;                               // blocks sent for
+    int n = 0, st = 0;                       // blocks sent for; the next unit and its phase
+    uint32_t phase = 0;
     bool ok = true;
     for (int it = blockIdx.x; it < p.n_items && ok; it += gridDim.x) {
       const Item x = item_of(p, it);
       for (int j0 = 0; j0 < x.blocks && ok; j0 += 32) {
         // lane l looks up the page of block j0 + l
         int pg = 0;
-        if (p.paged && j0 + lane < x.blocks) pg = p.seq_pt[x.b * p.max_pages + x.block(j0 + lane)];
+        if (p.paged && j0 + lane < x.blocks) pg = p.seq_pt[x.b * p.max_pages + x.block(j0 + lane) * kKeys / kBk];
         for (int i = 0; i < 32 && j0 + i < x.blocks; ++i, ++n) {
           const int page = __shfl_sync(0xffffffffu, pg, i);
           int go = 1;
           if (lane == 0) {
             const bool gone = p.paged && (page < 0 || page >= p.num_pages);
             // a page that there is not is read as zeros: from past the end of the pool
-            const int c1 = p.paged ? 0 : x.g, c2 = p.paged ? x.g : x.block(j0 + i) * kBk;
-            const int c3 = p.paged ? (gone ? static_cast<int>(p.num_pages) : page) : x.b;
+            const int t = x.block(j0 + i) * kKeys, c1 = p.paged ? t % kBk : t;
+            const int c4 = p.paged ? (gone ? static_cast<int>(p.num_pages) : page) : x.b;
             for (int kv = 0; kv < 2 && go; ++kv) {
-              const int u = 2 * n + kv, st = u % kUnits;
-              go = mbar_wait(&bar_empty[st], ((u / kUnits) & 1) ^ 1, abort_flag, p.dev_err);
+              go = wait(&bar_empty[st], phase ^ 1, abort_flag, p.dev_err);
               if (!go) break;
               if (kv == 0) s_gone[n % kNotes] = gone;
-              uint8_t* to = s_kv + st * kUnit;
               mbar_arrive_expect_tx(&bar_full[st], kUnit);
-              tma_load_4d(to, kv ? &vmap : &kmap, &bar_full[st], 0, c1, c2, c3);
-              tma_load_4d(to + kHalf, kv ? &vmap : &kmap, &bar_full[st], 64, c1, c2, c3);
+              tma_load_5d(s_kv + st * kUnit, kv ? &vmap : &kmap, &bar_full[st], 0, c1, 0, x.g, c4);
+              if (++st == kUnits) { st = 0; phase ^= 1; }
             }
             if (gone) report(p.dev_err, MSA_DEVERR_BAD_PAGE);
           }
@@ -189,171 +238,145 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         }
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // ===================== tcgen05 issuer =====================
-    // Per slot: S(j) of its item needs K(j), the item's Q tile (j = 0) and O(j - 1) issued before it; O(j) needs P(j) and
-    // V(j).  Whatever is ready is issued.
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_bf16(128, 128, false, false);
-      constexpr uint32_t idesc_o = idesc_bf16(128, 128, false, true);
-      int it[2];
-      int j[2] = {0, 0}, blocks[2] = {0, 0};  // the slot's next block of its item, and the item's blocks
-      int ns[2] = {0, 0}, no[2] = {0, 0};     // blocks of the CTA whose S / O is issued, or that the slot sits out
-      int waits[2] = {0, 0}, items[2] = {0, 0};   // S issued; items begun (phases of pready and qfull)
-      bool pending[2] = {false, false};       // S issued, O not yet
-      int free_k = 0, free_v = 0;             // blocks whose unit is given back
-      constexpr int kEnd = INT_MAX / 2;       // ns and no of a slot that has no item left
-      // the slot's next item, from item `i` on; the blocks of one that has no tile for it pass at once
-      auto take_item = [&](int s, int i) {
-        j[s] = 0;
-        for (; i < p.n_items; i += gridDim.x) {
-          const Item x = item_of(p, i);
-          blocks[s] = x.blocks;
-          if (x.blocks > 0 && s < x.tiles) break;
-          ns[s] += x.blocks;
-          no[s] += x.blocks;
+  } else if (warp < 3) {
+    // ===================== tcgen05 issuer of slot s (warp-uniform loop, lane 0 issues) =====================
+    // Step j of an item: O(j - 2), then S(j) into the buffer whose P that O reads.  So S is two blocks ahead and the
+    // softmax always has one to work on.
+    const int s = warp - 1;
+    constexpr uint32_t idesc_s = idesc_bf16(128, kKeys, false, false);
+    constexpr uint32_t idesc_o = idesc_bf16(128, 128, false, true);
+    const uint32_t sp = tmem + s * 256, out = sp + 128;
+    const uint64_t q_desc = sdesc_sw128(smem_u32(s_q + s * kQTile), 16, 1024), k_desc = sdesc_sw128(smem_u32(s_kv), 16, 1024),
+                   v_desc = sdesc_sw128(smem_u32(s_kv), kHalf, 1024);
+    int sk = 0, sv = 1;                      // units of the next K and V, and their phases
+    uint32_t pk = 0, pv = 0;
+    int n = 0, items = 0, sent = 0;          // blocks and items done, Q tiles sent for
+    bool ok = true;
+    auto next_k = [&] {
+      sk += 2;
+      if (sk >= kUnits) { sk -= kUnits; pk ^= 1; }
+    };
+    auto next_v = [&] {
+      sv += 2;
+      if (sv >= kUnits) { sv -= kUnits; pv ^= 1; }
+    };
+    // the Q tile of this slot's first item from `it` on that has blocks, once the last S of the one before is done
+    auto send_q = [&](int it) {
+      for (; it < p.n_items; it += gridDim.x) {
+        const Item x = item_of(p, it);
+        if (s >= x.tiles || x.blocks == 0) continue;
+        if (lane == 0 && wait(&bar_qempty[s], (sent & 1) ^ 1, abort_flag, p.dev_err)) {
+          mbar_arrive_expect_tx(&bar_qfull[s], static_cast<uint32_t>(p.nq * p.G) * 256);
+          for (int half = 0; half < 2; ++half)
+            tma_load_5d(s_q + s * kQTile + half * kQHalf, &qmap, &bar_qfull[s], 0, x.g * p.G, x.q0 + s * p.nq, half, x.b);
         }
-        it[s] = i;
-        if (i >= p.n_items) ns[s] = no[s] = kEnd;
-      };
-      // units that both slots have read (or will not) are free when the products issued so far are done
-      auto give_back = [&] {
-        for (const int n = min(ns[0], ns[1]); free_k < n && n < kEnd; ++free_k) umma_commit(&bar_empty[2 * free_k % kUnits]);
-        for (const int n = min(no[0], no[1]); free_v < n && n < kEnd; ++free_v) umma_commit(&bar_empty[(2 * free_v + 1) % kUnits]);
-      };
-      take_item(0, blockIdx.x);
-      take_item(1, blockIdx.x);
-      uint32_t spins = 0;
-      uint64_t idle_since = 0;
-      while (it[0] < p.n_items || it[1] < p.n_items) {
-        bool progress = false;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (it[s] >= p.n_items) continue;
-          if (pending[s] && mbar_test_wait(&bar_pready[s], (waits[s] - 1) & 1)) {
-            const int u = 2 * no[s] + 1, st = u % kUnits;
-            if (mbar_test_wait(&bar_full[st], (u / kUnits) & 1)) {
-              tc_fence_after();
-              const uint32_t vb = smem_u32(s_kv + st * kUnit);
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                umma_bf16_ts(tmem + s * 256 + 128, tmem + s * 256 + kk * 8, sdesc_sw128(vb + kk * 2048, kHalf, 1024), idesc_o,
-                             (j[s] > 0 || kk > 0) ? 1u : 0u);
-              ++no[s];
-              pending[s] = false;
-              if (++j[s] == blocks[s]) {
-                umma_commit(&bar_ofull[s]);
-                take_item(s, it[s] + gridDim.x);
-              }
-              give_back();
-              progress = true;
-              if (it[s] >= p.n_items) continue;
-            }
+        ++sent;
+        break;
+      }
+    };
+    send_q(blockIdx.x);
+    for (int it = blockIdx.x; it < p.n_items && ok; it += gridDim.x) {
+      const Item x = item_of(p, it);
+      const int blocks = __shfl_sync(0xffffffffu, x.blocks, 0);   // (from lane 0: the compiler then knows that the warp goes one way)
+      if (s >= __shfl_sync(0xffffffffu, x.tiles, 0)) {
+        // an item without a tile for this slot: its units pass
+        for (int j = 0; j < blocks && ok; ++j) {
+          ok = wait(&bar_full[sk], pk, abort_flag, p.dev_err) && wait(&bar_full[sv], pv, abort_flag, p.dev_err);
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok && lane == 0) {
+            mbar_arrive(&bar_empty[sk]);
+            mbar_arrive(&bar_empty[sv]);
           }
-          // (a slot is a block ahead of the other at most: further on, a unit's phase could be taken for the one before last)
-          if (!pending[s] && ns[s] <= ns[1 - s] + 1) {
-            const int u = 2 * ns[s], st = u % kUnits;
-            if ((j[s] > 0 || mbar_test_wait(&bar_qfull[s], items[s] & 1)) && mbar_test_wait(&bar_full[st], (u / kUnits) & 1)) {
-              tc_fence_after();
-              if (j[s] == 0) ++items[s];
-              const uint32_t qb = smem_u32(s_q + s * kUnit), kb = smem_u32(s_kv + st * kUnit);
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                umma_bf16(tmem + s * 256, sdesc_sw128(qb + (kk >> 2) * kHalf + 32 * (kk & 3), 16, 1024),
-                          sdesc_sw128(kb + (kk >> 2) * kHalf + 32 * (kk & 3), 16, 1024), idesc_s, kk > 0);
-              umma_commit(&bar_sfull[s]);
-              ++ns[s];
-              ++waits[s];
-              pending[s] = true;
-              give_back();
-              progress = true;
-            }
-          }
+          next_k();
+          next_v();
         }
-        if (progress) {
-          spins = 0;
-        } else if ((++spins & 63u) == 0) {
-          const uint64_t now = global_timer_ns();
-          if (spins == 64) idle_since = now;
-          if (*abort_flag) break;
-          if (now - idle_since > MSA_WAIT_LIMIT_NS) {
-            *abort_flag = 1;
-            report(p.dev_err, MSA_DEVERR_TIMEOUT);
-            break;
-          }
+        continue;
+      }
+      if (blocks == 0) continue;
+      for (int j = 0; j < blocks + 2; ++j) {
+        const uint32_t buf = (n + j) & 1;    // of O(j - 2) and S(j)
+        if (j >= 2) {
+          ok = wait(&bar_full[sv], pv, abort_flag, p.dev_err) && wait(&bar_pready[s][buf], ((n + j - 2) >> 1) & 1, abort_flag, p.dev_err);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            umma_ts_elect(out, sp + buf * kKeys + kk * 8, v_desc + sv * (kUnit / 16) + kk * (2048 / 16), idesc_o,
+                       (j > 2 || kk > 0) ? 1u : 0u);
+          commit_elect(&bar_empty[sv]);
+          commit_elect(&bar_ofull[s]);
+          if (j == blocks + 1) commit_elect(&bar_odone[s]);
+          next_v();
+        }
+        if (j < blocks) {
+          ok = wait(&bar_full[sk], pk, abort_flag, p.dev_err) && (j > 0 || wait(&bar_qfull[s], items & 1, abort_flag, p.dev_err));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_elect(sp + buf * kKeys, q_desc + (kk >> 2) * (kQHalf / 16) + 2 * (kk & 3),
+                    k_desc + sk * (kUnit / 16) + (kk >> 2) * (kHalf / 16) + 2 * (kk & 3), idesc_s, kk > 0);
+          commit_elect(&bar_sfull[s][buf]);
+          commit_elect(&bar_empty[sk]);
+          if (j == blocks - 1) commit_elect(&bar_qempty[s]);
+          next_k();
+        } else if (j == blocks) {
+          send_q(it + gridDim.x);
         }
       }
-      umma_commit(&bar_drain);
-      const uint64_t t0 = global_timer_ns();
-      while (!mbar_try_wait(&bar_drain, 0) && global_timer_ns() - t0 < MSA_WAIT_LIMIT_NS) {
-      }
+      n += blocks;
+      ++items;
     }
     __syncwarp();
-  } else {
+    commit_elect(&bar_drain[s]);
+    if (lane == 0) {
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(&bar_drain[s], 0) && global_timer_ns() - t0 < MSA_WAIT_LIMIT_NS) {
+      }
+      while (sent > 0 && *abort_flag && !mbar_try_wait(&bar_qfull[s], (sent - 1) & 1) && global_timer_ns() - t0 < MSA_WAIT_LIMIT_NS) {
+      }                                      // (a load in flight lands before the CTA exits)
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
     // ===================== softmax + epilogue of slot s (thread = row) =====================
-    const int s = (warp - 2) >> 2;
+    const int s = (warp >> 2) - 1;
     const int q = warp & 3;
     const int r = q * 32 + lane;
     const int query = r / p.G, head = r - query * p.G;
-    const bool leader = q == ((2 + 4 * s) & 3) && lane == 0;
     const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
-    const uint32_t sbase = tmem + lane_addr + s * 256;     // S, then P (bf16 pairs) in its first 64 columns
+    const uint32_t sbase = tmem + lane_addr + s * 256;     // two buffers: S, then P (bf16 pairs) in its first 32 columns
     const uint32_t obase = sbase + 128;
     const float sc = p.scale_log2;
-    int sent = 0;                                          // Q tiles sent for
-    auto send_q = [&](const Item& x) {
-      const uint32_t bytes = static_cast<uint32_t>(p.nq * p.G) * 128;
-      mbar_arrive_expect_tx(&bar_qfull[s], 2 * bytes);
-      tma_load_4d(s_q + s * kUnit, &qmap, &bar_qfull[s], 0, x.g * p.G, x.q0 + s * p.nq, x.b);
-      tma_load_4d(s_q + s * kUnit + kHalf, &qmap, &bar_qfull[s], 64, x.g * p.G, x.q0 + s * p.nq, x.b);
-      ++sent;
-    };
-    // this slot's next item from `it` on (one without blocks is a refused sequence: its rows are 0)
-    auto next_of = [&](int it, Item* x) {
-      for (; it < p.n_items; it += gridDim.x) {
-        *x = item_of(p, it);
-        if (s < x->tiles) break;
-      }
-      return it;
-    };
-    Item x;
-    int it = next_of(blockIdx.x, &x);
-    int nS = 0, nO = 0, n = 0;                             // waits done on sfull, ofull; blocks of the CTA so far
-    int seen = blockIdx.x;                                 // items whose blocks n counts
-    auto send_next = [&](int from) {                       // the Q tile of the next item with blocks
-      Item y;
-      for (int k = next_of(from, &y); k < p.n_items; k = next_of(k + gridDim.x, &y))
-        if (y.blocks > 0) {
-          send_q(y);
-          return;
-        }
-    };
-    if (leader) send_next(blockIdx.x);
+    int nS = 0, nI = 0, n = 0;                             // blocks done; items done; blocks of the CTA so far
     bool alive = true;
-    while (it < p.n_items && alive) {
-      for (; seen < it; seen += gridDim.x) n += item_of(p, seen).blocks;
+    for (int it = blockIdx.x; it < p.n_items && alive; it += gridDim.x) {
+      const Item x = item_of(p, it);
+      const int n0 = n;
+      n += x.blocks;
+      if (s >= x.tiles) continue;
       const int row = x.q0 + s * p.nq + query;             // of the sequence's S queries
       const bool real = query < p.nq && row < p.S;
       const int i = x.pos + s * p.nq + query;              // its position
       const int low = x.pos + s * p.nq, high = low + p.nq - 1;
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < x.blocks; ++j) {
-        const bool ok_s = mbar_wait(&bar_sfull[s], nS & 1, abort_flag, p.dev_err);
-        ++nS;
+      for (int j = 0; j < x.blocks; ++j, ++nS) {
+        const bool ok_s = wait(&bar_sfull[s][nS & 1], (nS >> 1) & 1, abort_flag, p.dev_err);
         if (!__all_sync(0xffffffffu, ok_s)) { alive = false; break; }
         tc_fence_after();
-        if (j == x.blocks - 1 && leader) send_next(it + gridDim.x);   // this item's Q tile is read
-        const int t0 = x.block(j) * kBk;
-        uint32_t v[4][32];
-#pragma unroll
-        for (int cc = 0; cc < 4; ++cc) tmem_ld32(sbase + cc * 32, v[cc]);
+        const uint32_t sb = sbase + (nS & 1) * kKeys;
+        const int t0 = x.block(j) * kKeys;
+        uint32_t v[2][32];
+        tmem_ld32(sb, v[0]);
+        tmem_ld32(sb + 32, v[1]);
         tmem_ld_wait();
-        const bool gone = p.paged && s_gone[(n + j) % kNotes] != 0;
-        if (gone || t0 + kBk - 1 > low || (t0 <= high - p.window && t0 + kBk > p.sinks)) {
+        const bool gone = p.paged && s_gone[(n0 + j) % kNotes] != 0;
+        if (gone || t0 + kKeys - 1 > low || (t0 <= high - p.window && t0 + kKeys > p.sinks)) {
           // some row does not see all of it: columns c <= last, and c >= from or c < sinks
           const int last = gone ? -1 : i - t0, from = i - p.window + 1 - t0, sinks = p.sinks - t0;
 #pragma unroll
-          for (int cc = 0; cc < 4; ++cc)
+          for (int cc = 0; cc < 2; ++cc)
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               const int c = cc * 32 + e;
@@ -362,73 +385,75 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         }
         float mx[4];
 #pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
-          mx[cc] = __uint_as_float(v[cc][0]);
+        for (int k = 0; k < 4; ++k) {
+          mx[k] = __uint_as_float(v[k >> 1][(k & 1) * 16]);
 #pragma unroll
-          for (int e = 1; e < 32; ++e) mx[cc] = fmaxf(mx[cc], __uint_as_float(v[cc][e]));
+          for (int e = 1; e < 16; ++e) mx[k] = fmaxf(mx[k], __uint_as_float(v[k >> 1][(k & 1) * 16 + e]));
         }
         const float bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;   // scale > 0: max of the scaled scores
         const bool up = bm > m + kRescale;
-        if (__any_sync(0xffffffffu, up)) {                 // O and the sum to the new max (O(j - 1) is done: S(j) came after it)
+        if (__any_sync(0xffffffffu, up)) {                 // O and the sum to the new max
           const float alpha = up ? fast_exp2(m - bm) : 1.f;
           if (up) m = bm;
           l *= alpha;
           if (j > 0) {
+            // (the O two before this block's is done, S came after it: the barrier is at most a phase behind)
+            const bool ok_o = wait(&bar_ofull[s], (nS - 1) & 1, abort_flag, p.dev_err);
+            if (!__all_sync(0xffffffffu, ok_o)) { alive = false; break; }
+            tc_fence_after();
 #pragma unroll
-            for (int cc = 0; cc < 8; ++cc) {
-              uint32_t o[16];
-              tmem_ld16(obase + cc * 16, o);
+            for (int cc = 0; cc < 4; ++cc) {
+              uint32_t o[32];
+              tmem_ld32(obase + cc * 32, o);
               tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tmem_st16(obase + cc * 16, o);
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st32(obase + cc * 32, o);
             }
           }
         }
         const float off = m == -INFINITY ? 0.f : -m;       // a row that has seen nothing yet
-        const uint64_t sc2 = pair(sc, sc), off2 = pair(off, off);
+        float by = sc;
+        if (__any_sync(0xffffffffu, fabsf(off) > kFusedMost)) {
+          // scores so large that the max's own rounding would count as one: scale and max in two roundings
+          by = 1.f;
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[cc][e] = __float_as_uint(__fmul_rn(__uint_as_float(v[cc][e]), sc));
+        }
+        const uint64_t sc2 = pair(by, by), off2 = pair(off, off);
         uint64_t sum2[2] = {0, 0};
-        auto form = [&](auto fused) {
+        uint32_t pw[32];
 #pragma unroll
-          for (int cc = 0; cc < 4; ++cc) {
-            uint32_t pw[16];
+        for (int cc = 0; cc < 2; ++cc) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float y = __uint_as_float(v[cc][e]), z = __uint_as_float(v[cc][e + 1]);
-              float a, b;
-              if (decltype(fused)::value) {
-                unpair(fma2(pair(y, z), sc2, off2), &a, &b);
-              } else {
-                a = __fadd_rn(__fmul_rn(y, sc), off);
-                b = __fadd_rn(__fmul_rn(z, sc), off);
-              }
-              a = fast_exp2(a);
-              b = fast_exp2(b);
-              sum2[(e >> 1) & 1] = add2(sum2[(e >> 1) & 1], pair(a, b));
-              pw[e >> 1] = pack_bf16x2(a, b);
-            }
-            tmem_st16(sbase + cc * 16, pw);                // P columns 16 cc .. hold keys 32 cc ..
+          for (int e = 0; e < 32; e += 2) {
+            float a, b;
+            unpair(fma2(pair(__uint_as_float(v[cc][e]), __uint_as_float(v[cc][e + 1])), sc2, off2), &a, &b);
+            a = fast_exp2(a);
+            b = fast_exp2(b);
+            sum2[(e >> 1) & 1] = add2(sum2[(e >> 1) & 1], pair(a, b));
+            pw[cc * 16 + (e >> 1)] = pack_bf16x2(a, b);
           }
-        };
-        // scale and max in one rounding, unless scores are so large that the max's own rounding would count as a score
-        if (__any_sync(0xffffffffu, fabsf(off) > kFusedMost)) form(std::false_type{});
-        else form(std::true_type{});
+        }
+        tmem_st32(sb, pw);                                 // P column c holds keys 2 c, 2 c + 1
         float a, b;
         unpair(add2(sum2[0], sum2[1]), &a, &b);
         l += a + b;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_pready[s]);
+        if (lane == 0) mbar_arrive(&bar_pready[s][nS & 1]);
       }
       if (!alive) break;
       // ---- epilogue: O complete -> O / l in bf16, LSE
       if (x.blocks > 0) {
-        const bool ok_o = mbar_wait(&bar_ofull[s], nO & 1, abort_flag, p.dev_err);
-        ++nO;
+        const bool ok_o = wait(&bar_odone[s], nI & 1, abort_flag, p.dev_err);
+        ++nI;
         if (!__all_sync(0xffffffffu, ok_o)) break;
         tc_fence_after();
-      } else if (leader) {
+      } else if (r == 0) {
         report(p.dev_err, MSA_DEVERR_BAD_LEN);
       }
       const float inv = l == 0.f ? 0.f : 1.0f / l;
@@ -454,12 +479,6 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       if (real && p.LSE != nullptr) p.LSE[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       // the O loads above are complete (wait::ld) before this slot's next pready arrive, which gates the next item's first O
       tc_fence_before();
-      it = next_of(it + gridDim.x, &x);
-    }
-    if (leader && sent > 0 && *abort_flag) {               // let a load in flight land before the CTA exits
-      const uint64_t since = global_timer_ns();
-      while (!mbar_try_wait(&bar_qfull[s], (sent - 1) & 1) && global_timer_ns() - since < MSA_WAIT_LIMIT_NS) {
-      }
     }
   }
 
@@ -486,23 +505,24 @@ msa_status launch_window_prefill(const msa_window_prefill_args& a, cudaStream_t 
   p.n_items = static_cast<int>(static_cast<int64_t>(p.pairs) * a.B * a.Hkv);   // (below 2^31: checked before)
   CUtensorMap qmap, kmap, vmap;
   auto u64 = [](int64_t v) { return static_cast<uint64_t>(v); };
+  // rows of 128 values are two halves of 64, each a tile of 128-byte rows: of a block both come in one box
   {
-    // Q as 4-D (d, h, s, b); box = 64 columns of all heads of a group, for a tile's queries
-    const uint64_t dims[4] = {u64(a.D), u64(a.Hq), u64(a.S), u64(a.B)};
-    const uint64_t strides[3] = {u64(a.Q_stride[2] * 2), u64(a.Q_stride[1] * 2), u64(a.Q_stride[0] * 2)};
-    const uint32_t box[4] = {64, static_cast<uint32_t>(G), static_cast<uint32_t>(p.nq), 1};
-    if (msa_status st = encode_tiled_map(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, a.Q, dims, strides, box,
+    // Q as (d, h, s, half, b); all heads of a group, a tile's queries (whose halves do not end where a swizzle's rows do)
+    const uint64_t dims[5] = {64, u64(a.Hq), u64(a.S), 2, u64(a.B)};
+    const uint64_t strides[4] = {u64(a.Q_stride[2] * 2), u64(a.Q_stride[1] * 2), 128, u64(a.Q_stride[0] * 2)};
+    const uint32_t box[5] = {64, static_cast<uint32_t>(G), static_cast<uint32_t>(p.nq), 1, 1};
+    if (msa_status st = encode_tiled_map(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, a.Q, dims, strides, box,
                                          CU_TENSOR_MAP_SWIZZLE_128B, "Q");
         st != MSA_OK)
       return st;
   }
   for (int kv = 0; kv < 2; ++kv) {
-    // K, V as (d, g, s, b) or pages (d, t, g, page); box = 64 columns of 128 tokens of one head
-    const int64_t* st3 = kv ? a.V_stride : a.K_stride;
-    const uint64_t dims[4] = {u64(a.D), u64(paged ? kBk : a.Hkv), u64(paged ? a.Hkv : a.S), u64(paged ? a.num_pages : a.B)};
-    const uint64_t strides[3] = {u64(st3[2] * 2), u64(st3[1] * 2), u64(st3[0] * 2)};
-    const uint32_t box[4] = {64, paged ? 128u : 1u, paged ? 1u : 128u, 1};
-    if (msa_status st = encode_tiled_map(kv ? &vmap : &kmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, kv ? a.V : a.K, dims, strides, box,
+    // K, V as (d, s, half, g, b) or pages (d, t, half, g, page); a block's tokens of one head
+    const int64_t* str = kv ? a.V_stride : a.K_stride;     // (b, s, g) or (page, g, t)
+    const uint64_t dims[5] = {64, u64(paged ? kBk : a.S), 2, u64(a.Hkv), u64(paged ? a.num_pages : a.B)};
+    const uint64_t strides[4] = {u64(str[paged ? 2 : 1] * 2), 128, u64(str[paged ? 1 : 2] * 2), u64(str[0] * 2)};
+    const uint32_t box[5] = {64, kKeys, 2, 1, 1};
+    if (msa_status st = encode_tiled_map(kv ? &vmap : &kmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, kv ? a.V : a.K, dims, strides, box,
                                          CU_TENSOR_MAP_SWIZZLE_128B, kv ? "V" : "K");
         st != MSA_OK)
       return st;
@@ -515,7 +535,7 @@ msa_status launch_window_prefill(const msa_window_prefill_args& a, cudaStream_t 
   p.O = static_cast<__nv_bfloat16*>(a.O);
   p.LSE = a.LSE;
   p.dev_err = a.dev_err;
-  const size_t smem = 1024 + static_cast<size_t>(2 + kUnits) * kUnit;
+  const size_t smem = 1024 + 2 * static_cast<size_t>(kQTile) + static_cast<size_t>(kUnits) * kUnit;
   if (smem > dev.max_smem_optin) return fail(MSA_ERR_UNSUPPORTED, "window prefill: not enough shared memory");
   cudaError_t e = cudaFuncSetAttribute(window_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(window_prefill)");
