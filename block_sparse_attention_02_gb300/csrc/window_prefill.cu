@@ -166,7 +166,7 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
 
   __shared__ __align__(8) uint64_t bar_qfull[2], bar_qempty[2], bar_full[kUnits], bar_empty[kUnits];
   // per slot; of S and P one for each of the two buffers: an S or P may be complete before the one before it is looked at
-  __shared__ __align__(8) uint64_t bar_sfull[2][2], bar_pready[2][2], bar_ofull[2], bar_odone[2], bar_drain[2];
+  __shared__ __align__(8) uint64_t bar_sfull[2][2], bar_pready[2][2], bar_odone[2][2], bar_drain[2];   // (odone: of an item's last two O)
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ volatile int s_gone[kNotes];    // of block n % kNotes: no such page
@@ -178,8 +178,7 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       mbar_init(&bar_qfull[i], 1);
       mbar_init(&bar_qempty[i], 1);
       for (int k = 0; k < 2; ++k) { mbar_init(&bar_sfull[i][k], 1); mbar_init(&bar_pready[i][k], 4); }
-      mbar_init(&bar_ofull[i], 1);
-      mbar_init(&bar_odone[i], 1);
+      for (int k = 0; k < 2; ++k) mbar_init(&bar_odone[i][k], 1);
       mbar_init(&bar_drain[i], 1);
     }
     s_abort = 0;
@@ -305,10 +304,9 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
             umma_ts_elect(out, sp + buf * kKeys + kk * 8, v_desc + sv * (kUnit / 16) + kk * (2048 / 16), idesc_o,
                        (j > 2 || kk > 0) ? 1u : 0u);
           commit_elect(&bar_empty[sv]);
-          commit_elect(&bar_ofull[s]);
-          if (j == blocks + 1) commit_elect(&bar_odone[s]);
           next_v();
         }
+        if (j >= blocks) commit_elect(&bar_odone[s][j - blocks]);   // O(j - 2), one of the last two
         if (j < blocks) {
           ok = wait(&bar_full[sk], pk, abort_flag, p.dev_err) && (j > 0 || wait(&bar_qfull[s], items & 1, abort_flag, p.dev_err));
           ok = __all_sync(0xffffffffu, ok);
@@ -397,8 +395,9 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           if (up) m = bm;
           l *= alpha;
           if (j > 0) {
-            // (the O two before this block's is done, S came after it: the barrier is at most a phase behind)
-            const bool ok_o = wait(&bar_ofull[s], (nS - 1) & 1, abort_flag, p.dev_err);
+            // O(j - 1) is done when S(j + 1), issued right behind it, is; behind the last S there is a commit for it
+            const bool ok_o = j + 1 < x.blocks ? wait(&bar_sfull[s][(nS + 1) & 1], ((nS + 1) >> 1) & 1, abort_flag, p.dev_err)
+                                               : wait(&bar_odone[s][0], nI & 1, abort_flag, p.dev_err);
             if (!__all_sync(0xffffffffu, ok_o)) { alive = false; break; }
             tc_fence_after();
 #pragma unroll
@@ -449,7 +448,7 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       if (!alive) break;
       // ---- epilogue: O complete -> O / l in bf16, LSE
       if (x.blocks > 0) {
-        const bool ok_o = wait(&bar_odone[s], nI & 1, abort_flag, p.dev_err);
+        const bool ok_o = wait(&bar_odone[s][1], nI & 1, abort_flag, p.dev_err);
         ++nI;
         if (!__all_sync(0xffffffffu, ok_o)) break;
         tc_fence_after();
