@@ -88,6 +88,11 @@ __device__ __forceinline__ float fast_exp2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   __nv_bfloat162 h2 = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h2);
@@ -343,6 +348,7 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     const int q = warp & 3;
     const int r = q * 32 + lane;
     const int query = r / p.G, head = r - query * p.G;
+    const int per_query = 65536 / p.G + 1;                 // (row * per_query) >> 16 is row / G
     const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
     const uint32_t sbase = tmem + lane_addr + s * 256;     // two buffers: S, then P (bf16 pairs) in its first 32 columns
     const uint32_t obase = sbase + 128;
@@ -384,11 +390,13 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         float mx[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          mx[k] = __uint_as_float(v[k >> 1][(k & 1) * 16]);
+          const uint32_t* y = v[k >> 1] + (k & 1) * 16;
+          mx[k] = max3(__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2]));
 #pragma unroll
-          for (int e = 1; e < 16; ++e) mx[k] = fmaxf(mx[k], __uint_as_float(v[k >> 1][(k & 1) * 16 + e]));
+          for (int e = 3; e < 15; e += 2) mx[k] = max3(mx[k], __uint_as_float(y[e]), __uint_as_float(y[e + 1]));
+          mx[k] = fmaxf(mx[k], __uint_as_float(y[15]));
         }
-        const float bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;   // scale > 0: max of the scaled scores
+        const float bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sc;   // scale > 0: max of the scaled scores
         const bool up = bm > m + kRescale;
         if (__any_sync(0xffffffffu, up)) {                 // O and the sum to the new max
           const float alpha = up ? fast_exp2(m - bm) : 1.f;
@@ -457,22 +465,46 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       }
       const float inv = l == 0.f ? 0.f : 1.0f / l;
       const int64_t at = (static_cast<int64_t>(x.b) * p.S + row) * p.Hq + x.g * p.G + head;
+      // A row's 256 bytes are one thread's; written so, each store would touch 32 lines.  Eight lanes exchange their rows'
+      // 16-byte chunks (an 8 x 8 transposition), so that they write 128 bytes of one row together.
+      const int row0 = x.q0 + s * p.nq;
+      const int queries = min(p.nq, p.S - row0);
+      __nv_bfloat16* tile = p.O + ((static_cast<int64_t>(x.b) * p.S + row0) * p.Hq + x.g * p.G) * kD + (lane & 7) * 8;
 #pragma unroll
-      for (int cc = 0; cc < 4; ++cc) {
-        uint32_t o[32];
-        tmem_ld32(obase + cc * 32, o);
+      for (int cc = 0; cc < 2; ++cc) {
+        uint32_t o[2][32];
+        tmem_ld32(obase + cc * 64, o[0]);
+        tmem_ld32(obase + cc * 64 + 32, o[1]);
         tmem_ld_wait();
-        if (real) {
-          uint4* to = reinterpret_cast<uint4*>(p.O + at * kD + cc * 32);
+        uint32_t w[8][4];
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint4 w;
-            w.x = pack_bf16x2(__uint_as_float(o[e + 0]) * inv, __uint_as_float(o[e + 1]) * inv);
-            w.y = pack_bf16x2(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-            w.z = pack_bf16x2(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-            w.w = pack_bf16x2(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-            to[e / 8] = l == 0.f ? make_uint4(0, 0, 0, 0) : w;   // (tensor memory may hold anything where nothing was added)
+        for (int c = 0; c < 8; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int k = c * 8 + e * 2;
+            w[c][e] = pack_bf16x2(__uint_as_float(o[k >> 5][k & 31]) * inv, __uint_as_float(o[k >> 5][(k & 31) + 1]) * inv);
+            if (l == 0.f) w[c][e] = 0;                     // (tensor memory may hold anything where nothing was added)
           }
+#pragma unroll
+        for (int bit = 1; bit < 8; bit <<= 1) {
+          const bool high = (lane & bit) != 0;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            if (c & bit) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? w[c][e] : w[c | bit][e], bit);
+              if (high) w[c][e] = got;
+              else w[c | bit][e] = got;
+            }
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {                      // chunk lane % 8 of row r - lane % 8 + c
+          const int rr = (r & ~7) + c, qq = (rr * per_query) >> 16;
+          if (qq < queries)
+            *reinterpret_cast<uint4*>(tile + (static_cast<int64_t>(qq) * p.Hq + rr - qq * p.G) * kD + cc * 64) =
+                make_uint4(w[c][0], w[c][1], w[c][2], w[c][3]);
         }
       }
       if (real && p.LSE != nullptr) p.LSE[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
