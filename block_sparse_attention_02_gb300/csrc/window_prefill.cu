@@ -19,10 +19,15 @@
 // slots' softmax and epilogue; a slot's softmax also sends for its next Q tile, once its last S is done.  Each slot goes
 // through its items on its own: S(j + 1) is issued right behind O(j), which reads P from the same columns (one thread's
 // MMAs run in order), and the other slot's products run meanwhile.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
+#include "launch_early.cuh"
 #include "msa_internal.h"
 #include "msa_ptx.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace msa {
 namespace {
@@ -33,7 +38,9 @@ constexpr int kQTile = 2 * kQHalf;
 constexpr int kHalf = kKeys * 64 * 2;        // 8 KiB: a block's rows x 64 bf16
 constexpr int kUnit = 2 * kHalf;             // 16 KiB: K or V of a block
 constexpr int kUnits = 10;                   // of K and V in shared memory
+constexpr int kMaxSplit = 8;                 // CTAs of an item
 constexpr int kNotes = 16;                   // blocks whose page's state is kept (more than are in flight)
+static_assert(kUnits * kUnit >= 2 * 128 * kD * 4 + 2 * 2 * 128 * 4, "room for two slots' outputs");
 constexpr int kThreads = 384;                // w0 TMA of K and V, w1-2 the slots' issuers, w4-7 slot 0, w8-11 slot 1
 constexpr int kTmemCols = 512;               // per slot: two of S / P (64 columns each) and O (128 columns)
 constexpr float kLog2e = 1.4426950408889634f;
@@ -42,7 +49,9 @@ constexpr float kRescale = 8.0f;             // log2 of the largest P before the
 constexpr float kFusedMost = 16777216.f;     // scores up to which scale and max go into one rounding
 
 struct Params {
-  int B, S, Hq, Hkv, G, nq, pairs;           // nq: queries of a tile; pairs: pairs of tiles of a sequence
+  int B, S, Hq, Hkv, G, nq;                  // nq: queries of a tile
+  int of_sequence;                           // items of a sequence: pairs of tiles, or (SPLIT) tiles
+  int split;                                 // SPLIT: CTAs of an item
   int window, sinks;
   int n_items;
   float scale_log2;
@@ -54,32 +63,42 @@ struct Params {
   int32_t* dev_err;
 };
 
-// A pair of tiles: queries q0 .. of sequence b, head g, at positions pos ..; blocks: sink_blocks ones from 0 on, then from
-// `first` on.
+// A pair of tiles (SPLIT: one tile): queries q0 .. of sequence b, head g, at positions pos ..  Its blocks are sink_blocks ones
+// from 0 on, then those from `first` on; a CTA's are `blocks` ones of this list from `from` on.
 struct Item {
-  int b, g, q0, pos, tiles, sink_blocks, first, blocks;
-  __device__ __forceinline__ int block(int j) const { return j < sink_blocks ? j : j - sink_blocks + first; }
+  int b, g, q0, pos, tiles, sink_blocks, first, from, blocks;
+  __device__ __forceinline__ int block(int j) const {
+    j += from;
+    return j < sink_blocks ? j : j - sink_blocks + first;
+  }
 };
-// The pairs with the most blocks first: from the last to the first of a sequence.
+// The items with the most blocks first: from the last to the first of a sequence.
+template <bool SPLIT>
 __device__ __forceinline__ Item item_of(const Params& p, int it) {
   Item x;
-  const int heads = p.B * p.Hkv;
-  const int pair = p.pairs - 1 - it / heads;
+  const int heads = p.B * p.Hkv, queries = SPLIT ? p.nq : 2 * p.nq;
+  const int i = p.of_sequence - 1 - it / heads;
   const int rest = it % heads;
   x.g = rest % p.Hkv;
   x.b = rest / p.Hkv;
-  x.q0 = pair * 2 * p.nq;
-  x.tiles = x.q0 + p.nq < p.S ? 2 : 1;
+  x.q0 = i * queries;
+  x.tiles = SPLIT || x.q0 + p.nq < p.S ? 2 : 1;
+  x.from = 0;
   const int start = p.paged ? p.q_pos[x.b] : 0;
   x.pos = start + x.q0;
   if (p.paged && (start < 0 || start + static_cast<int64_t>(p.S) > p.max_pages * kBk)) {
     x.sink_blocks = x.first = x.blocks = 0;
     return x;
   }
-  const int last = start + min(x.q0 + 2 * p.nq, p.S) - 1;
+  const int last = start + min(x.q0 + queries, p.S) - 1;
   x.first = max(x.pos - p.window + 1, 0) / kKeys;
   x.sink_blocks = min((min(p.sinks, last + 1) + kKeys - 1) / kKeys, x.first);
   x.blocks = x.sink_blocks + last / kKeys - x.first + 1;
+  if (SPLIT) {
+    const int per = (x.blocks + p.split - 1) / p.split;
+    x.from = min(static_cast<int>(blockIdx.x % p.split) * per, x.blocks);
+    x.blocks = min(per, x.blocks - x.from);
+  }
   return x;
 }
 
@@ -161,6 +180,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+template <bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap, const Params p) {
@@ -175,10 +195,12 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ volatile int s_gone[kNotes];    // of block n % kNotes: no such page
+  // SPLIT, at the end: the slots' outputs take the units' place, and behind them each row's max and sum
+  float(*s_ml)[2][128] = reinterpret_cast<float(*)[2][128]>(s_kv + 2 * 128 * kD * sizeof(float));
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    for (int i = 0; i < kUnits; ++i) { mbar_init(&bar_full[i], 1); mbar_init(&bar_empty[i], 2); }
+    for (int i = 0; i < kUnits; ++i) { mbar_init(&bar_full[i], 1); mbar_init(&bar_empty[i], SPLIT ? 1 : 2); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar_qfull[i], 1);
       mbar_init(&bar_qempty[i], 1);
@@ -194,18 +216,23 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     reinterpret_cast<uint4*>(s_q + (i & 3) * kQHalf + p.nq * p.G * 128)[i >> 2] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   if (warp == 1) tmem_alloc(&s_tmem, kTmemCols);
+  wait_for_stream();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   volatile int* abort_flag = &s_abort;
+  const int it0 = SPLIT ? blockIdx.x / p.split : blockIdx.x, stride = SPLIT ? p.n_items : gridDim.x;
+
+  // blocks of an item that slot s works on
+  auto own = [](const Item& x, int s) { return SPLIT ? (x.blocks + 1 - s) >> 1 : x.blocks; };
 
   if (warp == 0) {
     // ===================== TMA producer of K and V (warp-uniform loop, lane 0 issues) =====================
     int n = 0, st = 0;                       // blocks sent for; the next unit and its phase
     uint32_t phase = 0;
     bool ok = true;
-    for (int it = blockIdx.x; it < p.n_items && ok; it += gridDim.x) {
-      const Item x = item_of(p, it);
+    for (int it = it0; it < p.n_items && ok; it += stride) {
+      const Item x = item_of<SPLIT>(p, it);
       for (int j0 = 0; j0 < x.blocks && ok; j0 += 32) {
         // lane l looks up the page of block j0 + l
         int pg = 0;
@@ -252,36 +279,38 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     const uint32_t sp = tmem + s * 256, out = sp + 128;
     const uint64_t q_desc = sdesc_sw128(smem_u32(s_q + s * kQTile), 16, 1024), k_desc = sdesc_sw128(smem_u32(s_kv), 16, 1024),
                    v_desc = sdesc_sw128(smem_u32(s_kv), kHalf, 1024);
-    int sk = 0, sv = 1;                      // units of the next K and V, and their phases
+    // units of the next K and V, and their phases; SPLIT: the slots take the blocks in turn
+    int sk = SPLIT ? 2 * s : 0, sv = sk + 1;
     uint32_t pk = 0, pv = 0;
+    constexpr int kStep = SPLIT ? 4 : 2;
     int n = 0, items = 0, sent = 0;          // blocks and items done, Q tiles sent for
     bool ok = true;
     auto next_k = [&] {
-      sk += 2;
+      sk += kStep;
       if (sk >= kUnits) { sk -= kUnits; pk ^= 1; }
     };
     auto next_v = [&] {
-      sv += 2;
+      sv += kStep;
       if (sv >= kUnits) { sv -= kUnits; pv ^= 1; }
     };
     // the Q tile of this slot's first item from `it` on that has blocks, once the last S of the one before is done
     auto send_q = [&](int it) {
-      for (; it < p.n_items; it += gridDim.x) {
-        const Item x = item_of(p, it);
-        if (s >= x.tiles || x.blocks == 0) continue;
+      for (; it < p.n_items; it += stride) {
+        const Item x = item_of<SPLIT>(p, it);
+        if (s >= x.tiles || own(x, s) == 0) continue;
         if (lane == 0 && wait(&bar_qempty[s], (sent & 1) ^ 1, abort_flag, p.dev_err)) {
           mbar_arrive_expect_tx(&bar_qfull[s], static_cast<uint32_t>(p.nq * p.G) * 256);
           for (int half = 0; half < 2; ++half)
-            tma_load_5d(s_q + s * kQTile + half * kQHalf, &qmap, &bar_qfull[s], 0, x.g * p.G, x.q0 + s * p.nq, half, x.b);
+            tma_load_5d(s_q + s * kQTile + half * kQHalf, &qmap, &bar_qfull[s], 0, x.g * p.G, x.q0 + (SPLIT ? 0 : s * p.nq), half, x.b);
         }
         ++sent;
         break;
       }
     };
-    send_q(blockIdx.x);
-    for (int it = blockIdx.x; it < p.n_items && ok; it += gridDim.x) {
-      const Item x = item_of(p, it);
-      const int blocks = __shfl_sync(0xffffffffu, x.blocks, 0);   // (from lane 0: the compiler then knows that the warp goes one way)
+    send_q(it0);
+    for (int it = it0; it < p.n_items && ok; it += stride) {
+      const Item x = item_of<SPLIT>(p, it);
+      const int blocks = __shfl_sync(0xffffffffu, own(x, s), 0);   // (from lane 0: the compiler then knows that the warp goes one way)
       if (s >= __shfl_sync(0xffffffffu, x.tiles, 0)) {
         // an item without a tile for this slot: its units pass
         for (int j = 0; j < blocks && ok; ++j) {
@@ -326,7 +355,7 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           if (j == blocks - 1) commit_elect(&bar_qempty[s]);
           next_k();
         } else if (j == blocks) {
-          send_q(it + gridDim.x);
+          send_q(it + stride);
         }
       }
       n += blocks;
@@ -355,27 +384,28 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     const float sc = p.scale_log2;
     int nS = 0, nI = 0, n = 0;                             // blocks done; items done; blocks of the CTA so far
     bool alive = true;
-    for (int it = blockIdx.x; it < p.n_items && alive; it += gridDim.x) {
-      const Item x = item_of(p, it);
+    for (int it = it0; it < p.n_items && alive; it += stride) {
+      const Item x = item_of<SPLIT>(p, it);
       const int n0 = n;
       n += x.blocks;
       if (s >= x.tiles) continue;
-      const int row = x.q0 + s * p.nq + query;             // of the sequence's S queries
+      const int row0 = x.q0 + (SPLIT ? 0 : s * p.nq);      // the tile's first query, of the sequence's S
+      const int row = row0 + query;
       const bool real = query < p.nq && row < p.S;
-      const int i = x.pos + s * p.nq + query;              // its position
-      const int low = x.pos + s * p.nq, high = low + p.nq - 1;
+      const int low = x.pos + row0 - x.q0, high = low + p.nq - 1, i = low + query;   // positions: of the tile, and this row's
+      const int blocks = own(x, s);
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < x.blocks; ++j, ++nS) {
+      for (int j = 0; j < blocks; ++j, ++nS) {
         const bool ok_s = wait(&bar_sfull[s][nS & 1], (nS >> 1) & 1, abort_flag, p.dev_err);
         if (!__all_sync(0xffffffffu, ok_s)) { alive = false; break; }
         tc_fence_after();
         const uint32_t sb = sbase + (nS & 1) * kKeys;
-        const int t0 = x.block(j) * kKeys;
+        const int listed = SPLIT ? 2 * j + s : j, t0 = x.block(listed) * kKeys;
         uint32_t v[2][32];
         tmem_ld32(sb, v[0]);
         tmem_ld32(sb + 32, v[1]);
         tmem_ld_wait();
-        const bool gone = p.paged && s_gone[(n0 + j) % kNotes] != 0;
+        const bool gone = p.paged && s_gone[(n0 + listed) % kNotes] != 0;
         if (gone || t0 + kKeys - 1 > low || (t0 <= high - p.window && t0 + kKeys > p.sinks)) {
           // some row does not see all of it: columns c <= last, and c >= from or c < sinks
           const int last = gone ? -1 : i - t0, from = i - p.window + 1 - t0, sinks = p.sinks - t0;
@@ -404,7 +434,7 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           l *= alpha;
           if (j > 0) {
             // O(j - 1) is done when S(j + 1), issued right behind it, is; behind the last S there is a commit for it
-            const bool ok_o = j + 1 < x.blocks ? wait(&bar_sfull[s][(nS + 1) & 1], ((nS + 1) >> 1) & 1, abort_flag, p.dev_err)
+            const bool ok_o = j + 1 < blocks ? wait(&bar_sfull[s][(nS + 1) & 1], ((nS + 1) >> 1) & 1, abort_flag, p.dev_err)
                                                : wait(&bar_odone[s][0], nI & 1, abort_flag, p.dev_err);
             if (!__all_sync(0xffffffffu, ok_o)) { alive = false; break; }
             tc_fence_after();
@@ -455,7 +485,32 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       }
       if (!alive) break;
       // ---- epilogue: O complete -> O / l in bf16, LSE
-      if (x.blocks > 0) {
+      if (SPLIT) {
+        // both slots' products done: K's and V's units give way to the outputs, unscaled
+        const bool ok_o = (own(x, 0) == 0 || wait(&bar_odone[0][1], 0, abort_flag, p.dev_err)) &&
+                          (own(x, 1) == 0 || wait(&bar_odone[1][1], 0, abort_flag, p.dev_err));
+        if (!__all_sync(0xffffffffu, ok_o)) break;
+        tc_fence_after();
+        if (x.blocks == 0 && x.from == 0 && r == 0 && s == 0 && blockIdx.x % p.split == 0) report(p.dev_err, MSA_DEVERR_BAD_LEN);
+        s_ml[s][0][r] = m;
+        s_ml[s][1][r] = l;
+        float4* to = reinterpret_cast<float4*>(s_kv) + (s * 128 + r) * 32;
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc) {
+          uint32_t o[32];
+          tmem_ld32(obase + cc * 32, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {                    // (chunks in another order in every row: no two lanes meet a bank)
+            float4 w = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+            if (l == 0.f) w = make_float4(0.f, 0.f, 0.f, 0.f);
+            to[(cc * 8 + e) ^ (r & 31)] = w;
+          }
+        }
+        tc_fence_before();
+        break;
+      }
+      if (blocks > 0) {
         const bool ok_o = wait(&bar_odone[s][1], nI & 1, abort_flag, p.dev_err);
         ++nI;
         if (!__all_sync(0xffffffffu, ok_o)) break;
@@ -467,7 +522,6 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       const int64_t at = (static_cast<int64_t>(x.b) * p.S + row) * p.Hq + x.g * p.G + head;
       // A row's 256 bytes are one thread's; written so, each store would touch 32 lines.  Eight lanes exchange their rows'
       // 16-byte chunks (an 8 x 8 transposition), so that they write 128 bytes of one row together.
-      const int row0 = x.q0 + s * p.nq;
       const int queries = min(p.nq, p.S - row0);
       __nv_bfloat16* tile = p.O + ((static_cast<int64_t>(x.b) * p.S + row0) * p.Hq + x.g * p.G) * kD + (lane & 7) * 8;
 #pragma unroll
@@ -513,6 +567,45 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     }
   }
 
+  if (SPLIT) {
+    // the item's parts, two of each CTA, joined: four channels of a row by a thread
+    cg::cluster_group cluster = cg::this_cluster();
+    if (p.split > 1) cluster.sync(); else __syncthreads();
+    const Item x = item_of<SPLIT>(p, it0);
+    const int rows = min(p.nq, p.S - x.q0) * p.G, parts = 2 * p.split, ctas = p.split, mine = blockIdx.x % p.split;
+    if (*abort_flag == 0) {
+      for (int e = mine * kThreads + tid; e < rows * 32; e += ctas * kThreads) {
+        const int r = e >> 5, c = e & 31;
+        float m[2 * kMaxSplit], top = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 2 * kMaxSplit; ++k) {
+          m[k] = -INFINITY;
+          if (k < parts) m[k] = p.split > 1 ? *cluster.map_shared_rank(&s_ml[k & 1][0][r], k >> 1) : s_ml[k & 1][0][r];
+          top = fmaxf(top, m[k]);
+        }
+        float l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < 2 * kMaxSplit; ++k) {
+          if (k >= parts || m[k] == -INFINITY) continue;
+          const float f = fast_exp2(m[k] - top);
+          const float* sum = &s_ml[k & 1][1][r];
+          const float4* from = reinterpret_cast<const float4*>(s_kv) + ((k & 1) * 128 + r) * 32 + (c ^ (r & 31));
+          const float lk = p.split > 1 ? *cluster.map_shared_rank(sum, k >> 1) : *sum;
+          const float4 v = p.split > 1 ? *cluster.map_shared_rank(from, k >> 1) : *from;
+          l = fmaf(f, lk, l);
+          o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y); o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int query = r / p.G;
+        const int64_t at = (static_cast<int64_t>(x.b) * p.S + x.q0 + query) * p.Hq + x.g * p.G + r - query * p.G;
+        *reinterpret_cast<uint2*>(p.O + at * kD + 4 * c) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        if (c == 0 && p.LSE != nullptr) p.LSE[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
+      }
+    }
+    if (p.split > 1) cluster.sync();         // no CTA leaves while another reads its memory
+  }
+
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -531,9 +624,19 @@ msa_status launch_window_prefill(const msa_window_prefill_args& a, cudaStream_t 
   Params p = {};
   p.B = a.B; p.S = a.S; p.Hq = a.Hq; p.Hkv = a.Hkv; p.G = G;
   p.nq = 128 / G;
-  p.pairs = (a.S + 2 * p.nq - 1) / (2 * p.nq);
   p.window = std::min(a.window, 1 << 30); p.sinks = std::min(a.sinks, 1 << 30);   // positions lie below 2^30
-  p.n_items = static_cast<int>(static_cast<int64_t>(p.pairs) * a.B * a.Hkv);   // (below 2^31: checked before)
+  // Few tiles: each is a CTA's or a cluster's, whose slots share out its blocks and join their outputs in shared memory.
+  // (Clusters of more than two that nearly fill the GPU would not all fit at once.  A slot has two blocks at least.)
+  const int64_t tiles = static_cast<int64_t>((a.S + p.nq - 1) / p.nq) * a.B * a.Hkv;
+  const bool split = tiles <= dev.num_sms;
+  if (split) {
+    const int64_t reach = paged ? a.max_pages * kBk : a.S;
+    const int64_t most = std::min(reach / kKeys + 1, (int64_t(p.window) + p.nq) / kKeys + 2 + (int64_t(p.sinks) + kKeys - 1) / kKeys);
+    p.split = 1;
+    while (p.split < kMaxSplit && (p.split == 1 ? 2 * tiles <= dev.num_sms : 8 * p.split * tiles <= 3 * dev.num_sms) && 8 * p.split <= most) p.split *= 2;
+  }
+  p.of_sequence = split ? (a.S + p.nq - 1) / p.nq : (a.S + 2 * p.nq - 1) / (2 * p.nq);
+  p.n_items = static_cast<int>(static_cast<int64_t>(p.of_sequence) * a.B * a.Hkv);   // (below 2^31: checked before)
   CUtensorMap qmap, kmap, vmap;
   auto u64 = [](int64_t v) { return static_cast<uint64_t>(v); };
   // rows of 128 values are two halves of 64, each a tile of 128-byte rows: of a block both come in one box
@@ -568,11 +671,11 @@ msa_status launch_window_prefill(const msa_window_prefill_args& a, cudaStream_t 
   p.dev_err = a.dev_err;
   const size_t smem = 1024 + 2 * static_cast<size_t>(kQTile) + static_cast<size_t>(kUnits) * kUnit;
   if (smem > dev.max_smem_optin) return fail(MSA_ERR_UNSUPPORTED, "window prefill: not enough shared memory");
-  cudaError_t e = cudaFuncSetAttribute(window_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  auto* kernel = split ? window_prefill_kernel<true> : window_prefill_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(window_prefill)");
-  const int grid = std::min(dev.num_sms, p.n_items);
-  window_prefill_kernel<<<grid, kThreads, smem, stream>>>(qmap, kmap, vmap, p);
-  e = cudaGetLastError();
+  const int grid = split ? p.n_items * p.split : std::min(dev.num_sms, p.n_items);
+  e = launch_early(kernel, grid, kThreads, smem, stream, std::max(p.split, 1), qmap, kmap, vmap, p);
   if (e != cudaSuccess) return cuda_fail(e, "window_prefill_kernel launch");
   return MSA_OK;
 }
