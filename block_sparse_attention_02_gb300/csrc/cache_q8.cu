@@ -10,9 +10,11 @@
 // page left; one that starts later keeps the rows before it, and where it needs a larger scale these are rounded again
 // (the exponent moves, so only codes that become subnormal change).  So a block's scale is that of its own tokens alone.
 //
-// Work.  A CTA looks for the runs that start in its window of token rows.  Runs of up to 8 tokens go to a warp each, longer
-// ones to the CTA, which holds the run (at most 128 rows of 256 bytes) in registers between the maximum and the
-// rounding: every token is read once.
+// Work.  A CTA takes a window of token rows for one head of K or V: it reads their slots, and those behind them as far as a run
+// may reach, and stores the runs that start in the window.  Runs of up to 8 tokens go to a warp each, longer ones to the
+// CTA, which holds the run (at most 128 rows of 256 bytes) in registers between the maximum and the rounding: every token
+// is read once.  A window is as long as half a page, so that a prompt's CTAs have a run each or none; for few tokens it is one
+// row for each warp.
 #include "launch_early.cuh"
 #include "msa_internal.h"
 #include "msa_ptx.cuh"
@@ -24,7 +26,9 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kShort = 8;                      // rows of a run that a warp stores: 16 lanes a row, four rows a lane
 constexpr int kFewTokens = 1024;               // up to here a CTA's window is kWarps token rows, a run for every warp
-constexpr int kManyWindow = 32;
+constexpr int kManyWindow = 64;
+constexpr int kStoreCtas = 4;                  // per SM
+static_assert(kManyWindow + kBk + 1 <= kThreads, "a slot for every thread");
 constexpr unsigned kMaxGridY = 65535;
 
 struct StoreParams {
@@ -77,56 +81,76 @@ __device__ __forceinline__ void rescale_rows(uint8_t* codes, int rows, float f, 
   }
 }
 
-__global__ void __launch_bounds__(kThreads) append_q8_kernel(const StoreParams p) {
+__global__ void __launch_bounds__(kThreads, kStoreCtas) append_q8_kernel(const StoreParams p) {
   wait_for_stream();
   __shared__ uint32_t s_top[kWarps];
-  __shared__ int s_long[kManyWindow + 1];       // long runs of the window: first token rows, the count at the end
+  __shared__ int64_t s_slot[kThreads];           // of token rows begin - 1 ..
+  __shared__ int s_first[kManyWindow], s_rows[kManyWindow], s_long;   // long runs of the window
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const bool is_v = blockIdx.z != 0;
   const int64_t begin = static_cast<int64_t>(blockIdx.x) * p.window;
   const int64_t n_stride = is_v ? p.v0 : p.k0;
   const int part = lane & 15;                   // 16 bytes of a row
-  // rows of the run that starts at token row r in slot `at`, up to 32
-  auto run_length = [&](int64_t r, int64_t at) {
-    const bool in = r + lane < p.N && (at & (kBk - 1)) + lane < kBk && p.slots[r + lane] == at + lane;
-    const uint32_t stops = ~__ballot_sync(0xffffffffu, in);
-    return stops == 0 ? 32 : __ffs(stops) - 1;
-  };
-  if (tid == 0) s_long[kManyWindow] = 0;
+  const uint8_t* src = (is_v ? p.V + blockIdx.y * p.v1 : p.K + blockIdx.y * p.k1) + begin * n_stride + part * 16;
+  const int here = static_cast<int>(min(static_cast<int64_t>(p.window), p.N - begin));
+  // the first row of this warp does not wait for the slots
+  uint4 early = make_uint4(0, 0, 0, 0);
+  if (lane < 16 && warp < here) early = *reinterpret_cast<const uint4*>(src + warp * n_stride);
+  {
+    const int64_t r = begin + tid - 1;
+    s_slot[tid] = r >= 0 && r < p.N && tid < p.window + kBk + 1 ? p.slots[r] : -2;
+    if (tid == 0) s_long = 0;
+  }
   __syncthreads();
+  // rows of the run that starts at row r of the window; 0: none does, or it is not stored
+  auto run_at = [&](int r) {
+    const int64_t at = s_slot[r + 1];
+    if (at < 0 || at >= p.num_pages * kBk) {
+      if (at >= 0 && blockIdx.y == 0 && !is_v && lane == 0) report(p.dev_err, MSA_DEVERR_BAD_PAGE);
+      return 0;
+    }
+    const int t0 = static_cast<int>(at & (kBk - 1));
+    if (t0 != 0 && s_slot[r] == at - 1) return 0;
+    int n = 0;
+    for (int k = 0; k < kBk; k += 32) {
+      const uint32_t stops = ~__ballot_sync(0xffffffffu, t0 + k + lane < kBk && s_slot[r + 1 + k + lane] == at + k + lane);
+      if (stops != 0) return n + __ffs(stops) - 1;
+      n += 32;
+    }
+    return n;
+  };
+  uint8_t* all_codes = is_v ? p.V_codes : p.K_codes;
+  uint8_t* all_scales = is_v ? p.V_scales : p.K_scales;
   for (int h = blockIdx.y; h < p.Hkv; h += gridDim.y) {
-    const uint8_t* src = (is_v ? p.V + h * p.v1 : p.K + h * p.k1) + part * 16;
-    uint8_t* codes = (is_v ? p.V_codes : p.K_codes) + h * p.c1;
-    uint8_t* scales = (is_v ? p.V_scales : p.K_scales) + h * p.s1;
-    for (int64_t r = begin + warp; r < min(begin + p.window, p.N); r += kWarps) {
-      const uint8_t* row = src + r * n_stride;
-      uint4 v[kShort / 2];                      // (the first row's load does not wait for the slots)
-      v[0] = lane < 16 ? *reinterpret_cast<const uint4*>(row) : make_uint4(0, 0, 0, 0);
-      const int64_t at = p.slots[r], before = r > 0 ? p.slots[r - 1] : -2;
-      if (at < 0) continue;
-      const int64_t page = at / kBk;
-      const int t0 = static_cast<int>(at & (kBk - 1));
-      if (page >= p.num_pages) {
-        if (h == 0 && !is_v && lane == 0) report(p.dev_err, MSA_DEVERR_BAD_PAGE);
-        continue;
-      }
-      if (t0 != 0 && before == at - 1) continue;      // not a run's first row
-      const uint32_t stored = scales[page * p.s0];
-      const int n = run_length(r, at);
+    const uint8_t* rows = src + (h - blockIdx.y) * (is_v ? p.v1 : p.k1);
+    for (int r = warp; r < here; r += kWarps) {
+      const int n = run_at(r);
+      if (n == 0) continue;
       if (n > kShort) {
-        if (lane == 0 && h == blockIdx.y) s_long[atomicAdd(&s_long[kManyWindow], 1)] = static_cast<int>(r - begin);
+        if (lane == 0 && h == blockIdx.y) {
+          const int x = atomicAdd(&s_long, 1);
+          s_first[x] = r;
+          s_rows[x] = n;
+        }
         continue;
       }
+      const int64_t at = s_slot[r + 1], page = at / kBk;
+      const int t0 = static_cast<int>(at & (kBk - 1));
+      uint8_t* scale = all_scales + page * p.s0 + h * p.s1;
+      uint8_t* block = all_codes + page * p.c0 + h * p.c1;
+      const uint32_t stored = t0 > 0 ? *scale : 0;
+      const uint8_t* row = rows + r * n_stride;
+      uint4 v[kShort / 2];
       uint32_t m = 0;
 #pragma unroll
       for (int i = 0; i < kShort / 2; ++i) {
         const int k = 2 * i + (lane >> 4);
-        if (i > 0 || lane >= 16) v[i] = k < n ? *reinterpret_cast<const uint4*>(row + k * n_stride) : make_uint4(0, 0, 0, 0);
+        v[i] = i == 0 && r == warp && h == blockIdx.y && lane < 16 ? early
+               : k < n ? *reinterpret_cast<const uint4*>(row + k * n_stride) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int i = 0; i < kShort / 2; ++i) m = finite_max(m, v[i]);
       uint32_t byte = q8_byte_for(warp_top(m));
-      uint8_t* block = codes + page * p.c0;
       if (t0 > 0) {
         const uint32_t old = q8_byte(stored);
         if (byte > old) rescale_rows(block, t0, q8_inverse(byte - old + 127), lane, 32);
@@ -138,53 +162,34 @@ __global__ void __launch_bounds__(kThreads) append_q8_kernel(const StoreParams p
         const int k = 2 * i + (lane >> 4);
         if (k < n) *reinterpret_cast<uint2*>(block + (t0 + k) * kD + part * 8) = encode8(v[i], inv);
       }
-      if (lane == 0) scales[page * p.s0] = static_cast<uint8_t>(byte);
+      if (lane == 0) *scale = static_cast<uint8_t>(byte);
     }
     if (h == blockIdx.y) __syncthreads();
     // the long runs, one after another (in whatever order: they are of different pages)
-    for (int x = 0; x < s_long[kManyWindow]; ++x) {
-      const int64_t r = begin + s_long[x], at = p.slots[r], page = at / kBk;
-      const int t0 = static_cast<int>(at & (kBk - 1)), first = tid >> 4;
-      const uint32_t stored = scales[page * p.s0];
-      constexpr int kRows = kBk * 16 / kThreads;      // of a thread: first, first + 16, ..
-      uint4 v[kRows];
+    for (int x = 0; x < s_long; ++x) {
+      const int r = s_first[x], n = s_rows[x], first = tid >> 4;
+      const int64_t at = s_slot[r + 1], page = at / kBk;
+      const int t0 = static_cast<int>(at & (kBk - 1));
+      uint8_t* scale = all_scales + page * p.s0 + h * p.s1;
+      uint8_t* block = all_codes + page * p.c0 + h * p.c1;
+      const uint32_t stored = t0 > 0 ? *scale : 0;
+      const uint8_t* row = rows + (r + first) * n_stride;
+      constexpr int kEach = kBk * 16 / kThreads;      // rows of a thread: first, first + 16, ..
+      uint4 v[kEach];
       uint32_t m = 0;
-      bool in[kRows];
-      int64_t slot[kRows];
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const int k = first + i * (kThreads / 16);
-        in[i] = r + k < p.N && t0 + k < kBk;
-        slot[i] = in[i] ? p.slots[r + k] : -1;
-        v[i] = in[i] ? *reinterpret_cast<const uint4*>(src + (r + k) * n_stride) : make_uint4(0, 0, 0, 0);
-      }
-      // the run ends at the first row whose slot does not follow
-      int end = kBk;
+      for (int i = 0; i < kEach; ++i)
+        v[i] = first + i * (kThreads / 16) < n ? *reinterpret_cast<const uint4*>(row + i * (kThreads / 16) * n_stride) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int i = kRows - 1; i >= 0; --i) {
-        const int k = first + i * (kThreads / 16);
-        if (slot[i] != at + k) end = k;
-      }
-      end = __reduce_min_sync(0xffffffffu, end);
-      __syncthreads();                                // s_top is free
-      if (lane == 0) s_top[warp] = end;
-      __syncthreads();
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) end = min(end, static_cast<int>(s_top[w]));
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        in[i] = first + i * (kThreads / 16) < end;
-        if (in[i]) m = finite_max(m, v[i]);
-      }
+      for (int i = 0; i < kEach; ++i) m = finite_max(m, v[i]);
       const uint32_t mine = warp_top(m);
-      __syncthreads();                                // the ends are read
       if (lane == 0) s_top[warp] = mine;
       __syncthreads();
       uint32_t top = 0;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) top = max(top, s_top[w]);
+      __syncthreads();                                // the maxima are read, and the stored scale by every thread
       uint32_t byte = q8_byte_for(top);
-      uint8_t* block = codes + page * p.c0;
       if (t0 > 0) {
         const uint32_t old = q8_byte(stored);
         if (byte > old) rescale_rows(block, t0, q8_inverse(byte - old + 127), tid, kThreads);
@@ -192,10 +197,10 @@ __global__ void __launch_bounds__(kThreads) append_q8_kernel(const StoreParams p
       }
       const float inv = q8_inverse(byte);
 #pragma unroll
-      for (int i = 0; i < kRows; ++i)
-        if (in[i])
+      for (int i = 0; i < kEach; ++i)
+        if (first + i * (kThreads / 16) < n)
           *reinterpret_cast<uint2*>(block + (t0 + first + i * (kThreads / 16)) * kD + part * 8) = encode8(v[i], inv);
-      if (tid == 0) scales[page * p.s0] = static_cast<uint8_t>(byte);   // (every thread has read it: two barriers ago)
+      if (tid == 0) *scale = static_cast<uint8_t>(byte);
     }
   }
 }
