@@ -10,11 +10,13 @@
 // page left; one that starts later keeps the rows before it, and where it needs a larger scale these are rounded again
 // (the exponent moves, so only codes that become subnormal change).  So a block's scale is that of its own tokens alone.
 //
-// Work.  A CTA takes a window of token rows for one head of K or V: it reads their slots, and those behind them as far as a run
-// may reach, and stores the runs that start in the window.  Runs of up to 8 tokens go to a warp each, longer ones to the
-// CTA, which holds the run (at most 128 rows of 256 bytes) in registers between the maximum and the rounding: every token
-// is read once.  A window is as long as half a page, so that a prompt's CTAs have a run each or none; for few tokens it is one
-// row for each warp.
+// Work.  A CTA takes a window of token rows for one or a few heads of K or V: it reads their slots, and those behind them as
+// far as a run may reach, and stores the runs that start in the window, while the window's rows are on their way to L2.
+// Longer runs go to the CTA, which holds the run (at most 128 rows of 256 bytes) in registers between the maximum and the
+// rounding: every token is read once.  Runs of up to 8 tokens (decoded ones) go to half a warp each, for one head.  The window is a
+// page long, so that a prompt's CTAs have about one run; for few tokens it is short, and heads share a CTA where there would
+// be more CTAs than run at once.  Blocks that have to be rounded again wait until the end and are done by all warps (one warp alone
+// would need 5 us for a full one).
 #include "launch_early.cuh"
 #include "msa_internal.h"
 #include "msa_ptx.cuh"
@@ -24,16 +26,17 @@ namespace msa {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kShort = 8;                      // rows of a run that a warp stores: 16 lanes a row, four rows a lane
-constexpr int kFewTokens = 1024;               // up to here a CTA's window is kWarps token rows, a run for every warp
-constexpr int kManyWindow = 64;
+constexpr int kShort = 8;                      // rows of a run that half a warp stores
+constexpr int kHalves = 2 * kWarps, kDeep = 2; // half warps, and runs that each has in flight
+constexpr int kFewTokens = 1024;               // up to here a CTA's window is short
+constexpr int kFewWindow = 16, kManyWindow = kBk;
+constexpr int kFewHeads = 8;                   // heads of a CTA with a short window, at most
 constexpr int kStoreCtas = 4;                  // per SM
-static_assert(kManyWindow + kBk + 1 <= kThreads, "a slot for every thread");
 constexpr unsigned kMaxGridY = 65535;
 
 struct StoreParams {
   int64_t N, num_pages;
-  int Hkv, window;
+  int Hkv, window, heads;       // token rows and heads of a CTA
   const uint8_t *K, *V;
   int64_t k0, k1, v0, v1;       // byte strides (n, h)
   const int64_t* slots;
@@ -68,106 +71,133 @@ __device__ __forceinline__ uint2 encode8(uint4 v, float inv) {
 __device__ __forceinline__ void rescale_rows(uint8_t* codes, int rows, float f, int tid, int threads) {
   uint4* at = reinterpret_cast<uint4*>(codes);
   const int n = rows * 8;
-  for (int i = tid; i < n; i += 4 * threads) {
-    uint4 v[4];
+  constexpr int kDeep = 4;
+  for (int i = tid; i < n; i += kDeep * threads) {
+    uint4 v[kDeep];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < kDeep; ++k)
       if (i + k * threads < n) v[k] = at[i + k * threads];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < kDeep; ++k)
       if (i + k * threads < n)
         at[i + k * threads] = make_uint4(e4m3x4_rescaled(v[k].x, f), e4m3x4_rescaled(v[k].y, f), e4m3x4_rescaled(v[k].z, f),
                                          e4m3x4_rescaled(v[k].w, f));
   }
 }
+// A block whose scale grows: its page, its head, the rows before the new ones, and how far the exponent moves.
+struct Growth {
+  int page, head, rows, by;
+};
 
 __global__ void __launch_bounds__(kThreads, kStoreCtas) append_q8_kernel(const StoreParams p) {
   wait_for_stream();
   __shared__ uint32_t s_top[kWarps];
-  __shared__ int64_t s_slot[kThreads];           // of token rows begin - 1 ..
-  __shared__ int s_first[kManyWindow], s_rows[kManyWindow], s_long;   // long runs of the window
+  __shared__ int64_t s_slot[kManyWindow + kBk + 1];   // of token rows begin - 1 ..
+  __shared__ uint32_t s_break[(kManyWindow + kBk) / 32];   // bit i % 32 of word i / 32: row i does not go on where row i - 1 ended
+  __shared__ int s_run[kManyWindow], s_runs;   // short runs: first row, and rows << 16
+  __shared__ Growth s_growth[kManyWindow > kFewWindow * kFewHeads ? kManyWindow : kFewWindow * kFewHeads];
+  __shared__ int s_grown;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const bool is_v = blockIdx.z != 0;
   const int64_t begin = static_cast<int64_t>(blockIdx.x) * p.window;
-  const int64_t n_stride = is_v ? p.v0 : p.k0;
+  const int64_t n_stride = is_v ? p.v0 : p.k0, h_stride = is_v ? p.v1 : p.k1;
   const int part = lane & 15;                   // 16 bytes of a row
-  const uint8_t* src = (is_v ? p.V + blockIdx.y * p.v1 : p.K + blockIdx.y * p.k1) + begin * n_stride + part * 16;
+  const uint8_t* src = (is_v ? p.V : p.K) + begin * n_stride + part * 16;
+  const int h_lo = blockIdx.y * p.heads, h_hi = min(h_lo + p.heads, p.Hkv);
   const int here = static_cast<int>(min(static_cast<int64_t>(p.window), p.N - begin));
-  // the first row of this warp does not wait for the slots
-  uint4 early = make_uint4(0, 0, 0, 0);
-  if (lane < 16 && warp < here) early = *reinterpret_cast<const uint4*>(src + warp * n_stride);
-  {
-    const int64_t r = begin + tid - 1;
-    s_slot[tid] = r >= 0 && r < p.N && tid < p.window + kBk + 1 ? p.slots[r] : -2;
-    if (tid == 0) s_long = 0;
+  for (int i = tid; i < p.window + kBk + 1; i += kThreads) {
+    const int64_t r = begin + i - 1;
+    s_slot[i] = r >= 0 && r < p.N ? p.slots[r] : -2;
   }
+  for (int i = tid; i < here * (h_hi - h_lo) * 2; i += kThreads) {   // 128 bytes each
+    const int row = (i >> 1) % here, h = h_lo + (i >> 1) / here;
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(src - part * 16 + row * n_stride + h * h_stride + (i & 1) * 128));
+  }
+  if (tid == 0) s_grown = s_runs = 0;
   __syncthreads();
-  // rows of the run that starts at row r of the window; 0: none does, or it is not stored
-  auto run_at = [&](int r) {
-    const int64_t at = s_slot[r + 1];
-    if (at < 0 || at >= p.num_pages * kBk) {
-      if (at >= 0 && blockIdx.y == 0 && !is_v && lane == 0) report(p.dev_err, MSA_DEVERR_BAD_PAGE);
-      return 0;
+  bool bad = false;
+  for (int i = tid; i < kManyWindow + kBk; i += kThreads) {
+    bool is = true;
+    if (i < p.window + kBk) {
+      const int64_t at = s_slot[i + 1];
+      is = at < 0 || (at & (kBk - 1)) == 0 || s_slot[i] != at - 1;
+      bad |= i < p.window && at >= p.num_pages * kBk;
     }
-    const int t0 = static_cast<int>(at & (kBk - 1));
-    if (t0 != 0 && s_slot[r] == at - 1) return 0;
-    int n = 0;
-    for (int k = 0; k < kBk; k += 32) {
-      const uint32_t stops = ~__ballot_sync(0xffffffffu, t0 + k + lane < kBk && s_slot[r + 1 + k + lane] == at + k + lane);
-      if (stops != 0) return n + __ffs(stops) - 1;
-      n += 32;
+    const uint32_t word = __ballot_sync(0xffffffffu, is);
+    if (lane == 0) s_break[i >> 5] = word;
+  }
+  if (bad && blockIdx.y == 0 && !is_v) report(p.dev_err, MSA_DEVERR_BAD_PAGE);
+  __syncthreads();
+  // the first row at or behind row r of the window where a run may start; of a run that starts at r, its end
+  auto next_break = [&](int r) {
+    for (int w = r >> 5; w < (kManyWindow + kBk) / 32; ++w) {
+      const uint32_t word = s_break[w] & (w == r >> 5 ? ~0u << (r & 31) : ~0u);
+      if (word != 0) return w * 32 + __ffs(word) - 1;
     }
-    return n;
+    return kManyWindow + kBk;
   };
+  auto stored_at = [&](int r) { return s_slot[r + 1] >= 0 && s_slot[r + 1] < p.num_pages * kBk; };
   uint8_t* all_codes = is_v ? p.V_codes : p.K_codes;
   uint8_t* all_scales = is_v ? p.V_scales : p.K_scales;
-  for (int h = blockIdx.y; h < p.Hkv; h += gridDim.y) {
-    const uint8_t* rows = src + (h - blockIdx.y) * (is_v ? p.v1 : p.k1);
-    for (int r = warp; r < here; r += kWarps) {
-      const int n = run_at(r);
-      if (n == 0) continue;
-      if (n > kShort) {
-        if (lane == 0 && h == blockIdx.y) {
-          const int x = atomicAdd(&s_long, 1);
-          s_first[x] = r;
-          s_rows[x] = n;
-        }
-        continue;
-      }
-      const int64_t at = s_slot[r + 1], page = at / kBk;
-      const int t0 = static_cast<int>(at & (kBk - 1));
-      uint8_t* scale = all_scales + page * p.s0 + h * p.s1;
-      uint8_t* block = all_codes + page * p.c0 + h * p.c1;
-      const uint32_t stored = t0 > 0 ? *scale : 0;
-      const uint8_t* row = rows + r * n_stride;
-      uint4 v[kShort / 2];
-      uint32_t m = 0;
+  if (tid < here && (s_break[tid >> 5] >> (tid & 31) & 1) != 0 && stored_at(tid)) {
+    const int n = next_break(tid + 1) - tid;
+    if (n <= kShort) s_run[atomicAdd(&s_runs, 1)] = tid | n << 16;   // (in whatever order: they are of different pages)
+  }
+  __syncthreads();
+  const int heads = h_hi - h_lo, units = s_runs * heads;
+  for (int u0 = 0; u0 < units; u0 += kHalves * kDeep) {
+    int n[kDeep], t0[kDeep], head[kDeep];
+    int64_t page[kDeep];
+    const uint8_t* row[kDeep];
+    uint4 v[kDeep];
+    uint32_t old[kDeep];
 #pragma unroll
-      for (int i = 0; i < kShort / 2; ++i) {
-        const int k = 2 * i + (lane >> 4);
-        v[i] = i == 0 && r == warp && h == blockIdx.y && lane < 16 ? early
-               : k < n ? *reinterpret_cast<const uint4*>(row + k * n_stride) : make_uint4(0, 0, 0, 0);
+    for (int d = 0; d < kDeep; ++d) {
+      const int u = u0 + d * kHalves + warp * 2 + (lane >> 4);
+      const int run = u < units ? s_run[u / heads] : 0, r = run & 0xffff;
+      const int64_t at = s_slot[r + 1];
+      n[d] = run >> 16;
+      head[d] = h_lo + u % heads;
+      page[d] = at / kBk;
+      t0[d] = static_cast<int>(at & (kBk - 1));
+      row[d] = src + r * n_stride + head[d] * h_stride;
+      v[d] = make_uint4(0, 0, 0, 0);
+      old[d] = 0;
+      if (n[d] > 0) {
+        v[d] = *reinterpret_cast<const uint4*>(row[d]);
+        if (t0[d] > 0) old[d] = q8_byte(all_scales[page[d] * p.s0 + head[d] * p.s1]);
       }
+    }
 #pragma unroll
-      for (int i = 0; i < kShort / 2; ++i) m = finite_max(m, v[i]);
-      uint32_t byte = q8_byte_for(warp_top(m));
-      if (t0 > 0) {
-        const uint32_t old = q8_byte(stored);
-        if (byte > old) rescale_rows(block, t0, q8_inverse(byte - old + 127), lane, 32);
-        byte = max(byte, old);
+    for (int d = 0; d < kDeep; ++d) {
+      uint32_t m = finite_max(0, v[d]);
+      for (int k = 1; __any_sync(0xffffffffu, k < n[d]); ++k)
+        if (k < n[d]) m = finite_max(m, *reinterpret_cast<const uint4*>(row[d] + k * n_stride));
+      uint32_t top = max(m & 0xffffu, m >> 16);
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (n[d] == 0) continue;
+      const uint32_t byte = max(q8_byte_for(top), old[d]);
+      if (part == 0) {
+        if (old[d] != 0 && byte > old[d])
+          s_growth[atomicAdd(&s_grown, 1)] = Growth{static_cast<int>(page[d]), head[d], t0[d], static_cast<int>(byte - old[d])};
+        all_scales[page[d] * p.s0 + head[d] * p.s1] = static_cast<uint8_t>(byte);
       }
       const float inv = q8_inverse(byte);
-#pragma unroll
-      for (int i = 0; i < kShort / 2; ++i) {
-        const int k = 2 * i + (lane >> 4);
-        if (k < n) *reinterpret_cast<uint2*>(block + (t0 + k) * kD + part * 8) = encode8(v[i], inv);
-      }
-      if (lane == 0) *scale = static_cast<uint8_t>(byte);
+      uint8_t* to = all_codes + page[d] * p.c0 + head[d] * p.c1 + t0[d] * kD + part * 8;
+      *reinterpret_cast<uint2*>(to) = encode8(v[d], inv);
+      for (int k = 1; k < n[d]; ++k)
+        *reinterpret_cast<uint2*>(to + k * kD) = encode8(*reinterpret_cast<const uint4*>(row[d] + k * n_stride), inv);
     }
-    if (h == blockIdx.y) __syncthreads();
-    // the long runs, one after another (in whatever order: they are of different pages)
-    for (int x = 0; x < s_long; ++x) {
-      const int r = s_first[x], n = s_rows[x], first = tid >> 4;
+    __syncwarp();
+  }
+  for (int h = h_lo; h < h_hi; ++h) {
+    const uint8_t* rows = src + h * h_stride;
+    // the long runs, one after another
+    for (int r = next_break(0), end; r < here; r = end) {
+      end = next_break(r + 1);
+      if (end - r <= kShort || !stored_at(r)) continue;
+      const int n = end - r, first = tid >> 4;
       const int64_t at = s_slot[r + 1], page = at / kBk;
       const int t0 = static_cast<int>(at & (kBk - 1));
       uint8_t* scale = all_scales + page * p.s0 + h * p.s1;
@@ -202,6 +232,13 @@ __global__ void __launch_bounds__(kThreads, kStoreCtas) append_q8_kernel(const S
           *reinterpret_cast<uint2*>(block + (t0 + first + i * (kThreads / 16)) * kD + part * 8) = encode8(v[i], inv);
       if (tid == 0) *scale = static_cast<uint8_t>(byte);
     }
+  }
+  __syncthreads();
+  // the blocks that grew: a few by all warps, or many by one each
+  const int grown = s_grown, team = grown == 1 ? kWarps : grown == 2 ? kWarps / 2 : grown <= 4 ? kWarps / 4 : 1;
+  for (int x = warp / team; x < grown; x += kWarps / team) {
+    const Growth y = s_growth[x];
+    rescale_rows(all_codes + y.page * p.c0 + y.head * p.c1, y.rows, q8_inverse(y.by + 127), warp % team * 32 + lane, team * 32);
   }
 }
 
@@ -254,7 +291,15 @@ __global__ void __launch_bounds__(kThreads) expand_q8_kernel(const ExpandParams 
 msa_status launch_append_q8(const msa_append_q8_args& a, cudaStream_t stream) {
   StoreParams p;
   p.N = a.N; p.num_pages = a.cache.num_pages; p.Hkv = a.Hkv;
-  p.window = a.N <= kFewTokens ? kWarps : kManyWindow;
+  DeviceInfo dev;
+  if (msa_status st = current_device(&dev); st != MSA_OK) return st;
+  p.window = a.N <= kFewTokens ? kFewWindow : kManyWindow;
+  p.heads = 1;
+  if (a.N <= kFewTokens) {
+    const int64_t windows = (a.N + kFewWindow - 1) / kFewWindow;
+    while (p.heads < kFewHeads && 2 * windows * ((a.Hkv + p.heads - 1) / p.heads) > kStoreCtas * dev.num_sms) p.heads *= 2;
+  }
+  if (a.Hkv / p.heads >= static_cast<int>(kMaxGridY)) return fail(MSA_ERR_UNSUPPORTED, "8-bit store: too many heads");
   p.K = static_cast<const uint8_t*>(a.K);
   p.V = static_cast<const uint8_t*>(a.V);
   p.k0 = a.K_stride[0] * 2; p.k1 = a.K_stride[1] * 2;
@@ -267,7 +312,7 @@ msa_status launch_append_q8(const msa_append_q8_args& a, cudaStream_t stream) {
   p.c0 = a.cache.code_stride[0]; p.c1 = a.cache.code_stride[1];
   p.s0 = a.cache.scale_stride[0]; p.s1 = a.cache.scale_stride[1];
   p.dev_err = a.dev_err;
-  const dim3 grid(static_cast<unsigned>((a.N + p.window - 1) / p.window), std::min<unsigned>(static_cast<unsigned>(a.Hkv), kMaxGridY), 2);
+  const dim3 grid(static_cast<unsigned>((a.N + p.window - 1) / p.window), static_cast<unsigned>((a.Hkv + p.heads - 1) / p.heads), 2);
   const cudaError_t e = launch_early(append_q8_kernel, grid, kThreads, 0, stream, 1, p);
   if (e != cudaSuccess) return cuda_fail(e, "append_q8_kernel launch");
   return MSA_OK;
