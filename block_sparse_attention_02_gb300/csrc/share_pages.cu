@@ -6,13 +6,14 @@
 // holders beyond the first, so that pages given out by msa_plan_step (0) need nothing, and a page goes back on the stack
 // when the count would fall below 0.
 //
-// Each of the three index kernels is one thread-block cluster: its CTAs form the sums over the requests for themselves,
-// go through the table entries and the pages side by side, and meet at the cluster's barrier where one step needs all of
-// the step before (counts before the search for freed pages, marks before ranks, ranks before the table).  So a call is one
-// launch without scratch, lengths and counts may be updated in place, and whatever is counted by atomics is a sum, the
-// same in any order; freed pages and moves are ordered by page number.
+// Each of the three index kernels is one CTA, or for larger pools and tables one thread-block cluster: it forms the sums over
+// the requests for itself, goes through the table entries and the pages side by side, and meets at a barrier where one step
+// needs all of the step before (counts before the search for freed pages, marks before ranks, ranks before the table).  So a
+// call is one launch without scratch, lengths and counts may be updated in place, and whatever is counted by atomics is a sum,
+// the same in any order; freed pages and moves are ordered by page number.
 //
-// Bound: latency (the barriers, dependent loads of lengths, tables and counts).  The copies are bound by HBM.
+// Bound: latency (the barriers, of which a cluster's takes half a microsecond; dependent loads of lengths, tables and counts).
+// The copies are bound by HBM.
 #include <cooperative_groups.h>
 
 #include <climits>
@@ -26,17 +27,19 @@ namespace cg = cooperative_groups;
 namespace msa {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kAlone = 1024, kThreads = 512;              // threads of a CTA alone, and of a cluster's
 constexpr int kCluster = 8;                                // CTAs (the portable maximum)
 constexpr int kPer = kMaxDecodeBatch / kThreads;           // requests (or forks) of a thread in the sums, at most
+constexpr int kAloneItems = 1024;                          // entries or pages up to which a CTA works alone
+constexpr int kOwn = 4;                                    // pages of a thread that it looks at together
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 4;
 constexpr int kCopyChunk = kCopyThreads * kCopyUnroll * 16;   // bytes of a page that a CTA copies at a time
 
 // Exclusive prefix sum over the CTA's threads; the total in *total.
 __device__ __forceinline__ int block_exclusive(int v, int* total) {
-  __shared__ int s_warp[kThreads / 32 + 1];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ int s_warp[kAlone / 32 + 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   int inc = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -47,18 +50,18 @@ __device__ __forceinline__ int block_exclusive(int v, int* total) {
   if (lane == 31) s_warp[warp] = inc;
   __syncthreads();
   if (warp == 0) {
-    const int own = lane < kThreads / 32 ? s_warp[lane] : 0;
+    const int own = lane < warps ? s_warp[lane] : 0;
     int w = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, w, o);
       if (lane >= o) w += x;
     }
-    if (lane < kThreads / 32) s_warp[lane] = w - own;
-    if (lane == 31) s_warp[kThreads / 32] = w;
+    if (lane < warps) s_warp[lane] = w - own;
+    if (lane == 31) s_warp[kAlone / 32] = w;
   }
   __syncthreads();
-  *total = s_warp[kThreads / 32];
+  *total = s_warp[kAlone / 32];
   return s_warp[warp] + inc - v;
 }
 
@@ -72,57 +75,69 @@ __device__ __forceinline__ int last_at_most(const int* first, int n, int x) {
   return lo;
 }
 
-// A value of every CTA of the cluster: the sum over the CTAs before this one, and over all.
-struct ClusterSum {
-  int before, all;
+// The CTA, or the cluster's CTAs.
+struct Team {
+  int rank, ctas;
+  __device__ Team() : rank(blockIdx.x), ctas(gridDim.x) {}
+  __device__ __forceinline__ void sync() const {
+    if (ctas > 1) cg::this_cluster().sync();
+    else __syncthreads();
+  }
+  // `value` into place i of every CTA's array.  (Read by its own CTA after sync(): none leaves while another reads its memory.)
+  __device__ __forceinline__ void tell(int* array, int i, int value) const {
+    if (ctas == 1) array[i] = value;
+    else
+      for (int c = 0; c < ctas; ++c) *cg::this_cluster().map_shared_rank(array + i, c) = value;
+  }
+  __device__ __forceinline__ int first() const { return rank * blockDim.x + threadIdx.x; }
+  __device__ __forceinline__ int stride() const { return ctas * blockDim.x; }
 };
-__device__ __forceinline__ ClusterSum cluster_sum(cg::cluster_group cluster, int mine) {
-  __shared__ int s_value;
-  cluster.sync();                           // an earlier value is read
-  if (threadIdx.x == 0) s_value = mine;
-  cluster.sync();
-  ClusterSum r{0, 0};
-  for (unsigned c = 0; c < cluster.num_blocks(); ++c) {
-    const int v = *cluster.map_shared_rank(&s_value, c);
-    if (c < cluster.block_rank()) r.before += v;
-    r.all += v;
-  }
-  return r;
-}
-// (every kernel ends with a cluster barrier after its last look into another CTA's memory)
 
-__device__ __forceinline__ void copy_counts(const int32_t* from, int32_t* to, int64_t n, int64_t first, int64_t stride) {
+__device__ __forceinline__ void copy_counts(const int32_t* from, int32_t* to, int64_t n, const Team& team) {
   if (from == to) return;
-  for (int64_t i = first; i < n; i += stride) to[i] = from[i];
+#pragma unroll 4
+  for (int64_t i = team.first(); i < n; i += team.stride()) to[i] = from[i];
 }
 
-// The table entries of the requests: entry x is of request b = last_at_most(first, B, x), page x - first[b].  f(b, j) for
-// this thread's share, four searches and loads side by side.
-template <class F>
-__device__ __forceinline__ void for_entries(const int* first, int B, int total, int at, int stride, F f) {
-  for (int x = at; x < total; x += stride) {
-    const int b = last_at_most(first, B, x);
-    f(b, x - first[b]);
+// The table entries of the requests: entry x is of request b = last_at_most(first, B, x), page x - first[b].  For this thread's
+// share, four side by side: page = load(b, j), then use(b, j, page).
+template <class L, class U>
+__device__ __forceinline__ void for_entries(const int* first, int B, int total, const Team& team, L load, U use) {
+  constexpr int kDeep = 4;
+  for (int x0 = team.first(); x0 < total; x0 += kDeep * team.stride()) {
+    int b[kDeep], j[kDeep], page[kDeep];
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) {
+      const int x = x0 + i * team.stride();
+      b[i] = j[i] = page[i] = -1;
+      if (x < total) {
+        b[i] = last_at_most(first, B, x);
+        j[i] = x - first[b[i]];
+        page[i] = load(b[i], j[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i)
+      if (b[i] >= 0) use(b[i], j[i], page[i]);
   }
 }
 
-__global__ void __launch_bounds__(kThreads) fork_kernel(const msa_fork_args p) {
+__global__ void __launch_bounds__(kAlone) fork_kernel(const msa_fork_args p) {
   wait_for_stream();
   extern __shared__ int s_mem[];
   int* s_first = s_mem;                     // [F + 1] shared table entries of the forks before
   int* s_src = s_first + p.F + 1;           // [F] -1: not served
   int* s_dst = s_src + p.F;                 // [F]
   int* s_owner = s_dst + p.F;               // [B] the first fork that names a request
-  cg::cluster_group cluster = cg::this_cluster();
-  const int tid = threadIdx.x, F = p.F, rank = static_cast<int>(cluster.block_rank()), ctas = static_cast<int>(cluster.num_blocks());
-  const int at = rank * kThreads + tid, stride = ctas * kThreads;
+  const Team team;
+  const int tid = threadIdx.x, F = p.F, threads = blockDim.x;
   const int64_t cap = p.max_pages * kBk;
   const int raw = *p.free_count;
   const int count = static_cast<int>(min(max(static_cast<int64_t>(raw), int64_t(0)), p.free_cap));
   int32_t err = raw == count ? 0 : MSA_DEVERR_NO_PAGES;
-  for (int b = tid; b < p.B; b += kThreads) s_owner[b] = INT_MAX;
+  for (int b = tid; b < p.B; b += threads) s_owner[b] = INT_MAX;
   __syncthreads();
-  const int per = (F + kThreads - 1) / kThreads;
+  const int per = (F + threads - 1) / threads;
   int src[kPer], dst[kPer], L[kPer];
   int need = 0;
 #pragma unroll
@@ -194,21 +209,21 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const msa_fork_args p) {
     }
   }
   if (tid == 0) s_first[F] = total;
-  copy_counts(p.page_shares, p.page_shares_out, p.num_pages, at, stride);
-  if (rank == 0 && err != 0) report(p.dev_err, err);
+  copy_counts(p.page_shares, p.page_shares_out, p.num_pages, team);
+  if (team.rank == 0 && err != 0) report(p.dev_err, err);
   // the last CTA, which has the fewest table entries, writes lengths, copies and the stack's height; lengths of all first
   int len[kPer];
-  const int per_b = (p.B + kThreads - 1) / kThreads;
+  const int per_b = (p.B + threads - 1) / threads;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int b = tid + i * kThreads;
+    const int b = tid + i * threads;
     len[i] = i < per_b && b < p.B ? p.seq_len[b] : 0;
   }
-  cluster.sync();                           // lengths, counts and the stack's height are read, counts copied
-  if (rank == ctas - 1) {
+  team.sync();                              // lengths, counts and the stack's height are read, counts copied
+  if (team.rank == team.ctas - 1) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int b = tid + i * kThreads;
+      const int b = tid + i * threads;
       if (i < per_b && b < p.B && (s_owner[b] == INT_MAX || s_src[s_owner[b]] < 0)) p.seq_len_out[b] = len[i];
     }
 #pragma unroll
@@ -230,35 +245,47 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const msa_fork_args p) {
     if (tid == 0) *p.free_count_out = count - min(pages_needed, count);
   }
   bool bad = false;
-  for_entries(s_first, F, total, at, stride, [&](int x, int j) {
-    const int page = p.seq_pt[s_src[x] * p.max_pages + j];
-    p.seq_pt_out[s_dst[x] * p.max_pages + j] = page;
-    if (page >= 0 && page < p.num_pages) atomicAdd(p.page_shares_out + page, 1);
-    else bad = true;
-  });
+  for_entries(
+      s_first, F, total, team, [&](int x, int j) { return p.seq_pt[s_src[x] * p.max_pages + j]; },
+      [&](int x, int j, int page) {
+        p.seq_pt_out[s_dst[x] * p.max_pages + j] = page;
+        if (page >= 0 && page < p.num_pages) atomicAdd(p.page_shares_out + page, 1);
+        else bad = true;
+      });
   if (bad) report(p.dev_err, MSA_DEVERR_BAD_PAGE);
 }
 
-// The pages of one thread, when a cluster's threads share the pool's: [lo, hi), in order.
-__device__ __forceinline__ void own_pages(int64_t num_pages, int rank, int ctas, int* lo, int* hi) {
-  const int64_t threads = static_cast<int64_t>(ctas) * kThreads;
-  const int64_t per = ((num_pages + threads - 1) / threads + 3) / 4 * 4;
-  const int64_t at = (static_cast<int64_t>(rank) * kThreads + threadIdx.x) * per;
+// The pages of one thread, when all threads share the pool's: [lo, hi), in order.
+__device__ __forceinline__ void own_pages(int64_t num_pages, const Team& team, int* lo, int* hi) {
+  const int64_t per = (num_pages + team.stride() - 1) / team.stride();
+  const int64_t at = static_cast<int64_t>(team.first()) * per;
   *lo = static_cast<int>(min(at, num_pages));
   *hi = static_cast<int>(min(at + per, num_pages));
 }
+// f(x, value) for these pages, in order, kOwn values loaded together.
+template <class F>
+__device__ __forceinline__ void for_pages(const int32_t* values, int lo, int hi, F f) {
+  for (int x0 = lo; x0 < hi; x0 += kOwn) {
+    int v[kOwn];
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) v[i] = x0 + i < hi ? __ldcg(values + x0 + i) : 0;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i)
+      if (x0 + i < hi) f(x0 + i, v[i]);
+  }
+}
 
-__global__ void __launch_bounds__(kThreads) release_shared_kernel(const msa_release_shared_args p) {
+__global__ void __launch_bounds__(kAlone) release_shared_kernel(const msa_release_shared_args p) {
   wait_for_stream();
   extern __shared__ int s_first[];          // [B + 1] table entries of the ended requests before
-  cg::cluster_group cluster = cg::this_cluster();
-  const int tid = threadIdx.x, B = p.B, rank = static_cast<int>(cluster.block_rank()), ctas = static_cast<int>(cluster.num_blocks());
-  const int at = rank * kThreads + tid, stride = ctas * kThreads;
+  __shared__ int s_back[kCluster];          // pages that come back, of each CTA
+  const Team team;
+  const int tid = threadIdx.x, B = p.B, threads = blockDim.x;
   const int64_t cap = p.max_pages * kBk;
   const int raw = *p.free_count;
   const int64_t count = min(max(static_cast<int64_t>(raw), int64_t(0)), p.free_cap);
   int32_t err = raw == count ? 0 : MSA_DEVERR_NO_PAGES;
-  const int per = (B + kThreads - 1) / kThreads;
+  const int per = (B + threads - 1) / threads;
   int len[kPer], gone[kPer], sum = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -277,6 +304,7 @@ __global__ void __launch_bounds__(kThreads) release_shared_kernel(const msa_rele
       sum += gone[i];
     }
   }
+  copy_counts(p.page_shares, p.page_shares_out, p.num_pages, team);
   int total;
   int first = block_exclusive(sum, &total);
 #pragma unroll
@@ -286,9 +314,8 @@ __global__ void __launch_bounds__(kThreads) release_shared_kernel(const msa_rele
     first += gone[i];
   }
   if (tid == 0) s_first[B] = total;
-  copy_counts(p.page_shares, p.page_shares_out, p.num_pages, at, stride);
-  cluster.sync();                           // counts copied, lengths and the stack's height read
-  if (rank == ctas - 1) {
+  team.sync();                              // counts copied, lengths and the stack's height read
+  if (team.rank == team.ctas - 1) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int b = tid * per + i;
@@ -296,45 +323,50 @@ __global__ void __launch_bounds__(kThreads) release_shared_kernel(const msa_rele
     }
   }
   bool bad = false;
-  for_entries(s_first, B, total, at, stride, [&](int b, int j) {
-    const int page = p.seq_pt[b * p.max_pages + j];
-    if (page >= 0 && page < p.num_pages) atomicSub(p.page_shares_out + page, 1);
-    else bad = true;
-  });
-  cluster.sync();                           // every holder that ended is taken off
+  for_entries(
+      s_first, B, total, team, [&](int b, int j) { return p.seq_pt[b * p.max_pages + j]; },
+      [&](int, int, int page) {
+        if (page >= 0 && page < p.num_pages) atomicSub(p.page_shares_out + page, 1);
+        else bad = true;
+      });
+  team.sync();                              // every holder that ended is taken off
   int lo, hi, back = 0;
-  own_pages(p.num_pages, rank, ctas, &lo, &hi);
-  for (int x = lo; x < hi; ++x) back += __ldcg(p.page_shares_out + x) < 0 ? 1 : 0;
+  own_pages(p.num_pages, team, &lo, &hi);
+  for_pages(p.page_shares_out, lo, hi, [&](int, int left) { back += left < 0 ? 1 : 0; });
   int in_cta;
-  const int before = block_exclusive(back, &in_cta);
-  const ClusterSum sums = cluster_sum(cluster, in_cta);
-  int64_t to = count + sums.before + before;
-  for (int x = lo; x < hi; ++x) {
-    const int left = __ldcg(p.page_shares_out + x);
-    if (left >= 0) continue;
-    if (left < -1) bad = true;              // given up more often than it was held
-    p.page_shares_out[x] = 0;
-    if (to < p.free_cap) p.free_pages[to] = x;
-    ++to;
+  int before = block_exclusive(back, &in_cta);
+  if (tid == 0) team.tell(s_back, team.rank, in_cta);
+  team.sync();
+  int all = 0;
+  for (int c = 0; c < team.ctas; ++c) {
+    if (c < team.rank) before += s_back[c];
+    all += s_back[c];
   }
-  if (count + sums.all > p.free_cap) err |= MSA_DEVERR_NO_PAGES;
-  if (rank == 0 && tid == 0) *p.free_count_out = static_cast<int>(min(count + sums.all, p.free_cap));
+  int64_t to = count + before;
+  if (back > 0)
+    for_pages(p.page_shares_out, lo, hi, [&](int x, int left) {
+      if (left >= 0) return;
+      bad |= left < -1;                     // given up more often than it was held
+      p.page_shares_out[x] = 0;
+      if (to < p.free_cap) p.free_pages[to] = x;
+      ++to;
+    });
+  if (count + all > p.free_cap) err |= MSA_DEVERR_NO_PAGES;
+  if (team.rank == 0 && tid == 0) *p.free_count_out = static_cast<int>(min(count + all, p.free_cap));
   if (bad) err |= MSA_DEVERR_BAD_PAGE;
-  if ((bad || rank == 0) && err != 0) report(p.dev_err, err);
-  cluster.sync();
+  if ((bad || team.rank == 0) && err != 0) report(p.dev_err, err);
 }
 
-__global__ void __launch_bounds__(kThreads) compact_kernel(const msa_compact_args p) {
+__global__ void __launch_bounds__(kAlone) compact_kernel(const msa_compact_args p) {
   wait_for_stream();
   extern __shared__ int s_first[];          // [B + 1] table entries of the requests before
-  __shared__ int s_low;                     // of CTA 0: pages in use among the first n
-  cg::cluster_group cluster = cg::this_cluster();
-  const int tid = threadIdx.x, B = p.B, rank = static_cast<int>(cluster.block_rank()), ctas = static_cast<int>(cluster.num_blocks());
-  const int at = rank * kThreads + tid, stride = ctas * kThreads;
+  __shared__ int s_used[kCluster], s_low[1];   // pages in use: of each CTA's share, and among the first n
+  const Team team;
+  const int tid = threadIdx.x, B = p.B, threads = blockDim.x;
   const int64_t cap = p.max_pages * kBk, P = p.num_pages;
   int32_t err = 0;
   int32_t* const place = p.free_pages;      // until the end: whether a page is in use, then where it goes
-  const int per = (B + kThreads - 1) / kThreads;
+  const int per = (B + threads - 1) / threads;
   int pages[kPer], sum = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -347,6 +379,11 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const msa_compact_arg
     }
     sum += pages[i];
   }
+  for (int64_t x = team.first(); x < P; x += team.stride()) {
+    place[x] = 0;
+    p.move_src[x] = -1;
+    p.move_dst[x] = -1;
+  }
   int total;
   int first = block_exclusive(sum, &total);
 #pragma unroll
@@ -355,76 +392,74 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const msa_compact_arg
     if (i < per && b < B) s_first[b] = first;
     first += pages[i];
   }
-  if (tid == 0) s_first[B] = total;
-  for (int64_t x = at; x < P; x += stride) {
-    place[x] = 0;
-    p.move_src[x] = -1;
-    p.move_dst[x] = -1;
+  if (tid == 0) {
+    s_first[B] = total;
+    s_low[0] = 0;
   }
-  cluster.sync();
-  for_entries(s_first, B, total, at, stride, [&](int b, int j) {
-    const int page = p.seq_pt[b * p.max_pages + j];
-    if (page >= 0 && page < P) place[page] = 1;
-    else err |= MSA_DEVERR_BAD_PAGE;
-  });
-  cluster.sync();                           // every page in use is marked
+  team.sync();
+  for_entries(
+      s_first, B, total, team, [&](int b, int j) { return p.seq_pt[b * p.max_pages + j]; },
+      [&](int, int, int page) {
+        if (page >= 0 && page < P) place[page] = 1;
+        else err |= MSA_DEVERR_BAD_PAGE;
+      });
+  team.sync();                              // every page in use is marked
   int lo, hi, used = 0;
-  own_pages(P, rank, ctas, &lo, &hi);
-  for (int x = lo; x < hi; ++x) used += __ldcg(place + x);
+  own_pages(P, team, &lo, &hi);
+  for_pages(place, lo, hi, [&](int, int live) { used += live; });
   int in_cta;
   int before = block_exclusive(used, &in_cta);
-  const ClusterSum sums = cluster_sum(cluster, in_cta);
-  const int n = sums.all;                   // pages in use: they end up as 0 .. n - 1
-  before += sums.before;
-  if (lo < hi && lo <= n && n < hi) {       // (n = P: nothing lies behind)
-    int low = before;
-    for (int x = lo; x < n; ++x) low += __ldcg(place + x);
-    *cluster.map_shared_rank(&s_low, 0) = low;
+  if (tid == 0) team.tell(s_used, team.rank, in_cta);
+  team.sync();
+  int n = 0;                                // pages in use: they end up as 0 .. n - 1
+  for (int c = 0; c < team.ctas; ++c) {
+    if (c < team.rank) before += s_used[c];
+    n += s_used[c];
   }
-  cluster.sync();
-  const int low = n < P ? *cluster.map_shared_rank(&s_low, 0) : n;
-  // the k-th page in use behind the first n goes to the k-th free one among them
-  int rank_of = before;
-  for (int x = lo; x < hi; ++x) {
-    const int live = __ldcg(place + x);
-    if (live != 0 && x >= n) p.move_src[rank_of - low] = x;
-    if (live == 0 && x < n) p.move_dst[x - rank_of] = x;
-    rank_of += live;
-  }
-  cluster.sync();                           // the moves are known
-  rank_of = before;
-  for (int x = lo; x < hi; ++x) {
-    const int live = __ldcg(place + x);
+  // The k-th page in use behind the first n goes to the k-th free one among them.  Where the first n end, the pages in use
+  // before give the first rank behind.
+  int rank = before;
+  for_pages(place, lo, hi, [&](int x, int live) {
+    if (x == n) team.tell(s_low, 0, rank);
+    if (live == 0 && x < n) p.move_dst[x - rank] = x;
+    rank += live;
+  });
+  team.sync();                              // the free places are known
+  const int low = s_low[0];
+  rank = before;
+  for_pages(place, lo, hi, [&](int x, int live) {
     const int shares = live != 0 ? p.page_shares[x] : 0;
     if (x >= n) p.page_shares_out[x] = 0;
-    if (live != 0) {
-      const int to = x < n ? x : __ldcg(p.move_dst + (rank_of - low));
-      place[x] = to;
-      p.page_shares_out[to] = shares;
+    if (live == 0) return;
+    int to = x;
+    if (x >= n) {
+      to = __ldcg(p.move_dst + (rank - low));
+      p.move_src[rank - low] = x;
     }
-    rank_of += live;
-  }
-  cluster.sync();                           // where each page goes is known
-  for_entries(s_first, B, total, at, stride, [&](int b, int j) {
-    const int64_t i = b * p.max_pages + j;
-    const int page = p.seq_pt[i];
-    p.seq_pt_out[i] = page >= 0 && page < P ? __ldcg(place + page) : page;
+    place[x] = to;
+    p.page_shares_out[to] = shares;
+    ++rank;
   });
-  cluster.sync();                           // the places are read: the stack takes their room
-  for (int64_t x = at; x < p.free_cap; x += stride) p.free_pages[x] = x < P - n ? static_cast<int32_t>(P - 1 - x) : -1;
-  if (rank == 0 && tid == 0) *p.free_count = static_cast<int32_t>(P - n);
+  team.sync();                              // where each page goes is known
+  for_entries(
+      s_first, B, total, team, [&](int b, int j) { return p.seq_pt[b * p.max_pages + j]; },
+      [&](int b, int j, int page) { p.seq_pt_out[b * p.max_pages + j] = page >= 0 && page < P ? __ldcg(place + page) : page; });
+  team.sync();                              // the places are read: the stack takes their room
+  for (int64_t x = team.first(); x < p.free_cap; x += team.stride()) p.free_pages[x] = x < P - n ? static_cast<int32_t>(P - 1 - x) : -1;
+  if (team.rank == 0 && tid == 0) *p.free_count = static_cast<int32_t>(P - n);
   if (err != 0) report(p.dev_err, err);
 }
 
-// One cluster of as many CTAs as the entries and pages ask for, two at least.
+// One CTA, or one cluster where there are many entries and pages.
 template <class Args>
-msa_status launch_cluster(void (*kernel)(const Args), const Args& a, int64_t items, size_t smem, cudaStream_t stream, const char* what) {
-  const int ctas = static_cast<int>(std::min<int64_t>(std::max<int64_t>((items + kThreads - 1) / kThreads, 2), kCluster));
+msa_status launch_team(void (*kernel)(const Args), const Args& a, int64_t items, size_t smem, cudaStream_t stream, const char* what) {
   if (smem > (40u << 10)) {                 // with the sums' own shared memory past the 48 KiB default
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return cuda_fail(e, what);
   }
-  const cudaError_t e = launch_early(kernel, ctas, kThreads, smem, stream, ctas, a);
+  const bool alone = items <= kAloneItems;
+  const int ctas = alone ? 1 : kCluster;
+  const cudaError_t e = launch_early(kernel, ctas, alone ? kAlone : kThreads, smem, stream, ctas, a);
   if (e != cudaSuccess) return cuda_fail(e, what);
   return MSA_OK;
 }
@@ -487,18 +522,18 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_c
 
 msa_status launch_fork(const msa_fork_args& a, cudaStream_t stream) {
   const size_t smem = (3 * static_cast<size_t>(a.F) + a.B + 1) * sizeof(int);
-  return launch_cluster(fork_kernel, a, static_cast<int64_t>(a.F) * std::min<int64_t>(a.max_pages, 64), smem, stream, "fork_kernel launch");
+  return launch_team(fork_kernel, a, std::max<int64_t>(static_cast<int64_t>(a.F) * a.max_pages / 4, a.num_pages), smem, stream, "fork_kernel launch");
 }
 
 msa_status launch_release_shared(const msa_release_shared_args& a, cudaStream_t stream) {
   const size_t smem = (static_cast<size_t>(a.B) + 1) * sizeof(int);
-  return launch_cluster(release_shared_kernel, a, std::max<int64_t>(static_cast<int64_t>(a.B) * a.max_pages / 8, a.num_pages / 4), smem, stream,
+  return launch_team(release_shared_kernel, a, std::max<int64_t>(static_cast<int64_t>(a.B) * a.max_pages / 8, a.num_pages), smem, stream,
                         "release_shared_kernel launch");
 }
 
 msa_status launch_compact(const msa_compact_args& a, cudaStream_t stream) {
   const size_t smem = (static_cast<size_t>(a.B) + 1) * sizeof(int);
-  return launch_cluster(compact_kernel, a, a.num_pages, smem, stream, "compact_kernel launch");
+  return launch_team(compact_kernel, a, a.num_pages, smem, stream, "compact_kernel launch");
 }
 
 msa_status launch_copy_pages(const msa_copy_pages_args& a, cudaStream_t stream) {
