@@ -42,7 +42,6 @@ namespace {
 
 constexpr int kFew = 4, kMany = 8;                      // warps of a CTA: four, and for few long rows eight
 constexpr int kTile = 16;                               // tokens that a warp works on at a time
-constexpr int kStages = 2;                              // tiles of a warp in shared memory
 constexpr int kBins = 256;                              // that the dense form's units are counted by
 constexpr int kRowCost = 2;                             // pages' time that a row's end and the next one's start take
 constexpr int kMaxParts = 4;                            // CTAs of a row up to which they form a cluster
@@ -56,7 +55,9 @@ constexpr float kPShift = 8.f;                          // P is held as 2^(z - m
 constexpr float kNoMax = -FLT_MAX;                      // m before a first score: finite, so that no difference is NaN
 constexpr float kPMost = 32768.f;                       // most of a lane's sum of P (fp16 ends at 65504)
 
-enum Mode { kSparse, kDense, kWindow };
+// Dense rows and windows are shared out by the pages that each has; rows of at most k pages (selected ones, short windows) by k.
+enum Mode { kSparse, kShortWindow, kDense, kWindow };
+constexpr bool window_mode(Mode m) { return m == kWindow || m == kShortWindow; }
 
 struct Params {
   int B, Hq, Hkv, G, k;
@@ -300,9 +301,10 @@ __device__ __forceinline__ void attend_tile(const uint32_t (&q)[16], const float
   F::outputs(v, b0, b1, st->acc);
 }
 
-template <class F, Mode MODE, int kWarps, bool TREE>
+// STAGES: tiles of a warp in shared memory: two, three where there are few warps with bf16 pages.
+template <class F, Mode MODE, int kWarps, bool TREE, int STAGES>
 __global__ void __launch_bounds__(32 * kWarps, F::kSmWarps / kWarps) attn_rows_kernel(const Params p) {
-  constexpr bool DENSE = MODE != kSparse;
+  constexpr bool DENSE = MODE == kDense || MODE == kWindow, WINDOW = window_mode(MODE);
   constexpr int kThreads = 32 * kWarps;
   constexpr int kRep = 8 / kWarps;          // tiles of a page, and of the joined outputs' eight parts, those of a warp
   constexpr int kDeep = 8;                  // parts of a row that a lane loads at a time
@@ -317,11 +319,11 @@ __global__ void __launch_bounds__(32 * kWarps, F::kSmWarps / kWarps) attn_rows_k
   wait_for_stream();
 
   // what a sequence of L tokens (dense) shows its query: the first page of the window, and the sinks' pages before it
-  auto first_of = [&](int L) { return MODE == kWindow ? max(L - p.window, 0) : 0; };
-  auto sink_pages = [&](int first) { return MODE == kWindow ? min(static_cast<int>((min(p.sinks, first) + kBk - 1u) / kBk), first / kBk) : 0; };
+  auto first_of = [&](int L) { return WINDOW ? max(L - p.window, 0) : 0; };
+  auto sink_pages = [&](int first) { return WINDOW ? min(static_cast<int>((min(p.sinks, first) + kBk - 1u) / kBk), first / kBk) : 0; };
   // pages of one head of sequence x (dense) or of row x (sparse), and its units (dense)
   auto pages_of = [&](int x) {
-    if (!DENSE) return min(max(p.n[x], 0), p.k);
+    if (MODE == kSparse) return min(max(p.n[x], 0), p.k);
     const int L = p.seq_len[x];
     if (L <= 0 || L > p.max_pages * kBk) return 0;
     const int first = first_of(L);
@@ -412,13 +414,6 @@ __global__ void __launch_bounds__(32 * kWarps, F::kSmWarps / kWarps) attn_rows_k
       b = item;
       head = rem / row_pages;
       p0 = rem - head * row_pages;
-      seen.end = p.seq_len[b];
-      seen.first = first_of(seen.end);
-      seen.sinks = MODE == kWindow ? p.sinks : 0;
-      sink_end = sink_pages(seen.first);
-      skip = seen.first / kBk - sink_end;
-      live = (seen.end + kBk - 1) / kBk - skip;
-      list = p.seq_pt + b * p.max_pages;
     } else {
       item = static_cast<int>(u / p.row_units);
       rem = static_cast<int>(u - static_cast<int64_t>(item) * p.row_units);
@@ -426,10 +421,24 @@ __global__ void __launch_bounds__(32 * kWarps, F::kSmWarps / kWarps) attn_rows_k
       b = item / p.Hkv;
       head = item - b * p.Hkv;
       p0 = rem;
+    }
+    if (MODE == kSparse) {
       live = pages_of(item);
       seen.end = live == 0 ? 0 : (live - 1) * kBk + min(max(p.last_len[item], 0), kBk);
       seen.first = seen.sinks = 0;
       list = p.pt + static_cast<int64_t>(item) * p.k;
+    } else {
+      seen.end = p.seq_len[b];
+      if (!DENSE && (seen.end < 0 || seen.end > p.max_pages * kBk)) {
+        seen.end = 0;
+        if (head == 0 && p0 == 0 && tid == 0) report(p.dev_err, MSA_DEVERR_BAD_LEN);
+      }
+      seen.first = first_of(seen.end);
+      seen.sinks = WINDOW ? p.sinks : 0;
+      sink_end = sink_pages(seen.first);
+      skip = seen.first / kBk - sink_end;
+      live = (seen.end + kBk - 1) / kBk - skip;
+      list = p.seq_pt + b * p.max_pages;
     }
     const int row = b * p.Hkv + head;
     const int64_t row_first = u - p0;
@@ -450,12 +459,12 @@ __global__ void __launch_bounds__(32 * kWarps, F::kSmWarps / kWarps) attn_rows_k
     const int tok0 = warp * kRep * kTile;
     const int64_t in_block = head * p.c1 + (tok0 + F::row(lane)) * p.c2 + F::chunk(lane) * 16;
     const uint8_t *k_base = p.K + in_block, *v_base = p.V + in_block;
-    uint8_t* ring = s_ring + warp * (kStages * F::kTileBytes);
+    uint8_t* ring = s_ring + warp * (STAGES * F::kTileBytes);
     const uint32_t dk = smem_u32(ring) + F::k_at(lane), dv = smem_u32(ring) + kTile * F::kRow + F::v_at(lane);
     // Page ids (lane i: of the i-th of a run of 32 pages) and their blocks' scales (K's in the low byte) a run ahead
     auto page_id = [&](int n) {             // of the list's page p0 + n
       n += p0;
-      return n < p1 ? list[n + (MODE == kWindow && n >= sink_end ? skip : 0)] : -1;
+      return n < p1 ? list[n + (WINDOW && n >= sink_end ? skip : 0)] : -1;
     };
     auto scales_of = [&](int32_t id) {
       uint32_t x = 0;
@@ -476,14 +485,14 @@ __global__ void __launch_bounds__(32 * kWarps, F::kSmWarps / kWarps) attn_rows_k
     // where tile n starts in its sequence
     auto token_of = [&](int n) {
       const int j = p0 + n / kRep;
-      return (j + (MODE == kWindow && j >= sink_end ? skip : 0)) * kBk + tok0 + n % kRep * kTile;
+      return (j + (WINDOW && j >= sink_end ? skip : 0)) * kBk + tok0 + n % kRep * kTile;
     };
     // a tile that the query sees nothing of (window)
-    auto unseen = [&](int a) { return MODE == kWindow && a + kTile <= seen.first && a >= seen.sinks; };
+    auto unseen = [&](int a) { return WINDOW && a + kTile <= seen.first && a >= seen.sinks; };
     int into = 0, from = 0;                 // byte offsets of the ring's next stages
-    bool there[kStages] = {};               // whether a stage's tile was fetched
+    uint32_t there = 0;                     // bit n % 32: tile n was fetched
     auto fetch = [&](int n) {               // (n falls into the next run of 32 pages before its tiles do)
-      there[kStages - 1] = false;
+      there &= ~(1u << (n & 31));
       if (n < count) {
         const int page_n = n / kRep;
         if ((n & (32 * kRep - 1)) == 0 && n > 0) {
@@ -496,7 +505,7 @@ __global__ void __launch_bounds__(32 * kWarps, F::kSmWarps / kWarps) attn_rows_k
         const int32_t page = __shfl_sync(0xffffffffu, ids, page_n & 31);
         if (static_cast<uint32_t>(page) < pool_pages) {
           if (!unseen(token_of(n))) {
-            there[kStages - 1] = true;
+            there |= 1u << (n & 31);
             const int64_t off = page * p.c0 + n % kRep * kTile * p.c2;
             const uint8_t *k = k_base + off, *v = v_base + off;
 #pragma unroll
@@ -509,11 +518,11 @@ __global__ void __launch_bounds__(32 * kWarps, F::kSmWarps / kWarps) attn_rows_k
           report(p.dev_err, MSA_DEVERR_BAD_PAGE);
         }
       }
-      into = F::kTileBytes - into;
+      into = into == (STAGES - 1) * F::kTileBytes ? 0 : into + F::kTileBytes;
       copies_commit();
     };
-    fetch(0);
-    there[0] = there[1];
+#pragma unroll
+    for (int n = 0; n < STAGES - 1; ++n) fetch(n);
     if (F::kScaled) scales = scales_of(ids);
     // Q of head g as the products take it, in 8 bits' case as fp16 scaled by a power of two: pair e of its load i in q[4 i + e]
     uint32_t q[16];
@@ -558,27 +567,26 @@ __global__ void __launch_bounds__(32 * kWarps, F::kSmWarps / kWarps) attn_rows_k
     st.l[0] = st.l[1] = 0.f;
 
     for (int n = 0; n < count; ++n) {
-      copies_wait<kStages - 2>();
+      copies_wait<STAGES - 2>();
       __syncwarp();                         // every lane's share of tile n is there, and tile n - 1 is read
-      fetch(n + kStages - 1);
-      if (there[0]) {
+      fetch(n + STAGES - 1);
+      if ((there >> (n & 31) & 1) != 0) {
         const int a = token_of(n);
         float tile_coef[2] = {coef[0], coef[1]}, ev = 0.f;
         if (F::kScaled) {
-          // the fetch of the next tile may have moved on to the next run of pages
-          const bool moved = (n + 1 & (32 * kRep - 1)) == 0 && n + 1 < count;
+          // the fetches ahead may have moved on to the next run of pages
+          const bool moved = (min(n + STAGES - 1, count - 1) ^ n) >= 32 * kRep;
           const uint32_t x = __shfl_sync(0xffffffffu, moved ? old_scales : scales, n / kRep & 31);
           ev = static_cast<float>(static_cast<int>(x >> 8) - 127);
 #pragma unroll
           for (int c = 0; c < 2; ++c) tile_coef[c] = fmaxf(coef[c] * q8_scale(x & 0xffu), FLT_MIN);   // > 0: -inf stays so
         }
-        if (a + kTile <= seen.end && (MODE != kWindow || a >= seen.first || a + kTile <= seen.sinks))
+        if (a + kTile <= seen.end && (!WINDOW || a >= seen.first || a + kTile <= seen.sinks))
           attend_tile<F, true>(q, tile_coef, ev, ring + from, seen, a, g, t, &st);
         else
           attend_tile<F, false>(q, tile_coef, ev, ring + from, seen, a, g, t, &st);
       }
-      there[0] = there[1];
-      from = F::kTileBytes - from;
+      from = from == (STAGES - 1) * F::kTileBytes ? 0 : from + F::kTileBytes;
     }
     copies_wait<0>();
     if (F::kScaled) {                       // outputs and sum of p alone, without 2^-E: below 2^(15 + 80 + 20)
@@ -856,16 +864,16 @@ void take_cache(const msa_q8_cache& c, Params* p) {
   p->num_pages = c.num_pages;
 }
 
-template <class F, Mode MODE, int kWarps, bool TREE>
+template <class F, Mode MODE, int kWarps, bool TREE, int STAGES = 2>
 msa_status launch(const Params& p, int grid, int scratch_zeroed, cudaStream_t stream) {
   if (!scratch_zeroed) {   // otherwise zero by contract (every error-free call leaves them zero)
     const cudaError_t e = cudaMemsetAsync(p.group_counter, 0, kGroupBytes + static_cast<size_t>(p.B) * p.Hkv * sizeof(int32_t), stream);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(decode counters)");
   }
-  constexpr int smem = kWarps * std::max<int>(kStages * F::kTileBytes, kMaxG * kD * sizeof(float));
-  cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<F, MODE, kWarps, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  constexpr int smem = kWarps * std::max<int>(STAGES * F::kTileBytes, kMaxG * kD * sizeof(float));
+  cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<F, MODE, kWarps, TREE, STAGES>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(attn_rows)");
-  e = launch_early(attn_rows_kernel<F, MODE, kWarps, TREE>, grid, 32 * kWarps, smem, stream, std::max(p.parts, 1), p);
+  e = launch_early(attn_rows_kernel<F, MODE, kWarps, TREE, STAGES>, grid, 32 * kWarps, smem, stream, std::max(p.parts, 1), p);
   if (e != cudaSuccess) return cuda_fail(e, "attn_rows_kernel launch");
   return MSA_OK;
 }
@@ -904,9 +912,43 @@ msa_status launch_lists(Params p, int64_t most, int scratch_zeroed, cudaStream_t
   return MSA_OK;
 }
 
-// The most pages that a query sees: the window's (its first token anywhere in a page) and the sinks'.
-int64_t window_pages(int window, int sinks, int64_t max_pages) {
-  return std::min<int64_t>(max_pages, (static_cast<int64_t>(window) + kBk - 2) / kBk + 1 + (static_cast<int64_t>(sinks) + kBk - 1) / kBk);
+// Rows of up to k pages each.
+template <class F, Mode MODE>
+msa_status launch_rows(Params p, int scratch_zeroed, cudaStream_t stream) {
+  DeviceInfo dev;
+  if (msa_status st = current_device(&dev); st != MSA_OK) return st;
+  int room;
+  if (msa_status st = room_for<F>(kFew, &room); st != MSA_OK) return st;
+  const int rows = p.B * p.Hkv;
+  int grid = rows;
+  if (rows <= room) {
+    // Few rows: each is cut into equal parts, so that no CTA has pages of two rows.  Up to four parts are a cluster, which
+    // joins its row without the workspace; clusters of three and four that nearly fill the GPU do not all fit at once.
+    const int cluster = 16 * rows <= 3 * room ? 4 : 2 * rows <= room ? 2 : 1;
+    const int most = p.k <= 8 * cluster ? cluster : std::max((16 * rows <= room ? room / 2 : room) / rows, cluster);
+    const int per = (p.k + most - 1) / most;
+    const int parts = (p.k + per - 1) / per;
+    p.row_units = parts * per;
+    grid = rows * parts;
+    p.parts = parts == 2 || (parts <= kMaxParts && 4 * grid <= 3 * room) ? parts : 1;
+  } else {
+    p.row_units = p.k;                      // many rows: a CTA each, a new one where one ends
+  }
+  // Few CTAs: those over 8-bit pages get eight warps (8 rows of 16 pages 8.3 us for 9.6, 64 rows 12.1 for 13.1), those over
+  // bf16 pages, whose ring is twice as large, a third stage (64 rows of 17 pages 16.1 for 17.3).
+  if (grid <= 2 * dev.num_sms) return launch<F, MODE, F::kScaled ? kMany : kFew, false, F::kScaled ? 2 : 3>(p, grid, scratch_zeroed, stream);
+  return launch<F, MODE, kFew, false>(p, grid, scratch_zeroed, stream);
+}
+
+// A window's rows have at most the window's pages (its first token anywhere in a page) and the sinks'.
+template <class F>
+msa_status launch_window(Params p, int scratch_zeroed, cudaStream_t stream) {
+  const int64_t most = std::min<int64_t>(p.max_pages, (static_cast<int64_t>(p.window) + kBk - 2) / kBk + 1 + (static_cast<int64_t>(p.sinks) + kBk - 1) / kBk);
+  int room;
+  if (msa_status st = room_for<F>(kFew, &room); st != MSA_OK) return st;
+  if (most > kMaxK || 2 * p.B * p.Hkv > room) return launch_lists<F, kWindow>(p, most, scratch_zeroed, stream);
+  p.k = static_cast<int>(most);
+  return launch_rows<F, kShortWindow>(p, scratch_zeroed, stream);
 }
 
 }  // namespace
@@ -916,28 +958,11 @@ size_t attn_rows_workspace_size(int B, int Hkv) {
 }
 
 msa_status launch_sparse_decode_q8(const msa_decode_q8_args& a, void* ws, cudaStream_t stream) {
-  int room;
-  if (msa_status st = room_for<Q8>(kFew, &room); st != MSA_OK) return st;
   Params p = common_params(a, ws);
   take_cache(a.cache, &p);
   p.k = a.k;
   p.pt = a.pt; p.n = a.n; p.last_len = a.last_len;
-  const int rows = a.B * a.Hkv;
-  int grid = rows;
-  if (rows <= room) {
-    // Few rows: each is cut into equal parts, so that no CTA has pages of two rows.  Up to four parts are a cluster, which
-    // joins its row without the workspace; clusters of three and four that nearly fill the GPU do not all fit at once.
-    const int cluster = 16 * rows <= 3 * room ? 4 : 2 * rows <= room ? 2 : 1;
-    const int most = a.k <= 8 * cluster ? cluster : std::max((16 * rows <= room ? room / 2 : room) / rows, cluster);
-    const int per = (a.k + most - 1) / most;
-    const int parts = (a.k + per - 1) / per;
-    p.row_units = parts * per;
-    grid = rows * parts;
-    p.parts = parts == 2 || (parts <= kMaxParts && 4 * grid <= 3 * room) ? parts : 1;
-  } else {
-    p.row_units = a.k;                      // many rows: a CTA each, a new one where one ends
-  }
-  return launch<Q8, kSparse, kFew, false>(p, grid, a.scratch_zeroed, stream);
+  return launch_rows<Q8, kSparse>(p, a.scratch_zeroed, stream);
 }
 
 msa_status launch_dense_decode_q8(const msa_dense_decode_q8_args& a, void* ws, cudaStream_t stream) {
@@ -946,7 +971,7 @@ msa_status launch_dense_decode_q8(const msa_dense_decode_q8_args& a, void* ws, c
   p.seq_pt = a.seq_pt; p.seq_len = a.seq_len; p.max_pages = a.max_pages;
   p.window = a.window; p.sinks = a.sinks;
   if (a.window == 0) return launch_lists<Q8, kDense>(p, a.max_pages, a.scratch_zeroed, stream);
-  return launch_lists<Q8, kWindow>(p, window_pages(a.window, a.sinks, a.max_pages), a.scratch_zeroed, stream);
+  return launch_window<Q8>(p, a.scratch_zeroed, stream);
 }
 
 msa_status launch_window_decode(const msa_window_decode_args& a, void* ws, cudaStream_t stream) {
@@ -957,7 +982,7 @@ msa_status launch_window_decode(const msa_window_decode_args& a, void* ws, cudaS
   p.num_pages = a.num_pages;
   p.seq_pt = a.seq_pt; p.seq_len = a.seq_len; p.max_pages = a.max_pages;
   p.window = a.window; p.sinks = a.sinks;
-  return launch_lists<Bf16, kWindow>(p, window_pages(a.window, a.sinks, a.max_pages), a.scratch_zeroed, stream);
+  return launch_window<Bf16>(p, a.scratch_zeroed, stream);
 }
 
 }  // namespace msa
