@@ -66,7 +66,7 @@ struct Params {
 // A pair of tiles (SPLIT: one tile): queries q0 .. of sequence b, head g, at positions pos ..  Its blocks are sink_blocks ones
 // from 0 on, then those from `first` on; a CTA's are `blocks` ones of this list from `from` on.
 struct Item {
-  int b, g, q0, pos, tiles, sink_blocks, first, from, blocks;
+  int b, g, q0, pos, end, tiles, sink_blocks, first, from, blocks;   // (end: of the sequence's tokens)
   __device__ __forceinline__ int block(int j) const {
     j += from;
     return j < sink_blocks ? j : j - sink_blocks + first;
@@ -86,6 +86,7 @@ __device__ __forceinline__ Item item_of(const Params& p, int it) {
   x.from = 0;
   const int start = p.paged ? p.q_pos[x.b] : 0;
   x.pos = start + x.q0;
+  x.end = start + p.S;
   if (p.paged && (start < 0 || start + static_cast<int64_t>(p.S) > p.max_pages * kBk)) {
     x.sink_blocks = x.first = x.blocks = 0;
     return x;
@@ -332,6 +333,14 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           ok = wait(&bar_full[sv], pv, abort_flag, p.dev_err) && wait(&bar_pready[s][buf], ((n + j - 2) >> 1) & 1, abort_flag, p.dev_err);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
+          if (j == blocks + 1 && p.paged) {
+            // slots behind the sequence's last token may hold anything, and 0 * NaN is NaN: zeros (where it ends, in the last block)
+            const int live = x.end - x.block(SPLIT ? 2 * (j - 2) + s : j - 2) * kKeys;
+            for (int i = max(live, 0) * 8 + lane; i < kKeys * 8; i += 32)
+              for (int half = 0; half < 2; ++half) reinterpret_cast<uint4*>(s_kv + sv * kUnit + half * kHalf)[i] = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)

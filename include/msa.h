@@ -934,7 +934,8 @@ msa_status msa_window_attn_decode(const msa_window_decode_args *args, void *ws, 
  *     prefill, draft tokens).  K, V are pools [num_pages, Hkv, Bk, D], strides (page, g, t); seq_pt [B, max_pages],
  *     q_pos [B].  A sequence with q_pos < 0 or q_pos + S > max_pages * Bk gets O = 0 and LSE = -inf and raises
  *     MSA_DEVERR_BAD_LEN.  A page id outside [0, num_pages) is not read and its tokens are left out (MSA_DEVERR_BAD_PAGE).
- *     Pages without a seen token are not read; slots of the others that no query sees must hold finite values.
+ *     Pages without a seen token are not read.  Slots behind a sequence's last token may hold anything; its own tokens in
+ *     a page that is read must be finite, seen or not (as 0 * inf is NaN).
  * O [B, S, Hq, D] bf16 (dense), LSE [B, S, Hq] fp32 (dense, may be NULL).  P is rounded to bf16.  No workspace.
  * softmax_scale <= 0 selects 1 / sqrt(D).  S <= 2^30 and max_pages * Bk <= 2^30, B * S < 2^31. */
 typedef struct msa_window_prefill_args {

@@ -242,6 +242,22 @@ def test_chunk_bad_positions_and_pages(msa):
     check_prefill(Q[1:3], K, V, 100, 3, (O[1:3], LSE[1:3]), pt[1:3], pos[1:3])
 
 
+@pytest.mark.parametrize("pos,S", [([0, 5, 100, 127], 1), ([300, 61, 0, 90], 40), ([1000, 127, 64, 63], 130)])
+def test_chunk_anything_behind_the_last_token(msa, pos, S):
+    g, K, V, pt = paged([p + S for p in pos], 2, 14)
+    Q = torch.randn(4, S, 12, D, generator=g).bfloat16().cuda()
+    K, V = K.cuda(), V.cuda()
+    for window, sinks in ((100, 3), (1 << 30, 0)):
+        want = run_prefill(msa, Q, K, V, window, sinks, pt, pos)
+        wild = [x.clone() for x in (K, V)]
+        for b, p in enumerate(pos):
+            for t in range(p + S, -(-(p + S) // BK) * BK):
+                for x, v in zip(wild, (math.nan, -math.inf if t % 2 else math.nan)):
+                    x[pt[b, t // BK].item(), :, t % BK] = v
+        got = run_prefill(msa, Q, *wild, window, sinks, pt, pos)
+        assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+
+
 def test_graphs_and_streams(msa):
     lengths, S = [700, 300], 20
     g, K, V, pt = paged([L + S for L in lengths], 2, 13)
