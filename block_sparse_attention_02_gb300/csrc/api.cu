@@ -798,7 +798,7 @@ msa_status msa_fork_requests(const msa_fork_args* a, msa_stream_t stream) {
   if (msa_status st = check_tables(a->B, a->Bk, a->max_pages, a->free_cap); st != MSA_OK) return st;
   if (msa_status st = check_pool(a->num_pages); st != MSA_OK) return st;
   MSA_REQUIRE(a->F >= 0 && a->F <= kMaxDecodeBatch, MSA_ERR_UNSUPPORTED, "F = %d, supported 0..%d", a->F, kMaxDecodeBatch);
-  MSA_REQUIRE(static_cast<int64_t>(a->F) * a->max_pages < (int64_t(1) << 31), MSA_ERR_UNSUPPORTED,
+  MSA_REQUIRE(static_cast<int64_t>(a->F) * a->max_pages < (int64_t(1) << 30), MSA_ERR_UNSUPPORTED,
               "F * max_pages = %d * %" PRId64 " too large", a->F, a->max_pages);
   MSA_REQUIRE(a->F == 0 || (a->src && a->dst && a->copy_src && a->copy_dst), MSA_ERR_INVALID_ARG,
               "src, dst, copy_src and copy_dst must be non-NULL");
@@ -814,7 +814,7 @@ msa_status msa_release_shared_pages(const msa_release_shared_args* a, msa_stream
   MSA_REQUIRE(a != nullptr, MSA_ERR_INVALID_ARG, "args is NULL");
   if (msa_status st = check_tables(a->B, a->Bk, a->max_pages, a->free_cap); st != MSA_OK) return st;
   if (msa_status st = check_pool(a->num_pages); st != MSA_OK) return st;
-  MSA_REQUIRE(static_cast<int64_t>(a->B) * a->max_pages < (int64_t(1) << 31), MSA_ERR_UNSUPPORTED,
+  MSA_REQUIRE(static_cast<int64_t>(a->B) * a->max_pages < (int64_t(1) << 30), MSA_ERR_UNSUPPORTED,
               "B * max_pages = %d * %" PRId64 " too large", a->B, a->max_pages);
   MSA_REQUIRE(a->B == 0 || (a->seq_len && a->done && a->seq_pt && a->seq_len_out), MSA_ERR_INVALID_ARG,
               "seq_len, done, seq_pt and seq_len_out must be non-NULL");
@@ -830,7 +830,7 @@ msa_status msa_compact_pages(const msa_compact_args* a, msa_stream_t stream) {
   if (msa_status st = check_pool(a->num_pages); st != MSA_OK) return st;
   MSA_REQUIRE(a->free_cap >= a->num_pages, MSA_ERR_INVALID_ARG, "free_cap = %" PRId64 " is below num_pages = %" PRId64, a->free_cap,
               a->num_pages);
-  MSA_REQUIRE(static_cast<int64_t>(a->B) * a->max_pages < (int64_t(1) << 31), MSA_ERR_UNSUPPORTED,
+  MSA_REQUIRE(static_cast<int64_t>(a->B) * a->max_pages < (int64_t(1) << 30), MSA_ERR_UNSUPPORTED,
               "B * max_pages = %d * %" PRId64 " too large", a->B, a->max_pages);
   MSA_REQUIRE(a->B == 0 || (a->seq_len && a->seq_pt && a->seq_pt_out), MSA_ERR_INVALID_ARG,
               "seq_len, seq_pt and seq_pt_out must be non-NULL");

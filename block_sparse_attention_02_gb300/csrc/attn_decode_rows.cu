@@ -28,7 +28,6 @@
 #include <cuda_fp16.h>
 
 #include <cfloat>
-#include <type_traits>
 
 #include "launch_early.cuh"
 #include "msa_internal.h"

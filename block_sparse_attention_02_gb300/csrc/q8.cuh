@@ -22,12 +22,6 @@ __device__ __forceinline__ uint32_t q8_byte_for(uint32_t top) {
   return static_cast<uint32_t>(min(max(byte, kQ8First), kQ8Last));
 }
 
-// Two E4M3 bytes to fp16 (exact), the low byte in the low half.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t bytes) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(bytes)));
-  return r;
-}
 // Four E4M3 bytes to fp16 (exact): bytes 0, 1 in lo, 2, 3 in hi.
 __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t* lo, uint32_t* hi) {
   asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"

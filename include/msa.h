@@ -934,8 +934,8 @@ msa_status msa_window_attn_decode(const msa_window_decode_args *args, void *ws, 
  *     prefill, draft tokens).  K, V are pools [num_pages, Hkv, Bk, D], strides (page, g, t); seq_pt [B, max_pages],
  *     q_pos [B].  A sequence with q_pos < 0 or q_pos + S > max_pages * Bk gets O = 0 and LSE = -inf and raises
  *     MSA_DEVERR_BAD_LEN.  A page id outside [0, num_pages) is not read and its tokens are left out (MSA_DEVERR_BAD_PAGE).
- *     Pages without a seen token are not read.  Slots behind a sequence's last token may hold anything; its own tokens in
- *     a page that is read must be finite, seen or not (as 0 * inf is NaN).
+ *     Pages without a seen token are not read.  Slots behind a sequence's last token may hold anything.
+ * V of a sequence's own tokens must be finite where K is read, seen or not: a masked token's weight is 0, and 0 * inf is NaN.
  * O [B, S, Hq, D] bf16 (dense), LSE [B, S, Hq] fp32 (dense, may be NULL).  P is rounded to bf16.  No workspace.
  * softmax_scale <= 0 selects 1 / sqrt(D).  S <= 2^30 and max_pages * Bk <= 2^30, B * S < 2^31. */
 typedef struct msa_window_prefill_args {
@@ -980,7 +980,8 @@ msa_status msa_window_attn_prefill(const msa_window_prefill_args *args, msa_stre
  *     MSA_DEVERR_BAD_LEN.  A source may be named any number of times.
  *   - A fork that needs a page when none is left is left out, and so is every later one that needs one: MSA_DEVERR_NO_PAGES.
  *   - A shared page id outside [0, num_pages) is handed on uncounted: MSA_DEVERR_BAD_PAGE.
- * seq_len_out, seq_pt_out, free_count_out and page_shares_out may be the inputs.  B <= 4096, F <= 4096, num_pages <= 2^24. */
+ * seq_len_out, seq_pt_out, free_count_out and page_shares_out may be the inputs.  B <= 4096, F <= 4096, num_pages <= 2^24,
+ * F * max_pages < 2^30. */
 typedef struct msa_fork_args {
     int B, F, Bk;
     const int32_t *src;           /* [F] */
@@ -1011,7 +1012,7 @@ msa_status msa_fork_requests(const msa_fork_args *args, msa_stream_t stream);
  *   - A page id outside [0, num_pages) is dropped, one that more requests gave up than held it goes back once:
  *     MSA_DEVERR_BAD_PAGE.  Pages past free_cap are dropped: MSA_DEVERR_NO_PAGES, and so for the part of a
  *     free_count outside [0, free_cap].
- * seq_len_out, free_count_out and page_shares_out may be the inputs.  B <= 4096, num_pages <= 2^24. */
+ * seq_len_out, free_count_out and page_shares_out may be the inputs.  B <= 4096, num_pages <= 2^24, B * max_pages < 2^30. */
 typedef struct msa_release_shared_args {
     int B, Bk;
     const int32_t *seq_len;       /* [B] */
@@ -1044,7 +1045,7 @@ msa_status msa_release_shared_pages(const msa_release_shared_args *args, msa_str
  *   - A length outside [0, max_pages * Bk] counts as 0: MSA_DEVERR_BAD_LEN.  A page id outside [0, num_pages) stays as it is:
  *     MSA_DEVERR_BAD_PAGE.
  * seq_pt_out and page_shares_out may be the inputs.  free_cap >= num_pages; B <= 4096, num_pages <= 2^24,
- * B * max_pages < 2^31. */
+ * B * max_pages < 2^30. */
 typedef struct msa_compact_args {
     int B, Bk;
     const int32_t *seq_len;       /* [B] */

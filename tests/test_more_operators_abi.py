@@ -147,6 +147,9 @@ REFUSED = [
     ("msa_fork_requests", fork_args, dict(num_pages=0), INV), ("msa_fork_requests", fork_args, dict(num_pages=(1 << 24) + 1), INV),
     ("msa_fork_requests", fork_args, dict(max_pages=0), INV), ("msa_fork_requests", fork_args, dict(free_cap=-1), INV),
     ("msa_fork_requests", fork_args, dict(F=4096, max_pages=1 << 20), UNS),
+    ("msa_fork_requests", fork_args, dict(F=4096, max_pages=1 << 18), UNS),
+    ("msa_compact_pages", compact_args, dict(B=4096, max_pages=1 << 18), UNS),
+    ("msa_release_shared_pages", release_args, dict(B=4096, max_pages=1 << 18), UNS),
     *[("msa_fork_requests", fork_args, {n: None}, INV) for n in (
         "src", "dst", "seq_len", "seq_pt", "free_pages", "free_count", "page_shares", "seq_len_out", "seq_pt_out", "free_count_out",
         "page_shares_out", "copy_src", "copy_dst")],

@@ -285,3 +285,54 @@ def test_graphs_and_streams(msa):
     msa.msa_window_attn_prefill(Q, K, V, O, None, window=100, sinks=3, seq_pt=ptc, q_pos=pos, stream=s)
     s.synchronize()
     assert np.array_equal(host(O), want[0])
+
+
+def test_calls_and_graphs_share_a_workspace(msa):
+    """One zero-filled workspace, 8-bit and bf16 calls of several shapes in turn, eager and from two captured graphs."""
+    g, K, V, pt = paged([3000, 129, 0, 7000], 2, 15)
+    K, V, ptc, n = K.cuda(), V.cuda(), pt.cuda(), dev([3000, 129, 0, 7000])
+    Q = torch.randn(4, 12, D, generator=g).bfloat16().cuda()
+    cache = msa.q8_cache(K.shape[0], 2, "cuda")
+    page = torch.arange(K.shape[0] * BK, device="cuda")
+    msa.msa_cache_append_q8(*(x.transpose(1, 2).reshape(-1, 2, D).contiguous() for x in (K, V)), page, cache)
+    ws = torch.zeros(msa.msa_window_attn_decode_workspace_size(4, 2), dtype=torch.uint8, device="cuda")
+    out = [torch.zeros(4, 12, D, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    sparse = torch.stack([ptc[[0, 3]][:, :20]] * 2, 1).contiguous()                  # [2, Hkv, 20]
+
+    def all_bf16(o, ws):
+        msa.msa_window_attn_decode(Q, K, V, ptc, n, o, None, ws, window=1 << 30, scratch_zeroed=True)
+
+    def short(o, ws):
+        msa.msa_window_attn_decode(Q[1:], K, V, ptc[1:], n[1:], o[1:], None, ws, window=4000, sinks=200, scratch_zeroed=True)
+
+    def all_q8(o, ws):
+        msa.msa_dense_attn_decode_q8(Q, cache, ptc, n, o, None, ws, scratch_zeroed=True)
+
+    def some_q8(o, ws):
+        msa.msa_sparse_attn_decode_q8(Q[:2], cache, sparse, dev([[20, 7], [20, 20]]), dev([[128] * 2] * 2), o[:2], None, ws, scratch_zeroed=True)
+
+    calls = (all_bf16, short, all_q8, some_q8)
+    want = []
+    for call in calls:
+        o = torch.zeros_like(out[0])
+        call(o, torch.zeros_like(ws))
+        want.append(host(o))
+    for order in ((0, 1, 2, 3), (3, 2, 1, 0), (2, 0, 2, 1, 3, 0)):
+        for i in order:
+            out[i].zero_()
+            calls[i](out[i], ws)
+            assert np.array_equal(host(out[i]), want[i])
+    graphs = []
+    for i, j in ((2, 1), (0, 2)):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            calls[i](out[i], ws)
+            calls[j](out[j], ws)
+    for _ in range(2):
+        for graph, pair in zip(graphs, ((2, 1), (0, 2))):
+            for o in out:
+                o.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            for i in pair:
+                assert np.array_equal(host(out[i]), want[i])
