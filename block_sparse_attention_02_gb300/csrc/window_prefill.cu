@@ -5,20 +5,29 @@
 //     t <= i with t > i - window or t < sinks.
 //
 // A tile is 128 rows of one KV head: nq = 128 / G queries with all their G heads (126 rows for G = 6), row = query * G +
-// head.  So a tile's queries are few and their windows nearly one: it needs window / 128 + 1.2 blocks of 128 keys where 128
-// queries of one head need window / 128 + 2 (blocks start at multiples of 128, as pages do), and a handful of queries
-// (draft tokens) is one tile.  Two neighbouring tiles ("slots") share a stream of K/V blocks: the sinks' blocks, then those
-// from the window's first key on.
-//   S  = Q K_j^T   M = 128 rows, N = 128 keys, K = D   (tensor memory, 128 columns)
+// head.  So a tile's queries are few and their windows nearly one: it needs window / 64 + 1.3 blocks of 64 keys where 128
+// queries of one head need window / 64 + 3, and a handful of queries (draft tokens) is one tile.  Two neighbouring tiles
+// ("slots") share a stream of K/V blocks: the sinks' blocks, then those from the window's first key on.
+//   S  = Q K_j^T   M = 128 rows, N = 64 keys, K = D    (tensor memory, two buffers of 64 columns a slot)
 //   softmax (thread = row): block max, P = 2^(S * scale * log2 e - m) written back over S as bf16 pairs
-//   O += P V_j     M = 128, N = D, K = 128 keys, P read from tensor memory (128 columns)
+//   O += P V_j     M = 128, N = D, K = 64 keys, P read from tensor memory (128 columns a slot)
 // The running max m is updated lazily: O and the running sum are rescaled only when a block's max exceeds m by more than
 // 2^8, so P <= 256 and the result is exact whichever m is used.  Blocks that some row does not see whole are masked.
 //
-// Roles: warp 0 TMA of K and V (a ring of 32 KiB units, K and V apart), warp 1 tcgen05 issuer, warps 4-7 and 8-11 the two
-// slots' softmax and epilogue; a slot's softmax also sends for its next Q tile, once its last S is done.  Each slot goes
-// through its items on its own: S(j + 1) is issued right behind O(j), which reads P from the same columns (one thread's
-// MMAs run in order), and the other slot's products run meanwhile.
+// Roles: warp 0 TMA of K and V (a ring of ten 16 KiB units, K and V apart), warps 1 and 2 the slots' tcgen05 issuers, warps 4-7
+// and 8-11 their softmax and epilogue.  Each slot goes through its items on its own.  Its issuer keeps S two blocks ahead:
+// O(j - 2), then S(j) into the buffer whose P that product reads (a warp's products run in order).  An issuer's whole warp runs the
+// loop, and one lane's products and commits are under a predicate: branches on a lane would take the descriptors out of uniform
+// registers and 58 cycles a product, 170 to 190 a commit, which is more than the products themselves.
+//
+// Few tiles (SPLIT: at most one an SM): the two slots, and the CTAs of a cluster, share out the blocks of one tile and join
+// their outputs in shared memory.
+//
+// Bound: the tensor cores' operands, and tile ends.  S reads 6 KiB of shared memory a step of 16 channels, 48 cycles for 32 of products
+// (tensor memory has no room for Q: 2 x (64 + 64 + 128) columns), so a block takes 640 cycles of 512.  32,768 tokens of 8 x 6 heads, window
+// 512 / 2,048 / 8,192: 0.56 / 1.33 / 3.95 ms, which is 0.78 us a block of both slots (1,630 TFLOP/s) and 6 us a pair of tiles, for
+// masked blocks, the outputs (1.5 us), and what the slots' chains take to empty and fill.  131,072 tokens, window 2,048: 5.7 ms.
+// 128-key blocks without a second buffer: 11.5 ms; pairs of blocks (S with N = 128, no block ahead): 1.67 / 5.2 ms for 1.34 / 3.95.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -190,7 +199,7 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   uint8_t* s_q = smem;                       // [2] Q tiles
   uint8_t* s_kv = smem + 2 * kQTile;         // [kUnits] of K and V: unit 2 n is K of the CTA's n-th block, 2 n + 1 its V
 
-  __shared__ __align__(8) uint64_t bar_qfull[2], bar_qempty[2], bar_full[kUnits], bar_empty[kUnits];
+  __shared__ __align__(8) uint64_t bar_qfull[2], bar_qempty[2], bar_full[kUnits], bar_empty[kUnits], bar_end;
   // per slot; of S and P one for each of the two buffers: an S or P may be complete before the one before it is looked at
   __shared__ __align__(8) uint64_t bar_sfull[2][2], bar_pready[2][2], bar_odone[2][2], bar_drain[2];   // (odone: of an item's last two O)
   __shared__ uint32_t s_tmem;
@@ -209,6 +218,7 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       for (int k = 0; k < 2; ++k) mbar_init(&bar_odone[i][k], 1);
       mbar_init(&bar_drain[i], 1);
     }
+    mbar_init(&bar_end, 1);
     s_abort = 0;
     fence_mbar_init();
   }
@@ -230,7 +240,7 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   if (warp == 0) {
     // ===================== TMA producer of K and V (warp-uniform loop, lane 0 issues) =====================
     int n = 0, st = 0;                       // blocks sent for; the next unit and its phase
-    uint32_t phase = 0;
+    uint32_t phase = 0, end_phase = 0;
     bool ok = true;
     for (int it = it0; it < p.n_items && ok; it += stride) {
       const Item x = item_of<SPLIT>(p, it);
@@ -240,6 +250,9 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         if (p.paged && j0 + lane < x.blocks) pg = p.seq_pt[x.b * p.max_pages + x.block(j0 + lane) * kKeys / kBk];
         for (int i = 0; i < 32 && j0 + i < x.blocks; ++i, ++n) {
           const int page = __shfl_sync(0xffffffffu, pg, i);
+          // Slots of a page behind the sequence's last token may hold anything, and 0 * NaN is NaN: V's rows there become zeros
+          // before the unit is handed on.  (Only a sequence's last block waits for this.)
+          const bool ends = p.paged && j0 + i + 1 == x.blocks && x.end - x.block(j0 + i) * kKeys < kKeys;
           int go = 1;
           if (lane == 0) {
             const bool gone = p.paged && (page < 0 || page >= p.num_pages);
@@ -250,11 +263,23 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
               go = wait(&bar_empty[st], phase ^ 1, abort_flag, p.dev_err);
               if (!go) break;
               if (kv == 0) s_gone[n % kNotes] = gone;
-              mbar_arrive_expect_tx(&bar_full[st], kUnit);
-              tma_load_5d(s_kv + st * kUnit, kv ? &vmap : &kmap, &bar_full[st], 0, c1, 0, x.g, c4);
+              uint64_t* bar = kv && ends ? &bar_end : &bar_full[st];
+              mbar_arrive_expect_tx(bar, kUnit);
+              tma_load_5d(s_kv + st * kUnit, kv ? &vmap : &kmap, bar, 0, c1, 0, x.g, c4);
               if (++st == kUnits) { st = 0; phase ^= 1; }
             }
             if (gone) report(p.dev_err, MSA_DEVERR_BAD_PAGE);
+          }
+          if (ends) {
+            if (lane == 0 && go) go = wait(&bar_end, end_phase, abort_flag, p.dev_err);
+            end_phase ^= 1;
+            const int unit = __shfl_sync(0xffffffffu, (st == 0 ? kUnits : st) - 1, 0), all = __shfl_sync(0xffffffffu, go, 0);
+            __syncwarp();
+            for (int e = (x.end - x.block(j0 + i) * kKeys) * 8 + lane; all && e < kKeys * 8; e += 32)   // 16 bytes of each half
+              for (int half = 0; half < 2; ++half) reinterpret_cast<uint4*>(s_kv + unit * kUnit + half * kHalf)[e] = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && go) mbar_arrive(&bar_full[unit]);
           }
           if (!__shfl_sync(0xffffffffu, go, 0)) {
             ok = false;
@@ -271,7 +296,7 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     }
     __syncwarp();
   } else if (warp < 3) {
-    // ===================== tcgen05 issuer of slot s (warp-uniform loop, lane 0 issues) =====================
+    // ===================== tcgen05 issuer of slot s (warp-uniform loop, an elected lane issues) =====================
     // Step j of an item: O(j - 2), then S(j) into the buffer whose P that O reads.  So S is two blocks ahead and the
     // softmax always has one to work on.
     const int s = warp - 1;
@@ -333,14 +358,6 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           ok = wait(&bar_full[sv], pv, abort_flag, p.dev_err) && wait(&bar_pready[s][buf], ((n + j - 2) >> 1) & 1, abort_flag, p.dev_err);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          if (j == blocks + 1 && p.paged) {
-            // slots behind the sequence's last token may hold anything, and 0 * NaN is NaN: zeros (where it ends, in the last block)
-            const int live = x.end - x.block(SPLIT ? 2 * (j - 2) + s : j - 2) * kKeys;
-            for (int i = max(live, 0) * 8 + lane; i < kKeys * 8; i += 32)
-              for (int half = 0; half < 2; ++half) reinterpret_cast<uint4*>(s_kv + sv * kUnit + half * kHalf)[i] = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)
@@ -546,8 +563,13 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           for (int e = 0; e < 4; ++e) {
             const int k = c * 8 + e * 2;
             w[c][e] = pack_bf16x2(__uint_as_float(o[k >> 5][k & 31]) * inv, __uint_as_float(o[k >> 5][(k & 31) + 1]) * inv);
-            if (l == 0.f) w[c][e] = 0;                     // (tensor memory may hold anything where nothing was added)
           }
+        if (blocks == 0) {                                 // (tensor memory holds anything)
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[c][e] = 0;
+        }
 #pragma unroll
         for (int bit = 1; bit < 8; bit <<= 1) {
           const bool high = (lane & bit) != 0;

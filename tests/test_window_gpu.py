@@ -297,7 +297,7 @@ def test_calls_and_graphs_share_a_workspace(msa):
     msa.msa_cache_append_q8(*(x.transpose(1, 2).reshape(-1, 2, D).contiguous() for x in (K, V)), page, cache)
     ws = torch.zeros(msa.msa_window_attn_decode_workspace_size(4, 2), dtype=torch.uint8, device="cuda")
     out = [torch.zeros(4, 12, D, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
-    sparse = torch.stack([ptc[[0, 3]][:, :20]] * 2, 1).contiguous()                  # [2, Hkv, 20]
+    sparse = ptc[[0, 0, 3, 3], :20].contiguous()                                     # [2 * Hkv, 20]
 
     def all_bf16(o, ws):
         msa.msa_window_attn_decode(Q, K, V, ptc, n, o, None, ws, window=1 << 30, scratch_zeroed=True)
@@ -309,7 +309,7 @@ def test_calls_and_graphs_share_a_workspace(msa):
         msa.msa_dense_attn_decode_q8(Q, cache, ptc, n, o, None, ws, scratch_zeroed=True)
 
     def some_q8(o, ws):
-        msa.msa_sparse_attn_decode_q8(Q[:2], cache, sparse, dev([[20, 7], [20, 20]]), dev([[128] * 2] * 2), o[:2], None, ws, scratch_zeroed=True)
+        msa.msa_sparse_attn_decode_q8(Q[:2], cache, sparse, dev([20, 7, 20, 20]), dev([128] * 4), o[:2], None, ws, scratch_zeroed=True)
 
     calls = (all_bf16, short, all_q8, some_q8)
     want = []
