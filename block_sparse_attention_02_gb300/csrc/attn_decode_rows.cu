@@ -24,6 +24,11 @@
 // shared memory; parts of a row are joined in shared memory, a cluster's shared memory, or through the workspace by the
 // last CTA to arrive.  A window's pages are a list of their own: the sinks' pages, then those from the window's first
 // token on; tiles of them without a visible token are not fetched.
+//
+// Bound.  HBM for long rows: 8 x 60,001 tokens of eight heads 150 us (6.5 TB/s, 97 % of a copy), 1,048,576 tokens 317 us (100 %); the
+// conversions take a third of the issue slots (4 bits: two thirds).  A window of 4,096 over 64 sequences 69 us (84 %): rows'
+// starts and ends.  Few rows are a launch, lengths, page ids, three to four tiles and a join, one after another: 8 x 16
+// selected pages 10.6 us (floor 4.9), a window of 2,048 over 8 sequences of bf16 16.2 (10.0).
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 

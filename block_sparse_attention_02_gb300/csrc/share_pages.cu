@@ -6,14 +6,15 @@
 // holders beyond the first, so that pages given out by msa_plan_step (0) need nothing, and a page goes back on the stack
 // when the count would fall below 0.
 //
-// Each of the three index kernels is one CTA, or for larger pools and tables one thread-block cluster: it forms the sums over
+// Each of the three index kernels is one thread-block cluster, or one CTA for small pools and tables: it forms the sums over
 // the requests for itself, goes through the table entries and the pages side by side, and meets at a barrier where one step
 // needs all of the step before (counts before the search for freed pages, marks before ranks, ranks before the table).  So a
 // call is one launch without scratch, lengths and counts may be updated in place, and whatever is counted by atomics is a sum,
 // the same in any order; freed pages and moves are ordered by page number.
 //
-// Bound: latency (the barriers, of which a cluster's takes half a microsecond; dependent loads of lengths, tables and counts).
-// The copies are bound by HBM.
+// Bound: latency (the barriers, of which a cluster's takes half a microsecond; dependent loads of lengths, tables and counts): release
+// and fork of 64 requests in a pool of 3,463 pages 6.1 and 5.0 us, compaction of 2,048 pages 8.8.  The copies are bound by HBM: 512 pages of
+// 640 KB 107 us, 93 % of a copy's rate.
 #include <cooperative_groups.h>
 
 #include <climits>
@@ -30,7 +31,10 @@ namespace {
 constexpr int kAlone = 1024, kThreads = 512;              // threads of a CTA alone, and of a cluster's
 constexpr int kCluster = 8;                                // CTAs (the portable maximum)
 constexpr int kPer = kMaxDecodeBatch / kThreads;           // requests (or forks) of a thread in the sums, at most
-constexpr int kAloneItems = 1024;                          // entries or pages up to which a CTA works alone
+// Entries or pages up to which one CTA releases or compacts (compaction of 512 / 1,024 / 1,536 / 4,096 pages 6.1 / 7.1 / 8.7 / 14.4 us
+// for a cluster's 7.4 / 8.4 / 8.7 / 9.0, release of 1,024 / 8,192 5.4 / 12.7 for 5.3 / 6.2).  Forks, with one barrier, are a
+// cluster's at every size (128 pages 4.8 for 6.1).
+constexpr int kAloneItems = 1024;
 constexpr int kOwn = 4;                                    // pages of a thread that it looks at together
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 4;
@@ -122,7 +126,7 @@ __device__ __forceinline__ void for_entries(const int* first, int B, int total, 
   }
 }
 
-__global__ void __launch_bounds__(kAlone) fork_kernel(const msa_fork_args p) {
+__global__ void __launch_bounds__(kThreads) fork_kernel(const msa_fork_args p) {
   wait_for_stream();
   extern __shared__ int s_mem[];
   int* s_first = s_mem;                     // [F + 1] shared table entries of the forks before
@@ -450,14 +454,12 @@ __global__ void __launch_bounds__(kAlone) compact_kernel(const msa_compact_args 
   if (err != 0) report(p.dev_err, err);
 }
 
-// One CTA, or one cluster where there are many entries and pages.
 template <class Args>
-msa_status launch_team(void (*kernel)(const Args), const Args& a, int64_t items, size_t smem, cudaStream_t stream, const char* what) {
+msa_status launch_team(void (*kernel)(const Args), const Args& a, bool alone, size_t smem, cudaStream_t stream, const char* what) {
   if (smem > (40u << 10)) {                 // with the sums' own shared memory past the 48 KiB default
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return cuda_fail(e, what);
   }
-  const bool alone = items <= kAloneItems;
   const int ctas = alone ? 1 : kCluster;
   const cudaError_t e = launch_early(kernel, ctas, alone ? kAlone : kThreads, smem, stream, ctas, a);
   if (e != cudaSuccess) return cuda_fail(e, what);
@@ -522,18 +524,18 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_c
 
 msa_status launch_fork(const msa_fork_args& a, cudaStream_t stream) {
   const size_t smem = (3 * static_cast<size_t>(a.F) + a.B + 1) * sizeof(int);
-  return launch_team(fork_kernel, a, std::max<int64_t>(static_cast<int64_t>(a.F) * a.max_pages / 4, a.num_pages), smem, stream, "fork_kernel launch");
+  return launch_team(fork_kernel, a, false, smem, stream, "fork_kernel launch");
 }
 
 msa_status launch_release_shared(const msa_release_shared_args& a, cudaStream_t stream) {
   const size_t smem = (static_cast<size_t>(a.B) + 1) * sizeof(int);
-  return launch_team(release_shared_kernel, a, std::max<int64_t>(static_cast<int64_t>(a.B) * a.max_pages / 8, a.num_pages), smem, stream,
-                        "release_shared_kernel launch");
+  const bool alone = std::max<int64_t>(static_cast<int64_t>(a.B) * a.max_pages / 8, a.num_pages) <= kAloneItems;
+  return launch_team(release_shared_kernel, a, alone, smem, stream, "release_shared_kernel launch");
 }
 
 msa_status launch_compact(const msa_compact_args& a, cudaStream_t stream) {
   const size_t smem = (static_cast<size_t>(a.B) + 1) * sizeof(int);
-  return launch_team(compact_kernel, a, a.num_pages, smem, stream, "compact_kernel launch");
+  return launch_team(compact_kernel, a, a.num_pages <= kAloneItems, smem, stream, "compact_kernel launch");
 }
 
 msa_status launch_copy_pages(const msa_copy_pages_args& a, cudaStream_t stream) {
