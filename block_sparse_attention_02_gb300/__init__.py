@@ -674,7 +674,7 @@ def msa_fork_requests(src: torch.Tensor, dst: torch.Tensor, seq_len: torch.Tenso
     """Request dst[i] goes on from the cached tokens of request src[i] (see msa.h): full pages are shared, of a page that
     is partly filled the copy is named in copy_src, copy_dst for ``msa_copy_pages``.
 
-    src, dst, copy_src, copy_dst [F] int32 (src < 0: left out); seq_len [B], seq_pt [B,max_pages], free_pages [F] and
+    src, dst, copy_src, copy_dst [F] int32 (src < 0: left out); seq_len [B], seq_pt [B,max_pages], free_pages [cap] and
     free_count [1] as in ``msa_plan_step``; page_shares [num_pages] int32, a page's holders beyond the first (0 at the
     start).  The outputs may be the inputs.
     """
