@@ -197,7 +197,11 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* s_q = smem;                       // [2] Q tiles
-  uint8_t* s_kv = smem + 2 * kQTile;         // [kUnits] of K and V: unit 2 n is K of the CTA's n-th block, 2 n + 1 its V
+  // [kRings][kRing] units of K and V: of a ring's n-th block unit 2 n % kRing is K, the next one V.  With SPLIT, where the slots
+  // take the blocks in turn, each has a ring of its own: in a common one of ten a unit would go from slot to slot, and a slot
+  // that waits for its phase would take the phase before, still under way for the other slot, for the one before that.
+  constexpr int kRings = SPLIT ? 2 : 1, kRing = kUnits / kRings;
+  uint8_t* s_kv = smem + 2 * kQTile;
 
   __shared__ __align__(8) uint64_t bar_qfull[2], bar_qempty[2], bar_full[kUnits], bar_empty[kUnits], bar_end;
   // per slot; of S and P one for each of the two buffers: an S or P may be complete before the one before it is looked at
@@ -239,8 +243,8 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
 
   if (warp == 0) {
     // ===================== TMA producer of K and V (warp-uniform loop, lane 0 issues) =====================
-    int n = 0, st = 0;                       // blocks sent for; the next unit and its phase
-    uint32_t phase = 0, end_phase = 0;
+    int n = 0, sent = 0;                     // blocks and units sent for
+    uint32_t end_phase = 0;
     bool ok = true;
     for (int it = it0; it < p.n_items && ok; it += stride) {
       const Item x = item_of<SPLIT>(p, it);
@@ -253,27 +257,29 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           // Slots of a page behind the sequence's last token may hold anything, and 0 * NaN is NaN: V's rows there become zeros
           // before the unit is handed on.  (Only a sequence's last block waits for this.)
           const bool ends = p.paged && j0 + i + 1 == x.blocks && x.end - x.block(j0 + i) * kKeys < kKeys;
-          int go = 1;
+          int go = 1, st = 0;
           if (lane == 0) {
             const bool gone = p.paged && (page < 0 || page >= p.num_pages);
             // a page that there is not is read as zeros: from past the end of the pool
             const int t = x.block(j0 + i) * kKeys, c1 = p.paged ? t % kBk : t;
             const int c4 = p.paged ? (gone ? static_cast<int>(p.num_pages) : page) : x.b;
             for (int kv = 0; kv < 2 && go; ++kv) {
-              go = wait(&bar_empty[st], phase ^ 1, abort_flag, p.dev_err);
+              const int u = n / kRings * 2 + kv;               // of the block's ring
+              st = n % kRings * kRing + u % kRing;
+              go = wait(&bar_empty[st], (u / kRing & 1) ^ 1, abort_flag, p.dev_err);
               if (!go) break;
               if (kv == 0) s_gone[n % kNotes] = gone;
               uint64_t* bar = kv && ends ? &bar_end : &bar_full[st];
               mbar_arrive_expect_tx(bar, kUnit);
               tma_load_5d(s_kv + st * kUnit, kv ? &vmap : &kmap, bar, 0, c1, 0, x.g, c4);
-              if (++st == kUnits) { st = 0; phase ^= 1; }
+              ++sent;
             }
             if (gone) report(p.dev_err, MSA_DEVERR_BAD_PAGE);
           }
           if (ends) {
             if (lane == 0 && go) go = wait(&bar_end, end_phase, abort_flag, p.dev_err);
             end_phase ^= 1;
-            const int unit = __shfl_sync(0xffffffffu, (st == 0 ? kUnits : st) - 1, 0), all = __shfl_sync(0xffffffffu, go, 0);
+            const int unit = __shfl_sync(0xffffffffu, st, 0), all = __shfl_sync(0xffffffffu, go, 0);
             __syncwarp();
             for (int e = (x.end - x.block(j0 + i) * kKeys) * 8 + lane; all && e < kKeys * 8; e += 32)   // 16 bytes of each half
               for (int half = 0; half < 2; ++half) reinterpret_cast<uint4*>(s_kv + unit * kUnit + half * kHalf)[e] = make_uint4(0, 0, 0, 0);
@@ -290,9 +296,10 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     }
     if (lane == 0 && *abort_flag) {          // let loads in flight land before the CTA exits
       const uint64_t t0 = global_timer_ns();
-      for (int u = max(0, 2 * n - kUnits); u < 2 * n; ++u)
-        while (!mbar_try_wait(&bar_full[u % kUnits], (u / kUnits) & 1) && global_timer_ns() - t0 < MSA_WAIT_LIMIT_NS) {
-        }
+      for (int k = 0; k < kRings; ++k)
+        for (int all = (sent / 2 + kRings - 1 - k) / kRings * 2 + (sent / 2 % kRings == k ? sent & 1 : 0), u = max(0, all - kRing); u < all; ++u)
+          while (!mbar_try_wait(&bar_full[k * kRing + u % kRing], (u / kRing) & 1) && global_timer_ns() - t0 < MSA_WAIT_LIMIT_NS) {
+          }
     }
     __syncwarp();
   } else if (warp < 3) {
@@ -305,19 +312,19 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     const uint32_t sp = tmem + s * 256, out = sp + 128;
     const uint64_t q_desc = sdesc_sw128(smem_u32(s_q + s * kQTile), 16, 1024), k_desc = sdesc_sw128(smem_u32(s_kv), 16, 1024),
                    v_desc = sdesc_sw128(smem_u32(s_kv), kHalf, 1024);
-    // units of the next K and V, and their phases; SPLIT: the slots take the blocks in turn
-    int sk = SPLIT ? 2 * s : 0, sv = sk + 1;
+    // units of the next K and V, and their phases
+    const int ring_end = (SPLIT ? s + 1 : 1) * kRing;
+    int sk = ring_end - kRing, sv = sk + 1;
     uint32_t pk = 0, pv = 0;
-    constexpr int kStep = SPLIT ? 4 : 2;
     int n = 0, items = 0, sent = 0;          // blocks and items done, Q tiles sent for
     bool ok = true;
     auto next_k = [&] {
-      sk += kStep;
-      if (sk >= kUnits) { sk -= kUnits; pk ^= 1; }
+      sk += 2;
+      if (sk >= ring_end) { sk -= kRing; pk ^= 1; }
     };
     auto next_v = [&] {
-      sv += kStep;
-      if (sv >= kUnits) { sv -= kUnits; pv ^= 1; }
+      sv += 2;
+      if (sv >= ring_end) { sv -= kRing; pv ^= 1; }
     };
     // the Q tile of this slot's first item from `it` on that has blocks, once the last S of the one before is done
     auto send_q = [&](int it) {

@@ -336,3 +336,22 @@ def test_calls_and_graphs_share_a_workspace(msa):
             torch.cuda.synchronize()
             for i in pair:
                 assert np.array_equal(host(out[i]), want[i])
+
+
+def test_few_tiles_many_launches(msa):
+    """Draft tokens over pools whose first reads miss every cache: a K/V block that lands later than the other slot's blocks
+    behind it is waited for all the same.  (One launch in some 20,000 had run into the wait's limit.)"""
+    B, S, per = 8, 4, 400
+    g = torch.Generator(device="cuda").manual_seed(16)
+    pools = [[torch.randn(B * per, 8, BK, D, generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2)] for _ in range(2)]
+    pt = torch.randperm(B * per, generator=g, device="cuda").int().view(B, per)
+    Q, pos, e = torch.randn(B, S, 48, D, generator=g, device="cuda").bfloat16(), dev([per * BK - S] * B), dev([0])
+    out = [(torch.empty_like(Q), torch.empty(B, S, 48, device="cuda")) for _ in range(2)]
+    want = []
+    for i in range(40000):
+        (K, V), (O, LSE) = pools[i % 2], out[i % 2]
+        msa.msa_window_attn_prefill(Q, K, V, O, LSE, window=2048, sinks=4, seq_pt=pt, q_pos=pos, dev_err=e)
+        if i < 2:
+            want.append((O.clone(), LSE.clone()))
+        if i % 4000 >= 3998:
+            assert int(e.item()) == 0 and torch.equal(O, want[i % 2][0]) and torch.equal(LSE, want[i % 2][1])
