@@ -14,20 +14,25 @@
 // The running max m is updated lazily: O and the running sum are rescaled only when a block's max exceeds m by more than
 // 2^8, so P <= 256 and the result is exact whichever m is used.  Blocks that some row does not see whole are masked.
 //
-// Roles: warp 0 TMA of K and V (a ring of ten 16 KiB units, K and V apart), warps 1 and 2 the slots' tcgen05 issuers, warps 4-7
-// and 8-11 their softmax and epilogue.  Each slot goes through its items on its own.  Its issuer keeps S two blocks ahead:
+// Roles: warp 0 TMA of K and V (a ring of eight 16 KiB units, K and V apart; ten are no faster), warps 1 and 2 the slots' tcgen05
+// issuers, warps 4-7 and 8-11 their softmax, warps 12-15 the outputs of both.  Each slot goes through its items on its own.  Its issuer keeps S two blocks ahead:
 // O(j - 2), then S(j) into the buffer whose P that product reads (a warp's products run in order).  An issuer's whole warp runs the
 // loop, and one lane's products and commits are under a predicate: branches on a lane would take the descriptors out of uniform
 // registers and 58 cycles a product, 170 to 190 a commit, which is more than the products themselves.
 //
+// The softmax warps hold an item's first P back until the outputs of the item before are read.  What is rare in their
+// loop (rescaling) is not unrolled, so that it fits in the 128 registers of 512 threads.
+//
 // Few tiles (SPLIT: at most one an SM): the two slots, and the CTAs of a cluster, share out the blocks of one tile and join
-// their outputs in shared memory.
+// their outputs in shared memory; the softmax warps write them.
 //
 // Bound: the tensor cores' operands, and tile ends.  S reads 6 KiB of shared memory a step of 16 channels, 48 cycles for 32 of products
 // (tensor memory has no room for Q: 2 x (64 + 64 + 128) columns), so a block takes 640 cycles of 512.  32,768 tokens of 8 x 6 heads, window
-// 512 / 2,048 / 8,192: 0.56 / 1.33 / 3.95 ms, which is 0.78 us a block of both slots (1,630 TFLOP/s) and 6 us a pair of tiles, for
-// masked blocks, the outputs (1.5 us), and what the slots' chains take to empty and fill.  131,072 tokens, window 2,048: 5.7 ms.
-// 128-key blocks without a second buffer: 11.5 ms; pairs of blocks (S with N = 128, no block ahead): 1.67 / 5.2 ms for 1.34 / 3.95.
+// 512 / 2,048 / 8,192: 0.51 / 1.26 / 3.92 ms, which is 0.78 us a block of both slots (1,630 TFLOP/s) and 5 us a pair of tiles: masked
+// blocks (three of a tile; 0.5 us), the wait for the next Q (1 us), and what the slots' chains take to empty and fill.
+// With the outputs written by the softmax warps 0.55 / 1.31 / 3.94 ms, masks by comparisons instead of bits 0.52 / 1.27 / 3.92.
+// 128-key blocks without a second buffer: 131,072 tokens in 11.5 ms for 5.5; pairs of blocks (S with N = 128, no block ahead): 1.67 / 5.2 ms
+// where this form took 1.34 / 3.95.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -46,11 +51,15 @@ constexpr int kQHalf = 128 * 64 * 2;         // 16 KiB: 128 rows x 64 bf16
 constexpr int kQTile = 2 * kQHalf;
 constexpr int kHalf = kKeys * 64 * 2;        // 8 KiB: a block's rows x 64 bf16
 constexpr int kUnit = 2 * kHalf;             // 16 KiB: K or V of a block
-constexpr int kUnits = 10;                   // of K and V in shared memory
+// Units of K and V in shared memory.  Few tiles wait for HBM and gain by more (8 x 4 queries 19.9 us for 21.8 with eight), many do not
+// (131,072 tokens 5.47 ms with either).
+constexpr int units_of(bool split) { return split ? 10 : 8; }
 constexpr int kMaxSplit = 8;                 // CTAs of an item
+static_assert(units_of(true) * kUnit >= 2 * 128 * kD * 4, "room for two slots' outputs");
 constexpr int kNotes = 16;                   // blocks whose page's state is kept (more than are in flight)
-static_assert(kUnits * kUnit >= 2 * 128 * kD * 4 + 2 * 2 * 128 * 4, "room for two slots' outputs");
-constexpr int kThreads = 384;                // w0 TMA of K and V, w1-2 the slots' issuers, w4-7 slot 0, w8-11 slot 1
+
+// w0 TMA of K and V, w1-2 the slots' issuers, w4-7 slot 0, w8-11 slot 1, w12-15 outputs
+constexpr int kWorkers = 384, kAll = 512;
 constexpr int kTmemCols = 512;               // per slot: two of S / P (64 columns each) and O (128 columns)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -155,7 +164,7 @@ __device__ __forceinline__ void commit_elect(uint64_t* bar) {
 }
 // A bounded wait as mbar_wait, which reads the clock only after some tries: a read takes about as long as a block's products,
 // and most waits here are shorter.
-__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* dev_err) {
+__device__ __forceinline__ bool wait_here(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* dev_err) {
   uint64_t since = 0;
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -169,6 +178,9 @@ __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile 
       return false;
     }
   }
+}
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* dev_err) {
+  return wait_here(bar, parity, abort_flag, dev_err);
 }
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* dev_err) {
   return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag, dev_err);
@@ -191,26 +203,27 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 
 template <bool SPLIT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(SPLIT ? kWorkers : kAll, 1)
 window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap, const Params p) {
+  constexpr int kThreads = SPLIT ? kWorkers : kAll, kUnits = units_of(SPLIT), kRings = SPLIT ? 2 : 1, kRing = kUnits / kRings;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* s_q = smem;                       // [2] Q tiles
   // [kRings][kRing] units of K and V: of a ring's n-th block unit 2 n % kRing is K, the next one V.  With SPLIT, where the slots
   // take the blocks in turn, each has a ring of its own: in a common one of ten a unit would go from slot to slot, and a slot
   // that waits for its phase would take the phase before, still under way for the other slot, for the one before that.
-  constexpr int kRings = SPLIT ? 2 : 1, kRing = kUnits / kRings;
   uint8_t* s_kv = smem + 2 * kQTile;
 
   __shared__ __align__(8) uint64_t bar_qfull[2], bar_qempty[2], bar_full[kUnits], bar_empty[kUnits], bar_end;
   // per slot; of S and P one for each of the two buffers: an S or P may be complete before the one before it is looked at
-  __shared__ __align__(8) uint64_t bar_sfull[2][2], bar_pready[2][2], bar_odone[2][2], bar_drain[2];   // (odone: of an item's last two O)
+  __shared__ __align__(8) uint64_t bar_sfull[2][2], bar_pready[2][2], bar_odone[2][2], bar_drain[2], bar_stat[2], bar_ofree[2];   // (odone: of an item's last two O)
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ volatile int s_gone[kNotes];    // of block n % kNotes: no such page
-  // SPLIT, at the end: the slots' outputs take the units' place, and behind them each row's max and sum
-  float(*s_ml)[2][128] = reinterpret_cast<float(*)[2][128]>(s_kv + 2 * 128 * kD * sizeof(float));
+  __shared__ float s_inv[2][128];            // of a slot's finished tile: 1 / the rows' sums (0 of an empty row)
+  // SPLIT, at the end: the slots' outputs take the units' place, each row's max and sum that of Q
+  float(*s_ml)[2][128] = reinterpret_cast<float(*)[2][128]>(s_q);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -221,6 +234,8 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       for (int k = 0; k < 2; ++k) { mbar_init(&bar_sfull[i][k], 1); mbar_init(&bar_pready[i][k], 4); }
       for (int k = 0; k < 2; ++k) mbar_init(&bar_odone[i][k], 1);
       mbar_init(&bar_drain[i], 1);
+      mbar_init(&bar_stat[i], 4);
+      mbar_init(&bar_ofree[i], 4);
     }
     mbar_init(&bar_end, 1);
     s_abort = 0;
@@ -404,13 +419,12 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       }                                      // (a load in flight lands before the CTA exits)
     }
     __syncwarp();
-  } else if (warp >= 4) {
-    // ===================== softmax + epilogue of slot s (thread = row) =====================
+  } else if (warp >= 4 && warp < 12) {
+    // ===================== softmax of slot s (thread = row) =====================
     const int s = (warp >> 2) - 1;
     const int q = warp & 3;
     const int r = q * 32 + lane;
-    const int query = r / p.G, head = r - query * p.G;
-    const int per_query = 65536 / p.G + 1;                 // (row * per_query) >> 16 is row / G
+    const int query = r / p.G;
     const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
     const uint32_t sbase = tmem + lane_addr + s * 256;     // two buffers: S, then P (bf16 pairs) in its first 32 columns
     const uint32_t obase = sbase + 128;
@@ -423,8 +437,6 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       n += x.blocks;
       if (s >= x.tiles) continue;
       const int row0 = x.q0 + (SPLIT ? 0 : s * p.nq);      // the tile's first query, of the sequence's S
-      const int row = row0 + query;
-      const bool real = query < p.nq && row < p.S;
       const int low = x.pos + row0 - x.q0, high = low + p.nq - 1, i = low + query;   // positions: of the tile, and this row's
       const int blocks = own(x, s);
       float m = -INFINITY, l = 0.f;
@@ -440,15 +452,17 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         tmem_ld_wait();
         const bool gone = p.paged && s_gone[(n0 + listed) % kNotes] != 0;
         if (gone || t0 + kKeys - 1 > low || (t0 <= high - p.window && t0 + kKeys > p.sinks)) {
-          // some row does not see all of it: columns c <= last, and c >= from or c < sinks
+          // some row does not see all of it: columns c <= last, and c >= from or c < sinks; a bit each
           const int last = gone ? -1 : i - t0, from = i - p.window + 1 - t0, sinks = p.sinks - t0;
+          auto below = [](int n) { return n >= kKeys ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1; };
+          const uint64_t seen = below(last + 1) & (~below(from) | below(sinks));
 #pragma unroll
-          for (int cc = 0; cc < 2; ++cc)
+          for (int cc = 0; cc < 2; ++cc) {
+            const uint32_t bits = static_cast<uint32_t>(seen >> (32 * cc));
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int c = cc * 32 + e;
-              if (c > last || (c < from && c >= sinks)) v[cc][e] = 0xff800000u;   // -inf
-            }
+            for (int e = 0; e < 32; ++e)
+              if ((bits >> e & 1) == 0) v[cc][e] = 0xff800000u;   // -inf
+          }
         }
         float mx[4];
 #pragma unroll
@@ -467,11 +481,12 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           l *= alpha;
           if (j > 0) {
             // O(j - 1) is done when S(j + 1), issued right behind it, is; behind the last S there is a commit for it
-            const bool ok_o = j + 1 < blocks ? wait(&bar_sfull[s][(nS + 1) & 1], ((nS + 1) >> 1) & 1, abort_flag, p.dev_err)
-                                               : wait(&bar_odone[s][0], nI & 1, abort_flag, p.dev_err);
+            // (not a call: all of the scores are in registers)
+            const bool next = j + 1 < blocks;
+            const bool ok_o = wait_here(next ? &bar_sfull[s][(nS + 1) & 1] : &bar_odone[s][0], (next ? (nS + 1) >> 1 : nI) & 1, abort_flag, p.dev_err);
             if (!__all_sync(0xffffffffu, ok_o)) { alive = false; break; }
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1                                           // (rare; the scores are in registers)
             for (int cc = 0; cc < 4; ++cc) {
               uint32_t o[32];
               tmem_ld32(obase + cc * 32, o);
@@ -512,6 +527,11 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         unpair(add2(sum2[0], sum2[1]), &a, &b);
         l += a + b;
         tmem_st_wait();
+        if (!SPLIT && j == 0 && nI > 0) {                  // the tile before is read
+          const bool ok_o = wait(&bar_ofree[s], (nI & 1) ^ 1, abort_flag, p.dev_err);
+          if (!__all_sync(0xffffffffu, ok_o)) { alive = false; break; }
+          tc_fence_after();
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar_pready[s][nS & 1]);
@@ -544,65 +564,85 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         break;
       }
       if (blocks > 0) {
-        const bool ok_o = wait(&bar_odone[s][1], nI & 1, abort_flag, p.dev_err);
         ++nI;
-        if (!__all_sync(0xffffffffu, ok_o)) break;
-        tc_fence_after();
-      } else if (r == 0) {
-        report(p.dev_err, MSA_DEVERR_BAD_LEN);
+        s_inv[s][r] = l == 0.f ? 0.f : 1.0f / l;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_stat[s]);
       }
-      const float inv = l == 0.f ? 0.f : 1.0f / l;
-      const int64_t at = (static_cast<int64_t>(x.b) * p.S + row) * p.Hq + x.g * p.G + head;
-      // A row's 256 bytes are one thread's; written so, each store would touch 32 lines.  Eight lanes exchange their rows'
-      // 16-byte chunks (an 8 x 8 transposition), so that they write 128 bytes of one row together.
-      const int queries = min(p.nq, p.S - row0);
-      __nv_bfloat16* tile = p.O + ((static_cast<int64_t>(x.b) * p.S + row0) * p.Hq + x.g * p.G) * kD + (lane & 7) * 8;
+      if (p.LSE != nullptr && query < p.nq && row0 + query < p.S)
+        p.LSE[(static_cast<int64_t>(x.b) * p.S + row0 + query) * p.Hq + x.g * p.G + r - query * p.G] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    }
+  } else if (!SPLIT && warp >= 12) {
+    // ===================== outputs: O / l in bf16, LSE (thread = row) =====================
+    const int q = warp & 3;
+    const int r = q * 32 + lane;
+    const int per_query = 65536 / p.G + 1;                 // (row * per_query) >> 16 is row / G
+    int nI[2] = {0, 0};
+    bool alive = true;
+    for (int it = it0; it < p.n_items && alive; it += stride) {
+      const Item x = item_of<SPLIT>(p, it);
 #pragma unroll
-      for (int cc = 0; cc < 2; ++cc) {
-        uint32_t o[2][32];
-        tmem_ld32(obase + cc * 64, o[0]);
-        tmem_ld32(obase + cc * 64 + 32, o[1]);
-        tmem_ld_wait();
-        uint32_t w[8][4];
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int k = c * 8 + e * 2;
-            w[c][e] = pack_bf16x2(__uint_as_float(o[k >> 5][k & 31]) * inv, __uint_as_float(o[k >> 5][(k & 31) + 1]) * inv);
-          }
-        if (blocks == 0) {                                 // (tensor memory holds anything)
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[c][e] = 0;
+      for (int s = 0; s < 2; ++s) {
+        if (s >= x.tiles) break;
+        const int row0 = x.q0 + s * p.nq;                  // the tile's first query, of the sequence's S
+        const uint32_t obase = tmem + (static_cast<uint32_t>(q * 32) << 16) + s * 256 + 128;
+        float inv = 0.f;
+        if (x.blocks > 0) {
+          const bool ok_o = wait(&bar_stat[s], nI[s] & 1, abort_flag, p.dev_err) && wait(&bar_odone[s][1], nI[s] & 1, abort_flag, p.dev_err);
+          if (!__all_sync(0xffffffffu, ok_o)) { alive = false; break; }
+          ++nI[s];
+          inv = s_inv[s][r];
+          tc_fence_after();
+        } else if (r == 0) {
+          report(p.dev_err, MSA_DEVERR_BAD_LEN);
         }
+        uint32_t w[2][8][4];
 #pragma unroll
-        for (int bit = 1; bit < 8; bit <<= 1) {
-          const bool high = (lane & bit) != 0;
+        for (int cc = 0; cc < 4; ++cc) {
+          uint32_t o[32];
+          tmem_ld32(obase + cc * 32, o);
+          tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            if (c & bit) continue;
+          for (int k = 0; k < 32; k += 2) {
+            uint32_t& to = w[cc >> 1][(cc & 1) * 4 + (k >> 3)][(k >> 1) & 3];
+            to = pack_bf16x2(__uint_as_float(o[k]) * inv, __uint_as_float(o[k + 1]) * inv);
+            if (inv == 0.f) to = 0;                        // (tensor memory may hold anything where nothing was added)
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && x.blocks > 0) mbar_arrive(&bar_ofree[s]);
+        // A row's 256 bytes are one thread's; written so, each store would touch 32 lines.  Eight lanes exchange their rows'
+        // 16-byte chunks (an 8 x 8 transposition), so that they write 128 bytes of one row together.
+        const int queries = min(p.nq, p.S - row0);
+        __nv_bfloat16* tile = p.O + ((static_cast<int64_t>(x.b) * p.S + row0) * p.Hq + x.g * p.G) * kD + (lane & 7) * 8;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? w[c][e] : w[c | bit][e], bit);
-              if (high) w[c][e] = got;
-              else w[c | bit][e] = got;
+        for (int cc = 0; cc < 2; ++cc) {
+#pragma unroll
+          for (int bit = 1; bit < 8; bit <<= 1) {
+            const bool high = (lane & bit) != 0;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              if (c & bit) continue;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? w[cc][c][e] : w[cc][c | bit][e], bit);
+                if (high) w[cc][c][e] = got;
+                else w[cc][c | bit][e] = got;
+              }
             }
           }
-        }
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {                      // chunk lane % 8 of row r - lane % 8 + c
-          const int rr = (r & ~7) + c, qq = (rr * per_query) >> 16;
-          if (qq < queries)
-            *reinterpret_cast<uint4*>(tile + (static_cast<int64_t>(qq) * p.Hq + rr - qq * p.G) * kD + cc * 64) =
-                make_uint4(w[c][0], w[c][1], w[c][2], w[c][3]);
+          for (int c = 0; c < 8; ++c) {                    // chunk lane % 8 of row r - lane % 8 + c
+            const int rr = (r & ~7) + c, qq = (rr * per_query) >> 16;
+            if (qq < queries)
+              *reinterpret_cast<uint4*>(tile + (static_cast<int64_t>(qq) * p.Hq + rr - qq * p.G) * kD + cc * 64) =
+                  make_uint4(w[cc][c][0], w[cc][c][1], w[cc][c][2], w[cc][c][3]);
+          }
         }
       }
-      if (real && p.LSE != nullptr) p.LSE[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-      // the O loads above are complete (wait::ld) before this slot's next pready arrive, which gates the next item's first O
-      tc_fence_before();
     }
+    tc_fence_before();
   }
 
   if (SPLIT) {
@@ -707,13 +747,13 @@ msa_status launch_window_prefill(const msa_window_prefill_args& a, cudaStream_t 
   p.O = static_cast<__nv_bfloat16*>(a.O);
   p.LSE = a.LSE;
   p.dev_err = a.dev_err;
-  const size_t smem = 1024 + 2 * static_cast<size_t>(kQTile) + static_cast<size_t>(kUnits) * kUnit;
+  const size_t smem = 1024 + 2 * static_cast<size_t>(kQTile) + static_cast<size_t>(units_of(split)) * kUnit;
   if (smem > dev.max_smem_optin) return fail(MSA_ERR_UNSUPPORTED, "window prefill: not enough shared memory");
   auto* kernel = split ? window_prefill_kernel<true> : window_prefill_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(window_prefill)");
   const int grid = split ? p.n_items * p.split : std::min(dev.num_sms, p.n_items);
-  e = launch_early(kernel, grid, kThreads, smem, stream, std::max(p.split, 1), qmap, kmap, vmap, p);
+  e = launch_early(kernel, grid, split ? kWorkers : kAll, smem, stream, std::max(p.split, 1), qmap, kmap, vmap, p);
   if (e != cudaSuccess) return cuda_fail(e, "window_prefill_kernel launch");
   return MSA_OK;
 }
