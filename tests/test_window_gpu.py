@@ -355,3 +355,71 @@ def test_few_tiles_many_launches(msa):
             want.append((O.clone(), LSE.clone()))
         if i % 4000 >= 3998:
             assert int(e.item()) == 0 and torch.equal(O, want[i % 2][0]) and torch.equal(LSE, want[i % 2][1])
+
+
+# ---------------------------------------------------------------------------
+# more tiles than SMs: a CTA works on pairs of tiles, one after another
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (30, 4), (129, 128), (200, 140), (1 << 30, 5)])
+@pytest.mark.parametrize("B,S,Hkv,G", [(3, 500, 8, 6), (16, 130, 8, 1), (2, 700, 8, 8), (4, 333, 8, 7), (40, 21, 4, 6), (40, 22, 4, 6), (5, 200, 8, 3),
+                                       (3, 270, 16, 5), (9, 200, 8, 2), (8, 150, 8, 4), (200, 1, 1, 6)])
+def test_many_tiles(msa, window, sinks, B, S, Hkv, G):
+    g = torch.Generator().manual_seed(S + G)
+    Q = (torch.randn(B, S, Hkv * G, D, generator=g) * 1.5).bfloat16().cuda()
+    K, V = (torch.randn(B, S, Hkv, D, generator=g).bfloat16().cuda() for _ in range(2))
+    got = run_prefill(msa, Q, K, V, window, sinks)
+    assert got[2] == 0
+    nq = 128 // G
+    rows = sorted({r for r in (0, nq - 1, nq, 2 * nq - 1, 2 * nq, 63, 64, 128, 129, 199, S - nq, S - 1) if 0 <= r < S})
+    few = [0, B - 1]                             # (sequences that are checked; the others against the same one alone)
+    check_prefill(Q[few], K[few], V[few], window, sinks, (got[0][few], got[1][few]), rows=rows)
+    b = B // 2
+    one = run_prefill(msa, Q[b:b + 1], K[b:b + 1], V[b:b + 1], window, sinks)
+    # (each rounds P and O to bf16, 2^-8 of the largest value at most)
+    assert np.abs(one[0][0] - got[0][b]).max() <= 4 * 2.0 ** -8 * float(V[b].abs().max()) and np.abs(one[1][0] - got[1][b]).max() <= 1e-4
+    again = run_prefill(msa, Q, K, V, window, sinks)
+    assert np.array_equal(got[0], again[0]) and np.array_equal(got[1], again[1])
+
+
+@pytest.mark.parametrize("S,Hkv,G", [(40, 8, 6), (21, 8, 6), (70, 8, 8), (150, 8, 2)])
+@pytest.mark.parametrize("window,sinks", [(100, 3), (1 << 30, 0)])
+def test_many_tiles_over_pages(msa, S, Hkv, G, window, sinks):
+    """With positions and pages that are none, and anything in the slots behind the last tokens."""
+    pos = [0, 300, -1, 61, 127, 500, 64, 1 << 20, 10, 333, 700, 128, 5, 90, 211, 400, 1, 2, 3, 255, 256, 257]
+    g, K, V, pt = paged([(p + S if 0 <= p < 1000 else 1) for p in pos], Hkv, S)
+    pt[1, 0], pt[5, 2], pt[9, 1] = -1, K.shape[0] + 7, -5
+    Q = torch.randn(len(pos), S, Hkv * G, D, generator=g).bfloat16().cuda()
+    for b, p in enumerate(pos):
+        if 0 <= p < 1000:
+            for t in range(p + S, -(-(p + S) // BK) * BK):
+                if 0 <= pt[b, t // BK] < len(K):
+                    K[pt[b, t // BK], :, t % BK], V[pt[b, t // BK], :, t % BK] = math.nan, -math.inf if t % 2 else math.nan
+    K, V = K.cuda(), V.cuda()
+    got = run_prefill(msa, Q, K, V, window, sinks, pt, pos)
+    assert got[2] == msa.MSA_DEVERR_BAD_LEN | msa.MSA_DEVERR_BAD_PAGE
+    bad = [b for b, p in enumerate(pos) if not 0 <= p < 1000]
+    assert (got[0][bad] == 0).all() and np.isneginf(got[1][bad]).all()
+    few = [b for b in range(0, len(pos), 3) if b not in bad] + [1, 5]
+    check_prefill(Q[few], K, V, window, sinks, (got[0][few], got[1][few]), pt[few], [pos[b] for b in few],
+                  rows=sorted({0, min(15, S - 1), 20, min(21, S - 1), S - 1}))
+
+
+def test_many_tiles_large_scores_and_rising_ones(msa):
+    g = torch.Generator().manual_seed(18)
+    V = torch.randn(1, 900, 8, D, generator=g).bfloat16().cuda()
+    v = host(V)[0]
+    for size in (1e4, 1e9, 1e15):                # equal keys have equal weights, however large the scores
+        Q = torch.full((1, 900, 32, D), size, dtype=torch.bfloat16, device="cuda")
+        K = torch.ones(1, 900, 8, D, dtype=torch.bfloat16, device="cuda")
+        O, LSE, e = run_prefill(msa, Q, K, V, 64, 4)
+        for i in (0, 5, 63, 64, 500, 899):
+            for h in (0, 31):
+                x = v[ref.seen(i, 64, 4), h // 4]
+                assert np.all(np.abs(O[0, i, h] - x.mean(0)) <= np.abs(x.mean(0)) * 2.0 ** -8 + np.abs(x).mean(0) * 2.0 ** -8)
+    # every block's scores are far above those of the block before: the running maximum moves and O is rescaled each time
+    Q = torch.randn(1, 900, 32, D, generator=g).abs().bfloat16().cuda()
+    K = (torch.rand(1, 900, 8, D, generator=g) * (1 + torch.arange(900)[None, :, None, None] // 64)).bfloat16().cuda()
+    for K in (K, K.flip(1).contiguous()):
+        got = run_prefill(msa, Q, K, V, 1 << 30, 0)
+        check_prefill(Q, K, V, 1 << 30, 0, got, rows=[0, 20, 21, 63, 64, 130, 500, 899])
