@@ -15,9 +15,14 @@
 // 2^-24 of a head's largest value); P is rounded once to fp16 (2^-11).
 //   P is held as 2^(z - m + 8 + e - E), e the exponent of the V block and (m, E) a pair kept for each head: m the score
 // and E the block exponent of some token so far.  What counts is the size of p * 2^e, the contribution to O: kept as
-// two numbers the pair stays exact where m is large, and a block of small values beside one of large values (2^80 apart at
-// most) neither overflows nor drops out.  A tile whose sum passes 2^15 moves the pair; the sum of p itself, without 2^e, is
-// taken beside it in fp32.  bf16 values need no e: P is rounded to bf16 (2^-9), as everywhere over bf16 pages.
+// two numbers the pair stays exact where m is large, and a block of large values after small ones (2^80 apart at most) does
+// not overflow.  A tile whose sum passes 2^15 moves the pair; the sum of p itself, without 2^e, is taken beside it in fp32.
+//   A block of small values after large ones would end in fp16's subnormals (from 2^-14 of P on, for equal scores 2^22 apart), and
+// its channels may be ones that the large block leaves at 0.  So a tile whose e is more than kApart below E forms P against
+// its own largest score, and its products are added to O in fp32 times what is left, 2^(z_max - m + e - E).  A token's weight is
+// therefore off by 2^-11 of it, or by 2^-25 of the largest token's weight, whatever the blocks' scales.  (8 x 60,001 tokens with blocks
+// of like scales 151 us, with every block but the first 2^28 below it 168.)
+//   bf16 values need no e: P is rounded to bf16 (2^-8), as everywhere over bf16 pages.
 //
 // Work.  As in the 4-bit kernel: dense rows' pages form one list that CTAs share equally (or in whole parts of rows where
 // there are few), sparse rows go to a CTA or a few; a warp takes tiles of 16 tokens through a ring of its own in
@@ -58,6 +63,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPShift = 8.f;                          // P is held as 2^(z - m + 8)
 constexpr float kNoMax = -FLT_MAX;                      // m before a first score: finite, so that no difference is NaN
 constexpr float kPMost = 32768.f;                       // most of a lane's sum of P (fp16 ends at 65504)
+constexpr float kApart = 8.f;                           // a block's exponent may lie so far below E before its products are apart
 
 // Dense rows and windows are shared out by the pages that each has; rows of at most k pages (selected ones, short windows) by k.
 enum Mode { kSparse, kShortWindow, kDense, kWindow };
@@ -175,6 +181,24 @@ struct Q8 {
       mma(acc[2 * w + 1], a0, a1, a2, a3, b0, b1);
     }
   }
+  // acc += by[head] * (V^T P), the products in fp32 of their own first; rows i with keep[i] only.  (Rare: a word of V at a time, so
+  // that the registers are those of the common form.)
+  static __device__ __forceinline__ void outputs_apart(const uint8_t* tile, int g, int t, const bool (&keep)[4], uint32_t b0,
+                                                       uint32_t b1, const float (&by)[2], float (&acc)[8][4]) {
+    const uint8_t* at = tile + kTile * kRow + 2 * t * kRow + ((g ^ (t << 1)) & 7) * 16;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      uint32_t v[4], a[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = keep[i] ? *reinterpret_cast<const volatile uint32_t*>(at + ((i & 1) + 8 * (i >> 1)) * kRow + (w >> 1) * 4) : 0;
+      e4m3x4_to_f16(__byte_perm(v[0], v[1], w & 1 ? 0x7362 : 0x5140), &a[0], &a[1]);
+      e4m3x4_to_f16(__byte_perm(v[2], v[3], w & 1 ? 0x7362 : 0x5140), &a[2], &a[3]);
+      float own[4] = {0.f, 0.f, 0.f, 0.f};
+      mma(own, a[0], a[1], a[2], a[3], b0, b1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[w][i] = fmaf(own[i], by[i & 1], acc[w][i]);
+    }
+  }
 };
 
 struct Bf16 {
@@ -269,14 +293,20 @@ __device__ __forceinline__ void attend_tile(const uint32_t (&q)[16], const float
     }
   };
   form();
-  if (__any_sync(0xffffffffu, fmaxf(sum[0], sum[1]) > kPMost)) {
+  auto largest = [&](int c) {     // score of the tile, of head c (the same in every g)
+    float z = __fmul_rn(fmaxf(s[c], s[c + 2]), coef[c]);
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, o));
+    return z;
+  };
+  auto far_below = [&] { return F::kScaled && ev < fmaxf(st->E[0], st->E[1]) - kApart; };
+  bool apart = false;
+  if (__any_sync(0xffffffffu, fmaxf(sum[0], sum[1]) > kPMost || far_below())) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      float z = __fmul_rn(fmaxf(s[c], s[c + 2]), coef[c]);
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, o));
+      const float z = largest(c);
       const float ahead = (z - st->m[c]) + (F::kScaled ? ev - st->E[c] : 0.f);
-      if (ahead > 0.f) {      // (the same in every g)
+      if (ahead > 0.f) {
         const float f = ex2(-ahead);
         st->m[c] = z;
         if (F::kScaled) st->E[c] = ev;
@@ -289,18 +319,36 @@ __device__ __forceinline__ void attend_tile(const uint32_t (&q)[16], const float
       }
     }
     form();
+    apart = __any_sync(0xffffffffu, far_below());
   }
   const float down = F::kScaled ? power_of_two(-ev) : 1.f;
   st->l[0] = F::kScaled ? fmaf(sum[0], down, st->l[0]) : st->l[0] + sum[0];
   st->l[1] = F::kScaled ? fmaf(sum[1], down, st->l[1]) : st->l[1] + sum[1];
   // P^T: from (row g, heads 2t, 2t + 1) to (head g, rows 2t, 2t + 1)
+  auto sees = [&](int i) { return WHOLE || seen.has(a + 2 * t + (i & 1) + 8 * (i >> 1)); };
+  if constexpr (F::kScaled) {
+    if (apart) {
+      float by[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float z = largest(c), own = z == -INFINITY ? 0.f : z;
+#pragma unroll
+        for (int i = c; i < 4; i += 2) e[i] = ex2(__fadd_rn(__fadd_rn(__fmul_rn(s[i], coef[c]), -own), kPShift));
+        // (-inf: no token of the tile is seen, every P is 0, and m may be none yet)
+        by[c] = z == -INFINITY ? 0.f : ex2(__fadd_rn(__fadd_rn(own, -st->m[c]), ev - st->E[c]));
+      }
+      const bool keep[4] = {sees(0), sees(1), sees(2), sees(3)};
+      F::outputs_apart(tile, g, t, keep, transpose8x8(F::pack(e[0], e[1])), transpose8x8(F::pack(e[2], e[3])), by, st->acc);
+      return;
+    }
+  }
   const uint32_t b0 = transpose8x8(F::pack(e[0], e[1])), b1 = transpose8x8(F::pack(e[2], e[3]));
   typename F::Values v;
   F::load(tile, g, t, &v);
   if (!WHOLE) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (!seen.has(a + 2 * t + (i & 1) + 8 * (i >> 1))) F::drop(&v, i);
+      if (!sees(i)) F::drop(&v, i);
   }
   F::outputs(v, b0, b1, st->acc);
 }
