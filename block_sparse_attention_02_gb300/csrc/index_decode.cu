@@ -736,11 +736,14 @@ msa_status launch_index_decode_impl(const msa_index_args& a, bool mq, cudaStream
   if (select_after) p.sel = nullptr;
 
   const size_t qtile = static_cast<size_t>(shared || mq ? kSharedRows : 16) * kDI * 2;
-  const size_t smem = 1024 + kStages * kStageBytes + 2 * qtile + ((mq ? 3 : 2) * static_cast<size_t>(a.B) + 1) * 4;
+  auto smem_of = [&](size_t B) { return 1024 + kStages * kStageBytes + 2 * qtile + ((mq ? 3 : 2) * B + 1) * 4; };
+  const size_t smem = smem_of(a.B);
   if (smem > dev.max_smem_optin) return fail(MSA_ERR_UNSUPPORTED, "decode index score: batch too large for shared memory");
   auto kern = mq ? index_decode_kernel<false, true>
                  : shared ? index_decode_kernel<true, false> : index_decode_kernel<false, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  // The limit of the largest batch in every call: it belongs to the kernel, and another thread's call of fewer sequences must
+  // not lower it before this launch.
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem_of(kMaxDecodeBatch)));
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(index_decode)");
   if (p.sel != nullptr && !a.scratch_zeroed) {   // otherwise zero by contract (and unused without p.sel)
     e = cudaMemsetAsync(p.counter, 0, static_cast<size_t>(a.B) * a.Hkv * sizeof(int32_t), stream);

@@ -261,10 +261,12 @@ __global__ void __launch_bounds__(kPlanThreads) release_kernel(const msa_release
   if (bad) report(p.dev_err, MSA_DEVERR_BAD_PAGE);
 }
 
-// One CTA, a plain grid, or (an update in place with more than one CTA's rows) one cluster.
+// One CTA, a plain grid, or (an update in place with more than one CTA's rows) one cluster.  smem: of this call, at most `most`
+// (of any call).  The kernel's limit is the same in every call: it belongs to the kernel, and another thread's call of fewer
+// requests must not lower it before this launch.
 template <class Args>
 msa_status launch_rows(void (*kernel)(const Args, const bool), const Args& a, int64_t items, bool in_place, size_t smem,
-                       cudaStream_t stream, const char* what) {
+                       size_t most, cudaStream_t stream, const char* what) {
   DeviceInfo dev;
   if (msa_status st = current_device(&dev); st != MSA_OK) return st;
   // enough threads for the sums (8 requests each at most), few for the small steps that come once a token
@@ -272,7 +274,7 @@ msa_status launch_rows(void (*kernel)(const Args, const bool), const Args& a, in
   const int64_t want = std::max<int64_t>((items + threads - 1) / threads, 1);
   const int ctas = static_cast<int>(std::min<int64_t>(want, in_place ? kPlanCluster : 2 * dev.num_sms));
   if (smem > (40u << 10)) {   // with the prefix sums' own shared memory past the 48 KiB default
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
     if (e != cudaSuccess) return cuda_fail(e, what);
   }
   const cudaError_t e = launch_early(kernel, ctas, threads, smem, stream, in_place ? ctas : 1, a, in_place);
@@ -285,15 +287,16 @@ msa_status launch_rows(void (*kernel)(const Args, const bool), const Args& a, in
 msa_status launch_plan_step(const msa_plan_args& a, cudaStream_t stream) {
   const bool in_place = a.seq_len_out == a.seq_len || a.free_count_out == a.free_count;
   const size_t smem = (3 * static_cast<size_t>(a.B) + 2) * sizeof(int);
-  return launch_rows(plan_step_kernel, a, a.N, in_place, smem, stream, "plan_step_kernel launch");
+  return launch_rows(plan_step_kernel, a, a.N, in_place, smem, (3 * kMaxDecodeBatch + 2) * sizeof(int), stream,
+                     "plan_step_kernel launch");
 }
 
 msa_status launch_release_pages(const msa_release_args& a, cudaStream_t stream) {
   const bool in_place = a.seq_len_out == a.seq_len || a.free_count_out == a.free_count;
   const size_t smem = (static_cast<size_t>(a.B) + 1) * sizeof(int);
   // at most B * max_pages pages come back, a few of the requests' as a rule
-  return launch_rows(release_kernel, a, static_cast<int64_t>(a.B) * a.max_pages / 8, in_place, smem, stream,
-                     "release_kernel launch");
+  return launch_rows(release_kernel, a, static_cast<int64_t>(a.B) * a.max_pages / 8, in_place, smem,
+                     (kMaxDecodeBatch + 1) * sizeof(int), stream, "release_kernel launch");
 }
 
 }  // namespace msa

@@ -454,10 +454,12 @@ __global__ void __launch_bounds__(kAlone) compact_kernel(const msa_compact_args 
   if (err != 0) report(p.dev_err, err);
 }
 
+// smem: of this call, at most `most` (of any call).  The kernel's limit is the same in every call: it belongs to the kernel, and
+// another thread's call of fewer requests must not lower it before this launch.
 template <class Args>
-msa_status launch_team(void (*kernel)(const Args), const Args& a, bool alone, size_t smem, cudaStream_t stream, const char* what) {
+msa_status launch_team(void (*kernel)(const Args), const Args& a, bool alone, size_t smem, size_t most, cudaStream_t stream, const char* what) {
   if (smem > (40u << 10)) {                 // with the sums' own shared memory past the 48 KiB default
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
     if (e != cudaSuccess) return cuda_fail(e, what);
   }
   const int ctas = alone ? 1 : kCluster;
@@ -524,18 +526,20 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_c
 
 msa_status launch_fork(const msa_fork_args& a, cudaStream_t stream) {
   const size_t smem = (3 * static_cast<size_t>(a.F) + a.B + 1) * sizeof(int);
-  return launch_team(fork_kernel, a, false, smem, stream, "fork_kernel launch");
+  return launch_team(fork_kernel, a, false, smem, (4 * kMaxDecodeBatch + 1) * sizeof(int), stream, "fork_kernel launch");
 }
+
+constexpr size_t kTableSmem = (kMaxDecodeBatch + 1) * sizeof(int);
 
 msa_status launch_release_shared(const msa_release_shared_args& a, cudaStream_t stream) {
   const size_t smem = (static_cast<size_t>(a.B) + 1) * sizeof(int);
   const bool alone = std::max<int64_t>(static_cast<int64_t>(a.B) * a.max_pages / 8, a.num_pages) <= kAloneItems;
-  return launch_team(release_shared_kernel, a, alone, smem, stream, "release_shared_kernel launch");
+  return launch_team(release_shared_kernel, a, alone, smem, kTableSmem, stream, "release_shared_kernel launch");
 }
 
 msa_status launch_compact(const msa_compact_args& a, cudaStream_t stream) {
   const size_t smem = (static_cast<size_t>(a.B) + 1) * sizeof(int);
-  return launch_team(compact_kernel, a, a.num_pages <= kAloneItems, smem, stream, "compact_kernel launch");
+  return launch_team(compact_kernel, a, a.num_pages <= kAloneItems, smem, kTableSmem, stream, "compact_kernel launch");
 }
 
 msa_status launch_copy_pages(const msa_copy_pages_args& a, cudaStream_t stream) {
