@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const msa_fork_args p) {
     const int b = tid + i * threads;
     len[i] = i < per_b && b < p.B ? p.seq_len[b] : 0;
   }
+  bool bad = false;
   team.sync();                              // lengths, counts and the stack's height are read, counts copied
   if (team.rank == team.ctas - 1) {
 #pragma unroll
@@ -241,6 +242,8 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const msa_fork_args p) {
           from = p.seq_pt[src[i] * p.max_pages + L[i] / kBk];
           to = p.free_pages[page_at[i]];
           p.seq_pt_out[dst[i] * p.max_pages + L[i] / kBk] = to;
+          // a copy that msa_copy_pages cannot make, or takes for a row without one (a stack's height outside it is named already)
+          bad |= from < 0 || from >= p.num_pages || (raw == count && (to < 0 || to >= p.num_pages));
         }
       }
       p.copy_src[x] = from;
@@ -248,7 +251,6 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const msa_fork_args p) {
     }
     if (tid == 0) *p.free_count_out = count - min(pages_needed, count);
   }
-  bool bad = false;
   for_entries(
       s_first, F, total, team, [&](int x, int j) { return p.seq_pt[s_src[x] * p.max_pages + j]; },
       [&](int x, int j, int page) {

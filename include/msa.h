@@ -980,7 +980,8 @@ msa_status msa_window_attn_prefill(const msa_window_prefill_args *args, msa_stre
  *     empty or that an earlier i names: left out, MSA_DEVERR_BAD_ROW.  A length outside [0, max_pages * Bk]: left out,
  *     MSA_DEVERR_BAD_LEN.  A source may be named any number of times.
  *   - A fork that needs a page when none is left is left out, and so is every later one that needs one: MSA_DEVERR_NO_PAGES.
- *   - A shared page id outside [0, num_pages) is handed on uncounted: MSA_DEVERR_BAD_PAGE.
+ *   - A page id outside [0, num_pages), of the source's pages or of the stack's top, is handed on, uncounted where it is a shared
+ *     one and uncopied where it is that of the last page: MSA_DEVERR_BAD_PAGE.
  * seq_len_out, seq_pt_out, free_count_out and page_shares_out may be the inputs.  B <= 4096, F <= 4096, num_pages <= 2^24,
  * F * max_pages < 2^30. */
 typedef struct msa_fork_args {
