@@ -676,7 +676,7 @@ def msa_fork_requests(src: torch.Tensor, dst: torch.Tensor, seq_len: torch.Tenso
 
     src, dst, copy_src, copy_dst [F] int32 (src < 0: left out); seq_len [B], seq_pt [B,max_pages], free_pages [cap] and
     free_count [1] as in ``msa_plan_step``; page_shares [num_pages] int32, a page's holders beyond the first (0 at the
-    start).  The outputs may be the inputs.
+    start).  The outputs may be the inputs.  How a request is shortened whose pages others hold: msa.h.
     """
     status = _abi.binding().fork_requests(
         src, dst, seq_len, seq_pt, free_pages, free_count, page_shares, seq_len_out, seq_pt_out, free_count_out,
@@ -753,7 +753,8 @@ def msa_window_attn_prefill(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, O
 
     Q [B,S,Hq,D]; K, V [B,S,Hkv,D], or with ``seq_pt`` [B,max_pages] and ``q_pos`` [B] int32 the page pools [P,Hkv,Bk,D],
     query s of sequence b then at position q_pos[b] + s (its token in the pages already); all bf16.  O [B,S,Hq,D] bf16 and
-    LSE [B,S,Hq] fp32 (dense).
+    LSE [B,S,Hq] fp32 (dense).  V must be finite for all S (q_pos + S) tokens of a sequence, padding too: a token that a query
+    does not see has the weight 0 there, and 0 * inf is NaN.  Slots behind them may hold anything.
     """
     status = _abi.binding().window_attn_prefill(
         Q, K, V, O, LSE, softmax_scale, dev_err, stream, window, sinks, seq_pt, q_pos)

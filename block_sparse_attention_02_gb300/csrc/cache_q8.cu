@@ -8,7 +8,8 @@
 // Tokens come to a block a few at a time.  A call's tokens of one page are a run: consecutive token rows in consecutive
 // slots (msa_plan_step's rows are).  A run that starts at row 0 starts the block anew, whatever an earlier owner of the
 // page left; one that starts later keeps the rows before it, and where it needs a larger scale these are rounded again
-// (the exponent moves, so only codes that become subnormal change).  So a block's scale is that of its own tokens alone.
+// (the exponent moves, so only codes that become subnormal change).  So a block's scale is the largest that the tokens stored in it
+// since row 0 was last written needed: that of its own tokens, and of any that the program dropped again.
 //
 // Work.  A CTA takes a window of token rows for one or a few heads of K or V: it reads their slots, and those behind them as
 // far as a run may reach, and stores the runs that start in the window, while the window's rows are on their way to L2.

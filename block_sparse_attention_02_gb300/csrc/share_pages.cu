@@ -2,7 +2,7 @@
 // pool's front, and the copies that these need.
 //
 // A request that continues another one's text (parallel samples, beams) needs its cached tokens.  Its full pages are
-// never written again, so both may hold them; only the page that is partly filled is copied.  page_shares counts a page's
+// not written again (as long as lengths only grow), so both may hold them; only the page that is partly filled is copied.  page_shares counts a page's
 // holders beyond the first, so that pages given out by msa_plan_step (0) need nothing, and a page goes back on the stack
 // when the count would fall below 0.
 //

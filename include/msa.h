@@ -815,7 +815,10 @@ typedef struct msa_q8_cache {
  * whose tokens come otherwise, or twice, is left with codes and a scale that fit no sum of them.  Pages fill from row 0 on:
  * tokens from row 0 on start the block anew (scale of these tokens alone, whatever the page held before), tokens from
  * a later row on keep the rows before them.  Where these need a larger scale, the rows before are rounded
- * again (which changes only values that become subnormal codes).  Rows behind the last token keep their codes. */
+ * again (which changes only values that become subnormal codes).  Rows behind the last token keep their codes.
+ * So a block's scale is the largest that a token stored in it since row 0 was last written needed: where a request is shortened
+ * (rejected draft tokens) and goes on from a later row, that of the dropped tokens stays, and the values are right to
+ * that scale's step. */
 typedef struct msa_append_q8_args {
     int64_t N;
     int Hkv, D, Bk;
@@ -964,7 +967,7 @@ msa_status msa_window_attn_prefill(const msa_window_prefill_args *args, msa_stre
  * Pages that several requests hold
  *
  * A request may go on from another one's cached tokens (parallel samples, beams, a common prompt): both hold its full
- * pages, which no append writes again.  page_shares [num_pages] counts each page's holders beyond the first: 0 for free pages
+ * pages, which no append writes again (lengths that a program lowers: msa_fork_requests, at its end).  page_shares [num_pages] counts each page's holders beyond the first: 0 for free pages
  * and for those that msa_plan_step gave out, so that call knows nothing of it; the calls here keep it.  Where pages are
  * shared, ended requests go through msa_release_shared_pages instead of msa_release_pages.
  *
@@ -983,7 +986,13 @@ msa_status msa_window_attn_prefill(const msa_window_prefill_args *args, msa_stre
  *   - A page id outside [0, num_pages), of the source's pages or of the stack's top, is handed on, uncounted where it is a shared
  *     one and uncopied where it is that of the last page: MSA_DEVERR_BAD_PAGE.
  * seq_len_out, seq_pt_out, free_count_out and page_shares_out may be the inputs.  B <= 4096, F <= 4096, num_pages <= 2^24,
- * F * max_pages < 2^30. */
+ * F * max_pages < 2^30.
+ *
+ * A full page is not written again as long as lengths only grow.  A program may lower a request's length (rejected draft
+ * tokens) within its last page where that page's count is 0.  Further down, or into a page that others hold, its next tokens
+ * would overwrite theirs, and the pages behind its new end would be lost (to msa_plan_step and the releases; msa_compact_pages
+ * finds them).  Instead: msa_fork_requests into an empty row, with seq_len (of this call alone) holding the lower length of the source,
+ * which copies the page that it ends in, shared or not; then msa_release_shared_pages of the old row at its old length. */
 typedef struct msa_fork_args {
     int B, F, Bk;
     const int32_t *src;           /* [F] */
