@@ -30,6 +30,7 @@
 // (tensor memory has no room for Q: 2 x (64 + 64 + 128) columns), so a block takes 640 cycles of 512.  32,768 tokens of 8 x 6 heads, window
 // 512 / 2,048 / 8,192: 0.51 / 1.26 / 3.92 ms, which is 0.78 us a block of both slots (1,630 TFLOP/s) and 5 us a pair of tiles: masked
 // blocks (three of a tile; 0.5 us), the wait for the next Q (1 us), and what the slots' chains take to empty and fill.
+// Over pages 2 to 8 % more for the same tiles (0.47, 1.29 and 4.25 ms for 0.46, 1.21 and 4.05 in one run).
 // With the outputs written by the softmax warps 0.55 / 1.31 / 3.94 ms, masks by comparisons instead of bits 0.52 / 1.27 / 3.92.
 // 128-key blocks without a second buffer: 131,072 tokens in 11.5 ms for 5.5; pairs of blocks (S with N = 128, no block ahead): 1.67 / 5.2 ms
 // where this form took 1.34 / 3.95.

@@ -849,8 +849,9 @@ msa_status msa_cache_expand_q8(const msa_expand_q8_args *args, msa_stream_t stre
 
 /* msa_sparse_attn_decode over an 8-bit cache: rows, page table, outputs, empty rows, page ids and workspace rules as in
  * msa_sparse_attn_decode_q4.  Cached values are exact in the products' fp16 operands, the block scales multiply scores and
- * probabilities in fp32; Q is scaled by a power of two per head into fp16's range, P is rounded to fp16: a token's weight is
- * off by 2^-11 of it, or by 2^-25 of the largest token's weight, whatever the scales of its block and of the others are.
+ * probabilities in fp32; Q is scaled by a power of two per head into fp16's range (exact, but for values below 2^-17 of the
+ * head's largest: a multiple of 2^-24 of it), P is rounded to fp16: a token's weight is off by 2^-11 of it, or by 2^-25 of the
+ * largest token's weight, whatever the scales of its block and of the others are.
  * Slots past a row's last token may hold anything.  Workspace: msa_attn_decode_q8_workspace_size(B, Hkv) bytes. */
 typedef struct msa_decode_q8_args {
     int B, Hq, Hkv, D, Bk, k;
