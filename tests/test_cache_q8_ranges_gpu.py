@@ -105,3 +105,21 @@ def test_large_values_of_one_token(msa):  # noqa: F811
     O, LSE, e = base.run_dense(msa, Q, cache, pt, lengths)
     assert e == 0
     check_channels(Q, base.values(cache), [[base.places(pt[b].numpy(), np.arange(L))] * 4 for b, L in enumerate(lengths)], (O, LSE))
+
+
+@pytest.mark.parametrize("order", ["first", "mixed"])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (300, 5)])
+def test_anything_in_slots_that_are_not_seen(msa, order, window, sinks):  # noqa: F811
+    """Blocks far apart, NaN codes in every slot that no query sees: nothing changes."""
+    lengths = [700, 1290, 40] * 40
+    Q, cache, pt = base.dense_case(msa, lengths, 2, 6, 4)
+    g = torch.Generator().manual_seed(8)
+    own_channels(cache, [pt[b, :-(-L // BK)].tolist() for b, L in enumerate(lengths)], order, g)
+    want = base.run_dense(msa, Q, cache, pt, lengths, window, sinks)
+    for b, L in enumerate(lengths):
+        hidden = np.setdiff1d(np.arange(-(-L // BK) * BK), ref.seen(L - 1, window, sinks))
+        page, row = (torch.as_tensor(x, device="cuda").long() for x in base.places(pt[b].numpy(), hidden))
+        cache.K_codes[page, :, row] = 0x7F
+        cache.V_codes[page, :, row] = 0xFF
+    got = base.run_dense(msa, Q, cache, pt, lengths, window, sinks)
+    assert got[2] == 0 and np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
